@@ -57,7 +57,8 @@ typedef enum {
 
 typedef enum {
     RTS_F32 = 0,  /* IEEE binary32 */
-    RTS_BF16 = 1  /* bfloat16 bit patterns (uint16_t) */
+    RTS_BF16 = 1, /* bfloat16 bit patterns (uint16_t) */
+    RTS_E4M3 = 2  /* 8-bit float e4m3 (no infinities; index queries and keys only) */
 } rts_dtype;
 
 /* Human-readable name of an rts_status value (static storage). */
@@ -340,6 +341,187 @@ int merge_select_pairs_rank_major(const int32_t* gathered_pairs, int32_t world, 
  */
 int merge_select_pairs_row_major(const int32_t* gathered_pairs, int32_t world, int64_t rows,
                                  int32_t kc, int32_t k, int32_t* out_ids, hipStream_t stream);
+
+/*
+ * assign_slots -- places a batch's new tokens in a paged cache: block tables,
+ * slot map and row ends from the requests' lengths, in the forms that
+ * emit_rows (req_id, block_table), topk_rows (row_ends) and the calls below
+ * read.
+ *
+ * ctx_lens   int32 [reqs]: tokens of each request already in the cache.
+ * new_lens   int32 [reqs]: tokens that this step adds.  Negative lengths count
+ *            as 0.  Token t of the batch belongs to the request i with
+ *            query_starts[i] <= t < query_starts[i + 1].
+ * reqs       0 <= reqs <= 8192.
+ * tokens     capacity of the token outputs (a padded batch size); a request
+ *            that reaches past it has its new tokens cut there.
+ * block_size >= 1 tokens per block; stride_rows physical rows per block.
+ * free_blocks int32 [free_count]: ids of free blocks, taken in order.
+ * block_table int32 [reqs, ld_table], table_cols columns used, updated in
+ *            place: request i keeps its first ceil(ctx / block_size) entries
+ *            and gets the next free blocks in columns up to
+ *            ceil((ctx + new) / block_size); requests take in ascending order.
+ *            Where the list is exhausted the entry is -1; columns at or past
+ *            table_cols are not written, though their blocks are taken.
+ * query_starts int32 [reqs + 1]: exclusive sums of the (cut) new lengths.
+ * req_id, row_ends, slots  int32 [tokens]: for token t of request i at
+ *            position p = ctx + t - query_starts[i]: i, p + 1 and
+ *            block_table[i, p / block_size] * stride_rows + p % block_size
+ *            (computed in 64 bits, stored as its low 32 bits; -1 where the
+ *            entry is negative or past the table).  Tokens behind the last
+ *            request get -1, 0 and -1.
+ * used       int32 [1]: blocks taken; more than free_count means that the
+ *            list was too short.
+ * No output may overlap an input or another output.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (reqs > 8192, tokens or free_count >=
+ *         2^31), RTS_EHIP.
+ */
+int assign_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t reqs, int64_t tokens,
+                 int32_t block_size, int64_t stride_rows, const int32_t* free_blocks,
+                 int64_t free_count, int32_t* block_table, int32_t table_cols, int64_t ld_table,
+                 int32_t* query_starts, int32_t* req_id, int32_t* row_ends, int32_t* slots,
+                 int32_t* used, hipStream_t stream);
+
+/*
+ * indexer_logits -- the matrix that topk_rows selects from.  For query token t
+ * and key s < e_t = clamp(row_ends[t], 0, cols):
+ *   logits[t, s] = key_scales[s] * sum_h weights[t, h] * max(0, q[t, h, :] . keys[s, :])
+ * with products and sums in 32 bits and one rounding at the end.  A NaN
+ * product stays NaN.  Columns [e_t, ld_logits) are never written.
+ *
+ * q          [rows, heads, dim] of dtype RTS_BF16 or RTS_E4M3: row t at
+ *            q + t * ld_q, its heads contiguous; ld_q in elements.
+ * heads      1..128.  dim 64 or 128.
+ * keys       [cols, dim], the same dtype, row stride ld_keys elements.
+ * weights    float [rows, ld_weights], first heads columns (a query scale is
+ *            the caller's to multiply in).
+ * key_scales float [cols] or NULL (= 1).
+ * row_ends   int32 [rows] or NULL (= cols).
+ * logits     float or bf16 bits (logits_dtype RTS_F32 or RTS_BF16)
+ *            [rows, ld_logits], ld_logits >= cols.
+ * q and keys and their row strides must be multiples of 16 bytes.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 128, cols >= 2^31),
+ *         RTS_EHIP.
+ */
+int indexer_logits(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ld_q,
+                   const void* keys, int64_t cols, int64_t ld_keys, const float* weights,
+                   int64_t ld_weights, const float* key_scales, const int32_t* row_ends, void* logits,
+                   int logits_dtype, int64_t ld_logits, hipStream_t stream);
+
+/*
+ * indexer_logits_paged -- indexer_logits with the keys of each token's request
+ * read through its block table: column s of token t is the key at physical row
+ *   block_table[req_id[t], s / block_size] * stride_rows + s % block_size
+ * of key_cache [cache_rows, ld_keys] (key_scales [cache_rows] by the same row).
+ * A key without a physical row (a negative block id, a row outside
+ * [0, cache_rows), a block past table_cols) has the logit NaN, which topk_rows
+ * drops; a token whose req_id is outside [0, table_rows) has no columns.
+ * cols bounds every row end (ld_logits >= cols).  Neighbouring tokens of the
+ * same request share the reads of their keys.
+ * Errors: those of indexer_logits, RTS_EINVAL for block_size < 1, ld_table <
+ *         table_cols, stride_rows < 0.
+ */
+int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim,
+                         int64_t ld_q, const void* key_cache, int64_t cache_rows, int64_t ld_keys,
+                         const float* weights, int64_t ld_weights, const float* key_scales,
+                         const int32_t* req_id, const int32_t* row_ends, const int32_t* block_table,
+                         int64_t table_rows, int32_t table_cols, int64_t ld_table, int32_t block_size,
+                         int64_t stride_rows, int64_t cols, void* logits, int logits_dtype,
+                         int64_t ld_logits, hipStream_t stream);
+
+/*
+ * latent_attend_rows -- attention over selected rows of a latent cache: one
+ * vector c of d_latent + d_rope elements a cached token, shared by all heads,
+ * is the key, and its first d_latent elements are the value (the queries come
+ * with the key projection absorbed).  For row t and head h, over the entries
+ * j < counts[t] with 0 <= ids[t, j] < cache_rows:
+ *   z_j = scale * q[t, h, :] . cache[ids[t, j], :]
+ *   lse[t, h] = log sum_j exp z_j,   out[t, h, :] = sum_j exp(z_j - lse) cache[ids[t, j], :d_latent]
+ * Other entries (-1 tails among them) are not read and contribute nothing; a
+ * row without entries gives zeros and -inf.  An id that occurs twice counts
+ * twice.  ids and counts are what emit_rows and the selects' rows forms write.
+ *
+ * q          bf16 [rows, heads, d_latent + d_rope]: row t, head h at
+ *            q + t * ld_q + h * ld_head (elements).
+ * d_latent   256 or 512; d_rope 64.
+ * cache      bf16 [cache_rows, ld_cache].
+ * ids        int32 [rows, ld_ids], first k columns used.
+ * counts     int32 [rows] or NULL (= k); clamped to [0, k].
+ * out        bf16 [rows, heads, d_latent], contiguous.
+ * lse        float [rows, heads] or NULL.
+ * workspace  optional device scratch, 16-byte aligned, of at least
+ *            latent_attend_rows_workspace_size bytes: lets a small batch split
+ *            each row's entries over several workgroups.  NULL with 0 bytes
+ *            runs every row in one piece.  Calls in flight at the same time
+ *            need workspaces of their own.
+ * q, cache, out and their strides must be multiples of 16 bytes.
+ * Scores, softmax statistics and sums are held in 32 bits; the weights are
+ * rounded to bf16 for the products with the values.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (d_latent, d_rope, heads > 1024),
+ *         RTS_EWORKSPACE, RTS_EHIP.
+ */
+size_t latent_attend_rows_workspace_size(int64_t rows, int32_t heads, int32_t d_latent, int32_t k);
+int latent_attend_rows(const void* q, int64_t rows, int32_t heads, int32_t d_latent, int32_t d_rope,
+                       int64_t ld_q, int64_t ld_head, const void* cache, int64_t cache_rows,
+                       int64_t ld_cache, const int32_t* ids, int32_t k, int64_t ld_ids,
+                       const int32_t* counts, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * latent_attend_paged -- latent attention of a batch's new tokens over their
+ * requests' whole cache, read through the block table.  Request i has the new
+ * tokens query_starts[i] .. query_starts[i + 1] and ctx_lens[i] cached tokens
+ * before them; the new tokens' own vectors are already in the cache, at
+ * positions ctx_lens[i] + j.  Token j of a request sees every position below
+ * ctx_lens[i] and, of the new ones,
+ *   tree == NULL: positions up to its own (causal);
+ *   otherwise:    draft j' < 64 iff bit j' of tree[t] is set (a tree of drafted
+ *                 tokens: the bits of its ancestors and its own).
+ * Position p lies at physical row
+ *   block_table[i, p / block_size] * stride_rows + p % block_size;
+ * one without a physical row (as in indexer_logits_paged) is not seen.  What
+ * is not seen never reaches a result, NaN and infinities included.  A token
+ * that sees nothing gives zeros and -inf.  Rows of out and lse behind
+ * query_starts[reqs] are not written.
+ *
+ * q, out, lse as in latent_attend_rows, over tokens rows (tokens bounds
+ * query_starts).  query_starts int32 [reqs + 1], non-decreasing from 0.
+ * tree       uint64 [tokens] or NULL.
+ * max_len    an upper bound of ctx_lens[i] + new tokens; it sets how the keys
+ *            are split, results hold for any value >= 0.
+ * workspace  as in latent_attend_rows, latent_attend_paged_workspace_size bytes.
+ * Errors: as latent_attend_rows and indexer_logits_paged.
+ */
+size_t latent_attend_paged_workspace_size(int64_t tokens, int64_t reqs, int32_t heads,
+                                          int32_t d_latent, int64_t max_len);
+int latent_attend_paged(const void* q, int64_t tokens, int32_t heads, int32_t d_latent,
+                        int32_t d_rope, int64_t ld_q, int64_t ld_head, const void* cache,
+                        int64_t cache_rows, int64_t ld_cache, const int32_t* query_starts,
+                        const int32_t* ctx_lens, int64_t reqs, const uint64_t* tree,
+                        const int32_t* block_table, int32_t table_cols, int64_t ld_table,
+                        int32_t block_size, int64_t stride_rows, int64_t max_len, float scale,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ * merge_attend_rank_major -- joins the partial attentions of world ranks that
+ * each own a part of the rows (emit_rows per dcp_rank, then
+ * latent_attend_rows), read in place from the rank-major all-gather buffers:
+ *   lse[t, h] = log sum_r exp lse_r[t, h],  out = sum_r exp(lse_r - lse) parts_r
+ * A rank whose lse is -inf contributes nothing and its part is not read; if
+ * all are, the result is zeros and -inf.
+ *
+ * parts      [world, rows, heads, dim] of dtype RTS_BF16 or RTS_F32, contiguous.
+ * part_lse   float [world, rows, heads], contiguous.
+ * world 1..64; dim a multiple of 8, at most 2048.
+ * out        [rows, heads, dim] of out_dtype RTS_BF16 or RTS_F32, contiguous.
+ * lse        float [rows, heads] or NULL.
+ * parts and out must be 16-byte aligned.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EHIP.
+ */
+int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse, int32_t world,
+                            int64_t rows, int32_t heads, int32_t dim, void* out, int out_dtype,
+                            float* lse, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,9 +25,10 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 RTS_OK, RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EWORKSPACE, RTS_EHIP = 0, -1, -2, -3, -4
-RTS_F32, RTS_BF16 = 0, 1
+RTS_F32, RTS_BF16, RTS_E4M3 = 0, 1, 2
 
-_i64, _i32, _p, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+_i64, _i32, _p, _sz, _f32 = (ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t,
+                             ctypes.c_float)
 _lib.rts_status_string.argtypes = [ctypes.c_int]
 _lib.rts_status_string.restype = ctypes.c_char_p
 _lib.topk_rows_workspace_size.argtypes = [ctypes.c_int, _i64, _i64, _i32]
@@ -45,7 +47,24 @@ _lib.merge_select_rank_major_rows.argtypes = [_p, _i32, _i64, _i32, _i32, _p, _p
 _lib.merge_rescue_rank_major_rows.argtypes = [_p, _p, _i32, _i64, _i32, _i32, _p, _p, _p, _p]
 _lib.rescue_push.argtypes = [_p, _i32, _i32, _i64, _i32, _i32, _p, _p, _p]
 _lib.merge_rescue_rank_major.argtypes = [_p, _p, _i32, _i64, _i32, _i32, _p, _p, _p]
-for _f in (_lib.topk_rows, _lib.topk_rows_noalloc, _lib.pack_candidates, _lib.merge_select_rank_major, _lib.pack_pairs,
+_lib.assign_slots.argtypes = [_p, _p, _i64, _i64, _i32, _i64, _p, _i64, _p, _i32, _i64, _p, _p, _p, _p, _p,
+                              _p]
+_lib.indexer_logits.argtypes = [_p, ctypes.c_int, _i64, _i32, _i32, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _p,
+                                ctypes.c_int, _i64, _p]
+_lib.indexer_logits_paged.argtypes = [_p, ctypes.c_int, _i64, _i32, _i32, _i64, _p, _i64, _i64, _p, _i64, _p,
+                                      _p, _p, _p, _i64, _i32, _i64, _i32, _i64, _i64, _p, ctypes.c_int, _i64,
+                                      _p]
+_lib.latent_attend_rows_workspace_size.argtypes = [_i64, _i32, _i32, _i32]
+_lib.latent_attend_rows_workspace_size.restype = _sz
+_lib.latent_attend_rows.argtypes = [_p, _i64, _i32, _i32, _i32, _i64, _i64, _p, _i64, _i64, _p, _i32, _i64, _p,
+                                    _f32, _p, _p, _p, _sz, _p]
+_lib.latent_attend_paged_workspace_size.argtypes = [_i64, _i64, _i32, _i32, _i64]
+_lib.latent_attend_paged_workspace_size.restype = _sz
+_lib.latent_attend_paged.argtypes = [_p, _i64, _i32, _i32, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _p,
+                                     _p, _i32, _i64, _i32, _i64, _i64, _f32, _p, _p, _p, _sz, _p]
+_lib.merge_attend_rank_major.argtypes = [_p, ctypes.c_int, _p, _i32, _i64, _i32, _i32, _p, ctypes.c_int, _p, _p]
+for _f in (_lib.assign_slots, _lib.indexer_logits, _lib.indexer_logits_paged, _lib.latent_attend_rows,
+           _lib.latent_attend_paged, _lib.merge_attend_rank_major, _lib.topk_rows, _lib.topk_rows_noalloc, _lib.pack_candidates, _lib.merge_select_rank_major, _lib.pack_pairs,
            _lib.merge_select_pairs_rank_major, _lib.rescue_push, _lib.merge_rescue_rank_major,
            _lib.merge_select_row_major, _lib.merge_select_pairs_row_major, _lib.emit_rows,
            _lib.merge_select_rank_major_rows, _lib.merge_rescue_rank_major_rows):
@@ -468,6 +487,322 @@ def merge_select_pairs_rank_major(gathered_pairs: torch.Tensor, k: int,
                                               _dev(out, "out"), _stream(stream)),
            "merge_select_pairs_rank_major")
     return out
+
+
+def _launch(fn, where: str, device: torch.device, stream, scratch, *args) -> None:
+    """Calls ``fn(*args, stream)`` with ``device`` current.  Memory allocated here
+    for the call (``scratch``) is kept until a stream other than the current one
+    is done with it."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    else:
+        if stream.device != device:
+            raise ValueError(f"{where}: stream must belong to the device of the tensors")
+        for t in scratch:
+            t.record_stream(stream)
+    s = ctypes.c_void_p(stream.cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, s), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, s), where)
+
+
+def _on(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and (not isinstance(t, torch.Tensor) or t.device != device):
+            raise ValueError(f"{name} must be a tensor on {device}")
+
+
+def _gpu(t, name: str) -> torch.device:
+    _dev(t, name)
+    return t.device
+
+
+def _out(t, shape, dtype, device, name: str, made: list) -> torch.Tensor:
+    """A caller's output tensor, checked, or a new one (listed in ``made``)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        made.append(t)
+    elif t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
+    return t
+
+
+def _scratch(workspace, need: int, device, made: list):
+    """(tensor or None, bytes) of a call's workspace argument."""
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be "auto", None or a GPU tensor')
+        if not need:
+            return None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        made.append(ws)
+        return ws, need
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of q")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _table(block_table: torch.Tensor):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.shape[0] > 0 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [Q, B_max] with unit column stride")
+    rows, cols = block_table.shape
+    return rows, cols, (block_table.stride(0) if rows > 1 and cols > 0 else cols)
+
+
+class SlotMap(NamedTuple):
+    """What assign_slots returns, int32 each; see assign_slots in the header."""
+    query_starts: torch.Tensor  # [Q + 1]
+    req_id: torch.Tensor        # [tokens]
+    row_ends: torch.Tensor      # [tokens]
+    slots: torch.Tensor         # [tokens]
+    used: torch.Tensor          # [1]
+
+
+def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, block_table: torch.Tensor,
+                 free_blocks: torch.Tensor, block_size: int, stride_rows: int | None = None,
+                 out: SlotMap | None = None, stream=None) -> SlotMap:
+    """Places a batch's new tokens in the paged cache: extends ``block_table`` [Q, B_max] in
+    place from ``free_blocks`` and returns the batch's SlotMap; see assign_slots in the header.
+
+    ``stride_rows`` defaults to ``block_size``."""
+    device = _gpu(ctx_lens, "ctx_lens")
+    reqs = ctx_lens.shape[0] if ctx_lens.dim() == 1 else -1
+    for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens), ("free_blocks", free_blocks)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 vector")
+    if new_lens.shape[0] != reqs or block_table.shape[0] != reqs:
+        raise ValueError("new_lens and block_table must have one entry per request")
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    table_rows, table_cols, ld_table = _table(block_table)
+    _on(device, new_lens=new_lens, block_table=block_table, free_blocks=free_blocks)
+    made = []
+    if out is None:
+        flat = torch.empty(reqs + 2 + 3 * tokens, dtype=torch.int32, device=device)
+        made.append(flat)
+        out = SlotMap(*flat.split([reqs + 1, tokens, tokens, tokens, 1]))
+    else:
+        for name, t, n in zip(SlotMap._fields, out, (reqs + 1, tokens, tokens, tokens, 1)):
+            _out(t, (n,), torch.int32, device, name, made)
+    _launch(_lib.assign_slots, "assign_slots", device, stream, made, ctx_lens.data_ptr(),
+            new_lens.data_ptr(), reqs, tokens, block_size, block_size if stride_rows is None else stride_rows,
+            free_blocks.data_ptr(), free_blocks.shape[0], block_table.data_ptr(), table_cols, ld_table,
+            out.query_starts.data_ptr(), out.req_id.data_ptr(), out.row_ends.data_ptr(),
+            out.slots.data_ptr(), out.used.data_ptr())
+    return out
+
+
+_INDEX_DTYPES = {torch.bfloat16: RTS_BF16, torch.float8_e4m3fn: RTS_E4M3}
+_FLOAT_DTYPES = {torch.float32: RTS_F32, torch.bfloat16: RTS_BF16}
+
+
+def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols, made):
+    """What indexer_logits and indexer_logits_paged check alike."""
+    device = _gpu(q, "q")
+    if q.dtype not in _INDEX_DTYPES or keys.dtype != q.dtype:
+        raise TypeError("q and keys must both be bfloat16 or both float8_e4m3fn")
+    if q.dim() != 3 or q.stride(2) != 1 or q.stride(1) != q.shape[2]:
+        raise ValueError("q must be [rows, heads, dim] with contiguous heads")
+    rows, heads, dim = q.shape
+    n_keys, kdim, ld_keys = _rows_ld(keys, "keys")
+    if kdim != dim:
+        raise ValueError("q and keys must have the same last dimension")
+    if weights.dtype != torch.float32:
+        raise TypeError("weights must be float32")
+    w_rows, w_cols, ld_w = _rows_ld(weights, "weights")
+    if (w_rows, w_cols) != (rows, heads):
+        raise ValueError(f"weights must be [{rows}, {heads}]")
+    if key_scales is not None and (key_scales.dtype != torch.float32 or key_scales.dim() != 1 or
+                                   key_scales.shape[0] != n_keys or not key_scales.is_contiguous()):
+        raise ValueError(f"key_scales must be a contiguous float32 vector of {n_keys} entries")
+    row_ends = _int32_vec(row_ends, rows, "row_ends")
+    if out is None:
+        if out_dtype not in _FLOAT_DTYPES:
+            raise TypeError("out_dtype must be float32 or bfloat16")
+        out = torch.empty((rows, cols), dtype=out_dtype, device=device)
+        made.append(out)
+    if out.dtype not in _FLOAT_DTYPES:
+        raise TypeError("out must be float32 or bfloat16")
+    out_rows, out_cols, ld_out = _rows_ld(out, "out")
+    if out_rows < rows or out_cols < cols:
+        raise ValueError(f"out must hold at least [{rows}, {cols}] (got {tuple(out.shape)})")
+    _on(device, keys=keys, weights=weights, key_scales=key_scales, row_ends=row_ends, out=out)
+    ld_q = q.stride(0) if rows > 1 else heads * dim
+    if rows <= 1:
+        ld_out = max(ld_out, cols)
+    return device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def indexer_logits(q: torch.Tensor, keys: torch.Tensor, weights: torch.Tensor,
+                   key_scales: torch.Tensor | None = None, row_ends: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """The logits [rows, cols] that topk_rows selects from: for ``q`` [rows, heads, dim], ``keys``
+    [cols, dim] and ``weights`` [rows, heads], the weighted sum over heads of relu(q . k), times the
+    key's scale; see indexer_logits in the header.  Columns at or past a row's end are not written."""
+    made = []
+    cols = keys.shape[0]
+    device, rows, heads, dim, ld_q, _, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
+        q, keys, weights, key_scales, row_ends, out, out_dtype, cols, made)
+    _launch(_lib.indexer_logits, "indexer_logits", device, stream, made, q.data_ptr(),
+            _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, keys.data_ptr(), cols, ld_keys,
+            weights.data_ptr(), ld_w, _ptr(key_scales), _ptr(row_ends), out.data_ptr(),
+            _FLOAT_DTYPES[out.dtype], ld_out)
+    return out
+
+
+def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torch.Tensor,
+                         req_id: torch.Tensor, row_ends: torch.Tensor, block_table: torch.Tensor,
+                         block_size: int, cols: int, key_scales: torch.Tensor | None = None,
+                         stride_rows: int | None = None, out: torch.Tensor | None = None,
+                         out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """indexer_logits over the paged ``key_cache`` [cache_rows, dim] of each token's request (the
+    ``req_id`` and ``row_ends`` of assign_slots); see indexer_logits_paged in the header."""
+    made = []
+    if cols < 0:
+        raise ValueError("cols must not be negative")
+    device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
+        q, key_cache, weights, key_scales, row_ends, out, out_dtype, cols, made)
+    req_id = _int32_vec(req_id, rows, "req_id")
+    if req_id is None or row_ends is None:
+        raise ValueError("req_id and row_ends are required")
+    table_rows, table_cols, ld_table = _table(block_table)
+    _on(device, req_id=req_id, block_table=block_table)
+    _launch(_lib.indexer_logits_paged, "indexer_logits_paged", device, stream, made, q.data_ptr(),
+            _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, key_cache.data_ptr(), n_keys, ld_keys,
+            weights.data_ptr(), ld_w, _ptr(key_scales), req_id.data_ptr(), row_ends.data_ptr(),
+            block_table.data_ptr(), table_rows, table_cols, ld_table, block_size,
+            block_size if stride_rows is None else stride_rows, cols, out.data_ptr(),
+            _FLOAT_DTYPES[out.dtype], ld_out)
+    return out
+
+
+def _attend_inputs(q, cache, d_latent, out, lse, made):
+    """What latent_attend_rows and latent_attend_paged check alike."""
+    device = _gpu(q, "q")
+    if q.dtype != torch.bfloat16 or cache.dtype != torch.bfloat16:
+        raise TypeError("q and cache must be bfloat16")
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [rows, heads, d_latent + d_rope] with unit element stride")
+    rows, heads, d = q.shape
+    cache_rows, cd, ld_cache = _rows_ld(cache, "cache")
+    if cd != d or not 0 < d_latent <= d:
+        raise ValueError("q and cache must have the same last dimension, at least d_latent")
+    ld_head = q.stride(1) if heads > 1 else d
+    ld_q = q.stride(0) if rows > 1 else heads * d
+    out = _out(out, (rows, heads, d_latent), torch.bfloat16, device, "out", made)
+    lse = _out(lse, (rows, heads), torch.float32, device, "lse", made)
+    _on(device, cache=cache)
+    return device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse
+
+
+def latent_attend_rows_workspace_size(rows: int, heads: int, d_latent: int, k: int) -> int:
+    return int(_lib.latent_attend_rows_workspace_size(rows, heads, d_latent, k))
+
+
+def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, scale: float,
+                       d_latent: int = 512, counts: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace="auto", stream=None):
+    """Attention of ``q`` [rows, heads, d] over the rows ``ids`` [rows, k] of the latent ``cache``
+    [cache_rows, d], whose first ``d_latent`` elements are the values; ``ids`` and ``counts`` as emit_rows
+    writes them (rows_out, valid_out).  Returns (out [rows, heads, d_latent], lse [rows, heads]); see
+    latent_attend_rows in the header.  ``workspace`` as in topk_rows."""
+    made = []
+    device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
+        q, cache, d_latent, out, lse, made)
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    id_rows, k, ld_ids = _rows_ld(ids, "ids")
+    if id_rows != rows:
+        raise ValueError("ids must have one row per query row")
+    if rows <= 1:
+        ld_ids = max(ld_ids, k)
+    counts = _int32_vec(counts, rows, "counts")
+    _on(device, ids=ids, counts=counts)
+    ws, ws_bytes = _scratch(workspace, latent_attend_rows_workspace_size(rows, heads, d_latent, k)
+                            if isinstance(workspace, str) else 0, device, made)
+    _launch(_lib.latent_attend_rows, "latent_attend_rows", device, stream, made, q.data_ptr(), rows, heads,
+            d_latent, d - d_latent, ld_q, ld_head, cache.data_ptr(), cache_rows, ld_cache, ids.data_ptr(), k,
+            ld_ids, _ptr(counts), scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
+    return out, lse
+
+
+def latent_attend_paged_workspace_size(tokens: int, reqs: int, heads: int, d_latent: int,
+                                       max_len: int) -> int:
+    return int(_lib.latent_attend_paged_workspace_size(tokens, reqs, heads, d_latent, max_len))
+
+
+def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torch.Tensor,
+                        ctx_lens: torch.Tensor, block_table: torch.Tensor, block_size: int, scale: float,
+                        d_latent: int = 512, stride_rows: int | None = None,
+                        tree: torch.Tensor | None = None, max_len: int | None = None,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        workspace="auto", stream=None):
+    """Attention of a batch's new tokens ``q`` [tokens, heads, d] over their requests' whole paged
+    latent cache, causal or by the ancestor masks ``tree`` (int64 or uint64 [tokens], bit j: draft j of the
+    request is seen); ``query_starts`` as assign_slots writes it.  ``max_len`` bounds the requests' lengths
+    and only steers the split (default: what the table holds).  Returns (out, lse); see
+    latent_attend_paged in the header.  ``workspace`` as in topk_rows."""
+    made = []
+    device, tokens, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
+        q, cache, d_latent, out, lse, made)
+    table_rows, table_cols, ld_table = _table(block_table)
+    ctx_lens = _int32_vec(ctx_lens, table_rows, "ctx_lens")
+    query_starts = _int32_vec(query_starts, table_rows + 1, "query_starts")
+    if ctx_lens is None or query_starts is None:
+        raise ValueError("query_starts and ctx_lens are required")
+    if tree is not None and (tree.dtype not in (torch.int64, torch.uint64) or tree.dim() != 1 or
+                             tree.shape[0] < tokens or not tree.is_contiguous()):
+        raise ValueError(f"tree must be a contiguous 64-bit vector of >= {tokens} entries")
+    if max_len is None:
+        max_len = table_cols * block_size
+    _on(device, query_starts=query_starts, ctx_lens=ctx_lens, block_table=block_table, tree=tree)
+    ws, ws_bytes = _scratch(workspace,
+                            latent_attend_paged_workspace_size(tokens, table_rows, heads, d_latent, max_len)
+                            if isinstance(workspace, str) else 0, device, made)
+    _launch(_lib.latent_attend_paged, "latent_attend_paged", device, stream, made, q.data_ptr(), tokens,
+            heads, d_latent, d - d_latent, ld_q, ld_head, cache.data_ptr(), cache_rows, ld_cache,
+            query_starts.data_ptr(), ctx_lens.data_ptr(), table_rows, _ptr(tree), block_table.data_ptr(),
+            table_cols, ld_table, block_size, block_size if stride_rows is None else stride_rows, max_len,
+            scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
+    return out, lse
+
+
+def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.Tensor | None = None,
+                            out_dtype=None, out_lse: torch.Tensor | None = None, stream=None):
+    """Joins the partial attentions ``parts`` [W, rows, heads, dim] of W ranks by their ``lse``
+    [W, rows, heads]; returns (out [rows, heads, dim], lse [rows, heads]); see merge_attend_rank_major in
+    the header.  ``out_dtype`` defaults to the parts' type."""
+    device = _gpu(parts, "parts")
+    if parts.dtype not in _FLOAT_DTYPES:
+        raise TypeError("parts must be float32 or bfloat16")
+    if parts.dim() != 4 or not parts.is_contiguous():
+        raise ValueError("parts must be contiguous [W, rows, heads, dim]")
+    world, rows, heads, dim = parts.shape
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (world, rows, heads) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 [{world}, {rows}, {heads}]")
+    made = []
+    if out_dtype is None:
+        out_dtype = parts.dtype if out is None else out.dtype
+    if out_dtype not in _FLOAT_DTYPES:
+        raise TypeError("out must be float32 or bfloat16")
+    out = _out(out, (rows, heads, dim), out_dtype, device, "out", made)
+    out_lse = _out(out_lse, (rows, heads), torch.float32, device, "out_lse", made)
+    _on(device, lse=lse)
+    _launch(_lib.merge_attend_rank_major, "merge_attend_rank_major", device, stream, made, parts.data_ptr(),
+            _FLOAT_DTYPES[parts.dtype], lse.data_ptr(), world, rows, heads, dim, out.data_ptr(),
+            _FLOAT_DTYPES[out.dtype], out_lse.data_ptr())
+    return out, out_lse
 
 
 def raw_library() -> ctypes.CDLL:

@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librow_top_select.so")
 OBJDIR = os.path.join(HERE, "_build")
-SOURCES = ["rts_api.cpp", "rts_topk_rows.hip", "rts_merge.hip"]
+SOURCES = ["rts_api.cpp", "rts_topk_rows.hip", "rts_merge.hip", "rts_slots.hip",
+           "rts_indexer.hip", "rts_latent.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

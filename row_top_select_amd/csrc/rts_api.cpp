@@ -258,4 +258,201 @@ int merge_select_pairs_row_major(const int32_t* gathered_pairs, int32_t world, i
     return merge_pairs_checked(gathered_pairs, true, world, rows, kc, k, out_ids, stream);
 }
 
+int assign_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t reqs, int64_t tokens,
+                 int32_t block_size, int64_t stride_rows, const int32_t* free_blocks,
+                 int64_t free_count, int32_t* block_table, int32_t table_cols, int64_t ld_table,
+                 int32_t* query_starts, int32_t* req_id, int32_t* row_ends, int32_t* slots,
+                 int32_t* used, hipStream_t stream) {
+    if (reqs < 0 || tokens < 0 || block_size < 1 || stride_rows < 0 || free_count < 0 ||
+        table_cols < 0 || ld_table < table_cols)
+        return RTS_EINVAL;
+    if (reqs > rts::kMaxReqs || tokens > 0x7FFFFFFFll || free_count > 0x7FFFFFFFll)
+        return RTS_EUNSUPPORTED;
+    if (!query_starts || !used || (reqs > 0 && (!ctx_lens || !new_lens)) ||
+        (tokens > 0 && (!req_id || !row_ends || !slots)) || (free_count > 0 && !free_blocks) ||
+        (reqs > 0 && table_cols > 0 && !block_table))
+        return RTS_EINVAL;
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) ||
+        !aligned(block_table, 4) || !aligned(query_starts, 4) || !aligned(req_id, 4) ||
+        !aligned(row_ends, 4) || !aligned(slots, 4) || !aligned(used, 4))
+        return RTS_EINVAL;
+    return rts::launch_assign_slots(ctx_lens, new_lens, reqs, tokens, block_size, stride_rows, free_blocks,
+                                    free_count, block_table, table_cols, ld_table, query_starts, req_id,
+                                    row_ends, slots, used, stream);
+}
+
+namespace {
+// What indexer_logits and indexer_logits_paged check alike.
+int logits_args(const rts::LogitsArgs& a) {
+    if (a.dtype != RTS_BF16 && a.dtype != RTS_E4M3) return RTS_EINVAL;
+    if (a.logits_dtype != RTS_F32 && a.logits_dtype != RTS_BF16) return RTS_EINVAL;
+    if (a.rows < 0 || a.cols < 0 || a.heads < 1 || a.dim < 1 || a.ld_weights < a.heads ||
+        a.ld_logits < a.cols || a.ld_keys < a.dim || a.ld_q < (int64_t)a.heads * a.dim)
+        return RTS_EINVAL;
+    if (a.heads > 128 || (a.dim != 64 && a.dim != 128) || a.cols > 0x7FFFFFFFll || a.rows > 0x7FFFFFFFll)
+        return RTS_EUNSUPPORTED;
+    if (a.rows == 0 || a.cols == 0) return RTS_OK;
+    const int64_t esz = a.dtype == RTS_BF16 ? 2 : 1;
+    if (!a.q || !a.weights || !a.logits) return RTS_EINVAL;
+    if (!aligned(a.q, 16) || !aligned(a.keys, 16) || a.ld_q * esz % 16 != 0 || a.ld_keys * esz % 16 != 0 ||
+        !aligned(a.weights, 4) || !aligned(a.key_scales, 4) || !aligned(a.row_ends, 4) ||
+        !aligned(a.logits, a.logits_dtype == RTS_F32 ? 4 : 2))
+        return RTS_EINVAL;
+    return RTS_OK;
+}
+
+int pages_args(const int32_t* block_table, int64_t table_rows, int32_t table_cols, int64_t ld_table,
+               int32_t block_size, int64_t stride_rows, int64_t cache_rows) {
+    if (table_rows < 0 || table_cols < 0 || ld_table < table_cols || block_size < 1 || stride_rows < 0 ||
+        cache_rows < 0 || !aligned(block_table, 4) || (table_rows > 0 && table_cols > 0 && !block_table))
+        return RTS_EINVAL;
+    return RTS_OK;
+}
+}  // namespace
+
+int indexer_logits(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ld_q,
+                   const void* keys, int64_t cols, int64_t ld_keys, const float* weights,
+                   int64_t ld_weights, const float* key_scales, const int32_t* row_ends, void* logits,
+                   int logits_dtype, int64_t ld_logits, hipStream_t stream) {
+    rts::LogitsArgs a{};
+    a.q = q, a.keys = keys, a.weights = weights, a.key_scales = key_scales, a.row_ends = row_ends;
+    a.logits = logits, a.rows = rows, a.cols = cols, a.ld_q = ld_q, a.ld_keys = ld_keys;
+    a.ld_weights = ld_weights, a.ld_logits = ld_logits, a.heads = heads, a.dim = dim;
+    a.dtype = dtype, a.logits_dtype = logits_dtype;
+    const int rc = logits_args(a);
+    if (rc != RTS_OK) return rc;
+    if (rows == 0 || cols == 0) return RTS_OK;
+    if (!keys) return RTS_EINVAL;
+    return rts::launch_indexer_logits(a, stream);
+}
+
+int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim,
+                         int64_t ld_q, const void* key_cache, int64_t cache_rows, int64_t ld_keys,
+                         const float* weights, int64_t ld_weights, const float* key_scales,
+                         const int32_t* req_id, const int32_t* row_ends, const int32_t* block_table,
+                         int64_t table_rows, int32_t table_cols, int64_t ld_table, int32_t block_size,
+                         int64_t stride_rows, int64_t cols, void* logits, int logits_dtype,
+                         int64_t ld_logits, hipStream_t stream) {
+    rts::LogitsArgs a{};
+    a.q = q, a.keys = key_cache, a.weights = weights, a.key_scales = key_scales, a.row_ends = row_ends;
+    a.req_id = req_id, a.logits = logits, a.rows = rows, a.cols = cols, a.ld_q = ld_q;
+    a.ld_keys = ld_keys, a.ld_weights = ld_weights, a.ld_logits = ld_logits, a.heads = heads;
+    a.dim = dim, a.dtype = dtype, a.logits_dtype = logits_dtype;
+    int rc = logits_args(a);
+    if (rc != RTS_OK) return rc;
+    rc = pages_args(block_table, table_rows, table_cols, ld_table, block_size, stride_rows, cache_rows);
+    if (rc != RTS_OK) return rc;
+    if (rows == 0 || cols == 0) return RTS_OK;
+    if (!req_id || !row_ends || !aligned(req_id, 4) || (cache_rows > 0 && !key_cache)) return RTS_EINVAL;
+    a.pages = rts::make_pages(block_table, table_rows, table_cols, ld_table, block_size, stride_rows,
+                              cache_rows);
+    return rts::launch_indexer_logits(a, stream);
+}
+
+namespace {
+// What latent_attend_rows and latent_attend_paged check alike.
+int attend_args(const rts::AttendArgs& a, int32_t d_rope) {
+    if (a.rows < 0 || a.heads < 1 || a.d_latent < 1 || d_rope < 0 || a.cache_rows < 0) return RTS_EINVAL;
+    const int64_t d = (int64_t)a.d_latent + d_rope;
+    if (a.ld_cache < d || a.ld_head < d || a.ld_q < 0) return RTS_EINVAL;
+    if ((a.d_latent != 256 && a.d_latent != 512) || d_rope != 64 || a.heads > 1024 ||
+        a.rows > 0x7FFFFFFFll / a.heads)
+        return RTS_EUNSUPPORTED;
+    if (a.rows == 0) return RTS_OK;
+    if (!a.q || !a.out || (a.cache_rows > 0 && !a.cache)) return RTS_EINVAL;
+    if (!aligned(a.q, 16) || !aligned(a.cache, 16) || !aligned(a.out, 16) || a.ld_q % 8 != 0 ||
+        a.ld_head % 8 != 0 || a.ld_cache % 8 != 0 || !aligned(a.lse, 4))
+        return RTS_EINVAL;
+    return RTS_OK;
+}
+
+int attend_planned(const rts::AttendArgs& a, const rts::AttendPlan& plan, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+    if (workspace && workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
+    if (workspace && !aligned(workspace, 16)) return RTS_EINVAL;
+    return rts::launch_latent_attend(a, plan, workspace, stream);
+}
+}  // namespace
+
+size_t latent_attend_rows_workspace_size(int64_t rows, int32_t heads, int32_t d_latent, int32_t k) {
+    if (rows < 1 || heads < 1 || heads > 1024 || rows > 0x7FFFFFFFll / heads || k < 0 ||
+        (d_latent != 256 && d_latent != 512))
+        return 0;
+    return rts::plan_attend_rows(rows, heads, d_latent, k, true).ws_bytes;
+}
+
+int latent_attend_rows(const void* q, int64_t rows, int32_t heads, int32_t d_latent, int32_t d_rope,
+                       int64_t ld_q, int64_t ld_head, const void* cache, int64_t cache_rows,
+                       int64_t ld_cache, const int32_t* ids, int32_t k, int64_t ld_ids,
+                       const int32_t* counts, float scale, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+    rts::AttendArgs a{};
+    a.paged = false;
+    a.q = static_cast<const uint16_t*>(q), a.cache = static_cast<const uint16_t*>(cache);
+    a.out = static_cast<uint16_t*>(out), a.lse = lse, a.rows = rows, a.ld_q = ld_q, a.ld_head = ld_head;
+    a.cache_rows = cache_rows, a.ld_cache = ld_cache, a.heads = heads, a.d_latent = d_latent;
+    a.scale = scale, a.ids = ids, a.counts = counts, a.ld_ids = ld_ids, a.k = k;
+    if (k < 0 || ld_ids < k || (workspace_bytes > 0 && !workspace)) return RTS_EINVAL;
+    const int rc = attend_args(a, d_rope);
+    if (rc != RTS_OK) return rc;
+    if (rows == 0) return RTS_OK;
+    if ((k > 0 && !ids) || !aligned(ids, 4) || !aligned(counts, 4)) return RTS_EINVAL;
+    return attend_planned(a, rts::plan_attend_rows(rows, heads, d_latent, k, workspace != nullptr),
+                          workspace, workspace_bytes, stream);
+}
+
+size_t latent_attend_paged_workspace_size(int64_t tokens, int64_t reqs, int32_t heads,
+                                          int32_t d_latent, int64_t max_len) {
+    if (tokens < 1 || reqs < 1 || heads < 1 || heads > 1024 || tokens > 0x7FFFFFFFll / heads ||
+        max_len < 0 || (d_latent != 256 && d_latent != 512))
+        return 0;
+    return rts::plan_attend_paged(tokens, reqs, heads, d_latent, max_len, true).ws_bytes;
+}
+
+int latent_attend_paged(const void* q, int64_t tokens, int32_t heads, int32_t d_latent,
+                        int32_t d_rope, int64_t ld_q, int64_t ld_head, const void* cache,
+                        int64_t cache_rows, int64_t ld_cache, const int32_t* query_starts,
+                        const int32_t* ctx_lens, int64_t reqs, const uint64_t* tree,
+                        const int32_t* block_table, int32_t table_cols, int64_t ld_table,
+                        int32_t block_size, int64_t stride_rows, int64_t max_len, float scale,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+    rts::AttendArgs a{};
+    a.paged = true;
+    a.q = static_cast<const uint16_t*>(q), a.cache = static_cast<const uint16_t*>(cache);
+    a.out = static_cast<uint16_t*>(out), a.lse = lse, a.rows = tokens, a.ld_q = ld_q, a.ld_head = ld_head;
+    a.cache_rows = cache_rows, a.ld_cache = ld_cache, a.heads = heads, a.d_latent = d_latent;
+    a.scale = scale, a.query_starts = query_starts, a.ctx_lens = ctx_lens, a.reqs = reqs;
+    a.max_len = max_len, a.tree = tree;
+    if (reqs < 0 || max_len < 0 || (workspace_bytes > 0 && !workspace)) return RTS_EINVAL;
+    int rc = attend_args(a, d_rope);
+    if (rc != RTS_OK) return rc;
+    rc = pages_args(block_table, reqs, table_cols, ld_table, block_size, stride_rows, cache_rows);
+    if (rc != RTS_OK) return rc;
+    if (reqs > 0x7FFFFFFFll - tokens * heads) return RTS_EUNSUPPORTED;
+    if (tokens == 0 || reqs == 0) return RTS_OK;
+    if (!query_starts || !ctx_lens || !aligned(query_starts, 4) || !aligned(ctx_lens, 4) ||
+        !aligned(tree, 8))
+        return RTS_EINVAL;
+    a.pages = rts::make_pages(block_table, reqs, table_cols, ld_table, block_size, stride_rows, cache_rows);
+    return attend_planned(a, rts::plan_attend_paged(tokens, reqs, heads, d_latent, max_len,
+                                                    workspace != nullptr),
+                          workspace, workspace_bytes, stream);
+}
+
+int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse, int32_t world,
+                            int64_t rows, int32_t heads, int32_t dim, void* out, int out_dtype,
+                            float* lse, hipStream_t stream) {
+    if ((dtype != RTS_F32 && dtype != RTS_BF16) || (out_dtype != RTS_F32 && out_dtype != RTS_BF16))
+        return RTS_EINVAL;
+    if (world < 1 || world > 64 || rows < 0 || heads < 1 || dim < 8 || dim % 8 != 0) return RTS_EINVAL;
+    if (dim > 2048 || rows > 0x7FFFFFFFll / heads) return RTS_EUNSUPPORTED;
+    if (rows == 0) return RTS_OK;
+    if (!parts || !part_lse || !out) return RTS_EINVAL;
+    if (!aligned(parts, 16) || !aligned(out, 16) || !aligned(part_lse, 4) || !aligned(lse, 4))
+        return RTS_EINVAL;
+    return rts::launch_merge_attend(parts, dtype, part_lse, world, rows, heads, dim, out, out_dtype, lse,
+                                    nullptr, stream);
+}
+
 }  // extern "C"

@@ -78,4 +78,77 @@ int launch_emit_rows(const int32_t* ids, int64_t rows, int32_t k, int32_t world,
 int launch_merge_pairs(const int32_t* pairs, bool row_major, int32_t world, int64_t rows,
                        int32_t kc, int32_t k, int32_t* out_ids, hipStream_t stream);
 
+// ------------------------------------------------------------------ paged caches
+
+// Requests' block tables over a cache of physical rows.
+struct Pages {
+    const int32_t* table;  // [table_rows, ld]
+    int64_t table_rows, ld, stride_rows, cache_rows;
+    int32_t cols, block_size;
+    int32_t shift;  // log2(block_size), or -1 where it is no power of two
+};
+
+inline Pages make_pages(const int32_t* table, int64_t table_rows, int32_t cols, int64_t ld,
+                        int32_t block_size, int64_t stride_rows, int64_t cache_rows) {
+    int32_t shift = -1;
+    for (int32_t i = 0; i < 31; ++i)
+        if (block_size == (1 << i)) shift = i;
+    return Pages{table, table_rows, ld, stride_rows, cache_rows, cols, block_size, shift};
+}
+
+constexpr int64_t kMaxReqs = 8192;  // assign_slots keeps two sums a request in LDS
+
+int launch_assign_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t reqs, int64_t tokens,
+                        int32_t block_size, int64_t stride_rows, const int32_t* free_blocks,
+                        int64_t free_count, int32_t* block_table, int32_t table_cols, int64_t ld_table,
+                        int32_t* query_starts, int32_t* req_id, int32_t* row_ends, int32_t* slots,
+                        int32_t* used, hipStream_t stream);
+
+// The arguments of indexer_logits and indexer_logits_paged; req_id == nullptr:
+// the keys are rows [0, cols) of `keys`, the same for every token.
+struct LogitsArgs {
+    const void *q, *keys;
+    const float *weights, *key_scales;
+    const int32_t *row_ends, *req_id;
+    void* logits;
+    int64_t rows, cols, ld_q, ld_keys, ld_weights, ld_logits;
+    Pages pages;
+    int32_t heads, dim;
+    int dtype, logits_dtype;
+};
+int launch_indexer_logits(const LogitsArgs& a, hipStream_t stream);
+
+// The arguments of latent_attend_rows and latent_attend_paged.
+struct AttendArgs {
+    bool paged;  // which of the two (ids may be null in the rows form: k == 0)
+    const uint16_t *q, *cache;
+    uint16_t* out;
+    float* lse;                  // or nullptr
+    int64_t rows, ld_q, ld_head, cache_rows, ld_cache;
+    int32_t heads, d_latent;
+    float scale;
+    const int32_t *ids, *counts;                  // rows form
+    int64_t ld_ids;
+    int32_t k;
+    const int32_t *query_starts, *ctx_lens;       // paged form
+    int64_t reqs, max_len;
+    const uint64_t* tree;
+    Pages pages;
+};
+
+// How a call is cut into workgroups.
+struct AttendPlan {
+    int splits;       // pieces of the keys, joined by a second kernel when > 1
+    size_t ws_bytes;  // of the pieces' results
+};
+AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split);
+AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent,
+                             int64_t max_len, bool allow_split);
+int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t stream);
+
+// row_limit (device, or nullptr): rows at or past *row_limit are not written.
+int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
+                        int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
+                        const int32_t* row_limit, hipStream_t stream);
+
 }  // namespace rts
