@@ -13,9 +13,14 @@
 // A workgroup keeps the queries of a few tokens in LDS, in the order in which
 // lanes read them (16 bytes a lane, no bank conflicts), and each of its waves
 // streams 64 keys at a time straight into registers, where they serve all
-// those tokens.  Both operands are cut into 16-byte chunks by the same rule,
-// chunk 2 i + (lane >> 5) of a row being step i's: the order of a row's
-// elements within the product does not matter as long as both sides share it.
+// those tokens while the next 64 are on their way.
+//
+// e4m3 queries and keys are widened to bf16, which holds every e4m3 value, and
+// take the bf16 product: the 8-bit matrix instructions of this chip align the
+// products of a step before they add them and lose what lies 2^-16 below the
+// largest (1.4e-5 of the result on N(0, 1) data in 64- and 16-element steps
+// alike, against 1e-7 here), too much for a select by score.  The queries are
+// widened once a workgroup, the keys once for all its tokens.
 #include "rts_device.hpp"
 #include "rts_internal.h"
 #include "rts_paged.hpp"
@@ -25,33 +30,25 @@ namespace rts {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kLogitsWaves = 4;
 constexpr int kLogitsBlock = kLogitsWaves * kWave;
 constexpr int kKeyTile = 64;  // keys of a wave's step: two 32-column tiles
+constexpr int64_t kLogitsStep = kLogitsWaves * kKeyTile;
 
-// acc += the product over step i's chunks of a 32-head tile and a 32-key tile.
-// e4m3 takes two chunks a lane, bf16 one.
-template <bool E4M3, int NI>
-__device__ __forceinline__ f32x16 tile_product(const i32x4 (&a)[NI], const i32x4 (&k)[NI]) {
-    f32x16 acc = {};
-    if constexpr (E4M3) {
-#pragma unroll
-        for (int i = 0; i < NI; i += 2) {
-            const i32x8 x = __builtin_shufflevector(a[i], a[i + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const i32x8 y = __builtin_shufflevector(k[i], k[i + 1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, 0, 0, 0, 0, 0, 0);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a[i]),
-                                                          __builtin_bit_cast(bf16x8, k[i]), acc, 0, 0, 0);
-    }
-    return acc;
+// Two of the four e4m3 in `w` as bf16 (exact).
+template <bool HI>
+__device__ __forceinline__ int widen2(int w) {
+    return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+
+// 16 e4m3 as the bf16 operands of two product steps.
+__device__ __forceinline__ void widen16(i32x4 w, i32x4& lo, i32x4& hi) {
+    lo = i32x4{widen2<false>(w[0]), widen2<true>(w[0]), widen2<false>(w[1]), widen2<true>(w[1])};
+    hi = i32x4{widen2<false>(w[2]), widen2<true>(w[2]), widen2<false>(w[3]), widen2<true>(w[3])};
 }
 
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
@@ -59,36 +56,59 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
     *p = __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
 }
 
-// NI: 16-byte chunk pairs of a row.  tb tokens a workgroup, head_tiles tiles of
-// 32 heads (padded with zeros), `span` columns a workgroup.
-template <int NI, bool E4M3, bool PAGED, typename Out>
+// What a wave holds of its 64 keys: row chunks as they lie in memory (lane
+// half h has the 16-byte chunks 2 c + h of its two keys), and the factor of
+// the column that this lane stores (NaN: the key does not exist).
+template <int NC>
+struct Keys {
+    i32x4 raw[2][NC];
+    float scale;
+};
+
+// D elements a row; tb tokens a workgroup, head_tiles tiles of 32 heads
+// (padded with zeros), `span` columns a workgroup.
+//
+// Both operands of product step i cover the same 16 elements of a row in the
+// same order, which is all that the sum needs: bf16 step i, half h has chunk
+// 2 i + h; e4m3 steps 2 c and 2 c + 1, half h have the halves of chunk 2 c + h.
+template <int D, bool E4M3, bool PAGED, typename Out>
 __global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsArgs a, int tb, int head_tiles,
                                                                          int64_t span) {
+    constexpr int NI = D / 16;                // product steps
+    constexpr int kEsz = E4M3 ? 1 : 2;
+    constexpr int NC = D * kEsz / 32;         // chunk pairs of a row
     extern __shared__ __align__(16) char lds[];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, half = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t t0 = (int64_t)blockIdx.x * tb;
     const int n_tok = (int)(a.rows - t0 < tb ? a.rows - t0 : tb);
     const int hp = head_tiles * 32;
-    i32x4* lq = reinterpret_cast<i32x4*>(lds);                       // [tb][head_tiles][NI][64]
+    i32x4* lq = reinterpret_cast<i32x4*>(lds);                                // [tb][head_tiles][NI][64]
     float* lw = reinterpret_cast<float*>(lq + tb * head_tiles * NI * kWave);  // [tb][hp]
-    int32_t* le = reinterpret_cast<int32_t*>(lw + tb * hp);          // [tb] row ends
-    int32_t* lr = le + tb;                                           // [tb] requests
-    constexpr int kRowBytes = NI * 32;
-    constexpr int kEsz = E4M3 ? 1 : 2;
+    int32_t* le = reinterpret_cast<int32_t*>(lw + tb * hp);                   // [tb] row ends
+    int32_t* lr = le + tb;                                                    // [tb] requests
 
-    for (int i = tid; i < n_tok * head_tiles * NI * kWave; i += kLogitsBlock) {
-        const int l = i & 63, step = (i >> 6) % NI, th = (i >> 6) / NI;
-        const int tile = th % head_tiles, tok = th / head_tiles;
-        const int head = tile * 32 + (l & 31);
-        i32x4 v = {};
-        if (head < a.heads)
-            v = *reinterpret_cast<const i32x4*>(static_cast<const char*>(a.q) + (t0 + tok) * a.ld_q * kEsz +
-                                                (int64_t)head * kRowBytes + (2 * step + (l >> 5)) * 16);
-        lq[i] = v;
+    for (int th = wave; th < n_tok * head_tiles; th += kLogitsWaves) {
+        const int tok = th / head_tiles, head = (th - tok * head_tiles) * 32 + (lane & 31);
+        const char* src = static_cast<const char*>(a.q) + ((t0 + tok) * a.ld_q + (int64_t)head * D) * kEsz + half * 16;
+        i32x4 raw[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            raw[c] = i32x4{};
+            if (head < a.heads) raw[c] = *reinterpret_cast<const i32x4*>(src + c * 32);
+        }
+        i32x4* dst = lq + th * NI * kWave + lane;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if constexpr (E4M3)
+                widen16(raw[c], dst[2 * c * kWave], dst[(2 * c + 1) * kWave]);
+            else
+                dst[c * kWave] = raw[c];
+        }
     }
     for (int i = tid; i < n_tok * hp; i += kLogitsBlock) {
-        const int h = i % hp;
-        lw[i] = h < a.heads ? a.weights[(t0 + i / hp) * a.ld_weights + h] : 0.f;
+        const int t = i / hp, h = i - t * hp;
+        lw[i] = h < a.heads ? a.weights[(t0 + t) * a.ld_weights + h] : 0.f;
     }
     if (tid < n_tok) {
         const int64_t e = a.row_ends ? a.row_ends[t0 + tid] : a.cols;
@@ -116,60 +136,104 @@ __global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsA
         if constexpr (PAGED) {
             if (end > 0) page = a.pages.table + (int64_t)lr[ta] * a.pages.ld;
         }
-        for (int64_t c = c0 + wave * kKeyTile; c < cend; c += kLogitsWaves * kKeyTile) {
-            i32x4 k[2][NI];
+
+        auto load = [&](int64_t c, Keys<NC>& k) {
             int64_t phys[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int64_t key = c + u * 32 + (lane & 31);
-                if constexpr (PAGED)
-                    phys[u] = key < cend ? phys_row(a.pages, page, (int32_t)key) : -1;
-                else
-                    phys[u] = key < cend ? key : -1;
+                phys[u] = -1;
+                if (key < cend) {
+                    if constexpr (PAGED)
+                        phys[u] = phys_row(a.pages, page, (int32_t)key);
+                    else
+                        phys[u] = key;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
                 const char* kp = static_cast<const char*>(a.keys) + phys[u] * a.ld_keys * kEsz + half * 16;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    k[u][i] = i32x4{};
-                    if (phys[u] >= 0) k[u][i] = *reinterpret_cast<const i32x4*>(kp + i * 32);
+                for (int i = 0; i < NC; ++i) {
+                    k.raw[u][i] = i32x4{};
+                    if (phys[u] >= 0) k.raw[u][i] = *reinterpret_cast<const i32x4*>(kp + i * 32);
                 }
             }
             const int64_t mine = half ? phys[1] : phys[0];  // this lane stores column c + lane
-            float ks = 1.f;
-            if (a.key_scales && mine >= 0) ks = a.key_scales[mine];
-            if (mine < 0) ks = __builtin_nanf("");
+            k.scale = mine < 0 ? __builtin_nanf("") : 1.f;
+            if (a.key_scales && mine >= 0) k.scale = a.key_scales[mine];
+        };
+
+        auto score = [&](int64_t c, const i32x4 (&k)[2][NI], float scale) {
             for (int t = ta; t < tz; ++t) {
                 float sum[2] = {0.f, 0.f};
                 for (int tile = 0; tile < head_tiles; ++tile) {
                     const i32x4* qa = lq + (t * head_tiles + tile) * NI * kWave + lane;
-                    i32x4 x[NI];
+                    f32x16 s[2] = {};
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) x[i] = qa[i * kWave];
+                    for (int i = 0; i < NI; ++i) {
+                        const bf16x8 x = __builtin_bit_cast(bf16x8, qa[i * kWave]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                x, __builtin_bit_cast(bf16x8, k[u][i]), s[u], 0, 0, 0);
+                    }
                     const f32x4* w4 = reinterpret_cast<const f32x4*>(lw + t * hp + tile * 32) + half;
-                    f32x4 w[4];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) w[g] = w4[2 * g];  // heads 8 g + 4 half + (0..3)
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4 w = w4[2 * g];  // heads 8 g + 4 half + (0..3)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const f32x16 s = tile_product<E4M3, NI>(x, k[u]);
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            sum[u] = fmaf(w[r >> 2][r & 3], __builtin_elementwise_maximum(s[r], 0.f), sum[u]);
+                            for (int r = 0; r < 4; ++r)
+                                sum[u] = fmaf(w[r], __builtin_elementwise_maximum(s[u][4 * g + r], 0.f), sum[u]);
                     }
                 }
+                // Both halves' sums of the key tile that this half stores.
                 const float other = __shfl_xor(half ? sum[0] : sum[1], 32);
-                const float v = ((half ? sum[1] : sum[0]) + other) * ks;
+                const float v = ((half ? sum[1] : sum[0]) + other) * scale;
                 if (c + lane < le[t] && c + lane < cend)
                     store_logit(static_cast<Out*>(a.logits) + (t0 + t) * a.ld_logits + c + lane, v);
+            }
+        };
+
+        constexpr int64_t stride = kLogitsStep;
+        int64_t c = c0 + wave * kKeyTile;
+        if (c >= cend) continue;
+        Keys<NC> k0;
+        load(c, k0);
+        if constexpr (E4M3) {
+            for (; c < cend; c += stride) {
+                i32x4 k[2][NI];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) widen16(k0.raw[u][i], k[u][2 * i], k[u][2 * i + 1]);
+                const float scale = k0.scale;
+                if (c + stride < cend) load(c + stride, k0);
+                score(c, k, scale);
+            }
+        } else {
+            Keys<NC> k1;  // the two take turns, so that no register is copied
+            for (;;) {
+                if (c + stride < cend) load(c + stride, k1);
+                score(c, k0.raw, k0.scale);
+                c += stride;
+                if (c >= cend) break;
+                if (c + stride < cend) load(c + stride, k0);
+                score(c, k1.raw, k1.scale);
+                c += stride;
+                if (c >= cend) break;
             }
         }
     }
 }
 
-template <int NI, bool E4M3, bool PAGED, typename Out>
+template <int D, bool E4M3, bool PAGED, typename Out>
 static int launch_logits(const LogitsArgs& a, hipStream_t s) {
     const int head_tiles = (a.heads + 31) / 32;
-    const size_t per_token = (size_t)head_tiles * NI * kWave * 16 + head_tiles * 32 * 4 + 8;
-    int tb = (int)((72 << 10) / per_token);
+    const size_t per_token = (size_t)head_tiles * D * 64 + head_tiles * 32 * 4 + 8;
+    int tb = (int)((72 << 10) / per_token);  // two workgroups a CU
     if (tb > 16) tb = 16;
     if (PAGED) {  // about the tokens that one request has
         const int64_t each = a.pages.table_rows > 0 ? (a.rows + a.pages.table_rows - 1) / a.pages.table_rows : 1;
@@ -178,31 +242,32 @@ static int launch_logits(const LogitsArgs& a, hipStream_t s) {
     if (tb > a.rows) tb = (int)a.rows;
     if (tb < 1) tb = 1;
     const int64_t blocks_x = (a.rows + tb - 1) / tb;
-    constexpr int64_t kStep = kLogitsWaves * kKeyTile;
-    int64_t parts = (2048 + blocks_x - 1) / blocks_x;
-    const int64_t most = (a.cols + kStep - 1) / kStep;
-    if (parts > most) parts = most;
-    const int64_t span = ((a.cols + parts - 1) / parts + kStep - 1) / kStep * kStep;
-    parts = (a.cols + span - 1) / span;
-    hipLaunchKernelGGL((indexer_logits_kernel<NI, E4M3, PAGED, Out>),
+    const int64_t steps = (a.cols + kLogitsStep - 1) / kLogitsStep;
+    int64_t parts = (512 + blocks_x - 1) / blocks_x;
+    if (parts < (steps + 7) / 8) parts = (steps + 7) / 8;
+    if (parts > steps) parts = steps;
+    if (parts > 65535) parts = 65535;
+    const int64_t per = (steps + parts - 1) / parts;
+    parts = (steps + per - 1) / per;
+    hipLaunchKernelGGL((indexer_logits_kernel<D, E4M3, PAGED, Out>),
                        dim3((unsigned)blocks_x, (unsigned)parts), dim3(kLogitsBlock), per_token * tb, s, a, tb,
-                       head_tiles, span);
+                       head_tiles, per * kLogitsStep);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
-template <int NI, bool E4M3>
+template <int D, bool E4M3>
 static int launch_logits_as(const LogitsArgs& a, hipStream_t s) {
     if (a.req_id)
-        return a.logits_dtype == RTS_F32 ? launch_logits<NI, E4M3, true, float>(a, s)
-                                         : launch_logits<NI, E4M3, true, uint16_t>(a, s);
-    return a.logits_dtype == RTS_F32 ? launch_logits<NI, E4M3, false, float>(a, s)
-                                     : launch_logits<NI, E4M3, false, uint16_t>(a, s);
+        return a.logits_dtype == RTS_F32 ? launch_logits<D, E4M3, true, float>(a, s)
+                                         : launch_logits<D, E4M3, true, uint16_t>(a, s);
+    return a.logits_dtype == RTS_F32 ? launch_logits<D, E4M3, false, float>(a, s)
+                                     : launch_logits<D, E4M3, false, uint16_t>(a, s);
 }
 
 int launch_indexer_logits(const LogitsArgs& a, hipStream_t s) {
     if (a.dtype == RTS_BF16)
-        return a.dim == 128 ? launch_logits_as<8, false>(a, s) : launch_logits_as<4, false>(a, s);
-    return a.dim == 128 ? launch_logits_as<4, true>(a, s) : launch_logits_as<2, true>(a, s);
+        return a.dim == 128 ? launch_logits_as<128, false>(a, s) : launch_logits_as<64, false>(a, s);
+    return a.dim == 128 ? launch_logits_as<128, true>(a, s) : launch_logits_as<64, true>(a, s);
 }
 
 }  // namespace rts
