@@ -29,10 +29,19 @@ COMMON = [
     "-Wall", "-Wno-unused-parameter",
 ]
 
+# Flags of single sources.
+EXTRA = {
+    # Matrix products start with their results in vector registers and move to
+    # accumulation registers under pressure: the latent kernels hold 256
+    # registers of sums beside 16 of scores, and the other way round the scores
+    # push the sums out to scratch.
+    "rts_latent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+}
+
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "hip"]
     res = subprocess.run(cmd, capture_output=True, text=True)

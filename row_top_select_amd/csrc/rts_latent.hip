@@ -1,6 +1,34 @@
 // Attention over a latent cache (one vector a token is every head's key, its
 // leading part every head's value), over selected rows or whole paged
 // prefixes, and the join of partial results, for gfx950.
+//
+// For a block of query rows (heads of a token, or (token, head) pairs of a
+// request) over a list of keys, 32 keys at a time:
+//   S^T = K Q^T,  P^T = exp2(S^T c - m),  O^T += V^T P^T
+// with K [32, L + 64] in LDS and V its first L columns.  Both products are
+// formed transposed, so that a query row is a column of every 32x32 matrix
+// tile: a lane owns one query row (shared with the lane 32 further on), its
+// maximum, sum and rescaling factor are plain registers, and the weights come
+// out of the first product in the very registers that the second one reads
+// them from.  A contraction may take its terms in any order, so the second
+// product's 16 keys a step are those that the lane half holds (4 h + 0..3 and
+// 8 + 4 h + 0..3), and the transposing LDS reads deliver V in the same order.
+//
+// Q (144 registers) and O (64 to 256 registers) stay in registers; a wave has
+// a SIMD's registers for itself.  A workgroup is four waves of 32 query rows x
+// all values (HG = 4), 64 rows x half of the values (HG = 2) or 32 rows x a
+// quarter (HG = 1): with fewer rows than 128 the scores are formed more than
+// once, which costs matrix time where the rows' bytes bound the call.
+//
+// Key rows come through a ring of four 32-key stages, loaded straight into LDS
+// three stages ahead; where a row lies is looked up with scalar loads another
+// stage ahead.  16-byte chunks are XOR-ed within 256 bytes by the row number,
+// so that neither the row reads of the first product nor the transposed reads
+// of the second meet in a bank.
+//
+// The running maximum is only moved when a score exceeds it by 2^8: then, and
+// not at every step, O is rescaled.  Any reference gives the same quotient; a
+// weight of up to 2^8 costs neither the 32-bit sums nor bf16 precision.
 #include "rts_device.hpp"
 #include "rts_internal.h"
 #include "rts_paged.hpp"
@@ -8,96 +36,512 @@
 
 namespace rts {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kRope = 64;
+constexpr int kTile = 32;    // keys of a stage, query rows of a wave
+constexpr int kStages = 4;
+constexpr int kAttendWaves = 4;
+constexpr int kAttendBlock = kAttendWaves * kWave;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -3e38f;   // a maximum before the first score: exp2(x - kNoMax) stays 0 for x = -inf
+constexpr float kLazy = 8.f;       // how far (log2) a score may pass the maximum before O is rescaled
 
-__device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ uint16_t f32_bf16(float f) {
-    const __bf16 b = (__bf16)f;  // round to nearest even
-    return __builtin_bit_cast(uint16_t, b);
-}
-
-// The request of token t: the last i with starts[i] <= t (reqs if t is behind
-// the last token).
-__device__ __forceinline__ int64_t request_of(const int32_t* starts, int64_t reqs, int64_t t) {
-    if (t >= starts[reqs]) return reqs;
-    int64_t lo = 0, hi = reqs;
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (starts[mid] <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-// One wave per (row, head): lane l holds elements l + 64 i of the query and of
-// the sum, and the running maximum and sum of the softmax.
 template <int DL>
-__global__ __launch_bounds__(64) void latent_attend_simple_kernel(AttendArgs a) {
-    constexpr int NQ = (DL + kRope) / 64, NV = DL / 64;
-    const int64_t row = blockIdx.x / a.heads;
-    const int head = blockIdx.x % a.heads, lane = threadIdx.x;
-    int64_t n, ctx = 0, idx = 0, req = 0, news = 0;
-    if (!a.paged) {
-        n = a.k;
-        if (a.counts) n = a.counts[row] < 0 ? 0 : a.counts[row] < n ? a.counts[row] : n;
-    } else {
-        req = request_of(a.query_starts, a.reqs, row);
-        if (req >= a.reqs) return;
-        ctx = a.ctx_lens[req] > 0 ? a.ctx_lens[req] : 0;
-        idx = row - a.query_starts[req];
-        news = a.query_starts[req + 1] - a.query_starts[req];
-        n = ctx + news;
-    }
-    float q[NQ], o[NV], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < NQ; ++i) q[i] = bf16_f32(a.q[row * a.ld_q + head * a.ld_head + lane + 64 * i]);
-    for (int i = 0; i < NV; ++i) o[i] = 0.f;
-    for (int64_t j = 0; j < n; ++j) {
-        int64_t r;
-        if (!a.paged) {
-            r = a.ids[row * a.ld_ids + j];
-            if (r >= a.cache_rows) r = -1;
-        } else {
-            const int64_t d = j - ctx;
-            if (d >= 0 && (a.tree ? d >= 64 || !((a.tree[row] >> d) & 1) : d > idx)) continue;
-            r = phys_row(a.pages, a.pages.table + req * a.pages.ld, (int32_t)j);
-        }
-        if (r < 0) continue;
-        const uint16_t* c = a.cache + r * a.ld_cache;
-        float x[NQ], z = 0.f;
-        for (int i = 0; i < NQ; ++i) {
-            x[i] = bf16_f32(c[lane + 64 * i]);
-            z += q[i] * x[i];
-        }
-        for (int s = 32; s > 0; s >>= 1) z += __shfl_xor(z, s);
-        z *= a.scale * kLog2e;
-        const float mn = fmaxf(m, z), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(z - mn);
-        l = l * f + p;
-        for (int i = 0; i < NV; ++i) o[i] = o[i] * f + p * x[i];
-        m = mn;
-    }
-    const int64_t at = row * a.heads + head;
-    for (int i = 0; i < NV; ++i)
-        a.out[at * DL + lane + 64 * i] = f32_bf16(l == 0.f ? 0.f : o[i] / l);
-    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+constexpr int stage_bytes() { return kTile * (DL + kRope) * 2; }
+
+__device__ __forceinline__ uint16_t f32_bf16(float f) {
+    return __builtin_bit_cast(uint16_t, (__bf16)f);  // round to nearest even
 }
+
+// Where rows that do not exist are read from.
+__device__ const uint4 g_zero_row[(512 + kRope) * 2 / 16] = {};
+
+typedef __attribute__((address_space(4))) const int32_t* scalar_i32;  // read by scalar loads
+
+// 16 bytes a lane from global memory to LDS at base + 16 * lane, the source a
+// wave's address plus a lane's offset, or a lane's address.  Written in
+// assembly (no register is loaded) because the compiler cannot tell the ring's
+// stages apart: with the builtin it waits for every load under way before it
+// reads any stage.  The loop below counts the loads and waits itself.
+__device__ __forceinline__ uint32_t lds_offset(const char* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+__device__ __forceinline__ void load_to_lds(const char* src, int offset, uint32_t base) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" :: "{m0}"(base), "v"(offset), "s"(src) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const char* src, uint32_t base) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(base), "v"(src) : "memory");
+}
+
+// The 4-bit pattern that a row's latent chunks are XOR-ed with.  A row of 512
+// or 1024 bytes starts at bank 0; rows 0..15 differ (row reads), and among
+// rows 4 i + 0..3 and 4 i + 4..7 each 64-byte quarter occurs twice
+// (transposed reads of 8 rows x 64 bytes).
+__device__ __forceinline__ int chunk_xor(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+
+// Query rows and keys of one workgroup.
+struct Work {
+    int64_t q0;       // first token
+    int32_t head0;    // rows form: first head
+    int32_t flat0;    // paged form: first (token, head) pair of the request
+    int32_t tokens;   // paged form: the request's tokens
+    int32_t ctx;      // paged form: cached tokens
+    int32_t n;        // keys
+    int32_t masked;   // keys from here on need the rows' own limits
+    const int32_t* list;  // ids of the row, or the request's block-table row
+};
+
+template <int DL, int HG, bool PAGED>
+__global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendArgs a, int splits,
+                                                                        float* __restrict__ part_out,
+                                                                        float* __restrict__ part_lse) {
+    constexpr int DP = kAttendWaves / HG;      // parts of the values
+    constexpr int NT = DL / 32 / DP;           // output tiles of a wave
+    constexpr int NQ = (DL + kRope) / 16;      // steps of the first product
+    constexpr int NL = DL / 16;                // of them in the latent part
+    constexpr int kRowB = DL * 2;              // latent bytes of a key
+    constexpr int kStageB = stage_bytes<DL>();
+    constexpr int MB = 32 * HG;                // query rows of a workgroup
+    constexpr int kLoads = 8 * kRowB / 1024 + 1;  // loads of a wave and stage
+    extern __shared__ __align__(1024) char lds[];
+    char* valid = lds + kStages * kStageB;     // [stage][wave]: which of the wave's 8 rows exist
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int hg = wave % HG, dp = wave / HG;
+
+    Work w{};
+    if constexpr (!PAGED) {
+        const int blocks = (a.heads + MB - 1) / MB;
+        w.q0 = blockIdx.x / blocks;
+        w.head0 = (int)(blockIdx.x - w.q0 * blocks) * MB;
+        int n = a.k;
+        if (a.counts) n = a.counts[w.q0] < 0 ? 0 : a.counts[w.q0] < n ? a.counts[w.q0] : n;
+        w.n = __builtin_amdgcn_readfirstlane(n);
+        w.masked = w.n;
+        w.list = a.ids + w.q0 * a.ld_ids;
+    } else {
+        // Request i's row blocks start at block floor(starts[i] * heads / MB) + i,
+        // which leaves room for each request's own rounding up.
+        const int64_t b = blockIdx.x;
+        int64_t before = 0;
+        for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
+            const int64_t i = i0 + lane;
+            bool le = false;
+            if (i < a.reqs) {
+                const int64_t st = a.query_starts[i];
+                le = (st < 0 ? 0 : st) * a.heads / MB + i <= b;
+            }
+            const int got = __popcll(__ballot(le));
+            before += got;
+            if (got < 64) break;
+        }
+        const int64_t req = before - 1;  // >= 0: block 0 of request 0 is block 0
+        if (req < 0) return;
+        int64_t st = a.query_starts[req], en = a.query_starts[req + 1];
+        st = st < 0 ? 0 : st < a.rows ? st : a.rows;
+        en = en < st ? st : en < a.rows ? en : a.rows;
+        const int64_t flat = (b - (st * a.heads / MB + req)) * MB;
+        w.tokens = (int)(en - st);
+        if (flat < 0 || flat >= (int64_t)w.tokens * a.heads) return;
+        w.flat0 = (int)flat;
+        w.q0 = st;
+        const int32_t c = a.ctx_lens[req];
+        w.ctx = c < 0 ? 0 : c;
+        const int64_t first = flat / a.heads, last_row = (flat + MB - 1) / a.heads;
+        const int64_t last = last_row < w.tokens ? last_row : w.tokens - 1;
+        int64_t n = (int64_t)w.ctx + (a.tree ? (w.tokens < 64 ? w.tokens : 64) : last + 1);
+        const int64_t held = (int64_t)a.pages.cols * a.pages.block_size;
+        if (n > held) n = held;
+        if (n > 0x7FFFFFC0) n = 0x7FFFFFC0;
+        w.n = __builtin_amdgcn_readfirstlane((int)n);
+        const int64_t masked = (int64_t)w.ctx + (a.tree ? 0 : first + 1);
+        w.masked = __builtin_amdgcn_readfirstlane((int)(masked < w.n ? masked : w.n));
+        w.list = a.pages.table + req * a.pages.ld;
+    }
+
+    const int all = (w.n + kTile - 1) / kTile;   // stages
+    const int per = (all + splits - 1) / splits;
+    const int s0 = (int)blockIdx.y * per;
+    const int s1 = s0 + per < all ? s0 + per : all;
+
+    // This lane's query row.
+    int64_t token;
+    int head;
+    bool row_ok;
+    int idx = 0;                // paged: the token's place in its request
+    if constexpr (!PAGED) {
+        token = w.q0;
+        head = w.head0 + hg * 32 + col;
+        row_ok = head < a.heads;
+    } else {
+        const int f = w.flat0 + hg * 32 + col;
+        idx = f / a.heads;
+        head = f - idx * a.heads;
+        row_ok = idx < w.tokens;
+        token = w.q0 + idx;
+    }
+    const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+    uint64_t tree = 0;
+    if constexpr (PAGED) {
+        if (a.tree && row_ok) tree = a.tree[token];
+    }
+
+    // Row `i` of the wave's 8 rows of stage j: the id (rows form) or block id
+    // (paged form) that is read ahead.  Rows behind the last key read its entry.
+    struct Ahead { int32_t id[8]; };
+    const int last_key = w.n - 1;
+    auto block_of = [&](uint32_t e) {
+        return a.pages.shift >= 0 ? e >> a.pages.shift : e / (uint32_t)a.pages.block_size;
+    };
+    const uint32_t last_block = PAGED && w.n > 0 ? block_of((uint32_t)last_key) : 0;
+    auto look = [&](int j, Ahead& h) {
+        const scalar_i32 list = (scalar_i32)(uintptr_t)w.list;
+        const int e0 = j * kTile + wave * 8;
+        if constexpr (!PAGED) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h.id[i] = list[e0 + i < last_key ? e0 + i : last_key];
+        } else {
+            uint32_t blk = block_of((uint32_t)e0), in = (uint32_t)e0 - blk * (uint32_t)a.pages.block_size;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h.id[i] = list[blk < last_block ? blk : last_block];
+                const bool wrap = ++in == (uint32_t)a.pages.block_size;
+                in = wrap ? 0 : in;
+                blk += wrap ? 1 : 0;
+            }
+        }
+    };
+    // Starts the loads of the wave's 8 rows of stage j into the ring.
+    const int64_t ldb = a.ld_cache * 2;
+    const char* cache = reinterpret_cast<const char*>(a.cache);
+    const char* zero = reinterpret_cast<const char*>(g_zero_row);
+    auto fetch = [&](int j, const Ahead& h) {
+        const uint32_t slot = (uint32_t)(j & (kStages - 1));
+        const uint32_t stage = lds_offset(lds) + slot * kStageB;
+        const char* src[8];
+        uint32_t ok = 0, in = 0;
+        const int e0 = j * kTile + wave * 8;
+        if constexpr (PAGED) in = (uint32_t)e0 - block_of((uint32_t)e0) * (uint32_t)a.pages.block_size;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int64_t r = h.id[i];
+            if constexpr (PAGED) {
+                r = r < 0 ? -1 : r * a.pages.stride_rows + in;
+                in = in + 1 == (uint32_t)a.pages.block_size ? 0 : in + 1;
+            }
+            const bool there = r >= 0 && r < a.cache_rows && e0 + i < w.n;
+            src[i] = there ? cache + r * ldb : zero;
+            ok |= there ? 1u << i : 0u;
+        }
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));  // offsets are formed here and not kept in registers
+        const int half = lane >> 5, col = lane & 31;
+        if constexpr (kRowB == 1024) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                load_to_lds(src[i], (lane ^ chunk_xor(wave * 8 + i)) * 16, stage + (wave * 8 + i) * kRowB);
+        } else {  // two rows a load
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+                load_to_lds((half ? src[i + 1] : src[i]) + ((col ^ chunk_xor(wave * 8 + i + half)) * 16),
+                            stage + (wave * 8 + i) * kRowB);
+        }
+        const int r8 = lane >> 3;  // the rotary parts: 8 rows x 128 bytes
+        const char* mine = src[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mine = r8 == i ? src[i] : mine;
+        load_to_lds(mine + kRowB + (((lane & 7) ^ (((wave * 8 + r8) >> 1) & 7)) * 16),
+                    stage + kTile * kRowB + wave * 8 * (kRope * 2));
+        if (lane == 0) valid[slot * kAttendWaves + wave] = (char)ok;
+    };
+
+    Ahead ahead;
+    if (s0 < s1) {
+#pragma unroll
+        for (int p = 0; p < kStages - 1; ++p) {
+            if (s0 + p < s1) {
+                look(s0 + p, ahead);
+                fetch(s0 + p, ahead);
+            }
+        }
+        if (s0 + kStages - 1 < s1) look(s0 + kStages - 1, ahead);
+    }
+
+    bf16x8 q[NQ];
+    {
+        const uint16_t* qp = a.q + token * a.ld_q + (int64_t)head * a.ld_head + half * 8;
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            i32x4 v = {};
+            if (row_ok && a.scale != 0.f) v = *reinterpret_cast<const i32x4*>(qp + i * 16);
+            q[i] = __builtin_bit_cast(bf16x8, v ^ (int)flip);
+        }
+    }
+
+    // LDS offsets within a stage; the others differ by constants in the bits
+    // that the XOR leaves alone or by a further XOR.  First product: chunk
+    // 2 i + half of row col.
+    const int ka = col * kRowB + ((half ^ chunk_xor(col)) * 16);
+    const int kr = kTile * kRowB + col * (kRope * 2) + ((half ^ ((col >> 1) & 7)) * 16);
+    // Second product: each 16 lanes read 4 keys x 16 values and get a value's
+    // 4 keys a lane.
+    const int vrow = 4 * half + ((lane & 15) >> 2);
+    const int va = vrow * kRowB +
+                   (((dp * NT * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ chunk_xor(vrow)) * 16) + (lane & 1) * 8;
+
+    f32x16 o[NT] = {};
+    float m = kNoMax, l = 0.f;
+
+    for (int j = s0; j < s1; ++j) {
+        // Stage j has arrived (later ones may be under way), and every wave is
+        // done with the stage whose place the next loads take.
+        if (j + 2 < s1)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
+        else if (j + 1 < s1)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (j + kStages - 1 < s1) {
+            fetch(j + kStages - 1, ahead);
+            if (j + kStages < s1) look(j + kStages, ahead);
+        }
+        const int stage = (j & (kStages - 1)) * kStageB;
+
+        f32x16 s = {};
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int at = i < NL ? ((stage + ka) ^ ((i & 7) * 32)) + (i >> 3) * 256 : (stage + kr) ^ ((i - NL) * 32);
+            const bf16x8 k = *reinterpret_cast<const bf16x8*>(lds + at);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s, 0, 0, 0);
+        }
+
+        // Which of the 32 keys this lane's row sees.
+        uint32_t see = __builtin_amdgcn_readfirstlane(
+            *reinterpret_cast<const uint32_t*>(valid + (j & (kStages - 1)) * kAttendWaves));
+        const bool rows_differ = PAGED && j * kTile + kTile > w.masked;
+        if constexpr (PAGED) {
+            if (rows_differ) {
+                const int d0 = j * kTile - w.ctx;  // draft number of the stage's first key
+                uint32_t mine;
+                if (!a.tree) {
+                    const int upto = idx + 1 - d0;  // keys of the stage that are seen
+                    mine = upto >= 32 ? ~0u : upto <= 0 ? 0u : (1u << upto) - 1;
+                } else {
+                    const uint64_t live = w.tokens >= 64 ? ~0ull : (1ull << w.tokens) - 1;
+                    const uint64_t bits = tree & live;
+                    if (d0 >= 64)
+                        mine = 0;
+                    else if (d0 >= 0)
+                        mine = (uint32_t)(bits >> d0);
+                    else if (d0 > -32)
+                        mine = (uint32_t)(bits << -d0) | ((1u << -d0) - 1);
+                    else
+                        mine = ~0u;
+                }
+                see &= mine;
+            }
+        }
+        if (rows_differ || see != ~0u) {
+            const uint32_t bits = see >> (4 * half);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (!((bits >> ((r & 3) + 8 * (r >> 2))) & 1)) s[r] = -INFINITY;
+        }
+
+        float top = s[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+        {
+            const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * c;
+        }
+        if (__any(top > m + kLazy)) {
+            const float to = fmaxf(m, top);
+            if (j != s0) {
+                const float f = __builtin_amdgcn_exp2f(m - to);
+                l *= f;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[t][r] *= f;
+            }
+            m = to;
+        }
+        bf16x8 p[2];
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[r], c, -m));
+            sum += x;
+            p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
+        }
+        l += sum;
+
+        if constexpr (PAGED) {
+            if (rows_differ) {
+                // A key that only some rows see must not reach the others as
+                // 0 * NaN or 0 * inf.  Rows that do see it have it in their
+                // scores already, so its value may be taken as 0.
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                i32x4* v = reinterpret_cast<i32x4*>(lds + (j & (kStages - 1)) * kStageB);
+                for (int i = tid; i < kTile * kRowB / 16; i += kAttendBlock) {
+                    i32x4 x = v[i];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((x[e] & 0x7F80) == 0x7F80) x[e] &= 0xFFFF0000;
+                        if ((x[e] & 0x7F800000) == 0x7F800000) x[e] &= 0xFFFF;
+                    }
+                    v[i] = x;
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            }
+        }
+
+        typedef __attribute__((address_space(3))) bf16x4* lds_b4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int at = ((stage + va) ^ ((t & 3) * 64)) + (t >> 2) * 256 + k * 16 * kRowB;
+                const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + at));
+                const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + (at ^ 32) + 8 * kRowB));
+                const bf16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[k], o[t], 0, 0, 0);
+            }
+    }
+
+    {
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+        l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (!row_ok) return;
+    const int64_t rh = token * a.heads + head;
+    const float lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    const int64_t part = (int64_t)blockIdx.y * a.rows * a.heads + rh;
+    if (dp == 0 && half == 0) {
+        if (splits > 1)
+            part_lse[part] = lse;
+        else if (a.lse)
+            a.lse[rh] = lse;
+    }
+    if (splits > 1) {
+        if (lse == -INFINITY) return;  // the join reads no values of an empty part
+        float* dst = part_out + part * DL + dp * NT * 32 + 4 * half;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(dst + t * 32 + g * 8) =
+                    f32x4{o[t][4 * g] * inv, o[t][4 * g + 1] * inv, o[t][4 * g + 2] * inv, o[t][4 * g + 3] * inv};
+        return;
+    }
+    // The halves trade 4 values each, so that a lane stores 8 (16 bytes) of one
+    // group: the lower half those of group g, the upper those of g + 1.
+    uint16_t* dst = a.out + rh * DL + dp * NT * 32 + 8 * half;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t lo[2], hi[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lo[i] = f32_bf16(o[t][4 * g + 2 * i] * inv) | (uint32_t)f32_bf16(o[t][4 * g + 2 * i + 1] * inv) << 16;
+                hi[i] = f32_bf16(o[t][4 * g + 4 + 2 * i] * inv) | (uint32_t)f32_bf16(o[t][4 * g + 5 + 2 * i] * inv) << 16;
+            }
+            const auto x = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
+            *reinterpret_cast<uint4*>(dst + t * 32 + g * 8) = uint4{x[0], y[0], x[1], y[1]};
+        }
+}
+
+constexpr int kCus = 256;
+
+// The number of pieces that a call's keys are cut into: the one with the least
+// estimated time.  A workgroup takes a CU for itself, about 1 us a stage and
+// 4 us around them; pieces cost their 32-bit results' way out and back at
+// 4 TB/s and a second launch.
+static AttendPlan plan_splits(int64_t blocks, int64_t stages, int64_t out_rows, int32_t d_latent, bool allow) {
+    const double piece = (double)out_rows * d_latent * 8 / 4e6;  // us
+    int best = 1;
+    double best_us = 1e300;
+    const int64_t most = !allow ? 1 : stages < 64 ? stages : 64;
+    for (int s = 1; s == 1 || s <= most; ++s) {
+        const int64_t per = (stages + s - 1) / s;
+        const double us = (double)((blocks * s + kCus - 1) / kCus) * (per + 4.0) + (s > 1 ? 4.0 + s * piece : 0.0);
+        if (us < best_us) best_us = us, best = s;
+    }
+    const size_t ws = best > 1 ? (size_t)best * out_rows * (d_latent + 1) * 4 : 0;
+    return AttendPlan{best, (ws + 15) & ~size_t(15)};
+}
+
+// 32-row groups of a workgroup for blocks of about `rows` query rows.
+static int row_groups(int64_t rows) { return rows <= 32 ? 1 : rows <= 64 ? 2 : 4; }
 
 AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split) {
-    return AttendPlan{1, 0};
+    const int mb = 32 * row_groups(heads);
+    return plan_splits(rows * ((heads + mb - 1) / mb), ((int64_t)k + kTile - 1) / kTile, rows * heads, d_latent,
+                       allow_split);
+}
+
+// About the query rows that one request has.
+static int64_t rows_of_request(int64_t tokens, int64_t reqs, int32_t heads) {
+    return (tokens + reqs - 1) / reqs * heads;
 }
 
 AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent,
                              int64_t max_len, bool allow_split) {
-    return AttendPlan{1, 0};
+    const int64_t each = rows_of_request(tokens, reqs, heads);
+    const int mb = 32 * row_groups(each);
+    return plan_splits(reqs * ((each + mb - 1) / mb), (max_len + kTile - 1) / kTile, tokens * heads, d_latent,
+                       allow_split);
+}
+
+template <int DL, int HG, bool PAGED>
+static int launch_attend(const AttendArgs& a, int64_t blocks, int splits, void* workspace, hipStream_t s) {
+    if (blocks > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
+    const int64_t n = a.rows * a.heads;
+    float* part_out = static_cast<float*>(workspace);
+    float* part_lse = part_out ? part_out + (int64_t)splits * n * DL : nullptr;
+    constexpr size_t lds = kStages * stage_bytes<DL>() + kStages * kAttendWaves;
+    hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)blocks, (unsigned)splits),
+                       dim3(kAttendBlock), lds, s, a, splits, part_out, part_lse);
+    if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+    if (splits == 1) return RTS_OK;
+    return launch_merge_attend(part_out, RTS_F32, part_lse, splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
+                               PAGED ? a.query_starts + a.reqs : nullptr, s);
+}
+
+template <int DL, bool PAGED>
+static int launch_attend_rows_of(const AttendArgs& a, int splits, void* workspace, hipStream_t s) {
+    const int hg = row_groups(PAGED ? rows_of_request(a.rows, a.reqs, a.heads) : a.heads);
+    const int mb = 32 * hg;
+    const int64_t blocks = PAGED ? a.rows * a.heads / mb + a.reqs : a.rows * ((a.heads + mb - 1) / mb);
+    if (hg == 1) return launch_attend<DL, 1, PAGED>(a, blocks, splits, workspace, s);
+    if (hg == 2) return launch_attend<DL, 2, PAGED>(a, blocks, splits, workspace, s);
+    return launch_attend<DL, 4, PAGED>(a, blocks, splits, workspace, s);
 }
 
 int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
-    const dim3 g((unsigned)(a.rows * a.heads)), b(64);
-    if (a.d_latent == 512)
-        hipLaunchKernelGGL(latent_attend_simple_kernel<512>, g, b, 0, s, a);
-    else
-        hipLaunchKernelGGL(latent_attend_simple_kernel<256>, g, b, 0, s, a);
-    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+    if (a.paged)
+        return a.d_latent == 512 ? launch_attend_rows_of<512, true>(a, plan.splits, workspace, s)
+                                 : launch_attend_rows_of<256, true>(a, plan.splits, workspace, s);
+    return a.d_latent == 512 ? launch_attend_rows_of<512, false>(a, plan.splits, workspace, s)
+                             : launch_attend_rows_of<256, false>(a, plan.splits, workspace, s);
 }
 
 // --------------------------------------------------------------- rank merge
