@@ -29,6 +29,8 @@
 // The running maximum is only moved when a score exceeds it by 2^8: then, and
 // not at every step, O is rescaled.  Any reference gives the same quotient; a
 // weight of up to 2^8 costs neither the 32-bit sums nor bf16 precision.
+#include <type_traits>
+
 #include "rts_device.hpp"
 #include "rts_internal.h"
 #include "rts_paged.hpp"
@@ -77,6 +79,23 @@ __device__ __forceinline__ void load_to_lds(const char* src, int offset, uint32_
 }
 __device__ __forceinline__ void load_to_lds(const char* src, uint32_t base) {
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(base), "v"(src) : "memory");
+}
+
+// o += v p with the sums in accumulation registers, where the compiler would
+// put them only under pressure and with copies.  It does not see the product,
+// so the wait states are here: two after a vector instruction that wrote an
+// operand (s_nop 1, in the shadow of the product before), and sums_ready()
+// before other code reads the sums.
+__device__ __forceinline__ void add_product(f32x16& o, bf16x8 v, bf16x8 p) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(o) : "v"(v), "v"(p));
+}
+// Keeps a sum in accumulation registers at this point.
+__device__ __forceinline__ void pin(f32x16& o) { asm volatile("" : "+a"(o)); }
+template <int N>
+__device__ __forceinline__ void sums_ready(f32x16 (&o)[N]) {
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < N; ++t) pin(o[t]);
 }
 
 // The 4-bit pattern that a row's latent chunks are XOR-ed with.  A row of 512
@@ -218,14 +237,13 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             }
         }
     };
-    // Starts the loads of the wave's 8 rows of stage j into the ring.
+    // The loads of the wave's 8 rows of stage j into the ring, in kLoads pieces
+    // (piece `i` of `fetch`) that the loop spreads between its products.
     const int64_t ldb = a.ld_cache * 2;
     const char* cache = reinterpret_cast<const char*>(a.cache);
     const char* zero = reinterpret_cast<const char*>(g_zero_row);
-    auto fetch = [&](int j, const Ahead& h) {
-        const uint32_t slot = (uint32_t)(j & (kStages - 1));
-        const uint32_t stage = lds_offset(lds) + slot * kStageB;
-        const char* src[8];
+    struct Rows { const char* src[8]; uint32_t ok; };
+    auto locate = [&](int j, const Ahead& h, Rows& rows) {
         uint32_t ok = 0, in = 0;
         const int e0 = j * kTile + wave * 8;
         if constexpr (PAGED) in = (uint32_t)e0 - block_of((uint32_t)e0) * (uint32_t)a.pages.block_size;
@@ -236,42 +254,59 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 r = r < 0 ? -1 : r * a.pages.stride_rows + in;
                 in = in + 1 == (uint32_t)a.pages.block_size ? 0 : in + 1;
             }
-            const bool there = r >= 0 && r < a.cache_rows && e0 + i < w.n;
-            src[i] = there ? cache + r * ldb : zero;
+            const bool there = r >= 0 && r < a.cache_rows && e0 + i < w.n && j < s1;
+            int64_t at = (there ? r : 0) * ldb;
+            asm("" : "+s"(at));  // a select each, not a branch around the product
+            rows.src[i] = (there ? cache : zero) + at;
             ok |= there ? 1u << i : 0u;
         }
+        rows.ok = ok;
+    };
+    auto fetch = [&](int j, const Rows& rows, int i) {
+        const uint32_t slot = (uint32_t)(j & (kStages - 1));
+        const uint32_t stage = lds_offset(lds) + slot * kStageB;
         int lane = tid & 63;
         asm volatile("" : "+v"(lane));  // offsets are formed here and not kept in registers
         const int half = lane >> 5, col = lane & 31;
-        if constexpr (kRowB == 1024) {
+        if (i < kLoads - 1) {
+            if constexpr (kRowB == 1024)
+                load_to_lds(rows.src[i], (lane ^ chunk_xor(wave * 8 + i)) * 16, stage + (wave * 8 + i) * kRowB);
+            else  // two rows a load
+                load_to_lds((half ? rows.src[2 * i + 1] : rows.src[2 * i]) +
+                                ((col ^ chunk_xor(wave * 8 + 2 * i + half)) * 16),
+                            stage + (wave * 8 + 2 * i) * kRowB);
+        } else {  // the rotary parts: 8 rows x 128 bytes
+            const int r8 = lane >> 3;
+            uint64_t x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                load_to_lds(src[i], (lane ^ chunk_xor(wave * 8 + i)) * 16, stage + (wave * 8 + i) * kRowB);
-        } else {  // two rows a load
+            for (int e = 0; e < 8; ++e) {
+                x[e] = (uint64_t)(uintptr_t)rows.src[e];
+                asm("" : "+s"(x[e]));  // chosen between in registers, not by address
+            }
 #pragma unroll
-            for (int i = 0; i < 8; i += 2)
-                load_to_lds((half ? src[i + 1] : src[i]) + ((col ^ chunk_xor(wave * 8 + i + half)) * 16),
-                            stage + (wave * 8 + i) * kRowB);
+            for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2 * d) x[e] = r8 & d ? x[e + d] : x[e];
+            const char* mine = reinterpret_cast<const char*>((uintptr_t)x[0]);
+            load_to_lds(mine + kRowB + (((lane & 7) ^ (((wave * 8 + r8) >> 1) & 7)) * 16),
+                        stage + kTile * kRowB + wave * 8 * (kRope * 2));
+            if (lane == 0) valid[slot * kAttendWaves + wave] = (char)rows.ok;
         }
-        const int r8 = lane >> 3;  // the rotary parts: 8 rows x 128 bytes
-        const char* mine = src[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) mine = r8 == i ? src[i] : mine;
-        load_to_lds(mine + kRowB + (((lane & 7) ^ (((wave * 8 + r8) >> 1) & 7)) * 16),
-                    stage + kTile * kRowB + wave * 8 * (kRope * 2));
-        if (lane == 0) valid[slot * kAttendWaves + wave] = (char)ok;
     };
 
+    // The ring is always filled (behind the last stage with the zero row), so
+    // that the number of loads under way is the same at every stage.
     Ahead ahead;
     if (s0 < s1) {
 #pragma unroll
         for (int p = 0; p < kStages - 1; ++p) {
-            if (s0 + p < s1) {
-                look(s0 + p, ahead);
-                fetch(s0 + p, ahead);
-            }
+            Rows rows;
+            look(s0 + p, ahead);
+            locate(s0 + p, ahead, rows);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) fetch(s0 + p, rows, i);
         }
-        if (s0 + kStages - 1 < s1) look(s0 + kStages - 1, ahead);
+        look(s0 + kStages - 1, ahead);
     }
 
     bf16x8 q[NQ];
@@ -298,33 +333,60 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                    (((dp * NT * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ chunk_xor(vrow)) * 16) + (lane & 1) * 8;
 
     f32x16 o[NT] = {};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) pin(o[t]);  // sums of their own, not copies of one zero
     float m = kNoMax, l = 0.f;
 
-    for (int j = s0; j < s1; ++j) {
-        // Stage j has arrived (later ones may be under way), and every wave is
-        // done with the stage whose place the next loads take.
-        if (j + 2 < s1)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
-        else if (j + 1 < s1)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // Waits until a stage has arrived, AFTER later ones being under way, and
+    // every wave is done with what it read before.
+    auto arrive = [&](auto after) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(after)::value * kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (j + kStages - 1 < s1) {
-            fetch(j + kStages - 1, ahead);
-            if (j + kStages < s1) look(j + kStages, ahead);
-        }
+    };
+    constexpr int GQ = 4, NG = NQ / GQ;  // the first product in groups, each read one group ahead
+    static_assert(NG == kLoads, "one piece of the next loads a group");
+    auto read_k = [&](int j, int g, bf16x8 (&k)[GQ]) {
         const int stage = (j & (kStages - 1)) * kStageB;
-
-        f32x16 s = {};
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int at = i < NL ? ((stage + ka) ^ ((i & 7) * 32)) + (i >> 3) * 256 : (stage + kr) ^ ((i - NL) * 32);
-            const bf16x8 k = *reinterpret_cast<const bf16x8*>(lds + at);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s, 0, 0, 0);
+        for (int i = 0; i < GQ; ++i) {
+            const int st = g * GQ + i;
+            const int at = st < NL ? ((stage + ka) ^ ((st & 7) * 32)) + (st >> 3) * 256
+                                   : (stage + kr) ^ ((st - NL) * 32);
+            k[i] = *reinterpret_cast<const bf16x8*>(lds + at);
         }
+    };
+    typedef __attribute__((address_space(3))) bf16x4* lds_b4;
+    // The values of output tile t, in the two steps' order.
+    auto read_v = [&](int j, int t, bf16x8 (&v)[2]) {
+        const int stage = (j & (kStages - 1)) * kStageB;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int at = ((stage + va) ^ ((t & 3) * 64)) + (t >> 2) * 256 + k * 16 * kRowB;
+            const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + at));
+            const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + (at ^ 32) + 8 * kRowB));
+            v[k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
 
+    f32x16 s = {};
+    if (s0 < s1) {
+        arrive(std::integral_constant<int, kStages - 2>{});
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            bf16x8 k[GQ];
+            read_k(s0, g, k);
+#pragma unroll
+            for (int i = 0; i < GQ; ++i)
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[i], q[g * GQ + i], s, 0, 0, 0);
+        }
+    }
+
+    // Stage j's scores are in s.  A pass forms the scores of stage j + 1 while
+    // the weights of stage j are computed, then adds stage j's values.
+    for (int j = s0; j < s1; ++j) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) pin(o[t]);  // they stay there from pass to pass
         // Which of the 32 keys this lane's row sees.
         uint32_t see = __builtin_amdgcn_readfirstlane(
             *reinterpret_cast<const uint32_t*>(valid + (j & (kStages - 1)) * kAttendWaves));
@@ -370,20 +432,50 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             if (j != s0) {
                 const float f = __builtin_amdgcn_exp2f(m - to);
                 l *= f;
+                sums_ready(o);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < NT; ++t) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) o[t][r] *= f;
+                    pin(o[t]);  // one tile at a time in vector registers
+                }
             }
             m = to;
         }
+
         bf16x8 p[2];
         float sum = 0.f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        auto weigh = [&](int r) {
             const float x = __builtin_amdgcn_exp2f(fmaf(s[r], c, -m));
             sum += x;
             p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
+        };
+        bf16x8 v[2][2];
+        f32x16 next = {};
+        if (j + 1 < s1) {
+            // After this the place of stage j - 1 is free for stage j + 3.
+            arrive(std::integral_constant<int, kStages - 3>{});
+            Rows rows;
+            locate(j + kStages - 1, ahead, rows);
+            bf16x8 k[2][GQ];
+            read_k(j + 1, 0, k[0]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (g + 1 < NG) read_k(j + 1, g + 1, k[(g + 1) & 1]);
+                else read_v(j, 0, v[0]);
+                fetch(j + kStages - 1, rows, g);
+#pragma unroll
+                for (int i = 0; i < GQ; ++i)
+                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[g & 1][i], q[g * GQ + i], next, 0, 0, 0);
+#pragma unroll
+                for (int r = g * 16 / NG; r < (g + 1) * 16 / NG; ++r) weigh(r);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            look(j + kStages, ahead);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) weigh(r);
+            if (!PAGED || !rows_differ) read_v(j, 0, v[0]);
         }
         l += sum;
 
@@ -395,40 +487,40 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                i32x4* v = reinterpret_cast<i32x4*>(lds + (j & (kStages - 1)) * kStageB);
+                i32x4* x16 = reinterpret_cast<i32x4*>(lds + (j & (kStages - 1)) * kStageB);
                 for (int i = tid; i < kTile * kRowB / 16; i += kAttendBlock) {
-                    i32x4 x = v[i];
+                    i32x4 x = x16[i];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if ((x[e] & 0x7F80) == 0x7F80) x[e] &= 0xFFFF0000;
                         if ((x[e] & 0x7F800000) == 0x7F800000) x[e] &= 0xFFFF;
                     }
-                    v[i] = x;
+                    x16[i] = x;
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
+                read_v(j, 0, v[0]);
             }
         }
 
-        typedef __attribute__((address_space(3))) bf16x4* lds_b4;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+            if (t + 1 < NT) read_v(j, t + 1, v[(t + 1) & 1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int at = ((stage + va) ^ ((t & 3) * 64)) + (t >> 2) * 256 + k * 16 * kRowB;
-                const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + at));
-                const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + (at ^ 32) + 8 * kRowB));
-                const bf16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[k], o[t], 0, 0, 0);
-            }
+            for (int k = 0; k < 2; ++k) add_product(o[t], v[t & 1][k], p[k]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        s = next;
     }
 
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is loaded into LDS behind the workgroup's end
     {
         const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
         l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
+    sums_ready(o);
     if (!row_ok) return;
     const int64_t rh = token * a.heads + head;
     const float lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
