@@ -457,7 +457,8 @@ int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, 
  * q, cache, out and their strides must be multiples of 16 bytes.
  * Scores, softmax statistics and sums are held in 32 bits; the weights are
  * rounded to bf16 for the products with the values.
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (d_latent, d_rope, heads > 1024),
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (d_latent, d_rope, heads > 1024,
+ *         cache_rows >= 2^31),
  *         RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t latent_attend_rows_workspace_size(int64_t rows, int32_t heads, int32_t d_latent, int32_t k);

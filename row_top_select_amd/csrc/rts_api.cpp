@@ -356,7 +356,7 @@ int attend_args(const rts::AttendArgs& a, int32_t d_rope) {
     const int64_t d = (int64_t)a.d_latent + d_rope;
     if (a.ld_cache < d || a.ld_head < d || a.ld_q < 0) return RTS_EINVAL;
     if ((a.d_latent != 256 && a.d_latent != 512) || d_rope != 64 || a.heads > 1024 ||
-        a.rows > 0x7FFFFFFFll / a.heads)
+        a.rows > 0x7FFFFFFFll / a.heads || a.cache_rows > 0x7FFFFFFFll)
         return RTS_EUNSUPPORTED;
     if (a.rows == 0) return RTS_OK;
     if (!a.q || !a.out || (a.cache_rows > 0 && !a.cache)) return RTS_EINVAL;

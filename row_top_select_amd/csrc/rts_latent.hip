@@ -21,10 +21,16 @@
 // once, which costs matrix time where the rows' bytes bound the call.
 //
 // Key rows come through a ring of four 32-key stages, loaded straight into LDS
-// three stages ahead; where a row lies is looked up with scalar loads another
-// stage ahead.  16-byte chunks are XOR-ed within 256 bytes by the row number,
-// so that neither the row reads of the first product nor the transposed reads
-// of the second meet in a bank.
+// three stages ahead; where a row lies (its id, or its block-table entry) comes
+// the same way another two stages ahead.  A stage is stored by 64-element
+// columns, [column][key][128 bytes]: a load of 8 keys x 128 bytes is then 64
+// lanes in a row, and a lane's nine loads differ by constants only.  A wave has
+// eight issue slots a matrix instruction and needs most of them for LDS reads
+// and the softmax, so the loads must cost few (with 1024-byte rows and scalar
+// address arithmetic they made the loop issue-bound: 33% matrix busy).
+// 16-byte chunks of a 128-byte row are XOR-ed by the key's number, so that
+// neither the row reads of the first product nor the transposed reads of the
+// second meet in a bank.
 //
 // The running maximum is only moved when a score exceeds it by 2^8: then, and
 // not at every step, O is rescaled.  Any reference gives the same quotient; a
@@ -47,6 +53,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kRope = 64;
 constexpr int kTile = 32;    // keys of a stage, query rows of a wave
 constexpr int kStages = 4;
+constexpr int kEntryStages = 8;  // of list entries, read two stages further ahead
 constexpr int kAttendWaves = 4;
 constexpr int kAttendBlock = kAttendWaves * kWave;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,21 +71,28 @@ __device__ __forceinline__ uint16_t f32_bf16(float f) {
 // Where rows that do not exist are read from.
 __device__ const uint4 g_zero_row[(512 + kRope) * 2 / 16] = {};
 
-typedef __attribute__((address_space(4))) const int32_t* scalar_i32;  // read by scalar loads
-
-// 16 bytes a lane from global memory to LDS at base + 16 * lane, the source a
-// wave's address plus a lane's offset, or a lane's address.  Written in
-// assembly (no register is loaded) because the compiler cannot tell the ring's
-// stages apart: with the builtin it waits for every load under way before it
-// reads any stage.  The loop below counts the loads and waits itself.
-__device__ __forceinline__ uint32_t lds_offset(const char* p) {
+// LDS by its byte address.
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
+}
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
-__device__ __forceinline__ void load_to_lds(const char* src, int offset, uint32_t base) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" :: "{m0}"(base), "v"(offset), "s"(src) : "memory");
-}
+
+// SIZE bytes a lane from global memory, src + OFFSET, to LDS at base + OFFSET +
+// SIZE * lane.  Written in assembly (no register is loaded) because the
+// compiler cannot tell the ring's stages apart: with the builtin it waits for
+// every load under way before it reads any stage.  The loop below counts the
+// loads and waits itself.
+template <int SIZE, int OFFSET>
 __device__ __forceinline__ void load_to_lds(const char* src, uint32_t base) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(base), "v"(src) : "memory");
+    if constexpr (SIZE == 16)
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" :: "{m0}"(base), "v"(src), "n"(OFFSET)
+                     : "memory");
+    else
+        asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off offset:%2" :: "{m0}"(base), "v"(src), "n"(OFFSET)
+                     : "memory");
 }
 
 // o += v p with the sums in accumulation registers, where the compiler would
@@ -98,11 +112,22 @@ __device__ __forceinline__ void sums_ready(f32x16 (&o)[N]) {
     for (int t = 0; t < N; ++t) pin(o[t]);
 }
 
-// The 4-bit pattern that a row's latent chunks are XOR-ed with.  A row of 512
-// or 1024 bytes starts at bank 0; rows 0..15 differ (row reads), and among
-// rows 4 i + 0..3 and 4 i + 4..7 each 64-byte quarter occurs twice
-// (transposed reads of 8 rows x 64 bytes).
-__device__ __forceinline__ int chunk_xor(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+// The 3-bit pattern that a key's chunks are XOR-ed with.  A pair of keys fills
+// the banks, so the 8 pairs among 16 keys have patterns of their own (row
+// reads), and of any 4 neighbouring pairs two take the upper half of their 128
+// bytes (transposed reads of 8 keys x 64 bytes).
+__device__ __forceinline__ int chunk_xor(int key) {
+    return ((key >> 1) & 1) << 2 | ((key >> 2) & 1) << 1 | ((key >> 3) & 1);
+}
+
+// f(integral_constant 0), ..., f(integral_constant N - 1).
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
 
 // Query rows and keys of one workgroup.
 struct Work {
@@ -123,13 +148,13 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     constexpr int DP = kAttendWaves / HG;      // parts of the values
     constexpr int NT = DL / 32 / DP;           // output tiles of a wave
     constexpr int NQ = (DL + kRope) / 16;      // steps of the first product
-    constexpr int NL = DL / 16;                // of them in the latent part
-    constexpr int kRowB = DL * 2;              // latent bytes of a key
     constexpr int kStageB = stage_bytes<DL>();
+    constexpr int kColumnB = kTile * 128;      // a column of a stage
     constexpr int MB = 32 * HG;                // query rows of a workgroup
-    constexpr int kLoads = 8 * kRowB / 1024 + 1;  // loads of a wave and stage
-    extern __shared__ __align__(1024) char lds[];
-    char* valid = lds + kStages * kStageB;     // [stage][wave]: which of the wave's 8 rows exist
+    constexpr int kLoads = DL / 64 + 1;        // columns: loads of a wave and stage
+    extern __shared__ __align__(1024) char lds_memory[];
+    const uint32_t lds = lds_address(lds_memory);
+    const uint32_t entries = lds + kStages * kStageB;  // [wave][stage % 8][64]: ids or block ids of 32 keys, twice
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -212,101 +237,55 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         if (a.tree && row_ok) tree = a.tree[token];
     }
 
-    // Row `i` of the wave's 8 rows of stage j: the id (rows form) or block id
-    // (paged form) that is read ahead.  Rows behind the last key read its entry.
-    struct Ahead { int32_t id[8]; };
-    const int last_key = w.n - 1;
     auto block_of = [&](uint32_t e) {
         return a.pages.shift >= 0 ? e >> a.pages.shift : e / (uint32_t)a.pages.block_size;
     };
-    const uint32_t last_block = PAGED && w.n > 0 ? block_of((uint32_t)last_key) : 0;
-    auto look = [&](int j, Ahead& h) {
-        const scalar_i32 list = (scalar_i32)(uintptr_t)w.list;
-        const int e0 = j * kTile + wave * 8;
-        if constexpr (!PAGED) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h.id[i] = list[e0 + i < last_key ? e0 + i : last_key];
-        } else {
-            uint32_t blk = block_of((uint32_t)e0), in = (uint32_t)e0 - blk * (uint32_t)a.pages.block_size;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h.id[i] = list[blk < last_block ? blk : last_block];
-                const bool wrap = ++in == (uint32_t)a.pages.block_size;
-                in = wrap ? 0 : in;
-                blk += wrap ? 1 : 0;
-            }
-        }
+    // Reads the list's entries of stage j's 32 keys into the wave's own copy.
+    const uint32_t my_entries = entries + wave * (kEntryStages * 256);
+    auto look = [&](int j) {
+        const uint32_t e = (uint32_t)j * kTile + col;
+        uint32_t at = e < (uint32_t)w.n ? e : (uint32_t)(w.n - 1);
+        if constexpr (PAGED) at = block_of(at);
+        load_to_lds<4, 0>(reinterpret_cast<const char*>(w.list) + (uint64_t)at * 4,
+                          my_entries + (j & (kEntryStages - 1)) * 256);
     };
-    // The loads of the wave's 8 rows of stage j into the ring, in kLoads pieces
-    // (piece `i` of `fetch`) that the loop spreads between its products.
+    // The physical row of key `i` of stage j, negative where there is none.
+    auto row_of = [&](int j, int i) {
+        const int entry = lds_read<int>(my_entries + (j & (kEntryStages - 1)) * 256 + i * 4);
+        const uint32_t e = (uint32_t)j * kTile + i;
+        int64_t r = entry;
+        if constexpr (PAGED) {
+            r = (int64_t)entry * a.pages.stride_rows + (e - block_of(e) * (uint32_t)a.pages.block_size);
+            r = entry < 0 ? -1 : r;
+        }
+        return r < a.cache_rows && e < (uint32_t)w.n && j < s1 ? (int)r : -1;
+    };
+    // The loads of the wave's 8 keys of stage j into the ring, a column each;
+    // lane l brings chunk l % 8 of key l / 8.
     const int64_t ldb = a.ld_cache * 2;
-    const char* cache = reinterpret_cast<const char*>(a.cache);
-    const char* zero = reinterpret_cast<const char*>(g_zero_row);
-    struct Rows { const char* src[8]; uint32_t ok; };
-    auto locate = [&](int j, const Ahead& h, Rows& rows) {
-        uint32_t ok = 0, in = 0;
-        const int e0 = j * kTile + wave * 8;
-        if constexpr (PAGED) in = (uint32_t)e0 - block_of((uint32_t)e0) * (uint32_t)a.pages.block_size;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int64_t r = h.id[i];
-            if constexpr (PAGED) {
-                r = r < 0 ? -1 : r * a.pages.stride_rows + in;
-                in = in + 1 == (uint32_t)a.pages.block_size ? 0 : in + 1;
-            }
-            const bool there = r >= 0 && r < a.cache_rows && e0 + i < w.n && j < s1;
-            int64_t at = (there ? r : 0) * ldb;
-            asm("" : "+s"(at));  // a select each, not a branch around the product
-            rows.src[i] = (there ? cache : zero) + at;
-            ok |= there ? 1u << i : 0u;
-        }
-        rows.ok = ok;
+    auto source = [&](int j) {
+        const int i = wave * 8 + (lane >> 3);
+        const int r = row_of(j, i);
+        const char* row = r < 0 ? reinterpret_cast<const char*>(g_zero_row)
+                                : reinterpret_cast<const char*>(a.cache) + r * ldb;
+        return row + (((lane & 7) ^ chunk_xor(i)) * 16);
     };
-    auto fetch = [&](int j, const Rows& rows, int i) {
-        const uint32_t slot = (uint32_t)(j & (kStages - 1));
-        const uint32_t stage = lds_offset(lds) + slot * kStageB;
-        int lane = tid & 63;
-        asm volatile("" : "+v"(lane));  // offsets are formed here and not kept in registers
-        const int half = lane >> 5, col = lane & 31;
-        if (i < kLoads - 1) {
-            if constexpr (kRowB == 1024)
-                load_to_lds(rows.src[i], (lane ^ chunk_xor(wave * 8 + i)) * 16, stage + (wave * 8 + i) * kRowB);
-            else  // two rows a load
-                load_to_lds((half ? rows.src[2 * i + 1] : rows.src[2 * i]) +
-                                ((col ^ chunk_xor(wave * 8 + 2 * i + half)) * 16),
-                            stage + (wave * 8 + 2 * i) * kRowB);
-        } else {  // the rotary parts: 8 rows x 128 bytes
-            const int r8 = lane >> 3;
-            uint64_t x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = (uint64_t)(uintptr_t)rows.src[e];
-                asm("" : "+s"(x[e]));  // chosen between in registers, not by address
-            }
-#pragma unroll
-            for (int d = 1; d < 8; d *= 2)
-#pragma unroll
-                for (int e = 0; e < 8; e += 2 * d) x[e] = r8 & d ? x[e + d] : x[e];
-            const char* mine = reinterpret_cast<const char*>((uintptr_t)x[0]);
-            load_to_lds(mine + kRowB + (((lane & 7) ^ (((wave * 8 + r8) >> 1) & 7)) * 16),
-                        stage + kTile * kRowB + wave * 8 * (kRope * 2));
-            if (lane == 0) valid[slot * kAttendWaves + wave] = (char)rows.ok;
-        }
+    auto fetch = [&](int j, const char* src, auto column) {
+        constexpr int i = decltype(column)::value;
+        load_to_lds<16, i * 128>(src, lds + (j & (kStages - 1)) * kStageB + i * (kColumnB - 128) + wave * 1024);
     };
 
     // The ring is always filled (behind the last stage with the zero row), so
     // that the number of loads under way is the same at every stage.
-    Ahead ahead;
     if (s0 < s1) {
 #pragma unroll
-        for (int p = 0; p < kStages - 1; ++p) {
-            Rows rows;
-            look(s0 + p, ahead);
-            locate(s0 + p, ahead, rows);
+        for (int p = 0; p < kStages + 1; ++p) look(s0 + p);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) fetch(s0 + p, rows, i);
+        for (int p = 0; p < kStages - 1; ++p) {
+            const char* src = source(s0 + p);
+            each<kLoads>([&](auto i) { fetch(s0 + p, src, i); });
         }
-        look(s0 + kStages - 1, ahead);
     }
 
     bf16x8 q[NQ];
@@ -321,16 +300,15 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         }
     }
 
-    // LDS offsets within a stage; the others differ by constants in the bits
-    // that the XOR leaves alone or by a further XOR.  First product: chunk
-    // 2 i + half of row col.
-    const int ka = col * kRowB + ((half ^ chunk_xor(col)) * 16);
-    const int kr = kTile * kRowB + col * (kRope * 2) + ((half ^ ((col >> 1) & 7)) * 16);
+    // First product: chunk 2 i + half of key col; the XOR of two steps' chunks
+    // and a column's offset are constants.
+    const uint32_t ka = lds + col * 128 + ((half ^ chunk_xor(col)) * 16);
     // Second product: each 16 lanes read 4 keys x 16 values and get a value's
     // 4 keys a lane.
-    const int vrow = 4 * half + ((lane & 15) >> 2);
-    const int va = vrow * kRowB +
-                   (((dp * NT * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ chunk_xor(vrow)) * 16) + (lane & 1) * 8;
+    const int vkey = 4 * half + ((lane & 15) >> 2);
+    const uint32_t va = lds + (dp * NT / 2) * kColumnB + vkey * 128 +
+                        (((dp * NT & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ chunk_xor(vkey)) * 16 +
+                        (lane & 1) * 8;
 
     f32x16 o[NT] = {};
 #pragma unroll
@@ -346,36 +324,45 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     };
     constexpr int GQ = 4, NG = NQ / GQ;  // the first product in groups, each read one group ahead
     static_assert(NG == kLoads, "one piece of the next loads a group");
-    auto read_k = [&](int j, int g, bf16x8 (&k)[GQ]) {
-        const int stage = (j & (kStages - 1)) * kStageB;
+    auto read_k = [&](const uint32_t (&at)[4], int g, bf16x8 (&k)[GQ]) {
 #pragma unroll
-        for (int i = 0; i < GQ; ++i) {
-            const int st = g * GQ + i;
-            const int at = st < NL ? ((stage + ka) ^ ((st & 7) * 32)) + (st >> 3) * 256
-                                   : (stage + kr) ^ ((st - NL) * 32);
-            k[i] = *reinterpret_cast<const bf16x8*>(lds + at);
+        for (int i = 0; i < GQ; ++i) k[i] = lds_read<bf16x8>(at[i] + g * kColumnB);
+    };
+    auto k_addresses = [&](int j, uint32_t (&at)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at[i] = (ka + (j & (kStages - 1)) * kStageB) ^ (i * 32);
+            asm("" : "+v"(at[i]));  // four registers, and the columns in the reads' offsets
         }
     };
     typedef __attribute__((address_space(3))) bf16x4* lds_b4;
-    // The values of output tile t, in the two steps' order.
-    auto read_v = [&](int j, int t, bf16x8 (&v)[2]) {
-        const int stage = (j & (kStages - 1)) * kStageB;
+    // The values of output tile t, in the two steps' order; at: [t & 1][lower, upper 8 keys].
+    auto read_v = [&](const uint32_t (&at)[2][2], int t, bf16x8 (&v)[2]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int at = ((stage + va) ^ ((t & 3) * 64)) + (t >> 2) * 256 + k * 16 * kRowB;
-            const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + at));
-            const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(lds + (at ^ 32) + 8 * kRowB));
+            const int off = (t >> 1) * kColumnB + k * 16 * 128;
+            const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(uintptr_t)(at[t & 1][0] + off));
+            const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_b4)(uintptr_t)(at[t & 1][1] + off + 1024));
             v[k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    auto v_addresses = [&](int j, uint32_t (&at)[2][2]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at[i >> 1][i & 1] = (va + (j & (kStages - 1)) * kStageB) ^ ((i >> 1) * 64 + (i & 1) * 16);
+            asm("" : "+v"(at[i >> 1][i & 1]));
         }
     };
 
     f32x16 s = {};
     if (s0 < s1) {
         arrive(std::integral_constant<int, kStages - 2>{});
+        uint32_t at[4];
+        k_addresses(s0, at);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             bf16x8 k[GQ];
-            read_k(s0, g, k);
+            read_k(at, g, k);
 #pragma unroll
             for (int i = 0; i < GQ; ++i)
                 s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[i], q[g * GQ + i], s, 0, 0, 0);
@@ -388,8 +375,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 #pragma unroll
         for (int t = 0; t < NT; ++t) pin(o[t]);  // they stay there from pass to pass
         // Which of the 32 keys this lane's row sees.
-        uint32_t see = __builtin_amdgcn_readfirstlane(
-            *reinterpret_cast<const uint32_t*>(valid + (j & (kStages - 1)) * kAttendWaves));
+        uint32_t see = (uint32_t)__ballot(row_of(j, col) >= 0);
         const bool rows_differ = PAGED && j * kTile + kTile > w.masked;
         if constexpr (PAGED) {
             if (rows_differ) {
@@ -451,31 +437,34 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
         };
         bf16x8 v[2][2];
+        uint32_t v_at[2][2];
+        v_addresses(j, v_at);
         f32x16 next = {};
         if (j + 1 < s1) {
             // After this the place of stage j - 1 is free for stage j + 3.
             arrive(std::integral_constant<int, kStages - 3>{});
-            Rows rows;
-            locate(j + kStages - 1, ahead, rows);
+            look(j + kStages + 1);
+            const char* src = source(j + kStages - 1);
+            uint32_t at[4];
+            k_addresses(j + 1, at);
             bf16x8 k[2][GQ];
-            read_k(j + 1, 0, k[0]);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (g + 1 < NG) read_k(j + 1, g + 1, k[(g + 1) & 1]);
-                else read_v(j, 0, v[0]);
-                fetch(j + kStages - 1, rows, g);
+            read_k(at, 0, k[0]);
+            each<NG>([&](auto group) {
+                constexpr int g = decltype(group)::value;
+                if constexpr (g + 1 < NG) read_k(at, g + 1, k[(g + 1) & 1]);
+                else read_v(v_at, 0, v[0]);
+                fetch(j + kStages - 1, src, group);
 #pragma unroll
                 for (int i = 0; i < GQ; ++i)
                     next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[g & 1][i], q[g * GQ + i], next, 0, 0, 0);
 #pragma unroll
                 for (int r = g * 16 / NG; r < (g + 1) * 16 / NG; ++r) weigh(r);
                 __builtin_amdgcn_sched_barrier(0);
-            }
-            look(j + kStages, ahead);
+            });
         } else {
 #pragma unroll
             for (int r = 0; r < 16; ++r) weigh(r);
-            if (!PAGED || !rows_differ) read_v(j, 0, v[0]);
+            if (!PAGED || !rows_differ) read_v(v_at, 0, v[0]);
         }
         l += sum;
 
@@ -487,8 +476,8 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                i32x4* x16 = reinterpret_cast<i32x4*>(lds + (j & (kStages - 1)) * kStageB);
-                for (int i = tid; i < kTile * kRowB / 16; i += kAttendBlock) {
+                i32x4* x16 = reinterpret_cast<i32x4*>(lds_memory + (j & (kStages - 1)) * kStageB);
+                for (int i = tid; i < kTile * DL * 2 / 16; i += kAttendBlock) {
                     i32x4 x = x16[i];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -500,13 +489,13 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                read_v(j, 0, v[0]);
+                read_v(v_at, 0, v[0]);
             }
         }
 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            if (t + 1 < NT) read_v(j, t + 1, v[(t + 1) & 1]);
+            if (t + 1 < NT) read_v(v_at, t + 1, v[(t + 1) & 1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) add_product(o[t], v[t & 1][k], p[k]);
             __builtin_amdgcn_sched_barrier(0);
@@ -609,7 +598,7 @@ static int launch_attend(const AttendArgs& a, int64_t blocks, int splits, void* 
     const int64_t n = a.rows * a.heads;
     float* part_out = static_cast<float*>(workspace);
     float* part_lse = part_out ? part_out + (int64_t)splits * n * DL : nullptr;
-    constexpr size_t lds = kStages * stage_bytes<DL>() + kStages * kAttendWaves;
+    constexpr size_t lds = kStages * stage_bytes<DL>() + kAttendWaves * kEntryStages * 256;
     hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)blocks, (unsigned)splits),
                        dim3(kAttendBlock), lds, s, a, splits, part_out, part_lse);
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;

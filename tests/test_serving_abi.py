@@ -87,7 +87,7 @@ def test_latent_refusals(call):
                dict(cache=ODD), dict(out=ODD), dict(lse=ODD), dict(ld_q=9220), dict(ld_head=580), dict(ld_cache=580),
                dict(ws_bytes=64)):
         assert call(**kw) == EINVAL, kw
-    for kw in (dict(dl=128), dict(dr=32), dict(heads=1025), dict(rows=1 << 28)):
+    for kw in (dict(dl=128), dict(dr=32), dict(heads=1025), dict(rows=1 << 28), dict(cache_rows=1 << 31)):
         assert call(**kw) == EUNSUP, kw
     assert call(rows=0) == 0
 
