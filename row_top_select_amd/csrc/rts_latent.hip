@@ -160,42 +160,55 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hg = wave % HG, dp = wave / HG;
 
+    // Pieces of a block are neighbours.
+    const int64_t block = blockIdx.x / (uint32_t)splits;
+    const int split = (int)(blockIdx.x - (uint32_t)block * (uint32_t)splits);
+
     Work w{};
     if constexpr (!PAGED) {
         const int blocks = (a.heads + MB - 1) / MB;
-        w.q0 = blockIdx.x / blocks;
-        w.head0 = (int)(blockIdx.x - w.q0 * blocks) * MB;
+        w.q0 = block / blocks;
+        w.head0 = (int)(block - w.q0 * blocks) * MB;
         int n = a.k;
         if (a.counts) n = a.counts[w.q0] < 0 ? 0 : a.counts[w.q0] < n ? a.counts[w.q0] : n;
         w.n = __builtin_amdgcn_readfirstlane(n);
         w.masked = w.n;
         w.list = a.ids + w.q0 * a.ld_ids;
     } else {
-        // Request i's row blocks start at block floor(starts[i] * heads / MB) + i,
-        // which leaves room for each request's own rounding up.
-        const int64_t b = blockIdx.x;
-        int64_t before = 0;
+        // The request and row block of this block: a running sum of the
+        // requests' blocks, 64 requests at a time.  Blocks follow each other
+        // without gaps (empty ones among them would leave shader engines idle,
+        // since workgroups go around them in turn).
+        int64_t before = 0, req = -1, flat = 0;
         for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
             const int64_t i = i0 + lane;
-            bool le = false;
+            int64_t st = 0, en = 0;
             if (i < a.reqs) {
-                const int64_t st = a.query_starts[i];
-                le = (st < 0 ? 0 : st) * a.heads / MB + i <= b;
+                st = a.query_starts[i];
+                en = a.query_starts[i + 1];
+                st = st < 0 ? 0 : st < a.rows ? st : a.rows;
+                en = en < st ? st : en < a.rows ? en : a.rows;
             }
-            const int got = __popcll(__ballot(le));
-            before += got;
-            if (got < 64) break;
+            const int own = (int)(((en - st) * a.heads + MB - 1) / MB);
+            int sum = own;  // inclusive
+            for (int d = 1; d < 64; d <<= 1) {
+                const int up = __shfl_up(sum, d);
+                if (lane >= d) sum += up;
+            }
+            const uint64_t past = __ballot(before + sum > block);
+            if (past) {
+                const int at = __ffsll((unsigned long long)past) - 1;
+                req = i0 + at;
+                w.q0 = __shfl(st, at);
+                w.tokens = (int)(__shfl(en, at) - w.q0);
+                flat = (block - before - __shfl(sum - own, at)) * MB;
+                break;
+            }
+            before += __shfl(sum, 63);
         }
-        const int64_t req = before - 1;  // >= 0: block 0 of request 0 is block 0
         if (req < 0) return;
-        int64_t st = a.query_starts[req], en = a.query_starts[req + 1];
-        st = st < 0 ? 0 : st < a.rows ? st : a.rows;
-        en = en < st ? st : en < a.rows ? en : a.rows;
-        const int64_t flat = (b - (st * a.heads / MB + req)) * MB;
-        w.tokens = (int)(en - st);
-        if (flat < 0 || flat >= (int64_t)w.tokens * a.heads) return;
+        req = __builtin_amdgcn_readfirstlane((int)req);
         w.flat0 = (int)flat;
-        w.q0 = st;
         const int32_t c = a.ctx_lens[req];
         w.ctx = c < 0 ? 0 : c;
         const int64_t first = flat / a.heads, last_row = (flat + MB - 1) / a.heads;
@@ -212,7 +225,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 
     const int all = (w.n + kTile - 1) / kTile;   // stages
     const int per = (all + splits - 1) / splits;
-    const int s0 = (int)blockIdx.y * per;
+    const int s0 = split * per;
     const int s1 = s0 + per < all ? s0 + per : all;
 
     // This lane's query row.
@@ -513,7 +526,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     if (!row_ok) return;
     const int64_t rh = token * a.heads + head;
     const float lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
-    const int64_t part = (int64_t)blockIdx.y * a.rows * a.heads + rh;
+    const int64_t part = (int64_t)split * a.rows * a.heads + rh;
     if (dp == 0 && half == 0) {
         if (splits > 1)
             part_lse[part] = lse;
@@ -594,13 +607,14 @@ AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_
 
 template <int DL, int HG, bool PAGED>
 static int launch_attend(const AttendArgs& a, int64_t blocks, int splits, void* workspace, hipStream_t s) {
-    if (blocks > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
+    const int64_t grid = blocks * splits;
+    if (grid > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
     const int64_t n = a.rows * a.heads;
     float* part_out = static_cast<float*>(workspace);
     float* part_lse = part_out ? part_out + (int64_t)splits * n * DL : nullptr;
     constexpr size_t lds = kStages * stage_bytes<DL>() + kAttendWaves * kEntryStages * 256;
-    hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)blocks, (unsigned)splits),
-                       dim3(kAttendBlock), lds, s, a, splits, part_out, part_lse);
+    hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)grid), dim3(kAttendBlock), lds, s, a,
+                       splits, part_out, part_lse);
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;
     if (splits == 1) return RTS_OK;
     return launch_merge_attend(part_out, RTS_F32, part_lse, splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
@@ -611,7 +625,8 @@ template <int DL, bool PAGED>
 static int launch_attend_rows_of(const AttendArgs& a, int splits, void* workspace, hipStream_t s) {
     const int hg = row_groups(PAGED ? rows_of_request(a.rows, a.reqs, a.heads) : a.heads);
     const int mb = 32 * hg;
-    const int64_t blocks = PAGED ? a.rows * a.heads / mb + a.reqs : a.rows * ((a.heads + mb - 1) / mb);
+    // Paged: no more than this, whatever the requests' lengths are.
+    const int64_t blocks = PAGED ? a.rows * a.heads / mb + (a.reqs < a.rows ? a.reqs : a.rows) : a.rows * ((a.heads + mb - 1) / mb);
     if (hg == 1) return launch_attend<DL, 1, PAGED>(a, blocks, splits, workspace, s);
     if (hg == 2) return launch_attend<DL, 2, PAGED>(a, blocks, splits, workspace, s);
     return launch_attend<DL, 4, PAGED>(a, blocks, splits, workspace, s);
