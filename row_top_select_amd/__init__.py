@@ -489,33 +489,41 @@ def merge_select_pairs_rank_major(gathered_pairs: torch.Tensor, k: int,
     return out
 
 
+# torch.cuda.current_stream(device).cuda_stream without the Stream object,
+# which costs as much as a small call's launch; where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch(fn, where: str, device: torch.device, stream, scratch, *args) -> None:
     """Calls ``fn(*args, stream)`` with ``device`` current.  Memory allocated here
     for the call (``scratch``) is kept until a stream other than the current one
     is done with it."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        s = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     else:
         if stream.device != device:
             raise ValueError(f"{where}: stream must belong to the device of the tensors")
         for t in scratch:
             t.record_stream(stream)
-    s = ctypes.c_void_p(stream.cuda_stream)
+        s = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, s), where)
+        status = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, s), where)
+            status = fn(*args, s)
+    if status != RTS_OK:
+        raise RtsError(status, where)
 
 
 def _on(device: torch.device, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and (not isinstance(t, torch.Tensor) or t.device != device):
+        if t is not None and t.device != device:
             raise ValueError(f"{name} must be a tensor on {device}")
 
 
 def _gpu(t, name: str) -> torch.device:
-    _dev(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
     return t.device
 
 
@@ -586,7 +594,7 @@ def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, bl
     if out is None:
         flat = torch.empty(reqs + 2 + 3 * tokens, dtype=torch.int32, device=device)
         made.append(flat)
-        out = SlotMap(*flat.split([reqs + 1, tokens, tokens, tokens, 1]))
+        out = SlotMap(*torch.split_with_sizes(flat, (reqs + 1, tokens, tokens, tokens, 1)))
     else:
         for name, t, n in zip(SlotMap._fields, out, (reqs + 1, tokens, tokens, tokens, 1)):
             _out(t, (n,), torch.int32, device, name, made)

@@ -644,21 +644,30 @@ int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* work
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ f32x8 load8(const float* p) {
-    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-    return f32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-}
-__device__ __forceinline__ f32x8 load8(const uint16_t* p) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    f32x8 r;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// 8 elements as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    uint4 w;
+    __device__ __forceinline__ f32x8 widen() const {
+        f32x8 r;
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = __uint_as_float(w[i] << 16);
-        r[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            r[2 * i] = __uint_as_float(x[i] << 16);
+            r[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        }
+        return r;
     }
-    return r;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 lo, hi;
+    __device__ __forceinline__ f32x8 widen() const {
+        return f32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    }
+};
 __device__ __forceinline__ void store8(float* p, f32x8 v) {
     reinterpret_cast<float4*>(p)[0] = float4{v[0], v[1], v[2], v[3]};
     reinterpret_cast<float4*>(p)[1] = float4{v[4], v[5], v[6], v[7]};
@@ -674,7 +683,10 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
 // out = sum_r e^(lse_r - lse) parts_r.  One thread per 8 elements of one
 // (row, head), so each part is read once in 16-byte loads and nothing passes
 // between threads; the world statistics are re-read by the dim / 8 threads of
-// a (row, head) from the caches.
+// a (row, head) from the caches.  kMergeAhead parts are on their way at a
+// time, also while the maximum is still being found.
+constexpr int kMergeAhead = 4;
+
 template <typename In, typename Out>
 __global__ __launch_bounds__(256) void merge_attend_kernel(
     const In* __restrict__ parts, const float* __restrict__ part_lse, int world, int64_t n, int dim8,
@@ -684,26 +696,47 @@ __global__ __launch_bounds__(256) void merge_attend_kernel(
     const int64_t rh = i / dim8;
     const int d = (int)(i - rh * dim8) * 8;
     if (row_limit && rh / heads >= *row_limit) return;
-    float m = -INFINITY;
-    for (int r = 0; r < world; ++r) m = fmaxf(m, part_lse[r * n + rh]);
+    const In* mine = parts + rh * dim8 * 8 + d;
+    const int64_t step = n * dim8 * 8;
+    const float* stat = part_lse + rh;
+
+    float x[kMergeAhead];
+    Raw8<In> v[kMergeAhead];
+    // Parts r0.. of the world; one that is empty or does not exist is not read.
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kMergeAhead; ++u) x[u] = r0 + u < world ? stat[(r0 + u) * n] : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kMergeAhead; ++u) {
+            v[u] = Raw8<In>{};
+            if (x[u] != -INFINITY) v[u] = *reinterpret_cast<const Raw8<In>*>(mine + (r0 + u) * step);
+        }
+    };
+    load(0);
+    float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    for (int r = kMergeAhead; r < world; ++r) m = fmaxf(m, stat[r * n]);
     f32x8 acc = {};
     float total = 0.f;
-    if (m > -INFINITY) {
-        for (int r = 0; r < world; ++r) {
-            const float x = part_lse[r * n + rh];
-            if (x == -INFINITY) continue;
-            const float w = __builtin_amdgcn_exp2f((x - m) * kLog2e);
-            total += w;
-            const f32x8 v = load8(parts + (r * n + rh) * dim8 * 8 + d);
+    if (m != -INFINITY) {
+        for (int r0 = 0;;) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+            for (int u = 0; u < kMergeAhead; ++u) {
+                const float w = __builtin_amdgcn_exp2f((x[u] - m) * kLog2e);
+                total += w;
+                const f32x8 e = v[u].widen();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, e[k], acc[k]);
+            }
+            r0 += kMergeAhead;
+            if (r0 >= world) break;
+            load(r0);
         }
         const float inv = 1.f / total;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
     }
     store8(out + rh * dim8 * 8 + d, acc);
-    if (lse && d == 0) lse[rh] = m > -INFINITY ? m + __builtin_amdgcn_logf(total) * kLn2 : m;
+    if (lse && d == 0) lse[rh] = m != -INFINITY ? m + __builtin_amdgcn_logf(total) * kLn2 : m;
 }
 
 int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
