@@ -139,6 +139,7 @@ struct AttendArgs {
 // How a call is cut into workgroups.
 struct AttendPlan {
     int splits;       // pieces of the keys, joined by a second kernel when > 1
+    int groups;       // 32-row groups of query rows a workgroup
     size_t ws_bytes;  // of the pieces' results
 };
 AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split);

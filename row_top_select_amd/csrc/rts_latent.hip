@@ -565,44 +565,45 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 
 constexpr int kCus = 256;
 
-// The number of pieces that a call's keys are cut into: the one with the least
-// estimated time.  A workgroup takes a CU for itself, about 1 us a stage and
-// 4 us around them; pieces cost their 32-bit results' way out and back at
-// 4 TB/s and a second launch.
-static AttendPlan plan_splits(int64_t blocks, int64_t stages, int64_t out_rows, int32_t d_latent, bool allow) {
-    const double piece = (double)out_rows * d_latent * 8 / 4e6;  // us
-    int best = 1;
+// How a call is cut: the row groups of a workgroup (1, 2 or 4 of 32 query
+// rows) and the pieces of the keys that take the least estimated time.  A
+// workgroup has a CU for itself.  Measured on 256 busy CUs, a stage takes 1.5,
+// 1.75 or 2.05 us with 1, 2 or 4 groups (1.15 to 1.5 us on one CU) and what
+// lies around the stages 7, 11 or 16 us; pieces cost a second launch and the
+// way of their 32-bit results out and back at 4 TB/s.  Small batches so take
+// fewer rows a workgroup and large ones more: 64 tokens x 128 heads x 2048 keys
+// runs with 2 groups and 2 pieces, 1024 tokens with 4 groups and one.
+static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, int64_t out_rows,
+                              int32_t d_latent, bool allow) {
+    constexpr double kStageUs[3] = {1.5, 1.75, 2.05}, kAroundUs[3] = {7, 11, 16};
+    const double piece = (double)out_rows * d_latent * 8 / 4e6;
+    const int most = !allow ? 1 : (int)(stages < 1 ? 1 : stages < 64 ? stages : 64);
+    AttendPlan best{1, 4, 0};
     double best_us = 1e300;
-    const int64_t most = !allow ? 1 : stages < 64 ? stages : 64;
-    for (int s = 1; s == 1 || s <= most; ++s) {
-        const int64_t per = (stages + s - 1) / s;
-        const double us = (double)((blocks * s + kCus - 1) / kCus) * (per + 4.0) + (s > 1 ? 4.0 + s * piece : 0.0);
-        if (us < best_us) best_us = us, best = s;
+    for (int g = 0; g < 3; ++g) {
+        const int hg = 1 << g;
+        const int64_t blocks = units * ((rows_each + 32 * hg - 1) / (32 * hg));
+        for (int s = 1; s <= most; ++s) {
+            const int64_t per = (stages + s - 1) / s;
+            const double us = (double)((blocks * s + kCus - 1) / kCus) * (per * kStageUs[g] + kAroundUs[g]) +
+                              (s > 1 ? 4.0 + s * piece : 0.0);
+            if (us < best_us) best_us = us, best.splits = s, best.groups = hg;
+        }
     }
-    const size_t ws = best > 1 ? (size_t)best * out_rows * (d_latent + 1) * 4 : 0;
-    return AttendPlan{best, (ws + 15) & ~size_t(15)};
+    if (best.splits > 1) best.ws_bytes = ((size_t)best.splits * out_rows * (d_latent + 1) * 4 + 15) & ~size_t(15);
+    return best;
 }
-
-// 32-row groups of a workgroup for blocks of about `rows` query rows.
-static int row_groups(int64_t rows) { return rows <= 32 ? 1 : rows <= 64 ? 2 : 4; }
 
 AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split) {
-    const int mb = 32 * row_groups(heads);
-    return plan_splits(rows * ((heads + mb - 1) / mb), ((int64_t)k + kTile - 1) / kTile, rows * heads, d_latent,
-                       allow_split);
+    return plan_pieces(rows, heads, ((int64_t)k + kTile - 1) / kTile, rows * heads, d_latent, allow_split);
 }
 
-// About the query rows that one request has.
-static int64_t rows_of_request(int64_t tokens, int64_t reqs, int32_t heads) {
-    return (tokens + reqs - 1) / reqs * heads;
-}
-
+// Goes by the mean number of tokens a request.
 AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent,
                              int64_t max_len, bool allow_split) {
-    const int64_t each = rows_of_request(tokens, reqs, heads);
-    const int mb = 32 * row_groups(each);
-    return plan_splits(reqs * ((each + mb - 1) / mb), (max_len + kTile - 1) / kTile, tokens * heads, d_latent,
-                       allow_split);
+    const int64_t active = reqs < tokens ? reqs : tokens;
+    return plan_pieces(active, (tokens + active - 1) / active * heads, (max_len + kTile - 1) / kTile,
+                       tokens * heads, d_latent, allow_split);
 }
 
 template <int DL, int HG, bool PAGED>
@@ -622,22 +623,22 @@ static int launch_attend(const AttendArgs& a, int64_t blocks, int splits, void* 
 }
 
 template <int DL, bool PAGED>
-static int launch_attend_rows_of(const AttendArgs& a, int splits, void* workspace, hipStream_t s) {
-    const int hg = row_groups(PAGED ? rows_of_request(a.rows, a.reqs, a.heads) : a.heads);
-    const int mb = 32 * hg;
+static int launch_attend_of(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
+    const int mb = 32 * plan.groups;
     // Paged: no more than this, whatever the requests' lengths are.
-    const int64_t blocks = PAGED ? a.rows * a.heads / mb + (a.reqs < a.rows ? a.reqs : a.rows) : a.rows * ((a.heads + mb - 1) / mb);
-    if (hg == 1) return launch_attend<DL, 1, PAGED>(a, blocks, splits, workspace, s);
-    if (hg == 2) return launch_attend<DL, 2, PAGED>(a, blocks, splits, workspace, s);
-    return launch_attend<DL, 4, PAGED>(a, blocks, splits, workspace, s);
+    const int64_t blocks = PAGED ? a.rows * a.heads / mb + (a.reqs < a.rows ? a.reqs : a.rows)
+                                 : a.rows * ((a.heads + mb - 1) / mb);
+    if (plan.groups == 1) return launch_attend<DL, 1, PAGED>(a, blocks, plan.splits, workspace, s);
+    if (plan.groups == 2) return launch_attend<DL, 2, PAGED>(a, blocks, plan.splits, workspace, s);
+    return launch_attend<DL, 4, PAGED>(a, blocks, plan.splits, workspace, s);
 }
 
 int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
     if (a.paged)
-        return a.d_latent == 512 ? launch_attend_rows_of<512, true>(a, plan.splits, workspace, s)
-                                 : launch_attend_rows_of<256, true>(a, plan.splits, workspace, s);
-    return a.d_latent == 512 ? launch_attend_rows_of<512, false>(a, plan.splits, workspace, s)
-                             : launch_attend_rows_of<256, false>(a, plan.splits, workspace, s);
+        return a.d_latent == 512 ? launch_attend_of<512, true>(a, plan, workspace, s)
+                                 : launch_attend_of<256, true>(a, plan, workspace, s);
+    return a.d_latent == 512 ? launch_attend_of<512, false>(a, plan, workspace, s)
+                             : launch_attend_of<256, false>(a, plan, workspace, s);
 }
 
 // --------------------------------------------------------------- rank merge
