@@ -400,7 +400,7 @@ int assign_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t reqs,
  * logits     float or bf16 bits (logits_dtype RTS_F32 or RTS_BF16)
  *            [rows, ld_logits], ld_logits >= cols.
  * q and keys and their row strides must be multiples of 16 bytes.
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 128, cols >= 2^31),
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 128, cols >= 2^31, ld_keys > 2^30),
  *         RTS_EHIP.
  */
 int indexer_logits(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t ld_q,
@@ -419,7 +419,7 @@ int indexer_logits(const void* q, int dtype, int64_t rows, int32_t heads, int32_
  * cols bounds every row end (ld_logits >= cols).  Neighbouring tokens of the
  * same request share the reads of their keys.
  * Errors: those of indexer_logits, RTS_EINVAL for block_size < 1, ld_table <
- *         table_cols, stride_rows < 0.
+ *         table_cols, stride_rows < 0, RTS_EUNSUPPORTED for cache_rows >= 2^31.
  */
 int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, int32_t dim,
                          int64_t ld_q, const void* key_cache, int64_t cache_rows, int64_t ld_keys,

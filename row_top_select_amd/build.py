@@ -29,14 +29,13 @@ COMMON = [
     "-Wall", "-Wno-unused-parameter",
 ]
 
-# Flags of single sources.
-EXTRA = {
-    # Matrix products start with their results in vector registers and move to
-    # accumulation registers under pressure: the latent kernels hold 256
-    # registers of sums beside 16 of scores, and the other way round the scores
-    # push the sums out to scratch.
-    "rts_latent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-}
+# Flags of single sources.  Matrix products start with their results in vector
+# registers and move to accumulation registers only under pressure.  The other
+# way round the indexer spends 2 of 6 vector instructions a product on copying
+# results back, and the latent kernels, which hold 256 registers of sums beside
+# 16 of scores, push sums out to scratch.
+_VECTOR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"rts_latent.hip": _VECTOR_RESULTS, "rts_indexer.hip": _VECTOR_RESULTS}
 
 
 def _compile(src: str) -> str:

@@ -289,7 +289,8 @@ int logits_args(const rts::LogitsArgs& a) {
     if (a.rows < 0 || a.cols < 0 || a.heads < 1 || a.dim < 1 || a.ld_weights < a.heads ||
         a.ld_logits < a.cols || a.ld_keys < a.dim || a.ld_q < (int64_t)a.heads * a.dim)
         return RTS_EINVAL;
-    if (a.heads > 128 || (a.dim != 64 && a.dim != 128) || a.cols > 0x7FFFFFFFll || a.rows > 0x7FFFFFFFll)
+    if (a.heads > 128 || (a.dim != 64 && a.dim != 128) || a.cols > 0x7FFFFFFFll ||
+        a.rows > 0x7FFFFFFFll || a.ld_keys > (1 << 30))
         return RTS_EUNSUPPORTED;
     if (a.rows == 0 || a.cols == 0) return RTS_OK;
     const int64_t esz = a.dtype == RTS_BF16 ? 2 : 1;
@@ -342,6 +343,7 @@ int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, 
     if (rc != RTS_OK) return rc;
     rc = pages_args(block_table, table_rows, table_cols, ld_table, block_size, stride_rows, cache_rows);
     if (rc != RTS_OK) return rc;
+    if (cache_rows > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
     if (rows == 0 || cols == 0) return RTS_OK;
     if (!req_id || !row_ends || !aligned(req_id, 4) || (cache_rows > 0 && !key_cache)) return RTS_EINVAL;
     a.pages = rts::make_pages(block_table, table_rows, table_cols, ld_table, block_size, stride_rows,

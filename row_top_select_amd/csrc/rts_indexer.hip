@@ -11,9 +11,13 @@
 // costs no masking.
 //
 // A workgroup keeps the queries of a few tokens in LDS, in the order in which
-// lanes read them (16 bytes a lane, no bank conflicts), and each of its waves
-// streams 64 keys at a time straight into registers, where they serve all
-// those tokens while the next 64 are on their way.
+// lanes read them (16 bytes a lane, no bank conflicts).  Each of its waves
+// streams 64 keys at a time through a ring of its own in LDS into registers,
+// where they serve all those tokens.  The ring is loaded straight from memory,
+// whole rows next to each other: read into registers at once, as the product
+// wants them (16 bytes of 32 rows), the same keys came at 3.4 TB/s whatever the
+// number of heads.  16-byte chunks are XOR-ed by the key's number so that the
+// reads do not meet in a bank.  Waves wait for their own loads only.
 //
 // e4m3 queries and keys are widened to bf16, which holds every e4m3 value, and
 // take the bf16 product: the 8-bit matrix instructions of this chip align the
@@ -21,6 +25,8 @@
 // largest (1.4e-5 of the result on N(0, 1) data in 64- and 16-element steps
 // alike, against 1e-7 here), too much for a select by score.  The queries are
 // widened once a workgroup, the keys once for all its tokens.
+#include <type_traits>
+
 #include "rts_device.hpp"
 #include "rts_internal.h"
 #include "rts_paged.hpp"
@@ -30,14 +36,11 @@ namespace rts {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLogitsWaves = 4;
-constexpr int kLogitsBlock = kLogitsWaves * kWave;
 constexpr int kKeyTile = 64;  // keys of a wave's step: two 32-column tiles
-constexpr int64_t kLogitsStep = kLogitsWaves * kKeyTile;
+constexpr int kRingInts = 2;  // steps of block-table entries and of key scales that a wave holds
 
 // Two of the four e4m3 in `w` as bf16 (exact).
 template <bool HI>
@@ -56,39 +59,58 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
     *p = __builtin_bit_cast(uint16_t, (__bf16)v);  // round to nearest even
 }
 
-// What a wave holds of its 64 keys: row chunks as they lie in memory (lane
-// half h has the 16-byte chunks 2 c + h of its two keys), and the factor of
-// the column that this lane stores (NaN: the key does not exist).
-template <int NC>
-struct Keys {
-    i32x4 raw[2][NC];
-    float scale;
+// What stands in for the keys of an empty cache; the factors of keys without
+// scales and of keys that do not exist.
+__device__ const uint4 g_no_key[256 / 16] = {};
+__device__ const float g_key_factor[2] = {1.f, __builtin_nanf("")};
+
+// Sizes of one kernel.
+template <int D, bool E4M3>
+struct LogitsShape {
+    static constexpr int kEsz = E4M3 ? 1 : 2;
+    static constexpr int kRowB = D * kEsz;         // bytes of a key
+    static constexpr int NI = D / 16;              // product steps
+    static constexpr int NC = kRowB / 32;          // 16-byte chunk pairs of a key
+    static constexpr int kStageB = kKeyTile * kRowB;
+    static constexpr int kLoads = kStageB / 1024 + 1;  // of a stage: rows and scales
+    // 64 keys of 256 bytes in a ring and 64 registers of them: half the waves.
+    static constexpr int kWaves = kRowB == 256 ? 4 : 8;
+    static constexpr int kStep = kWaves * kKeyTile;
+    static constexpr int ring_bytes(int stages) {
+        return kWaves * (stages * kStageB + 2 * kRingInts * kKeyTile * 4);
+    }
 };
 
 // D elements a row; tb tokens a workgroup, head_tiles tiles of 32 heads
-// (padded with zeros), `span` columns a workgroup.
+// (padded with zeros), `span` columns a workgroup, `stages` (1 or 2) of the
+// waves' rings.
 //
 // Both operands of product step i cover the same 16 elements of a row in the
 // same order, which is all that the sum needs: bf16 step i, half h has chunk
 // 2 i + h; e4m3 steps 2 c and 2 c + 1, half h have the halves of chunk 2 c + h.
 template <int D, bool E4M3, bool PAGED, typename Out>
-__global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsArgs a, int tb, int head_tiles,
-                                                                         int64_t span) {
-    constexpr int NI = D / 16;                // product steps
-    constexpr int kEsz = E4M3 ? 1 : 2;
-    constexpr int NC = D * kEsz / 32;         // chunk pairs of a row
-    extern __shared__ __align__(16) char lds[];
+__global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void indexer_logits_kernel(
+    LogitsArgs a, int tb, int head_tiles, int64_t span, int stages) {
+    using S = LogitsShape<D, E4M3>;
+    constexpr int NI = S::NI, NC = S::NC, kEsz = S::kEsz, kBlock = S::kWaves * kWave;
+    constexpr int NCH = S::kRowB / 16;               // chunks of a row
+    constexpr int kPairRows = 16 / NCH;              // rows in 256 bytes of LDS
+    extern __shared__ __align__(1024) char lds_memory[];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int64_t t0 = (int64_t)blockIdx.x * tb;
     const int n_tok = (int)(a.rows - t0 < tb ? a.rows - t0 : tb);
     const int hp = head_tiles * 32;
-    i32x4* lq = reinterpret_cast<i32x4*>(lds);                                // [tb][head_tiles][NI][64]
-    float* lw = reinterpret_cast<float*>(lq + tb * head_tiles * NI * kWave);  // [tb][hp]
-    int32_t* le = reinterpret_cast<int32_t*>(lw + tb * hp);                   // [tb] row ends
-    int32_t* lr = le + tb;                                                    // [tb] requests
+    char* ring_memory = lds_memory + wave * (S::ring_bytes(stages) / S::kWaves);
+    const uint32_t ring = lds_address(ring_memory);                    // [stages][64 keys]
+    const uint32_t entries = ring + stages * S::kStageB;               // [kRingInts][64]
+    const uint32_t scales = entries + kRingInts * kKeyTile * 4;        // [kRingInts][64]
+    i32x4* lq = reinterpret_cast<i32x4*>(lds_memory + S::ring_bytes(stages));  // [tb][head_tiles][NI][64]
+    float* lw = reinterpret_cast<float*>(lq + tb * head_tiles * NI * kWave);   // [tb][hp]
+    int32_t* le = reinterpret_cast<int32_t*>(lw + tb * hp);                    // [tb] row ends
+    int32_t* lr = le + tb;                                                     // [tb] requests
 
-    for (int th = wave; th < n_tok * head_tiles; th += kLogitsWaves) {
+    for (int th = wave; th < n_tok * head_tiles; th += S::kWaves) {
         const int tok = th / head_tiles, head = (th - tok * head_tiles) * 32 + (lane & 31);
         const char* src = static_cast<const char*>(a.q) + ((t0 + tok) * a.ld_q + (int64_t)head * D) * kEsz + half * 16;
         i32x4 raw[NC];
@@ -106,7 +128,7 @@ __global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsA
                 dst[c * kWave] = raw[c];
         }
     }
-    for (int i = tid; i < n_tok * hp; i += kLogitsBlock) {
+    for (int i = tid; i < n_tok * hp; i += kBlock) {
         const int t = i / hp, h = i - t * hp;
         lw[i] = h < a.heads ? a.weights[(t0 + t) * a.ld_weights + h] : 0.f;
     }
@@ -122,6 +144,11 @@ __global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsA
     }
     __syncthreads();
 
+    const int ends = le[lane < n_tok ? lane : 0];  // lane t: of token t
+    // An empty cache is never read: its keys do not exist, and row 0 is zeros.
+    const bool no_keys = PAGED && a.pages.cache_rows == 0;
+    const char* keys = no_keys ? reinterpret_cast<const char*>(g_no_key) : static_cast<const char*>(a.keys);
+    const uint32_t ld_bytes = (uint32_t)(a.ld_keys * kEsz);
     const int64_t c0 = (int64_t)blockIdx.y * span;
     // Runs of tokens that share their keys: all of them, or one request's.
     for (int ta = 0, tz; ta < n_tok; ta = tz) {
@@ -131,127 +158,254 @@ __global__ __launch_bounds__(kLogitsBlock, 2) void indexer_logits_kernel(LogitsA
             end = le[tz] > end ? le[tz] : end;
             ++tz;
         }
+        end = __builtin_amdgcn_readfirstlane(end);
+        tz = __builtin_amdgcn_readfirstlane(tz);
         const int64_t cend = c0 + span < end ? c0 + span : end;
-        const int32_t* page = nullptr;
+        const int64_t first = c0 + wave * kKeyTile;  // this wave's first column
+        if (first >= cend) continue;
+        const int steps = (int)((cend - first + S::kStep - 1) / S::kStep);
+        const int32_t* page = reinterpret_cast<const int32_t*>(g_no_key);
+        uint32_t last_block = 0;
         if constexpr (PAGED) {
-            if (end > 0) page = a.pages.table + (int64_t)lr[ta] * a.pages.ld;
+            if (a.pages.cols > 0) {
+                page = a.pages.table + (int64_t)lr[ta] * a.pages.ld;
+                last_block = (uint32_t)(a.pages.cols - 1);
+            }
         }
 
-        auto load = [&](int64_t c, Keys<NC>& k) {
-            int64_t phys[2];
+        // Reads the block-table entries of step n's keys, one a lane.
+        auto look = [&](int n) {
+            if constexpr (PAGED) {
+                const int64_t key = first + (int64_t)n * S::kStep + lane;
+                uint32_t at = block_of(a.pages, (uint32_t)(key < cend ? key : cend - 1));
+                at = at < last_block ? at : last_block;
+                load_to_lds<4, 0>(reinterpret_cast<const char*>(page) + (uint64_t)at * 4,
+                                  entries + (n & (kRingInts - 1)) * (kKeyTile * 4));
+            }
+        };
+        // Starts the loads of step n's keys and their factors.  A key that does
+        // not exist has row 0 in its place and the factor NaN; behind the last
+        // column the last key, whose scores are not stored.
+        auto fetch = [&](int n) {
+            int lane = tid & (kWave - 1);
+            asm volatile("" : "+v"(lane));  // offsets are formed here and not kept in registers
+            const int64_t key = first + (int64_t)n * S::kStep + lane;
+            int row = (int)(key < cend ? key : cend - 1);
+            const char* factor = reinterpret_cast<const char*>(g_key_factor);
+            if constexpr (PAGED) {
+                const int entry = lds_read<int>(entries + (n & (kRingInts - 1)) * (kKeyTile * 4) + lane * 4);
+                row = phys_row(a.pages, entry, (uint32_t)row);
+                if (row < 0) factor = reinterpret_cast<const char*>(g_key_factor + 1);
+            }
+            if (a.key_scales && row >= 0) factor = reinterpret_cast<const char*>(a.key_scales + row);
+            row = row < 0 ? 0 : row;
+            // This lane loads a chunk of key i * (64 / NCH) + lane / NCH.
+            int rows[S::kStageB / 1024];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t key = c + u * 32 + (lane & 31);
-                phys[u] = -1;
-                if (key < cend) {
-                    if constexpr (PAGED)
-                        phys[u] = phys_row(a.pages, page, (int32_t)key);
-                    else
-                        phys[u] = key;
+            for (int i = 0; i < S::kStageB / 1024; ++i) {
+                if constexpr (PAGED) {
+                    rows[i] = __shfl(row, i * (64 / NCH) + lane / NCH);
+                } else {
+                    const int64_t k = first + (int64_t)n * S::kStep + i * (64 / NCH) + lane / NCH;
+                    rows[i] = (int)(k < cend ? k : cend - 1);
                 }
             }
+            load_to_lds<4, 0>(factor, scales + (n & (kRingInts - 1)) * (kKeyTile * 4));
+            const uint32_t stage = ring + (stages == 2 ? (n & 1) * S::kStageB : 0);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const char* kp = static_cast<const char*>(a.keys) + phys[u] * a.ld_keys * kEsz + half * 16;
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    k.raw[u][i] = i32x4{};
-                    if (phys[u] >= 0) k.raw[u][i] = *reinterpret_cast<const i32x4*>(kp + i * 32);
-                }
+            for (int i = 0; i < S::kStageB / 1024; ++i) {
+                const int k = i * (64 / NCH) + lane / NCH;
+                const int chunk = (lane % NCH) ^ ((k / kPairRows) & (NCH - 1));
+                load_to_lds<16, 0>(keys + (uint64_t)(uint32_t)rows[i] * ld_bytes + chunk * 16, stage + i * 1024);
             }
-            const int64_t mine = half ? phys[1] : phys[0];  // this lane stores column c + lane
-            k.scale = mine < 0 ? __builtin_nanf("") : 1.f;
-            if (a.key_scales && mine >= 0) k.scale = a.key_scales[mine];
+        };
+        // Step n's keys have arrived; those of a later step may be under way.
+        auto arrive = [&](bool later) {
+            if (later)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kLoads) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        };
+        // Chunk 2 c + half of key u * 32 + lane % 32.
+        auto read_key = [&](int n, int u, int c) {
+            const int k = lane & 31;
+            const uint32_t at = ring + (stages == 2 ? (n & 1) * S::kStageB : 0) + u * 32 * S::kRowB + k * S::kRowB;
+            return lds_read<i32x4>(at + (((2 * c + half) ^ ((k / kPairRows) & (NCH - 1))) * 16));
         };
 
-        auto score = [&](int64_t c, const i32x4 (&k)[2][NI], float scale) {
-            for (int t = ta; t < tz; ++t) {
-                float sum[2] = {0.f, 0.f};
-                for (int tile = 0; tile < head_tiles; ++tile) {
-                    const i32x4* qa = lq + (t * head_tiles + tile) * NI * kWave + lane;
-                    f32x16 s[2] = {};
+        // Entries are two steps deep: those of a step are asked for when the
+        // step before has used its place, and before the keys that may still be
+        // under way when they are needed.
+        look(0);
+        look(1);
+        if constexpr (PAGED) arrive(false);
+        fetch(0);
+        if (stages == 2) {
+            look(2);
+            if (steps > 1) fetch(1);
+        }
+
+        // The items of a wave's work are (step, token, head tile), in that order.
+        // A turn forms the products of one item while the weighted sum of the
+        // item before it is taken, so that the matrix unit and the vector unit
+        // both have work in one wave.  Queries and weights are re-read for the
+        // item after as soon as their registers are used.
+        const int item0 = ta * head_tiles, items = (tz - ta) * head_tiles;
+        i32x4 x[NI];
+        f32x4 w[4];
+        f32x16 even[2] = {}, odd[2] = {};  // the scores of every other item
+        float sum[2] = {0.f, 0.f};
+        auto read_x = [&](int item, int i) { x[i] = lq[((item0 + item) * NI + i) * kWave + lane]; };
+        auto read_w = [&](int item, int g) {  // heads 8 g + 4 half + (0..3) of the item's tile
+            w[g] = *(reinterpret_cast<const f32x4*>(lw + (item0 + item) * 32) + half + 2 * g);
+        };
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const bf16x8 x = __builtin_bit_cast(bf16x8, qa[i * kWave]);
+        for (int i = 0; i < NI; ++i) read_x(0, i);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                x, __builtin_bit_cast(bf16x8, k[u][i]), s[u], 0, 0, 0);
-                    }
-                    const f32x4* w4 = reinterpret_cast<const f32x4*>(lw + t * hp + tile * 32) + half;
+        for (int g = 0; g < 4; ++g) read_w(0, g);
+
+        int item = 0, next_item = items > 1 ? 1 : 0;  // whose products are formed; the one after
+        int tile = head_tiles, token = ta - 1;        // what is summed: before the first item, nothing
+        const int64_t ld_out = a.ld_logits * (int64_t)sizeof(Out);
+        char* const out_row = static_cast<char*>(a.logits) + (t0 + ta) * ld_out;
+        char* out = out_row;                          // where the wave's 64 columns of the summed token start
+        int sum_c = 0;
+        float sum_scale = 0.f;
+        auto turn = [&](const i32x4 (&k)[2][NI], const f32x16 (&s)[2], f32x16 (&next)[2], auto products) {
+            constexpr bool kProducts = decltype(products)::value;
+            next[0] = next[1] = f32x16{};
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x4 w = w4[2 * g];  // heads 8 g + 4 half + (0..3)
+            for (int i = 0; i < NI; ++i) {
+                if constexpr (kProducts) {
+                    const bf16x8 q = __builtin_bit_cast(bf16x8, x[i]);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                sum[u] = fmaf(w[r], __builtin_elementwise_maximum(s[u][4 * g + r], 0.f), sum[u]);
-                    }
+                    for (int u = 0; u < 2; ++u)
+                        next[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q, __builtin_bit_cast(bf16x8, k[u][i]),
+                                                                          next[u], 0, 0, 0);
+                    read_x(next_item, i);
                 }
+#pragma unroll
+                for (int r = i * 16 / NI; r < (i + 1) * 16 / NI; ++r) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        sum[u] = fmaf(w[r >> 2][r & 3], __builtin_elementwise_maximum(s[u][r], 0.f), sum[u]);
+                    if (kProducts && (r & 3) == 3) read_w(item, r >> 2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (++tile < head_tiles) return;
+            if (token >= ta) {
                 // Both halves' sums of the key tile that this half stores.
-                const float other = __shfl_xor(half ? sum[0] : sum[1], 32);
-                const float v = ((half ? sum[1] : sum[0]) + other) * scale;
-                if (c + lane < le[t] && c + lane < cend)
-                    store_logit(static_cast<Out*>(a.logits) + (t0 + t) * a.ld_logits + c + lane, v);
+                const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[0]), __float_as_uint(sum[1]),
+                                                                false, false);
+                const float v = (__uint_as_float(z[0]) + __uint_as_float(z[1])) * sum_scale;
+                const int end = __builtin_amdgcn_readlane(ends, token);
+                if (lane < (end < (int)cend ? end : (int)cend) - sum_c)
+                    store_logit(reinterpret_cast<Out*>(out) + lane, v);
+                out += ld_out;
+            }
+            sum[0] = sum[1] = 0.f;
+            tile = 0;
+            token = token + 1 < tz ? token + 1 : ta;
+        };
+        // All items of the step at column c, two a pass so that no score is copied.
+        bool in_odd = false;  // where the scores of the item before are
+        auto step = [&](int64_t c, const i32x4 (&k)[2][NI], float scale) {
+            auto done = [&](int n) {
+                item = next_item;
+                next_item = next_item + 1 < items ? next_item + 1 : 0;
+                if (n == 0) {  // from here on this step's items are summed
+                    sum_c = (int)c;
+                    sum_scale = scale;
+                    out = out_row + c * (int64_t)sizeof(Out);
+                }
+            };
+            int n = 0;
+            if (in_odd) {
+                turn(k, odd, even, std::true_type{});
+                done(n++);
+            }
+            for (; n + 1 < items; n += 2) {
+                turn(k, even, odd, std::true_type{});
+                done(n);
+                turn(k, odd, even, std::true_type{});
+                done(n + 1);
+            }
+            in_odd = n < items;
+            if (in_odd) {
+                turn(k, even, odd, std::true_type{});
+                done(n);
             }
         };
 
-        constexpr int64_t stride = kLogitsStep;
-        int64_t c = c0 + wave * kKeyTile;
-        if (c >= cend) continue;
-        Keys<NC> k0;
-        load(c, k0);
-        if constexpr (E4M3) {
-            for (; c < cend; c += stride) {
-                i32x4 k[2][NI];
+        i32x4 k[2][NI];
+        for (int n = 0; n < steps; ++n) {
+            arrive(stages == 2 && n + 1 < steps);
+            const float scale = lds_read<float>(scales + (n & (kRingInts - 1)) * (kKeyTile * 4) + lane * 4);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) widen16(k0.raw[u][i], k[u][2 * i], k[u][2 * i + 1]);
-                const float scale = k0.scale;
-                if (c + stride < cend) load(c + stride, k0);
-                score(c, k, scale);
-            }
-        } else {
-            Keys<NC> k1;  // the two take turns, so that no register is copied
-            for (;;) {
-                if (c + stride < cend) load(c + stride, k1);
-                score(c, k0.raw, k0.scale);
-                c += stride;
-                if (c >= cend) break;
-                if (c + stride < cend) load(c + stride, k0);
-                score(c, k1.raw, k1.scale);
-                c += stride;
-                if (c >= cend) break;
-            }
+                for (int c = 0; c < NC; ++c) {
+                    const i32x4 raw = read_key(n, u, c);
+                    if constexpr (E4M3)
+                        widen16(raw, k[u][2 * c], k[u][2 * c + 1]);
+                    else
+                        k[u][c] = raw;
+                }
+            // The keys are in registers: their place takes those of `stages` steps on.
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            look(n + stages + 1);
+            if (n + stages < steps) fetch(n + stages);
+            step(first + (int64_t)n * S::kStep, k, scale);
         }
+        if (in_odd)
+            turn(k, odd, even, std::false_type{});
+        else
+            turn(k, even, odd, std::false_type{});
+        arrive(false);  // entries behind the last step
     }
 }
 
 template <int D, bool E4M3, bool PAGED, typename Out>
 static int launch_logits(const LogitsArgs& a, hipStream_t s) {
+    using S = LogitsShape<D, E4M3>;
+    constexpr int kLds = 160 << 10;
     const int head_tiles = (a.heads + 31) / 32;
-    const size_t per_token = (size_t)head_tiles * D * 64 + head_tiles * 32 * 4 + 8;
-    int tb = (int)((72 << 10) / per_token);  // two workgroups a CU
-    if (tb > 16) tb = 16;
-    if (PAGED) {  // about the tokens that one request has
-        const int64_t each = a.pages.table_rows > 0 ? (a.rows + a.pages.table_rows - 1) / a.pages.table_rows : 1;
-        if (tb > each) tb = (int)each;
+    const int per_token = head_tiles * D * 64 + head_tiles * 32 * 4 + 8;
+    // Tokens that share keys: all, or about those of one request.
+    int64_t want = a.rows;
+    if (PAGED) {
+        const int64_t reqs = a.pages.table_rows < a.rows ? a.pages.table_rows : a.rows;
+        want = reqs > 0 ? (a.rows + reqs - 1) / reqs : 1;
     }
-    if (tb > a.rows) tb = (int)a.rows;
-    if (tb < 1) tb = 1;
-    const int64_t blocks_x = (a.rows + tb - 1) / tb;
-    const int64_t steps = (a.cols + kLogitsStep - 1) / kLogitsStep;
-    int64_t parts = (512 + blocks_x - 1) / blocks_x;
-    if (parts < (steps + 7) / 8) parts = (steps + 7) / 8;
-    if (parts > steps) parts = steps;
-    if (parts > 65535) parts = 65535;
-    const int64_t per = (steps + parts - 1) / parts;
-    parts = (steps + per - 1) / per;
+    // Two stages of keys where few tokens leave little time for the next one.
+    const int stages = S::ring_bytes(2) + per_token * want <= kLds ? 2 : 1;
+    const int64_t fit = (kLds - S::ring_bytes(stages)) / per_token;
+    const int64_t most = want < 16 ? (want < fit ? want : fit) : (fit < 16 ? fit : 16);
+    const int64_t steps = (a.cols + S::kStep - 1) / S::kStep;
+    // Tokens a workgroup and columns a workgroup by estimated time: a workgroup
+    // takes a CU, 6 us around its steps, 0.5 us a step and kItemUs a head tile
+    // of a token in a step (64 keys a wave through the matrix unit).  Where
+    // this leaves a round of the 256 CUs half empty it costs most.
+    constexpr double kItemUs = (D / 128.0) * (S::kWaves / 4) * 0.25;
+    int64_t tb = 1, per = steps;
+    double best = 1e300;
+    for (int64_t t = 1; t <= most; ++t) {
+        const int64_t bx = (a.rows + t - 1) / t;
+        for (int round = 1; round <= 4; ++round) {
+            int64_t parts = 256 * round / bx;
+            parts = parts < 1 ? 1 : parts > steps ? steps : parts;
+            const int64_t p = (steps + parts - 1) / parts;
+            const double us = (double)((bx * ((steps + p - 1) / p) + 255) / 256) *
+                              (6.0 + p * (0.5 + t * head_tiles * kItemUs));
+            if (us < best) best = us, tb = t, per = p;
+        }
+    }
+    const int64_t blocks_x = (a.rows + tb - 1) / tb, parts = (steps + per - 1) / per;
+    if (parts > 65535) return RTS_EUNSUPPORTED;
     hipLaunchKernelGGL((indexer_logits_kernel<D, E4M3, PAGED, Out>),
-                       dim3((unsigned)blocks_x, (unsigned)parts), dim3(kLogitsBlock), per_token * tb, s, a, tb,
-                       head_tiles, per * kLogitsStep);
+                       dim3((unsigned)blocks_x, (unsigned)parts), dim3(S::kWaves * kWave),
+                       S::ring_bytes(stages) + per_token * tb, s, a, (int)tb, head_tiles, per * S::kStep, stages);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 

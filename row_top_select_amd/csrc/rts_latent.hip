@@ -71,30 +71,6 @@ __device__ __forceinline__ uint16_t f32_bf16(float f) {
 // Where rows that do not exist are read from.
 __device__ const uint4 g_zero_row[(512 + kRope) * 2 / 16] = {};
 
-// LDS by its byte address.
-template <typename T>
-__device__ __forceinline__ T lds_read(uint32_t at) {
-    return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
-}
-__device__ __forceinline__ uint32_t lds_address(const char* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
-
-// SIZE bytes a lane from global memory, src + OFFSET, to LDS at base + OFFSET +
-// SIZE * lane.  Written in assembly (no register is loaded) because the
-// compiler cannot tell the ring's stages apart: with the builtin it waits for
-// every load under way before it reads any stage.  The loop below counts the
-// loads and waits itself.
-template <int SIZE, int OFFSET>
-__device__ __forceinline__ void load_to_lds(const char* src, uint32_t base) {
-    if constexpr (SIZE == 16)
-        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2" :: "{m0}"(base), "v"(src), "n"(OFFSET)
-                     : "memory");
-    else
-        asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off offset:%2" :: "{m0}"(base), "v"(src), "n"(OFFSET)
-                     : "memory");
-}
-
 // o += v p with the sums in accumulation registers, where the compiler would
 // put them only under pressure and with copies.  It does not see the product,
 // so the wait states are here: two after a vector instruction that wrote an
@@ -250,15 +226,12 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         if (a.tree && row_ok) tree = a.tree[token];
     }
 
-    auto block_of = [&](uint32_t e) {
-        return a.pages.shift >= 0 ? e >> a.pages.shift : e / (uint32_t)a.pages.block_size;
-    };
     // Reads the list's entries of stage j's 32 keys into the wave's own copy.
     const uint32_t my_entries = entries + wave * (kEntryStages * 256);
     auto look = [&](int j) {
         const uint32_t e = (uint32_t)j * kTile + col;
         uint32_t at = e < (uint32_t)w.n ? e : (uint32_t)(w.n - 1);
-        if constexpr (PAGED) at = block_of(at);
+        if constexpr (PAGED) at = block_of(a.pages, at);
         load_to_lds<4, 0>(reinterpret_cast<const char*>(w.list) + (uint64_t)at * 4,
                           my_entries + (j & (kEntryStages - 1)) * 256);
     };
@@ -266,12 +239,12 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     auto row_of = [&](int j, int i) {
         const int entry = lds_read<int>(my_entries + (j & (kEntryStages - 1)) * 256 + i * 4);
         const uint32_t e = (uint32_t)j * kTile + i;
-        int64_t r = entry;
-        if constexpr (PAGED) {
-            r = (int64_t)entry * a.pages.stride_rows + (e - block_of(e) * (uint32_t)a.pages.block_size);
-            r = entry < 0 ? -1 : r;
-        }
-        return r < a.cache_rows && e < (uint32_t)w.n && j < s1 ? (int)r : -1;
+        int r;
+        if constexpr (PAGED)
+            r = phys_row(a.pages, entry, e);
+        else
+            r = entry < a.cache_rows ? entry : -1;
+        return e < (uint32_t)w.n && j < s1 ? r : -1;
     };
     // The loads of the wave's 8 keys of stage j into the ring, a column each;
     // lane l brings chunk l % 8 of key l / 8.

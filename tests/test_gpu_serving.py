@@ -209,6 +209,22 @@ def test_indexer_logits_paged(rts, dtype, counts, heads, dim, block, ctx):
         assert (got[t, ends[t]:] == 77.0).all()
 
 
+def test_paged_calls_without_pages(rts):
+    say("paged calls on an empty table and an empty cache")
+    q, keys, w, _ = index_inputs(4, 3, 32, 128, 64, torch.bfloat16)
+    for keys_d, table in ((keys.to(DEV), torch.empty(2, 0, dtype=torch.int32, device=DEV)),
+                          (keys[:0].to(DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV))):
+        got = rts.indexer_logits_paged(q.to(DEV).view(3, 32, 128), keys_d, w.contiguous().to(DEV), i32([0, 1, 1]),
+                                       i32([5, 40, 0]), table, 16, 40, out=torch.zeros(3, 40, device=DEV)).cpu()
+        assert torch.isnan(got[0, :5]).all() and torch.isnan(got[1]).all()
+        assert (got[0, 5:] == 0).all() and (got[2] == 0).all()
+    lq, cache = latent_inputs(5, 3, 16, 512, 64)
+    for cache_d, table in ((cache.to(DEV), torch.empty(2, 0, dtype=torch.int32, device=DEV)),
+                           (cache[:0].to(DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV))):
+        out, lse = rts.latent_attend_paged(lq.to(DEV), cache_d, i32([0, 1, 3]), i32([9, 20]), table, 16, 0.07)
+        assert (out == 0).all() and (lse == -math.inf).all()
+
+
 # ---------------------------------------------------------- latent attention
 
 def latent_inputs(seed, rows, heads, latent, cache_rows, sharp=1.0):

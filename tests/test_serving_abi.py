@@ -56,13 +56,14 @@ def test_indexer_logits_refusals(paged):
                dict(out=ODD), dict(ld_q=1028), dict(ld_keys=132)):
         assert logits(paged, **kw) == EINVAL, kw
     for kw in (dict(heads=129, ld_q=129 * 128, ld_w=129), dict(dim=96), dict(dim=256, ld_q=2048, ld_keys=256),
-               dict(cols=1 << 31, ld_out=1 << 31)):
+               dict(cols=1 << 31, ld_out=1 << 31), dict(ld_keys=(1 << 30) + 16)):
         assert logits(paged, **kw) == EUNSUP, kw
     assert logits(paged, rows=0) == 0 and logits(paged, cols=0) == 0
     if paged:
         for kw in (dict(cache_rows=-1), dict(req=None), dict(ends=None), dict(table=None), dict(t_rows=-1),
                    dict(t_cols=-1), dict(ld_t=3), dict(block=0), dict(stride=-1), dict(req=ODD), dict(table=ODD)):
             assert logits(True, **kw) == EINVAL, kw
+        assert logits(True, cache_rows=1 << 31) == EUNSUP
 
 
 def rows(**kw):
