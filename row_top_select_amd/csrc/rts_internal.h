@@ -138,8 +138,9 @@ struct AttendArgs {
 
 // How a call is cut into workgroups.
 struct AttendPlan {
-    int splits;       // pieces of the keys, joined by a second kernel when > 1
+    int splits;       // pieces of a row's keys (at most, in the paged form), joined by a second kernel when > 1
     int groups;       // 32-row groups of query rows a workgroup
+    int target;       // workgroups that the pieces are to fill
     size_t ws_bytes;  // of the pieces' results
 };
 AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split);

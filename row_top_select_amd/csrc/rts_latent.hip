@@ -117,8 +117,61 @@ struct Work {
     const int32_t* list;  // ids of the row, or the request's block-table row
 };
 
+// x of the lane that CTRL names within rows of 16 lanes or of the rows before
+// (0x111.. row shifts by 1.., 0x142 and 0x143 the last lane of the row or half
+// before); `none` where there is no such lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int from_lane(int none, int x) {
+    return __builtin_amdgcn_update_dpp(none, x, CTRL, ROWS, 0xF, false);
+}
+// Inclusive sums over the wave's lanes: a few cycles a step, where a shuffle
+// through LDS takes a hundred.
+__device__ __forceinline__ int wave_sums(int x) {
+    x += from_lane<0x111, 0xF>(0, x);
+    x += from_lane<0x112, 0xF>(0, x);
+    x += from_lane<0x114, 0xF>(0, x);
+    x += from_lane<0x118, 0xF>(0, x);
+    x += from_lane<0x142, 0xA>(0, x);
+    x += from_lane<0x143, 0xC>(0, x);
+    return x;
+}
+__device__ __forceinline__ float wave_total(float x) {
+    auto get = [](int v) { return __int_as_float(v); };
+    x += get(from_lane<0x111, 0xF>(0, __float_as_int(x)));
+    x += get(from_lane<0x112, 0xF>(0, __float_as_int(x)));
+    x += get(from_lane<0x114, 0xF>(0, __float_as_int(x)));
+    x += get(from_lane<0x118, 0xF>(0, __float_as_int(x)));
+    x += get(from_lane<0x142, 0xA>(0, __float_as_int(x)));
+    x += get(from_lane<0x143, 0xC>(0, __float_as_int(x)));
+    return get(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+__device__ __forceinline__ int wave_most(int x) {  // of numbers >= 0
+    auto most = [](int p, int q) { return p > q ? p : q; };
+    x = most(x, from_lane<0x111, 0xF>(0, x));
+    x = most(x, from_lane<0x112, 0xF>(0, x));
+    x = most(x, from_lane<0x114, 0xF>(0, x));
+    x = most(x, from_lane<0x118, 0xF>(0, x));
+    x = most(x, from_lane<0x142, 0xA>(0, x));
+    x = most(x, from_lane<0x143, 0xC>(0, x));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// Paged form: how many keys of its request a token's rows may see, `upto` being
+// the tokens of the request up to it.
+__device__ __forceinline__ int keys_seen(const AttendArgs& a, int ctx, int tokens, int upto) {
+    int64_t n = (int64_t)ctx + (a.tree ? (tokens < 64 ? tokens : 64) : upto);
+    const int64_t held = (int64_t)a.pages.cols * a.pages.block_size;
+    n = n < held ? n : held;
+    return (int)(n < 0x7FFFFFC0 ? n : 0x7FFFFFC0);
+}
+
+// The pieces of `stages` at `chunk` a piece; a row block without keys is one.
+__device__ __forceinline__ int pieces_of(int stages, int chunk) {
+    return stages > chunk ? (stages + chunk - 1) / chunk : 1;
+}
+
 template <int DL, int HG, bool PAGED>
-__global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendArgs a, int splits,
+__global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendArgs a, int splits, int target,
                                                                         float* __restrict__ part_out,
                                                                         float* __restrict__ part_lse) {
     constexpr int DP = kAttendWaves / HG;      // parts of the values
@@ -136,13 +189,13 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hg = wave % HG, dp = wave / HG;
 
-    // Pieces of a block are neighbours.
-    const int64_t block = blockIdx.x / (uint32_t)splits;
-    const int split = (int)(blockIdx.x - (uint32_t)block * (uint32_t)splits);
-
+    int split;       // which piece of the block's keys, of how many
+    int pieces = splits;
     Work w{};
     if constexpr (!PAGED) {
         const int blocks = (a.heads + MB - 1) / MB;
+        const int64_t block = blockIdx.x / (uint32_t)splits;
+        split = (int)(blockIdx.x - (uint32_t)block * (uint32_t)splits);
         w.q0 = block / blocks;
         w.head0 = (int)(block - w.q0 * blocks) * MB;
         int n = a.k;
@@ -151,56 +204,93 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         w.masked = w.n;
         w.list = a.ids + w.q0 * a.ld_ids;
     } else {
-        // The request and row block of this block: a running sum of the
-        // requests' blocks, 64 requests at a time.  Blocks follow each other
-        // without gaps (empty ones among them would leave shader engines idle,
-        // since workgroups go around them in turn).
+        // A request's tokens, row blocks and stages (of its last block).
+        struct Request { int64_t st; int tokens, ctx, blocks, stages; };
+        auto request = [&](int64_t i) {
+            Request r{};
+            if (i >= a.reqs) return r;
+            int64_t st = a.query_starts[i], en = a.query_starts[i + 1];
+            st = st < 0 ? 0 : st < a.rows ? st : a.rows;
+            en = en < st ? st : en < a.rows ? en : a.rows;
+            r.st = st;
+            r.tokens = (int)(en - st);
+            r.ctx = a.ctx_lens[i] < 0 ? 0 : a.ctx_lens[i];
+            r.blocks = (int)(((en - st) * a.heads + MB - 1) / MB);
+            r.stages = (keys_seen(a, r.ctx, r.tokens, r.tokens) + kTile - 1) / kTile;
+            return r;
+        };
+        // Lengths differ, so the pieces are of about one size, not of one
+        // number a request: the smallest size tried, upwards in steps of 1/16,
+        // with which all requests' pieces are no more than `target` workgroups.
+        // The grid has room for `target` and one piece a block, which is
+        // enough for any size tried (all are at least total / target).
+        const Request of_lane = request(lane);  // the first 64 are read once
+        auto requests = [&](int64_t i0) { return i0 == 0 ? of_lane : request(i0 + lane); };
+        int chunk = 0x7FFFFFFF;
+        if (splits > 1) {
+            float total = 0.f, blocks = 0.f;
+            int longest = 0;
+            for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
+                const Request r = requests(i0);
+                total += wave_total((float)r.blocks * (float)r.stages);
+                blocks += wave_total((float)r.blocks);
+                const int most = wave_most(r.blocks > 0 ? r.stages : 0);
+                longest = most > longest ? most : longest;
+            }
+            // Rounding up costs about half a piece a block.
+            const float room = (float)target - 0.5f * blocks;
+            const float least = total * 1.0001f / (room > 0.5f * (float)target ? room : 0.5f * (float)target) + 1.f;
+            chunk = (longest + splits - 1) / splits;
+            chunk = chunk > (int)least ? chunk : (int)least;
+            for (int tries = 0; tries < 8; ++tries) {
+                float sum = 0.f;
+                for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
+                    const Request r = requests(i0);
+                    sum += wave_total((float)r.blocks * (float)pieces_of(r.stages, chunk));
+                }
+                if (sum <= (float)target) break;
+                chunk += chunk / 16 + 1;
+            }
+            chunk = __builtin_amdgcn_readfirstlane(chunk);
+        }
+        // This workgroup's request, row block and piece: a running sum of the
+        // requests' workgroups, 64 requests at a time.  They follow each other
+        // without gaps (idle ones among them would leave shader engines
+        // without work, since workgroups go around them in turn).
         int64_t before = 0, req = -1, flat = 0;
         for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
-            const int64_t i = i0 + lane;
-            int64_t st = 0, en = 0;
-            if (i < a.reqs) {
-                st = a.query_starts[i];
-                en = a.query_starts[i + 1];
-                st = st < 0 ? 0 : st < a.rows ? st : a.rows;
-                en = en < st ? st : en < a.rows ? en : a.rows;
-            }
-            const int own = (int)(((en - st) * a.heads + MB - 1) / MB);
-            int sum = own;  // inclusive
-            for (int d = 1; d < 64; d <<= 1) {
-                const int up = __shfl_up(sum, d);
-                if (lane >= d) sum += up;
-            }
-            const uint64_t past = __ballot(before + sum > block);
+            const Request r = requests(i0);
+            const int mine = pieces_of(r.stages, chunk), own = r.blocks * mine;
+            const int sum = wave_sums(own);
+            const uint64_t past = __ballot(before + sum > (int64_t)blockIdx.x);
             if (past) {
                 const int at = __ffsll((unsigned long long)past) - 1;
                 req = i0 + at;
-                w.q0 = __shfl(st, at);
-                w.tokens = (int)(__shfl(en, at) - w.q0);
-                flat = (block - before - __shfl(sum - own, at)) * MB;
+                w.q0 = __builtin_amdgcn_readlane((int)r.st, at);
+                w.tokens = __builtin_amdgcn_readlane(r.tokens, at);
+                w.ctx = __builtin_amdgcn_readlane(r.ctx, at);
+                pieces = __builtin_amdgcn_readlane(mine, at);
+                const int in = (int)((int64_t)blockIdx.x - before) - __builtin_amdgcn_readlane(sum - own, at);
+                flat = (int64_t)(in / pieces) * MB;
+                split = in % pieces;
                 break;
             }
-            before += __shfl(sum, 63);
+            before += __builtin_amdgcn_readlane(sum, 63);
         }
         if (req < 0) return;
         req = __builtin_amdgcn_readfirstlane((int)req);
         w.flat0 = (int)flat;
-        const int32_t c = a.ctx_lens[req];
-        w.ctx = c < 0 ? 0 : c;
         const int64_t first = flat / a.heads, last_row = (flat + MB - 1) / a.heads;
-        const int64_t last = last_row < w.tokens ? last_row : w.tokens - 1;
-        int64_t n = (int64_t)w.ctx + (a.tree ? (w.tokens < 64 ? w.tokens : 64) : last + 1);
-        const int64_t held = (int64_t)a.pages.cols * a.pages.block_size;
-        if (n > held) n = held;
-        if (n > 0x7FFFFFC0) n = 0x7FFFFFC0;
-        w.n = __builtin_amdgcn_readfirstlane((int)n);
+        const int last = (int)(last_row < w.tokens ? last_row : w.tokens - 1);
+        const int n = keys_seen(a, w.ctx, w.tokens, last + 1);
+        w.n = __builtin_amdgcn_readfirstlane(n);
         const int64_t masked = (int64_t)w.ctx + (a.tree ? 0 : first + 1);
         w.masked = __builtin_amdgcn_readfirstlane((int)(masked < w.n ? masked : w.n));
         w.list = a.pages.table + req * a.pages.ld;
     }
 
     const int all = (w.n + kTile - 1) / kTile;   // stages
-    const int per = (all + splits - 1) / splits;
+    const int per = (all + pieces - 1) / pieces;
     const int s0 = split * per;
     const int s1 = s0 + per < all ? s0 + per : all;
 
@@ -501,9 +591,11 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     const float lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
     const int64_t part = (int64_t)split * a.rows * a.heads + rh;
     if (dp == 0 && half == 0) {
-        if (splits > 1)
+        if (splits > 1) {
             part_lse[part] = lse;
-        else if (a.lse)
+            if (split == 0)  // the join sees `splits` parts of every row
+                for (int p = pieces; p < splits; ++p) part_lse[(int64_t)p * a.rows * a.heads + rh] = -INFINITY;
+        } else if (a.lse)
             a.lse[rh] = lse;
     }
     if (splits > 1) {
@@ -551,7 +643,7 @@ static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, 
     constexpr double kStageUs[3] = {1.5, 1.75, 2.05}, kAroundUs[3] = {7, 11, 16};
     const double piece = (double)out_rows * d_latent * 8 / 4e6;
     const int most = !allow ? 1 : (int)(stages < 1 ? 1 : stages < 64 ? stages : 64);
-    AttendPlan best{1, 4, 0};
+    AttendPlan best{1, 4, 1, 0};
     double best_us = 1e300;
     for (int g = 0; g < 3; ++g) {
         const int hg = 1 << g;
@@ -560,50 +652,59 @@ static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, 
             const int64_t per = (stages + s - 1) / s;
             const double us = (double)((blocks * s + kCus - 1) / kCus) * (per * kStageUs[g] + kAroundUs[g]) +
                               (s > 1 ? 4.0 + s * piece : 0.0);
-            if (us < best_us) best_us = us, best.splits = s, best.groups = hg;
+            if (us < best_us) best_us = us, best.splits = s, best.groups = hg, best.target = (int)(blocks * s);
         }
     }
-    if (best.splits > 1) best.ws_bytes = ((size_t)best.splits * out_rows * (d_latent + 1) * 4 + 15) & ~size_t(15);
     return best;
 }
 
-AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split) {
-    return plan_pieces(rows, heads, ((int64_t)k + kTile - 1) / kTile, rows * heads, d_latent, allow_split);
+static AttendPlan with_workspace(AttendPlan p, int64_t out_rows, int32_t d_latent) {
+    if (p.splits > 1) p.ws_bytes = ((size_t)p.splits * out_rows * (d_latent + 1) * 4 + 15) & ~size_t(15);
+    return p;
 }
 
-// Goes by the mean number of tokens a request.
+AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, bool allow_split) {
+    return with_workspace(plan_pieces(rows, heads, ((int64_t)k + kTile - 1) / kTile, rows * heads, d_latent,
+                                      allow_split), rows * heads, d_latent);
+}
+
+// Goes by the mean number of tokens a request.  Pieces are of one size there,
+// so a long request may have twice the mean number of them.
 AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent,
                              int64_t max_len, bool allow_split) {
     const int64_t active = reqs < tokens ? reqs : tokens;
-    return plan_pieces(active, (tokens + active - 1) / active * heads, (max_len + kTile - 1) / kTile,
-                       tokens * heads, d_latent, allow_split);
+    AttendPlan p = plan_pieces(active, (tokens + active - 1) / active * heads, (max_len + kTile - 1) / kTile,
+                               tokens * heads, d_latent, allow_split);
+    if (p.splits > 1) p.splits = p.splits < 32 ? 2 * p.splits : 64;
+    return with_workspace(p, tokens * heads, d_latent);
 }
 
 template <int DL, int HG, bool PAGED>
-static int launch_attend(const AttendArgs& a, int64_t blocks, int splits, void* workspace, hipStream_t s) {
-    const int64_t grid = blocks * splits;
+static int launch_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
+    constexpr int kRows = 32 * HG;
+    // Paged: no more row blocks than this, whatever the requests' lengths are,
+    // and one piece a block more than `target` at most.
+    const int64_t blocks = PAGED ? a.rows * a.heads / kRows + (a.reqs < a.rows ? a.reqs : a.rows)
+                                 : a.rows * ((a.heads + kRows - 1) / kRows);
+    const int64_t grid = plan.splits == 1 ? blocks : PAGED ? blocks + plan.target : blocks * plan.splits;
     if (grid > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
     const int64_t n = a.rows * a.heads;
     float* part_out = static_cast<float*>(workspace);
-    float* part_lse = part_out ? part_out + (int64_t)splits * n * DL : nullptr;
+    float* part_lse = part_out ? part_out + (int64_t)plan.splits * n * DL : nullptr;
     constexpr size_t lds = kStages * stage_bytes<DL>() + kAttendWaves * kEntryStages * 256;
     hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)grid), dim3(kAttendBlock), lds, s, a,
-                       splits, part_out, part_lse);
+                       plan.splits, plan.target, part_out, part_lse);
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;
-    if (splits == 1) return RTS_OK;
-    return launch_merge_attend(part_out, RTS_F32, part_lse, splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
+    if (plan.splits == 1) return RTS_OK;
+    return launch_merge_attend(part_out, RTS_F32, part_lse, plan.splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
                                PAGED ? a.query_starts + a.reqs : nullptr, s);
 }
 
 template <int DL, bool PAGED>
 static int launch_attend_of(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
-    const int mb = 32 * plan.groups;
-    // Paged: no more than this, whatever the requests' lengths are.
-    const int64_t blocks = PAGED ? a.rows * a.heads / mb + (a.reqs < a.rows ? a.reqs : a.rows)
-                                 : a.rows * ((a.heads + mb - 1) / mb);
-    if (plan.groups == 1) return launch_attend<DL, 1, PAGED>(a, blocks, plan.splits, workspace, s);
-    if (plan.groups == 2) return launch_attend<DL, 2, PAGED>(a, blocks, plan.splits, workspace, s);
-    return launch_attend<DL, 4, PAGED>(a, blocks, plan.splits, workspace, s);
+    if (plan.groups == 1) return launch_attend<DL, 1, PAGED>(a, plan, workspace, s);
+    if (plan.groups == 2) return launch_attend<DL, 2, PAGED>(a, plan, workspace, s);
+    return launch_attend<DL, 4, PAGED>(a, plan, workspace, s);
 }
 
 int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t s) {
@@ -657,8 +758,8 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
 // out = sum_r e^(lse_r - lse) parts_r.  One thread per 8 elements of one
 // (row, head), so each part is read once in 16-byte loads and nothing passes
 // between threads; the world statistics are re-read by the dim / 8 threads of
-// a (row, head) from the caches.  kMergeAhead parts are on their way at a
-// time, also while the maximum is still being found.
+// a (row, head) from the caches.  kMergeAhead parts are on their way while as
+// many are added, the first also while the maximum is still being found.
 constexpr int kMergeAhead = 4;
 
 template <typename In, typename Out>
@@ -674,36 +775,42 @@ __global__ __launch_bounds__(256) void merge_attend_kernel(
     const int64_t step = n * dim8 * 8;
     const float* stat = part_lse + rh;
 
-    float x[kMergeAhead];
-    Raw8<In> v[kMergeAhead];
+    struct Group { float x[kMergeAhead]; Raw8<In> v[kMergeAhead]; };
     // Parts r0.. of the world; one that is empty or does not exist is not read.
-    auto load = [&](int r0) {
+    auto load = [&](int r0, Group& g) {
 #pragma unroll
-        for (int u = 0; u < kMergeAhead; ++u) x[u] = r0 + u < world ? stat[(r0 + u) * n] : -INFINITY;
+        for (int u = 0; u < kMergeAhead; ++u) g.x[u] = r0 + u < world ? stat[(r0 + u) * n] : -INFINITY;
 #pragma unroll
         for (int u = 0; u < kMergeAhead; ++u) {
-            v[u] = Raw8<In>{};
-            if (x[u] != -INFINITY) v[u] = *reinterpret_cast<const Raw8<In>*>(mine + (r0 + u) * step);
+            g.v[u] = Raw8<In>{};
+            if (g.x[u] != -INFINITY) g.v[u] = *reinterpret_cast<const Raw8<In>*>(mine + (r0 + u) * step);
         }
     };
-    load(0);
-    float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    Group even, odd;
+    load(0, even);
+    float m = fmaxf(fmaxf(even.x[0], even.x[1]), fmaxf(even.x[2], even.x[3]));
+#pragma unroll 8
     for (int r = kMergeAhead; r < world; ++r) m = fmaxf(m, stat[r * n]);
     f32x8 acc = {};
     float total = 0.f;
+    auto add = [&](const Group& g) {
+#pragma unroll
+        for (int u = 0; u < kMergeAhead; ++u) {
+            const float w = __builtin_amdgcn_exp2f((g.x[u] - m) * kLog2e);
+            total += w;
+            const f32x8 e = g.v[u].widen();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, e[k], acc[k]);
+        }
+    };
     if (m != -INFINITY) {
         for (int r0 = 0;;) {
-#pragma unroll
-            for (int u = 0; u < kMergeAhead; ++u) {
-                const float w = __builtin_amdgcn_exp2f((x[u] - m) * kLog2e);
-                total += w;
-                const f32x8 e = v[u].widen();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, e[k], acc[k]);
-            }
-            r0 += kMergeAhead;
+            if ((r0 += kMergeAhead) < world) load(r0, odd);
+            add(even);
             if (r0 >= world) break;
-            load(r0);
+            if ((r0 += kMergeAhead) < world) load(r0, even);
+            add(odd);
+            if (r0 >= world) break;
         }
         const float inv = 1.f / total;
 #pragma unroll
