@@ -257,7 +257,8 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         // requests' workgroups, 64 requests at a time.  They follow each other
         // without gaps (idle ones among them would leave shader engines
         // without work, since workgroups go around them in turn).
-        int64_t before = 0, req = -1, flat = 0;
+        int64_t before = 0, req = -1;
+        int flat = 0;
         for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
             const Request r = requests(i0);
             const int mine = pieces_of(r.stages, chunk), own = r.blocks * mine;
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 w.ctx = __builtin_amdgcn_readlane(r.ctx, at);
                 pieces = __builtin_amdgcn_readlane(mine, at);
                 const int in = (int)((int64_t)blockIdx.x - before) - __builtin_amdgcn_readlane(sum - own, at);
-                flat = (int64_t)(in / pieces) * MB;
+                flat = in / pieces * MB;
                 split = in % pieces;
                 break;
             }
@@ -279,9 +280,10 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         }
         if (req < 0) return;
         req = __builtin_amdgcn_readfirstlane((int)req);
-        w.flat0 = (int)flat;
-        const int64_t first = flat / a.heads, last_row = (flat + MB - 1) / a.heads;
-        const int last = (int)(last_row < w.tokens ? last_row : w.tokens - 1);
+        if (flat < 0 || flat >= (int64_t)w.tokens * a.heads) return;
+        w.flat0 = flat;
+        const int first = flat / a.heads, last_row = first + (flat - first * a.heads + MB - 1) / a.heads;
+        const int last = last_row < w.tokens ? last_row : w.tokens - 1;
         const int n = keys_seen(a, w.ctx, w.tokens, last + 1);
         w.n = __builtin_amdgcn_readfirstlane(n);
         const int64_t masked = (int64_t)w.ctx + (a.tree ? 0 : first + 1);
@@ -398,6 +400,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    constexpr int KB = 2, VB = 3;         // groups of keys and tiles of values in registers
     constexpr int GQ = 4, NG = NQ / GQ;  // the first product in groups, each read one group ahead
     static_assert(NG == kLoads, "one piece of the next loads a group");
     auto read_k = [&](const uint32_t (&at)[4], int g, bf16x8 (&k)[GQ]) {
@@ -445,13 +448,24 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         }
     }
 
-    // Stage j's scores are in s.  A pass forms the scores of stage j + 1 while
-    // the weights of stage j are computed, then adds stage j's values.
+    // Stage j's scores are in s, with their maximum, the keys that exist and the
+    // next rows to load.  A pass forms the scores of stage j + 1 while the
+    // weights of stage j are computed, then adds stage j's values while what
+    // the next pass begins with is made ready.
+    float top = s[0];
+    uint32_t exist = 0;
+    const char* src = nullptr;
+    if (s0 < s1) {
+#pragma unroll
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+        exist = (uint32_t)__ballot(row_of(s0, col) >= 0);
+        src = source(s0 + kStages - 1);
+    }
     for (int j = s0; j < s1; ++j) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) pin(o[t]);  // they stay there from pass to pass
         // Which of the 32 keys this lane's row sees.
-        uint32_t see = (uint32_t)__ballot(row_of(j, col) >= 0);
+        uint32_t see = exist;
         const bool rows_differ = PAGED && j * kTile + kTile > w.masked;
         if constexpr (PAGED) {
             if (rows_differ) {
@@ -480,11 +494,10 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (!((bits >> ((r & 3) + 8 * (r >> 2))) & 1)) s[r] = -INFINITY;
-        }
-
-        float top = s[0];
+            top = s[0];
 #pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+        }
         {
             const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
             top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * c;
@@ -512,27 +525,31 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             sum += x;
             p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
         };
-        bf16x8 v[2][2];
+        bf16x8 v[VB][2];
         uint32_t v_at[2][2];
         v_addresses(j, v_at);
+        auto first_v = [&] {
+#pragma unroll
+            for (int t = 0; t < VB - 1 && t < NT; ++t) read_v(v_at, t, v[t]);
+        };
         f32x16 next = {};
         if (j + 1 < s1) {
             // After this the place of stage j - 1 is free for stage j + 3.
             arrive(std::integral_constant<int, kStages - 3>{});
-            look(j + kStages + 1);
-            const char* src = source(j + kStages - 1);
             uint32_t at[4];
             k_addresses(j + 1, at);
-            bf16x8 k[2][GQ];
-            read_k(at, 0, k[0]);
+            bf16x8 k[KB][GQ];
+#pragma unroll
+            for (int g = 0; g < KB - 1; ++g) read_k(at, g, k[g]);
+            look(j + kStages + 1);
             each<NG>([&](auto group) {
                 constexpr int g = decltype(group)::value;
-                if constexpr (g + 1 < NG) read_k(at, g + 1, k[(g + 1) & 1]);
-                else read_v(v_at, 0, v[0]);
+                if constexpr (g + KB - 1 < NG) read_k(at, g + KB - 1, k[(g + KB - 1) % KB]);
+                if constexpr (g + 1 == NG) first_v();
                 fetch(j + kStages - 1, src, group);
 #pragma unroll
                 for (int i = 0; i < GQ; ++i)
-                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[g & 1][i], q[g * GQ + i], next, 0, 0, 0);
+                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[g % KB][i], q[g * GQ + i], next, 0, 0, 0);
 #pragma unroll
                 for (int r = g * 16 / NG; r < (g + 1) * 16 / NG; ++r) weigh(r);
                 __builtin_amdgcn_sched_barrier(0);
@@ -540,7 +557,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         } else {
 #pragma unroll
             for (int r = 0; r < 16; ++r) weigh(r);
-            if (!PAGED || !rows_differ) read_v(v_at, 0, v[0]);
+            if (!PAGED || !rows_differ) first_v();
         }
         l += sum;
 
@@ -552,28 +569,42 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                i32x4* x16 = reinterpret_cast<i32x4*>(lds_memory + (j & (kStages - 1)) * kStageB);
-                for (int i = tid; i < kTile * DL * 2 / 16; i += kAttendBlock) {
-                    i32x4 x = x16[i];
+                constexpr int kEach = kTile * DL * 2 / 16 / kAttendBlock;
+                i32x4* x16 = reinterpret_cast<i32x4*>(lds_memory + (j & (kStages - 1)) * kStageB) + tid;
+                i32x4 x[kEach];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) x[i] = x16[i * kAttendBlock];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    bool bad = false;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if ((x[e] & 0x7F80) == 0x7F80) x[e] &= 0xFFFF0000;
-                        if ((x[e] & 0x7F800000) == 0x7F800000) x[e] &= 0xFFFF;
+                        const bool lo = (x[i][e] & 0x7F80) == 0x7F80, hi = (x[i][e] & 0x7F800000) == 0x7F800000;
+                        x[i][e] &= (lo ? 0xFFFF0000 : ~0u) & (hi ? 0xFFFF : ~0u);
+                        bad |= lo | hi;
                     }
-                    x16[i] = x;
+                    if (bad) x16[i * kAttendBlock] = x[i];
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
-                read_v(v_at, 0, v[0]);
+                first_v();
             }
         }
 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            if (t + 1 < NT) read_v(v_at, t + 1, v[(t + 1) & 1]);
+            if (t + VB - 1 < NT) read_v(v_at, t + VB - 1, v[(t + VB - 1) % VB]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) add_product(o[t], v[t & 1][k], p[k]);
+            for (int k = 0; k < 2; ++k) add_product(o[t], v[t % VB][k], p[k]);
+            if (t == 0) {
+                exist = (uint32_t)__ballot(row_of(j + 1, col) >= 0);
+                src = source(j + kStages);
+            }
+            if (t == NT / 2) top = next[0];
+            if (t >= NT / 2)
+#pragma unroll
+                for (int r = (t - NT / 2) * 32 / NT; r < (t - NT / 2 + 1) * 32 / NT; ++r) top = fmaxf(top, next[r]);
             __builtin_amdgcn_sched_barrier(0);
         }
         s = next;
