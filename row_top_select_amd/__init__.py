@@ -615,7 +615,7 @@ def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols,
     device = _gpu(q, "q")
     if q.dtype not in _INDEX_DTYPES or keys.dtype != q.dtype:
         raise TypeError("q and keys must both be bfloat16 or both float8_e4m3fn")
-    if q.dim() != 3 or q.stride(2) != 1 or q.stride(1) != q.shape[2]:
+    if q.dim() != 3 or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
         raise ValueError("q must be [rows, heads, dim] with contiguous heads")
     rows, heads, dim = q.shape
     n_keys, kdim, ld_keys = _rows_ld(keys, "keys")

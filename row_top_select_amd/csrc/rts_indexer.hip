@@ -81,9 +81,12 @@ struct LogitsShape {
     }
 };
 
-// D elements a row; tb tokens a workgroup, head_tiles tiles of 32 heads
-// (padded with zeros), `span` columns a workgroup, `stages` (1 or 2) of the
-// waves' rings.
+// D elements a row; tb tokens a workgroup, head_tiles tiles of 32 heads, `span`
+// columns a workgroup, `stages` (1 or 2) of the waves' rings.
+//
+// The heads that fill up the last tile are copies of the last head, and its
+// weight is dealt out to it and them in halves (w/2, w/4, ..), which is exact.
+// Zeros in their place would turn a key's infinity into NaN.
 //
 // Both operands of product step i cover the same 16 elements of a row in the
 // same order, which is all that the sum needs: bf16 step i, half h has chunk
@@ -111,14 +114,12 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
     int32_t* lr = le + tb;                                                     // [tb] requests
 
     for (int th = wave; th < n_tok * head_tiles; th += S::kWaves) {
-        const int tok = th / head_tiles, head = (th - tok * head_tiles) * 32 + (lane & 31);
+        const int tok = th / head_tiles, row = (th - tok * head_tiles) * 32 + (lane & 31);
+        const int head = row < a.heads ? row : a.heads - 1;
         const char* src = static_cast<const char*>(a.q) + ((t0 + tok) * a.ld_q + (int64_t)head * D) * kEsz + half * 16;
         i32x4 raw[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            raw[c] = i32x4{};
-            if (head < a.heads) raw[c] = *reinterpret_cast<const i32x4*>(src + c * 32);
-        }
+        for (int c = 0; c < NC; ++c) raw[c] = *reinterpret_cast<const i32x4*>(src + c * 32);
         i32x4* dst = lq + th * NI * kWave + lane;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -129,8 +130,10 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
         }
     }
     for (int i = tid; i < n_tok * hp; i += kBlock) {
-        const int t = i / hp, h = i - t * hp;
-        lw[i] = h < a.heads ? a.weights[(t0 + t) * a.ld_weights + h] : 0.f;
+        const int t = i / hp, h = i - t * hp, last = a.heads - 1;
+        const float w = a.weights[(t0 + t) * a.ld_weights + (h < last ? h : last)];
+        const int halvings = h < last ? 0 : h < hp - 1 ? h - last + 1 : h - last;
+        lw[i] = ldexpf(w, -halvings);
     }
     if (tid < n_tok) {
         const int64_t e = a.row_ends ? a.row_ends[t0 + tid] : a.cols;
@@ -402,7 +405,7 @@ static int launch_logits(const LogitsArgs& a, hipStream_t s) {
         }
     }
     const int64_t blocks_x = (a.rows + tb - 1) / tb, parts = (steps + per - 1) / per;
-    if (parts > 65535) return RTS_EUNSUPPORTED;
+    if (blocks_x > kMaxThreads / (S::kWaves * kWave)) return RTS_EUNSUPPORTED;
     hipLaunchKernelGGL((indexer_logits_kernel<D, E4M3, PAGED, Out>),
                        dim3((unsigned)blocks_x, (unsigned)parts), dim3(S::kWaves * kWave),
                        S::ring_bytes(stages) + per_token * tb, s, a, (int)tb, head_tiles, per * S::kStep, stages);

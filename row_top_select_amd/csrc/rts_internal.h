@@ -96,6 +96,8 @@ inline Pages make_pages(const int32_t* table, int64_t table_rows, int32_t cols, 
     return Pages{table, table_rows, ld, stride_rows, cache_rows, cols, block_size, shift};
 }
 
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;  // of one launch, along x
+
 constexpr int64_t kMaxReqs = 8192;  // assign_slots keeps two sums a request in LDS
 
 int launch_assign_slots(const int32_t* ctx_lens, const int32_t* new_lens, int64_t reqs, int64_t tokens,

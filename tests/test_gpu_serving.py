@@ -146,24 +146,45 @@ def test_indexer_logits(rts, dtype, rows, heads, dim, cols, pad):
             assert (got[t, e:] == 77.0).all(), "columns behind the row's end were written"
 
 
-def test_indexer_logits_non_finite(rts):
-    say("logits: NaN and infinities stay in their column")
-    q, keys, w, _ = index_inputs(3, 4, 32, 128, 200, torch.bfloat16)
+@pytest.mark.parametrize("heads", [32, 5, 33])
+def test_indexer_logits_non_finite(rts, heads):
+    say("logits: NaN and infinities stay in their column, and infinities are ordinary", heads)
+    g = gen(3)
+    q = torch.rand(4, heads, 128, generator=g).bfloat16() + 0.5   # positive: an infinity keeps its sign
+    keys = torch.randn(200, 128, generator=g).bfloat16()
+    w = torch.rand(4, heads, generator=g) + 0.5
+    w[1] = -w[1]
     keys[17, 3] = math.nan
     keys[40, 0] = math.inf
+    keys[41, 5] = -math.inf
     keys[199] = math.nan
     ends = torch.tensor([200, 199, 40, 17], dtype=torch.int32)
-    got = rts.indexer_logits(q.to(DEV).view(4, 32, 128), keys.to(DEV), w.contiguous().to(DEV),
-                             row_ends=ends.to(DEV)).cpu()
+    got = rts.indexer_logits(q.to(DEV), keys.to(DEV), w.to(DEV), row_ends=ends.to(DEV)).cpu()
     fine = torch.ones(200, dtype=torch.bool)
-    fine[[17, 40, 199]] = False
+    fine[[17, 40, 41, 199]] = False
     for t in range(4):
         e = int(ends[t])
         ok = fine[:e]
-        want, bound = ref.logits(q[t].view(32, 128), keys[:e][ok], w[t], None)
+        want, bound = ref.logits(q[t], keys[:e][ok], w[t], None)
         ref.assert_close(got[t, :e][ok], want, bound, f"row {t}")
-        assert torch.isnan(got[t, :e][torch.arange(e) == 17]).all()
-        assert not torch.isfinite(got[t, :e][torch.arange(e) == 40]).any()
+        at = torch.arange(e)
+        assert torch.isnan(got[t, :e][(at == 17) | (at == 199)]).all()
+        assert (got[t, :e][at == 40] == (-math.inf if t == 1 else math.inf)).all()
+        assert (got[t, :e][at == 41] == 0).all()
+
+
+def test_indexer_logits_e4m3_nan(rts):
+    say("logits: e4m3 NaN stays in its column and its row")
+    q, keys, w, ks = index_inputs(3, 3, 32, 128, 70, torch.float8_e4m3fn)
+    keys.view(torch.uint8)[33, 100] = 0x7F
+    q.view(torch.uint8)[2, 5] = 0xFF
+    got = rts.indexer_logits(q.to(DEV).view(3, 32, 128), keys.to(DEV), w.contiguous().to(DEV),
+                             key_scales=ks.to(DEV)).cpu()
+    assert torch.isnan(got[:, 33]).all() and torch.isnan(got[2]).all()
+    ok = torch.arange(70) != 33
+    for t in range(2):
+        want, bound = ref.logits(q[t].view(32, 128), keys[ok], w[t], ks[ok])
+        ref.assert_close(got[t, ok], want, bound, f"row {t}")
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "e4m3"])
@@ -513,6 +534,17 @@ def test_merge_attend(rts, dtype, out_dtype, world, rows, heads, dim):
         ob = ob * (1 + ref.BF16) + o.abs() * ref.BF16
     ref.assert_close(out, o, ob, "out")
     ref.assert_close(total, l, lb, "lse")
+
+
+def test_merge_attend_nan(rts):
+    say("merge: a NaN part beside empty ones stays NaN")
+    parts = torch.randn(3, 2, 4, 64, generator=gen(9))
+    lse = torch.full((3, 2, 4), -math.inf)
+    lse[1, 0] = math.nan
+    lse[2, 1] = 3.0
+    out, total = rts.merge_attend_rank_major(parts.to(DEV), lse.to(DEV))
+    assert torch.isnan(out[0]).all() and torch.isnan(total[0]).all()
+    assert torch.equal(out[1].cpu(), parts[2, 1]) and (total[1] == 3.0).all()
 
 
 # ------------------------------------------------------------- all together
