@@ -60,6 +60,7 @@ constexpr int kRope = 64;
 constexpr int kTile = 32;    // keys of a stage, query rows of a wave
 constexpr int kStages = 4;
 constexpr int kEntryStages = 8;  // of list entries, read two stages further ahead
+constexpr int kLeastPiece = 4;   // stages: what lies around a piece takes as long as 5 to 8
 constexpr int kAttendWaves = 4;
 constexpr int kAttendBlock = kAttendWaves * kWave;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -248,6 +249,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             const float least = total * 1.0001f / (room > 0.5f * (float)target ? room : 0.5f * (float)target) + 1.f;
             chunk = (longest + splits - 1) / splits;
             chunk = chunk > (int)least ? chunk : (int)least;
+            chunk = chunk > kLeastPiece ? chunk : kLeastPiece;
             for (int tries = 0; tries < 8; ++tries) {
                 float sum = 0.f;
                 for (int64_t i0 = 0; i0 < a.reqs; i0 += 64) {
@@ -672,9 +674,11 @@ constexpr int kCus = 256;
 // workgroup has a CU for itself.  Measured on 256 busy CUs, a stage takes 1.5,
 // 1.75 or 2.05 us with 1, 2 or 4 groups (1.15 to 1.5 us on one CU) and what
 // lies around the stages 7, 11 or 16 us; pieces cost a second launch and the
-// way of their 32-bit results out and back at 4 TB/s.  Small batches so take
-// fewer rows a workgroup and large ones more: 64 tokens x 128 heads x 2048 keys
-// runs with 2 groups and 2 pieces, 1024 tokens with 4 groups and one.
+// way of their 32-bit results out and back at 4 TB/s.  Measured (groups/pieces:
+// us), the rule's choice first: 64 tokens x 128 heads x 2048 keys 4/4: 69, 2/2:
+// 82, 2/1: 100, 1/1: 120; 8 tokens 1/7: 31, 1/8: 37, 4/8: 41, 4/4: 49; 64 tokens
+// x 16 heads 1/4: 40, 1/2: 55, 1/8: 53; 1024 tokens x 128 heads x 512 keys 4/1:
+// 186, 2/1: 295, 4/2: 431.
 static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, int64_t out_rows,
                               int32_t d_latent, bool allow) {
     constexpr double kStageUs[3] = {1.5, 1.75, 2.05}, kAroundUs[3] = {7, 11, 16};
@@ -796,7 +800,8 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
 // (row, head), so each part is read once in 16-byte loads and nothing passes
 // between threads; the world statistics are re-read by the dim / 8 threads of
 // a (row, head) from the caches.  kMergeAhead parts are on their way while as
-// many are added, the first also while the maximum is still being found.
+// many are added, the first also while the maximum is still being found.  Bound
+// by the bytes: 8 ranks x 1000 x 128 x 512 in bf16 take 207 us, 5.7 TB/s.
 constexpr int kMergeAhead = 4;
 
 template <typename In, typename Out>

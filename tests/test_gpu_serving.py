@@ -230,6 +230,23 @@ def test_indexer_logits_paged(rts, dtype, counts, heads, dim, block, ctx):
         assert (got[t, ends[t]:] == 77.0).all()
 
 
+def test_indexer_logits_far_offsets(rts):
+    say("logits: a key cache past 4 GiB, output rows past 4 GiB")
+    rows = 40_000_000
+    keys = torch.zeros(rows, 128, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    block = 64
+    at = torch.tensor([rows // block - 1, 3, rows // block - 2, 0])
+    q, some, w, _ = index_inputs(8, 2, 32, 128, 4 * block, torch.float8_e4m3fn)
+    for i, b in enumerate(at.tolist()):
+        keys.view(torch.uint8)[b * block:(b + 1) * block] = some[i * block:(i + 1) * block].view(torch.uint8).to(DEV)
+    far = torch.empty(2, 1_300_000_000, device=DEV)[:, :256]
+    got = rts.indexer_logits_paged(q.to(DEV).view(2, 32, 128), keys, w.contiguous().to(DEV), i32([0, 0]), i32([256, 255]),
+                                   at.int().to(DEV)[None], block, 256, out=far).cpu()
+    for t, e in ((0, 256), (1, 255)):
+        want, bound = ref.logits(q[t].view(32, 128), some[:e], w[t], None)
+        ref.assert_close(got[t, :e], want, bound, f"row {t}")
+
+
 def test_paged_calls_without_pages(rts):
     say("paged calls on an empty table and an empty cache")
     q, keys, w, _ = index_inputs(4, 3, 32, 128, 64, torch.bfloat16)
@@ -419,6 +436,44 @@ def test_latent_paged(rts, ctx, new, heads, latent, block, pad):
     b = check_paged(rts, q, cache, starts, ctx, table, block, stride, 0.07, latent,
                     max_len=max(c + n for c, n in zip(ctx, new)))
     del a, b
+
+
+def test_latent_paged_many_and_very_ragged_requests(rts):
+    say("latent paged: 200 requests, some without tokens; one long request among short ones")
+    rng = np.random.default_rng(3)
+    ctx = rng.integers(0, 90, size=200).tolist()
+    new = rng.integers(0, 3, size=200).tolist()
+    q, cache, starts, table, stride = paged_setup(17, ctx, new, 16, 256, 16)
+    check_paged(rts, q, cache, starts, ctx, table, 16, stride, 0.07, 256)
+    check_paged(rts, q, cache, starts, ctx, table, 16, stride, 0.07, 256, workspace=None)
+    ctx, new = [5000, 0, 3, 40, 700, 1], [1, 1, 0, 2, 1, 1]
+    q, cache, starts, table, stride = paged_setup(18, ctx, new, 40, 512, 64)
+    for max_len in (5001, 64, 0, 1 << 40):  # any bound gives right results
+        check_paged(rts, q, cache, starts, ctx, table, 64, stride, 0.07, 512, max_len=max_len)
+
+
+def test_latent_many_heads(rts):
+    say("latent: 1024 heads")
+    q, cache = latent_inputs(19, 1, 1024, 256, 50)
+    check_rows(rts, q, cache, torch.arange(50).int()[None], None, 0.07, 256)
+
+
+def test_latent_calls_at_once(rts):
+    say("latent: calls on two streams at once, each with its own workspace")
+    q, cache = latent_inputs(20, 4, 32, 512, 3000)
+    qd, cd = q.to(DEV), cache.to(DEV)
+    lists = [torch.randint(0, 3000, (4, 1500), generator=gen(k)).int().to(DEV) for k in range(2)]
+    want = [rts.latent_attend_rows(qd, cd, ids, 0.07) for ids in lists]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k in range(2):
+            got[k].append(rts.latent_attend_rows(qd, cd, lists[k], 0.07, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for o, l in got[k]:
+            assert torch.equal(o, want[k][0]) and torch.equal(l, want[k][1])
 
 
 @pytest.mark.parametrize("ctx,new,heads,block", [([200, 0, 77], [8, 3, 1], 16, 16), ([129], [64], 4, 64),
@@ -635,3 +690,59 @@ def test_step_of_sparse_attention(rts):
         more = ref.BF16 * lat[chosen][:, :512].double().abs().amax(0)
         ref.assert_close(both[t], o, 2 * ob + more[None], f"merged out of token {t}")
         ref.assert_close(both_lse[t], l, 4 * lb + 1e-5, f"merged lse of token {t}")
+
+
+def test_captured_step(rts):
+    """The whole step in one graph, replayed after new lengths, queries and tables, with eager work
+    between the replays."""
+    say("a captured step, replayed")
+    block, reqs, tokens, cols_t, k, width = 16, 3, 8, 20, 32, 300
+    g = gen(31)
+    cache_rows = reqs * cols_t * block
+    latent = torch.randn(cache_rows, 576, generator=g).bfloat16().to(DEV)
+    keys = torch.randn(cache_rows, 128, generator=g).bfloat16().to(DEV)
+    q_index = torch.zeros(tokens, 16, 128, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(tokens, 16, device=DEV)
+    q = torch.zeros(tokens, 16, 576, dtype=torch.bfloat16, device=DEV)
+    ctx, new = i32([0] * reqs), i32([0] * reqs)
+    table = torch.zeros(reqs, cols_t, dtype=torch.int32, device=DEV)
+    free = torch.arange(reqs * cols_t, dtype=torch.int32, device=DEV)
+
+    def step():
+        m = rts.assign_slots(ctx, new, tokens, table, free, block)
+        logits = rts.indexer_logits_paged(q_index, keys, w, m.req_id, m.row_ends, table, block, width)
+        picked = rts.topk_rows(logits, k, row_ends=m.row_ends)
+        rows, valid = rts.emit_rows(picked, 1, 0, m.req_id, table, block, block)
+        out, lse = rts.latent_attend_rows(q, latent, rows, 0.07, counts=valid)
+        dense = torch.zeros_like(out)
+        rts.latent_attend_paged(q, latent, m.query_starts, ctx, table, block, 0.07, out=dense)
+        both = rts.merge_attend_rank_major(torch.stack([out, dense]), torch.stack([lse, lse]))
+        return [*m, picked, out, lse, dense, *both]
+
+    def set_inputs(seed):
+        h = gen(seed)
+        q_index.copy_(torch.randn(q_index.shape, generator=h))
+        w.copy_(torch.randn(w.shape, generator=h))
+        q.copy_(torch.randn(q.shape, generator=h))
+        ctx.copy_(torch.randint(0, 290, (reqs,), generator=h))
+        new.copy_(torch.randint(0, 4, (reqs,), generator=h))
+        table.copy_(torch.randperm(reqs * cols_t, generator=h).view(reqs, cols_t))
+
+    set_inputs(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in range(1, 6):
+        set_inputs(seed)
+        before = table.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in captured]
+        table.copy_(before)
+        for i, (x, y) in enumerate(zip(got, step())):
+            assert torch.equal(x, y), (seed, i)
