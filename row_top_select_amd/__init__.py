@@ -112,9 +112,12 @@ def _opt(t, name):
 
 
 def _rows_ld(t: torch.Tensor, name: str):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    return t.shape[0], t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return rows, cols, (ld if rows > 1 else cols)
 
 
 def _int32_vec(t, rows, name):
@@ -515,10 +518,10 @@ def _launch(fn, where: str, device: torch.device, stream, scratch, *args) -> Non
         raise RtsError(status, where)
 
 
-def _on(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
+def _on(device: torch.device, *tensors) -> None:
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} must be a tensor on {device}")
+            raise ValueError(f"all tensors must be on {device}, one is on {t.device}")
 
 
 def _gpu(t, name: str) -> torch.device:
@@ -556,11 +559,19 @@ def _scratch(workspace, need: int, device, made: list):
 
 
 def _table(block_table: torch.Tensor):
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            (block_table.shape[1] > 1 and block_table.shape[0] > 0 and block_table.stride(1) != 1):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [Q, B_max] with unit column stride")
-    rows, cols = block_table.shape
-    return rows, cols, (block_table.stride(0) if rows > 1 and cols > 0 else cols)
+    (rows, cols), (ld, step) = block_table.shape, block_table.stride()
+    if cols > 1 and rows > 0 and step != 1:
+        raise ValueError("block_table must be int32 [Q, B_max] with unit column stride")
+    return rows, cols, (ld if rows > 1 and cols > 0 else cols)
+
+
+def _int32_all(t: torch.Tensor, name: str) -> int:
+    """The length of a contiguous int32 vector."""
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector")
+    return t.shape[0]
 
 
 class SlotMap(NamedTuple):
@@ -580,16 +591,13 @@ def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, bl
 
     ``stride_rows`` defaults to ``block_size``."""
     device = _gpu(ctx_lens, "ctx_lens")
-    reqs = ctx_lens.shape[0] if ctx_lens.dim() == 1 else -1
-    for name, t in (("ctx_lens", ctx_lens), ("new_lens", new_lens), ("free_blocks", free_blocks)):
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 vector")
-    if new_lens.shape[0] != reqs or block_table.shape[0] != reqs:
+    reqs, n_free = _int32_all(ctx_lens, "ctx_lens"), _int32_all(free_blocks, "free_blocks")
+    table_rows, table_cols, ld_table = _table(block_table)
+    if _int32_all(new_lens, "new_lens") != reqs or table_rows != reqs:
         raise ValueError("new_lens and block_table must have one entry per request")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    table_rows, table_cols, ld_table = _table(block_table)
-    _on(device, new_lens=new_lens, block_table=block_table, free_blocks=free_blocks)
+    _on(device, new_lens, block_table, free_blocks)
     made = []
     if out is None:
         flat = torch.empty(reqs + 2 + 3 * tokens, dtype=torch.int32, device=device)
@@ -600,7 +608,7 @@ def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, bl
             _out(t, (n,), torch.int32, device, name, made)
     _launch(_lib.assign_slots, "assign_slots", device, stream, made, ctx_lens.data_ptr(),
             new_lens.data_ptr(), reqs, tokens, block_size, block_size if stride_rows is None else stride_rows,
-            free_blocks.data_ptr(), free_blocks.shape[0], block_table.data_ptr(), table_cols, ld_table,
+            free_blocks.data_ptr(), n_free, block_table.data_ptr(), table_cols, ld_table,
             out.query_starts.data_ptr(), out.req_id.data_ptr(), out.row_ends.data_ptr(),
             out.slots.data_ptr(), out.used.data_ptr())
     return out
@@ -615,9 +623,11 @@ def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols,
     device = _gpu(q, "q")
     if q.dtype not in _INDEX_DTYPES or keys.dtype != q.dtype:
         raise TypeError("q and keys must both be bfloat16 or both float8_e4m3fn")
-    if q.dim() != 3 or q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+    if q.dim() != 3:
         raise ValueError("q must be [rows, heads, dim] with contiguous heads")
-    rows, heads, dim = q.shape
+    (rows, heads, dim), (ld_q, head_step, step) = q.shape, q.stride()
+    if step != 1 or (heads > 1 and head_step != dim):
+        raise ValueError("q must be [rows, heads, dim] with contiguous heads")
     n_keys, kdim, ld_keys = _rows_ld(keys, "keys")
     if kdim != dim:
         raise ValueError("q and keys must have the same last dimension")
@@ -640,9 +650,9 @@ def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols,
     out_rows, out_cols, ld_out = _rows_ld(out, "out")
     if out_rows < rows or out_cols < cols:
         raise ValueError(f"out must hold at least [{rows}, {cols}] (got {tuple(out.shape)})")
-    _on(device, keys=keys, weights=weights, key_scales=key_scales, row_ends=row_ends, out=out)
-    ld_q = q.stride(0) if rows > 1 else heads * dim
+    _on(device, keys, weights, key_scales, row_ends, out)
     if rows <= 1:
+        ld_q = heads * dim
         ld_out = max(ld_out, cols)
     return device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out
 
@@ -684,7 +694,7 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
     if req_id is None or row_ends is None:
         raise ValueError("req_id and row_ends are required")
     table_rows, table_cols, ld_table = _table(block_table)
-    _on(device, req_id=req_id, block_table=block_table)
+    _on(device, req_id, block_table)
     _launch(_lib.indexer_logits_paged, "indexer_logits_paged", device, stream, made, q.data_ptr(),
             _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, key_cache.data_ptr(), n_keys, ld_keys,
             weights.data_ptr(), ld_w, _ptr(key_scales), req_id.data_ptr(), row_ends.data_ptr(),
@@ -699,17 +709,19 @@ def _attend_inputs(q, cache, d_latent, out, lse, made):
     device = _gpu(q, "q")
     if q.dtype != torch.bfloat16 or cache.dtype != torch.bfloat16:
         raise TypeError("q and cache must be bfloat16")
-    if q.dim() != 3 or q.stride(2) != 1:
+    if q.dim() != 3:
         raise ValueError("q must be [rows, heads, d_latent + d_rope] with unit element stride")
-    rows, heads, d = q.shape
+    (rows, heads, d), (ld_q, ld_head, step) = q.shape, q.stride()
+    if step != 1:
+        raise ValueError("q must be [rows, heads, d_latent + d_rope] with unit element stride")
     cache_rows, cd, ld_cache = _rows_ld(cache, "cache")
     if cd != d or not 0 < d_latent <= d:
         raise ValueError("q and cache must have the same last dimension, at least d_latent")
-    ld_head = q.stride(1) if heads > 1 else d
-    ld_q = q.stride(0) if rows > 1 else heads * d
+    ld_head = ld_head if heads > 1 else d
+    ld_q = ld_q if rows > 1 else heads * d
     out = _out(out, (rows, heads, d_latent), torch.bfloat16, device, "out", made)
     lse = _out(lse, (rows, heads), torch.float32, device, "lse", made)
-    _on(device, cache=cache)
+    _on(device, cache)
     return device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse
 
 
@@ -736,7 +748,7 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, 
     if rows <= 1:
         ld_ids = max(ld_ids, k)
     counts = _int32_vec(counts, rows, "counts")
-    _on(device, ids=ids, counts=counts)
+    _on(device, ids, counts)
     ws, ws_bytes = _scratch(workspace, latent_attend_rows_workspace_size(rows, heads, d_latent, k)
                             if isinstance(workspace, str) else 0, device, made)
     _launch(_lib.latent_attend_rows, "latent_attend_rows", device, stream, made, q.data_ptr(), rows, heads,
@@ -774,7 +786,7 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
         raise ValueError(f"tree must be a contiguous 64-bit vector of >= {tokens} entries")
     if max_len is None:
         max_len = table_cols * block_size
-    _on(device, query_starts=query_starts, ctx_lens=ctx_lens, block_table=block_table, tree=tree)
+    _on(device, query_starts, ctx_lens, block_table, tree)
     ws, ws_bytes = _scratch(workspace,
                             latent_attend_paged_workspace_size(tokens, table_rows, heads, d_latent, max_len)
                             if isinstance(workspace, str) else 0, device, made)
@@ -797,7 +809,7 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
     if parts.dim() != 4 or not parts.is_contiguous():
         raise ValueError("parts must be contiguous [W, rows, heads, dim]")
     world, rows, heads, dim = parts.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (world, rows, heads) or not lse.is_contiguous():
+    if lse.dtype != torch.float32 or lse.shape != (world, rows, heads) or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous float32 [{world}, {rows}, {heads}]")
     made = []
     if out_dtype is None:
@@ -806,7 +818,7 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
         raise TypeError("out must be float32 or bfloat16")
     out = _out(out, (rows, heads, dim), out_dtype, device, "out", made)
     out_lse = _out(out_lse, (rows, heads), torch.float32, device, "out_lse", made)
-    _on(device, lse=lse)
+    _on(device, lse)
     _launch(_lib.merge_attend_rank_major, "merge_attend_rank_major", device, stream, made, parts.data_ptr(),
             _FLOAT_DTYPES[parts.dtype], lse.data_ptr(), world, rows, heads, dim, out.data_ptr(),
             _FLOAT_DTYPES[out.dtype], out_lse.data_ptr())

@@ -681,18 +681,19 @@ constexpr int kCus = 256;
 // 186, 2/1: 295, 4/2: 431.
 static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, int64_t out_rows,
                               int32_t d_latent, bool allow) {
-    constexpr double kStageUs[3] = {1.5, 1.75, 2.05}, kAroundUs[3] = {7, 11, 16};
-    const double piece = (double)out_rows * d_latent * 8 / 4e6;
-    const int most = !allow ? 1 : (int)(stages < 1 ? 1 : stages < 64 ? stages : 64);
+    constexpr float kStageUs[3] = {1.5f, 1.75f, 2.05f}, kAroundUs[3] = {7.f, 11.f, 16.f};
+    const float piece = (float)out_rows * d_latent * 8 / 4e6f;
+    const uint32_t n = (uint32_t)(stages < 1 ? 1 : stages < 0x7FFFFFFF ? stages : 0x7FFFFFFF);
+    const uint32_t most = !allow ? 1 : n < 64 ? n : 64;
     AttendPlan best{1, 4, 1, 0};
-    double best_us = 1e300;
+    float best_us = 3e38f;
     for (int g = 0; g < 3; ++g) {
         const int hg = 1 << g;
         const int64_t blocks = units * ((rows_each + 32 * hg - 1) / (32 * hg));
-        for (int s = 1; s <= most; ++s) {
-            const int64_t per = (stages + s - 1) / s;
-            const double us = (double)((blocks * s + kCus - 1) / kCus) * (per * kStageUs[g] + kAroundUs[g]) +
-                              (s > 1 ? 4.0 + s * piece : 0.0);
+        for (uint32_t s = 1; s <= most; ++s) {
+            const uint32_t per = (n + s - 1) / s;
+            const float us = (float)((blocks * s + kCus - 1) / kCus) * (per * kStageUs[g] + kAroundUs[g]) +
+                             (s > 1 ? 4.f + s * piece : 0.f);
             if (us < best_us) best_us = us, best.splits = s, best.groups = hg, best.target = (int)(blocks * s);
         }
     }
@@ -714,8 +715,8 @@ AttendPlan plan_attend_rows(int64_t rows, int32_t heads, int32_t d_latent, int32
 AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent,
                              int64_t max_len, bool allow_split) {
     const int64_t active = reqs < tokens ? reqs : tokens;
-    AttendPlan p = plan_pieces(active, (tokens + active - 1) / active * heads, (max_len + kTile - 1) / kTile,
-                               tokens * heads, d_latent, allow_split);
+    AttendPlan p = plan_pieces(active, (tokens + active - 1) / active * heads,
+                               max_len / kTile + (max_len % kTile != 0), tokens * heads, d_latent, allow_split);
     if (p.splits > 1) p.splits = p.splits < 32 ? 2 * p.splits : 64;
     return with_workspace(p, tokens * heads, d_latent);
 }
