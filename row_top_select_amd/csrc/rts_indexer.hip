@@ -272,12 +272,13 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
         for (int g = 0; g < 4; ++g) read_w(0, g);
 
         int item = 0, next_item = items > 1 ? 1 : 0;  // whose products are formed; the one after
-        int tile = head_tiles, token = ta - 1;        // what is summed: before the first item, nothing
+        int tile = head_tiles - 1, token = tz - 1;    // what is summed: before the first item, nothing
         const int64_t ld_out = a.ld_logits * (int64_t)sizeof(Out);
         char* const out_row = static_cast<char*>(a.logits) + (t0 + ta) * ld_out;
         char* out = out_row;                          // where the wave's 64 columns of the summed token start
-        int sum_c = 0;
-        float sum_scale = 0.f;
+        const int limits = ends < (int)cend ? ends : (int)cend;
+        int step_c = 0, sum_c = 0x7FFFFFFF;           // first columns: of the step, of what is summed (not stored)
+        float step_scale = 0.f, sum_scale = 0.f;
         auto turn = [&](const i32x4 (&k)[2][NI], const f32x16 (&s)[2], f32x16 (&next)[2], auto products) {
             constexpr bool kProducts = decltype(products)::value;
             next[0] = next[1] = f32x16{};
@@ -301,47 +302,47 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (++tile < head_tiles) return;
-            if (token >= ta) {
-                // Both halves' sums of the key tile that this half stores.
-                const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[0]), __float_as_uint(sum[1]),
-                                                                false, false);
-                const float v = (__uint_as_float(z[0]) + __uint_as_float(z[1])) * sum_scale;
-                const int end = __builtin_amdgcn_readlane(ends, token);
-                if (lane < (end < (int)cend ? end : (int)cend) - sum_c)
-                    store_logit(reinterpret_cast<Out*>(out) + lane, v);
-                out += ld_out;
-            }
-            sum[0] = sum[1] = 0.f;
             tile = 0;
-            token = token + 1 < tz ? token + 1 : ta;
+            // Both halves' sums of the key tile that this half stores.
+            const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum[0]), __float_as_uint(sum[1]), false,
+                                                            false);
+            const float v = (__uint_as_float(z[0]) + __uint_as_float(z[1])) * sum_scale;
+            if (lane < __builtin_amdgcn_readlane(limits, token) - sum_c)
+                store_logit(reinterpret_cast<Out*>(out) + lane, v);
+            out += ld_out;
+            sum[0] = sum[1] = 0.f;
+            if (++token == tz) {  // from here on the items of the step under way are summed
+                token = ta;
+                sum_c = step_c;
+                sum_scale = step_scale;
+                out = out_row + step_c * (int64_t)sizeof(Out);
+            }
         };
         // All items of the step at column c, two a pass so that no score is copied.
         bool in_odd = false;  // where the scores of the item before are
-        auto step = [&](int64_t c, const i32x4 (&k)[2][NI], float scale) {
-            auto done = [&](int n) {
+        auto step = [&](int c, const i32x4 (&k)[2][NI], float scale) {
+            step_c = c;
+            step_scale = scale;
+            auto done = [&] {
                 item = next_item;
                 next_item = next_item + 1 < items ? next_item + 1 : 0;
-                if (n == 0) {  // from here on this step's items are summed
-                    sum_c = (int)c;
-                    sum_scale = scale;
-                    out = out_row + c * (int64_t)sizeof(Out);
-                }
             };
             int n = 0;
             if (in_odd) {
                 turn(k, odd, even, std::true_type{});
-                done(n++);
+                done();
+                ++n;
             }
             for (; n + 1 < items; n += 2) {
                 turn(k, even, odd, std::true_type{});
-                done(n);
+                done();
                 turn(k, odd, even, std::true_type{});
-                done(n + 1);
+                done();
             }
             in_odd = n < items;
             if (in_odd) {
                 turn(k, even, odd, std::true_type{});
-                done(n);
+                done();
             }
         };
 
@@ -363,7 +364,7 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             look(n + stages + 1);
             if (n + stages < steps) fetch(n + stages);
-            step(first + (int64_t)n * S::kStep, k, scale);
+            step((int)(first + (int64_t)n * S::kStep), k, scale);
         }
         if (in_odd)
             turn(k, odd, even, std::false_type{});
