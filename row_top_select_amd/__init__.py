@@ -101,6 +101,19 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(shape, dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory for a call on ``stream`` (None: the current stream).  A freed block of one stream's pool
+    may still be in use by what that stream has yet to run, so a call on another stream takes
+    memory from its own; it is given back when the current stream, which may read the
+    results, is done with it too."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dev(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -149,7 +162,7 @@ def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None
     rows, cols, ld = _rows_ld(logits, "logits")
     row_ends = _int32_vec(row_ends, rows, "row_ends")
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.int32, device=logits.device)
+        out = _new((rows, k), torch.int32, logits.device, stream)
     if out.dtype != torch.int32:
         raise TypeError("out must be int32")
     if out.device != logits.device:
@@ -163,7 +176,7 @@ def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None
     if isinstance(workspace, str) and workspace == "auto":
         need = topk_rows_workspace_size(dt, rows, cols, k)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=logits.device)
+            ws = _new(need, torch.uint8, logits.device, stream)
             ws_bytes = need
     elif workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.device != logits.device or \
@@ -220,7 +233,7 @@ def pack_candidates(logits_bf16: torch.Tensor, local_idx: torch.Tensor,
     row_ends = _int32_vec(row_ends, rows, "row_ends")
     width = n + n // 32
     if out is None:
-        out = torch.empty((rows, width), dtype=torch.int32, device=logits_bf16.device)
+        out = _new((rows, width), torch.int32, logits_bf16.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, width) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {width}]")
     _check(_lib.pack_candidates(_dev(logits_bf16, "logits"), rows, cols, ld,
@@ -240,11 +253,11 @@ def merge_select_rank_major(gathered: torch.Tensor, k: int, out: torch.Tensor | 
     if n + n // 32 != width:
         raise ValueError("gathered's last dimension must be n + n/32")
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.int32, device=gathered.device)
+        out = _new((rows, k), torch.int32, gathered.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, k) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {k}]")
     if sat_word is None and want_sat:
-        sat_word = torch.empty((rows,), dtype=torch.int32, device=gathered.device)
+        sat_word = _new((rows,), torch.int32, gathered.device, stream)
     _check(_lib.merge_select_rank_major(_dev(gathered, "gathered"), world, rows, n, k, _dev(out, "out"),
                                         _opt(sat_word, "sat_word"), _stream(stream)),
            "merge_select_rank_major")
@@ -313,11 +326,11 @@ def merge_select_row_major(gathered: torch.Tensor, k: int, out: torch.Tensor | N
     rows, world, _ = gathered.shape
     n = _packed_width(gathered, "gathered")
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.int32, device=gathered.device)
+        out = _new((rows, k), torch.int32, gathered.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, k) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {k}]")
     if sat_word is None and want_sat:
-        sat_word = torch.empty((rows,), dtype=torch.int32, device=gathered.device)
+        sat_word = _new((rows,), torch.int32, gathered.device, stream)
     _check(_lib.merge_select_row_major(_dev(gathered, "gathered"), world, rows, n, k, _dev(out, "out"),
                                        _opt(sat_word, "sat_word"), _stream(stream)),
            "merge_select_row_major")
@@ -334,7 +347,7 @@ def merge_select_pairs_row_major(gathered_pairs: torch.Tensor, k: int, world: in
     if world < 1 or wkc % world != 0:
         raise ValueError("the candidate dimension must be world * kc")
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.int32, device=g.device)
+        out = _new((rows, k), torch.int32, g.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, k) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {k}]")
     _check(_lib.merge_select_pairs_row_major(_dev(g, "gathered_pairs"), world, rows, wkc // world, k,
@@ -361,12 +374,12 @@ def emit_rows(ids: torch.Tensor, world: int, dcp_rank: int, req_id: torch.Tensor
     table_rows, table_cols = block_table.shape
     ld_table = block_table.stride(0) if table_rows > 1 else table_cols
     if rows_out is None:
-        rows_out = torch.empty((rows, k), dtype=torch.int32, device=ids.device)
+        rows_out = _new((rows, k), torch.int32, ids.device, stream)
     if rows_out.dtype != torch.int32 or rows_out.dim() != 2 or rows_out.shape[0] != rows or \
             rows_out.shape[1] < k or not rows_out.is_contiguous():
         raise ValueError(f"rows_out must be contiguous int32 [{rows}, >= {k}]")
     if valid_out is None:
-        valid_out = torch.empty((rows,), dtype=torch.int32, device=ids.device)
+        valid_out = _new((rows,), torch.int32, ids.device, stream)
     valid_out = _int32_vec(valid_out, rows, "valid_out")
     _check(_lib.emit_rows(_dev(ids, "ids"), rows, k, world, dcp_rank, _dev(req_id, "req_id"),
                           _dev(block_table, "block_table"), table_rows, table_cols, ld_table,
@@ -376,7 +389,7 @@ def emit_rows(ids: torch.Tensor, world: int, dcp_rank: int, req_id: torch.Tensor
 
 
 def _kv_rows(rows, k, dcp_rank, req_id, block_table, block_size, stride_rows, rows_out, valid_out,
-             device):
+             device, stream):
     req_id = _int32_vec(req_id, rows, "req_id")
     if req_id is None:
         raise ValueError("req_id is required")
@@ -386,12 +399,12 @@ def _kv_rows(rows, k, dcp_rank, req_id, block_table, block_size, stride_rows, ro
     table_rows, table_cols = block_table.shape
     ld_table = block_table.stride(0) if table_rows > 1 else table_cols
     if rows_out is None:
-        rows_out = torch.empty((rows, k), dtype=torch.int32, device=device)
+        rows_out = _new((rows, k), torch.int32, device, stream)
     if rows_out.dtype != torch.int32 or rows_out.dim() != 2 or rows_out.shape[0] != rows or \
             rows_out.shape[1] < k or not rows_out.is_contiguous():
         raise ValueError(f"rows_out must be contiguous int32 [{rows}, >= {k}]")
     if valid_out is None:
-        valid_out = torch.empty((rows,), dtype=torch.int32, device=device)
+        valid_out = _new((rows,), torch.int32, device, stream)
     valid_out = _int32_vec(valid_out, rows, "valid_out")
     kv = _KvRows(dcp_rank, req_id.data_ptr(), block_table.data_ptr(), table_rows, table_cols, ld_table,
                  block_size, stride_rows, rows_out.data_ptr(), rows_out.shape[1], valid_out.data_ptr())
@@ -411,7 +424,7 @@ def merge_select_rank_major_rows(gathered: torch.Tensor, k: int, dcp_rank: int, 
     world, rows, _ = gathered.shape
     n = _packed_width(gathered, "gathered")
     kv, rows_out, valid_out = _kv_rows(rows, k, dcp_rank, req_id, block_table, block_size, stride_rows,
-                                       rows_out, valid_out, gathered.device)
+                                       rows_out, valid_out, gathered.device, stream)
     if out_ids is not None and (out_ids.dtype != torch.int32 or tuple(out_ids.shape) != (rows, k) or
                                 not out_ids.is_contiguous()):
         raise ValueError(f"out_ids must be contiguous int32 [{rows}, {k}]")
@@ -435,7 +448,7 @@ def merge_rescue_rank_major_rows(gathered: torch.Tensor, recv: torch.Tensor, sat
     world, rows, _ = gathered.shape
     n = _packed_width(gathered, "gathered")
     kv, rows_out, valid_out = _kv_rows(rows, k, dcp_rank, req_id, block_table, block_size, stride_rows,
-                                       rows_out, valid_out, gathered.device)
+                                       rows_out, valid_out, gathered.device, stream)
     sat_word = _int32_vec(sat_word, rows, "sat_word")
     if (recv.dtype != torch.int32 or not recv.is_contiguous() or
             tuple(recv.shape) != (rows, rescue_slots(n, k), k + k // 32)):
@@ -466,7 +479,7 @@ def pack_pairs(logits: torch.Tensor, local_idx: torch.Tensor, rank: int, world: 
         ld_idx = max(ld_idx, kc)
     row_ends = _int32_vec(row_ends, rows, "row_ends")
     if out is None:
-        out = torch.empty((rows, kc, 2), dtype=torch.int32, device=logits.device)
+        out = _new((rows, kc, 2), torch.int32, logits.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, kc, 2) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {kc}, 2]")
     _check(_lib.pack_pairs(_dev(logits, "logits"), rows, cols, ld, _dev(local_idx, "local_idx"), kc,
@@ -483,7 +496,7 @@ def merge_select_pairs_rank_major(gathered_pairs: torch.Tensor, k: int,
         raise ValueError("gathered_pairs must be contiguous int32 [W, R, kc, 2]")
     world, rows, kc, _ = g.shape
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.int32, device=g.device)
+        out = _new((rows, k), torch.int32, g.device, stream)
     if out.dtype != torch.int32 or tuple(out.shape) != (rows, k) or not out.is_contiguous():
         raise ValueError(f"out must be contiguous int32 [{rows}, {k}]")
     _check(_lib.merge_select_pairs_rank_major(_dev(g, "gathered_pairs"), world, rows, kc, k,
@@ -497,17 +510,13 @@ def merge_select_pairs_rank_major(gathered_pairs: torch.Tensor, k: int,
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _launch(fn, where: str, device: torch.device, stream, scratch, *args) -> None:
-    """Calls ``fn(*args, stream)`` with ``device`` current.  Memory allocated here
-    for the call (``scratch``) is kept until a stream other than the current one
-    is done with it."""
+def _launch(fn, where: str, device: torch.device, stream, *args) -> None:
+    """Calls ``fn(*args, stream)`` with ``device`` current."""
     if stream is None:
         s = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     else:
         if stream.device != device:
             raise ValueError(f"{where}: stream must belong to the device of the tensors")
-        for t in scratch:
-            t.record_stream(stream)
         s = stream.cuda_stream
     if device.index == torch.cuda.current_device():
         status = fn(*args, s)
@@ -530,26 +539,23 @@ def _gpu(t, name: str) -> torch.device:
     return t.device
 
 
-def _out(t, shape, dtype, device, name: str, made: list) -> torch.Tensor:
-    """A caller's output tensor, checked, or a new one (listed in ``made``)."""
+def _out(t, shape, dtype, device, name: str, stream) -> torch.Tensor:
+    """A caller's output tensor, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        made.append(t)
+        t = _new(shape, dtype, device, stream)
     elif t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
     return t
 
 
-def _scratch(workspace, need: int, device, made: list):
+def _scratch(workspace, need: int, device, stream):
     """(tensor or None, bytes) of a call's workspace argument."""
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a GPU tensor')
         if not need:
             return None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        made.append(ws)
-        return ws, need
+        return _new(need, torch.uint8, device, stream), need
     if workspace is None:
         return None, 0
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
@@ -598,15 +604,13 @@ def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, bl
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     _on(device, new_lens, block_table, free_blocks)
-    made = []
     if out is None:
-        flat = torch.empty(reqs + 2 + 3 * tokens, dtype=torch.int32, device=device)
-        made.append(flat)
+        flat = _new(reqs + 2 + 3 * tokens, torch.int32, device, stream)
         out = SlotMap(*torch.split_with_sizes(flat, (reqs + 1, tokens, tokens, tokens, 1)))
     else:
         for name, t, n in zip(SlotMap._fields, out, (reqs + 1, tokens, tokens, tokens, 1)):
-            _out(t, (n,), torch.int32, device, name, made)
-    _launch(_lib.assign_slots, "assign_slots", device, stream, made, ctx_lens.data_ptr(),
+            _out(t, (n,), torch.int32, device, name, stream)
+    _launch(_lib.assign_slots, "assign_slots", device, stream, ctx_lens.data_ptr(),
             new_lens.data_ptr(), reqs, tokens, block_size, block_size if stride_rows is None else stride_rows,
             free_blocks.data_ptr(), n_free, block_table.data_ptr(), table_cols, ld_table,
             out.query_starts.data_ptr(), out.req_id.data_ptr(), out.row_ends.data_ptr(),
@@ -618,7 +622,7 @@ _INDEX_DTYPES = {torch.bfloat16: RTS_BF16, torch.float8_e4m3fn: RTS_E4M3}
 _FLOAT_DTYPES = {torch.float32: RTS_F32, torch.bfloat16: RTS_BF16}
 
 
-def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols, made):
+def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols, stream):
     """What indexer_logits and indexer_logits_paged check alike."""
     device = _gpu(q, "q")
     if q.dtype not in _INDEX_DTYPES or keys.dtype != q.dtype:
@@ -643,8 +647,7 @@ def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols,
     if out is None:
         if out_dtype not in _FLOAT_DTYPES:
             raise TypeError("out_dtype must be float32 or bfloat16")
-        out = torch.empty((rows, cols), dtype=out_dtype, device=device)
-        made.append(out)
+        out = _new((rows, cols), out_dtype, device, stream)
     if out.dtype not in _FLOAT_DTYPES:
         raise TypeError("out must be float32 or bfloat16")
     out_rows, out_cols, ld_out = _rows_ld(out, "out")
@@ -667,11 +670,10 @@ def indexer_logits(q: torch.Tensor, keys: torch.Tensor, weights: torch.Tensor,
     """The logits [rows, cols] that topk_rows selects from: for ``q`` [rows, heads, dim], ``keys``
     [cols, dim] and ``weights`` [rows, heads], the weighted sum over heads of relu(q . k), times the
     key's scale; see indexer_logits in the header.  Columns at or past a row's end are not written."""
-    made = []
     cols = keys.shape[0]
     device, rows, heads, dim, ld_q, _, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
-        q, keys, weights, key_scales, row_ends, out, out_dtype, cols, made)
-    _launch(_lib.indexer_logits, "indexer_logits", device, stream, made, q.data_ptr(),
+        q, keys, weights, key_scales, row_ends, out, out_dtype, cols, stream)
+    _launch(_lib.indexer_logits, "indexer_logits", device, stream, q.data_ptr(),
             _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, keys.data_ptr(), cols, ld_keys,
             weights.data_ptr(), ld_w, _ptr(key_scales), _ptr(row_ends), out.data_ptr(),
             _FLOAT_DTYPES[out.dtype], ld_out)
@@ -685,17 +687,16 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
                          out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """indexer_logits over the paged ``key_cache`` [cache_rows, dim] of each token's request (the
     ``req_id`` and ``row_ends`` of assign_slots); see indexer_logits_paged in the header."""
-    made = []
     if cols < 0:
         raise ValueError("cols must not be negative")
     device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
-        q, key_cache, weights, key_scales, row_ends, out, out_dtype, cols, made)
+        q, key_cache, weights, key_scales, row_ends, out, out_dtype, cols, stream)
     req_id = _int32_vec(req_id, rows, "req_id")
     if req_id is None or row_ends is None:
         raise ValueError("req_id and row_ends are required")
     table_rows, table_cols, ld_table = _table(block_table)
     _on(device, req_id, block_table)
-    _launch(_lib.indexer_logits_paged, "indexer_logits_paged", device, stream, made, q.data_ptr(),
+    _launch(_lib.indexer_logits_paged, "indexer_logits_paged", device, stream, q.data_ptr(),
             _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, key_cache.data_ptr(), n_keys, ld_keys,
             weights.data_ptr(), ld_w, _ptr(key_scales), req_id.data_ptr(), row_ends.data_ptr(),
             block_table.data_ptr(), table_rows, table_cols, ld_table, block_size,
@@ -704,7 +705,7 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
     return out
 
 
-def _attend_inputs(q, cache, d_latent, out, lse, made):
+def _attend_inputs(q, cache, d_latent, out, lse, stream):
     """What latent_attend_rows and latent_attend_paged check alike."""
     device = _gpu(q, "q")
     if q.dtype != torch.bfloat16 or cache.dtype != torch.bfloat16:
@@ -719,8 +720,8 @@ def _attend_inputs(q, cache, d_latent, out, lse, made):
         raise ValueError("q and cache must have the same last dimension, at least d_latent")
     ld_head = ld_head if heads > 1 else d
     ld_q = ld_q if rows > 1 else heads * d
-    out = _out(out, (rows, heads, d_latent), torch.bfloat16, device, "out", made)
-    lse = _out(lse, (rows, heads), torch.float32, device, "lse", made)
+    out = _out(out, (rows, heads, d_latent), torch.bfloat16, device, "out", stream)
+    lse = _out(lse, (rows, heads), torch.float32, device, "lse", stream)
     _on(device, cache)
     return device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse
 
@@ -737,9 +738,8 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, 
     [cache_rows, d], whose first ``d_latent`` elements are the values; ``ids`` and ``counts`` as emit_rows
     writes them (rows_out, valid_out).  Returns (out [rows, heads, d_latent], lse [rows, heads]); see
     latent_attend_rows in the header.  ``workspace`` as in topk_rows."""
-    made = []
     device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
-        q, cache, d_latent, out, lse, made)
+        q, cache, d_latent, out, lse, stream)
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
     id_rows, k, ld_ids = _rows_ld(ids, "ids")
@@ -750,8 +750,8 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, 
     counts = _int32_vec(counts, rows, "counts")
     _on(device, ids, counts)
     ws, ws_bytes = _scratch(workspace, latent_attend_rows_workspace_size(rows, heads, d_latent, k)
-                            if isinstance(workspace, str) else 0, device, made)
-    _launch(_lib.latent_attend_rows, "latent_attend_rows", device, stream, made, q.data_ptr(), rows, heads,
+                            if isinstance(workspace, str) else 0, device, stream)
+    _launch(_lib.latent_attend_rows, "latent_attend_rows", device, stream, q.data_ptr(), rows, heads,
             d_latent, d - d_latent, ld_q, ld_head, cache.data_ptr(), cache_rows, ld_cache, ids.data_ptr(), k,
             ld_ids, _ptr(counts), scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
     return out, lse
@@ -773,9 +773,8 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
     request is seen); ``query_starts`` as assign_slots writes it.  ``max_len`` bounds the requests' lengths
     and only steers the split (default: what the table holds).  Returns (out, lse); see
     latent_attend_paged in the header.  ``workspace`` as in topk_rows."""
-    made = []
     device, tokens, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
-        q, cache, d_latent, out, lse, made)
+        q, cache, d_latent, out, lse, stream)
     table_rows, table_cols, ld_table = _table(block_table)
     ctx_lens = _int32_vec(ctx_lens, table_rows, "ctx_lens")
     query_starts = _int32_vec(query_starts, table_rows + 1, "query_starts")
@@ -789,8 +788,8 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
     _on(device, query_starts, ctx_lens, block_table, tree)
     ws, ws_bytes = _scratch(workspace,
                             latent_attend_paged_workspace_size(tokens, table_rows, heads, d_latent, max_len)
-                            if isinstance(workspace, str) else 0, device, made)
-    _launch(_lib.latent_attend_paged, "latent_attend_paged", device, stream, made, q.data_ptr(), tokens,
+                            if isinstance(workspace, str) else 0, device, stream)
+    _launch(_lib.latent_attend_paged, "latent_attend_paged", device, stream, q.data_ptr(), tokens,
             heads, d_latent, d - d_latent, ld_q, ld_head, cache.data_ptr(), cache_rows, ld_cache,
             query_starts.data_ptr(), ctx_lens.data_ptr(), table_rows, _ptr(tree), block_table.data_ptr(),
             table_cols, ld_table, block_size, block_size if stride_rows is None else stride_rows, max_len,
@@ -811,15 +810,14 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
     world, rows, heads, dim = parts.shape
     if lse.dtype != torch.float32 or lse.shape != (world, rows, heads) or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous float32 [{world}, {rows}, {heads}]")
-    made = []
     if out_dtype is None:
         out_dtype = parts.dtype if out is None else out.dtype
     if out_dtype not in _FLOAT_DTYPES:
         raise TypeError("out must be float32 or bfloat16")
-    out = _out(out, (rows, heads, dim), out_dtype, device, "out", made)
-    out_lse = _out(out_lse, (rows, heads), torch.float32, device, "out_lse", made)
+    out = _out(out, (rows, heads, dim), out_dtype, device, "out", stream)
+    out_lse = _out(out_lse, (rows, heads), torch.float32, device, "out_lse", stream)
     _on(device, lse)
-    _launch(_lib.merge_attend_rank_major, "merge_attend_rank_major", device, stream, made, parts.data_ptr(),
+    _launch(_lib.merge_attend_rank_major, "merge_attend_rank_major", device, stream, parts.data_ptr(),
             _FLOAT_DTYPES[parts.dtype], lse.data_ptr(), world, rows, heads, dim, out.data_ptr(),
             _FLOAT_DTYPES[out.dtype], out_lse.data_ptr())
     return out, out_lse
