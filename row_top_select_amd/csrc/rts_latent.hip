@@ -4,7 +4,7 @@
 //
 // For a block of query rows (heads of a token, or (token, head) pairs of a
 // request) over a list of keys, 32 keys at a time:
-//   S^T = K Q^T,  P^T = exp2(S^T c - m),  O^T += V^T P^T
+//   S^T = K Q^T,  P^T = exp2((S^T - m) c),  O^T += V^T P^T
 // with K [32, L + 64] in LDS and V its first L columns.  Both products are
 // formed transposed, so that a query row is a column of every 32x32 matrix
 // tile: a lane owns one query row (shared with the lane 32 further on), its
@@ -38,6 +38,9 @@
 // a quarter busy, and deeper read-ahead of either operand changes nothing.  With
 // 16 heads the rows' bytes bound it: 256 CUs take a stage each 1.5 us, 6 TB/s.
 //
+// The maximum m is one of products, before the scale: the difference is taken
+// first, so that the greatest weight is 1 for scores of any size (S c - m with
+// m = round(max S c) is off by 2^-25 of the score: 2^128 and more past 2^31).
 // The running maximum is only moved when a score exceeds it by 2^8: then, and
 // not at every step, O is rescaled.  Any reference gives the same quotient; a
 // weight of up to 2^8 costs neither the 32-bit sums nor bf16 precision.
@@ -65,7 +68,8 @@ constexpr int kAttendWaves = 4;
 constexpr int kAttendBlock = kAttendWaves * kWave;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -3e38f;   // a maximum before the first score: exp2(x - kNoMax) stays 0 for x = -inf
+// A maximum before the first score: no finite score is below it, and x - kNoMax is -inf for x = -inf.
+constexpr float kNoMax = -3.402823466e38f;
 constexpr float kLazy = 8.f;       // how far (log2) a score may pass the maximum before O is rescaled
 
 template <int DL>
@@ -321,6 +325,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         token = w.q0 + idx;
     }
     const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+    const float lazy = kLazy / c;
     uint64_t tree = 0;
     if constexpr (PAGED) {
         if (a.tree && row_ok) tree = a.tree[token];
@@ -508,12 +513,12 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         }
         {
             const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-            top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * c;
+            top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
         }
-        if (__any(top > m + kLazy)) {
+        if (__any(top > m + lazy)) {
             const float to = fmaxf(m, top);
             if (j != s0) {
-                const float f = __builtin_amdgcn_exp2f(m - to);
+                const float f = __builtin_amdgcn_exp2f((m - to) * c);
                 l *= f;
                 sums_ready(o);
 #pragma unroll
@@ -529,7 +534,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         bf16x8 p[2];
         float sum = 0.f;
         auto weigh = [&](int r) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(s[r], c, -m));
+            const float x = __builtin_amdgcn_exp2f((s[r] - m) * c);
             sum += x;
             p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
         };
@@ -627,7 +632,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     sums_ready(o);
     if (!row_ok) return;
     const int64_t rh = token * a.heads + head;
-    const float lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    const float lse = l == 0.f ? -INFINITY : m * fabsf(a.scale) + __builtin_amdgcn_logf(l) * kLn2;
     const int64_t part = (int64_t)split * a.rows * a.heads + rh;
     if (dp == 0 && half == 0) {
         if (splits > 1) {
