@@ -439,7 +439,9 @@ int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, 
  *   lse[t, h] = log sum_j exp z_j,   out[t, h, :] = sum_j exp(z_j - lse) cache[ids[t, j], :d_latent]
  * Other entries (-1 tails among them) are not read and contribute nothing; a
  * row without entries gives zeros and -inf.  An id that occurs twice counts
- * twice.  ids and counts are what emit_rows and the selects' rows forms write.
+ * twice.  A score of -inf has the weight 0 (and 0 times a value that is not
+ * finite is NaN); where all are -inf, all weights are 0 and lse is -inf.
+ * ids and counts are what emit_rows and the selects' rows forms write.
  *
  * q          bf16 [rows, heads, d_latent + d_rope]: row t, head h at
  *            q + t * ld_q + h * ld_head (elements).

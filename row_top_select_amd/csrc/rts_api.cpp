@@ -454,7 +454,7 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
     if (!aligned(parts, 16) || !aligned(out, 16) || !aligned(part_lse, 4) || !aligned(lse, 4))
         return RTS_EINVAL;
     return rts::launch_merge_attend(parts, dtype, part_lse, world, rows, heads, dim, out, out_dtype, lse,
-                                    nullptr, stream);
+                                    nullptr, false, stream);
 }
 
 }  // extern "C"

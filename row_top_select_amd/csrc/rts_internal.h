@@ -150,9 +150,10 @@ AttendPlan plan_attend_paged(int64_t tokens, int64_t reqs, int32_t heads, int32_
                              int64_t max_len, bool allow_split);
 int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* workspace, hipStream_t stream);
 
-// row_limit (device, or nullptr): rows at or past *row_limit are not written.
+// row_limit (device, or nullptr): rows at or past *row_limit are not written.  pieces: the parts are those of
+// one call's rows, where the lse of a part that saw keys, all with scores of -inf, is the lowest finite number.
 int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
                         int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
-                        const int32_t* row_limit, hipStream_t stream);
+                        const int32_t* row_limit, bool pieces, hipStream_t stream);
 
 }  // namespace rts

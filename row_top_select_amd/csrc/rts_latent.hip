@@ -70,10 +70,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum before the first score: no finite score is below it, and x - kNoMax is -inf for x = -inf.
 constexpr float kNoMax = -3.402823466e38f;
+// The next number: a maximum of scores that are all -inf (weights 0, but 0 times what is not finite is NaN).
+constexpr float kLeastMax = -3.402823264e38f;
 constexpr float kLazy = 8.f;       // how far (log2) a score may pass the maximum before O is rescaled
 
 template <int DL>
 constexpr int stage_bytes() { return kTile * (DL + kRope) * 2; }
+// Paged form: which values of a stage's keys are not finite, a bit each, and which keys have any.
+template <int DL>
+constexpr int flaw_bytes() { return kTile * DL / 8 + 16; }
 
 __device__ __forceinline__ uint16_t f32_bf16(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);  // round to nearest even
@@ -195,6 +200,9 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     extern __shared__ __align__(1024) char lds_memory[];
     const uint32_t lds = lds_address(lds_memory);
     const uint32_t entries = lds + kStages * kStageB;  // [wave][stage % 8][64]: ids or block ids of 32 keys, twice
+
+    char* const flaws = lds_memory + kStages * kStageB + kAttendWaves * kEntryStages * 256;  // [key][DL bits]
+    int* const flawed_keys = reinterpret_cast<int*>(flaws + kTile * DL / 8);
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -366,6 +374,9 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         load_to_lds<16, i * 128>(src, lds + (j & (kStages - 1)) * kStageB + i * (kColumnB - 128) + wave * 1024);
     };
 
+    if constexpr (PAGED) {  // read behind the barriers of a stage
+        for (int i = tid; i < flaw_bytes<DL>() / 4; i += kAttendBlock) reinterpret_cast<int*>(flaws)[i] = 0;
+    }
     // The ring is always filled (behind the last stage with the zero row), so
     // that the number of loads under way is the same at every stage.
     if (s0 < s1) {
@@ -515,6 +526,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
             const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
             top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
         }
+        if (see) m = fmaxf(m, kLeastMax);
         if (__any(top > m + lazy)) {
             const float to = fmaxf(m, top);
             if (j != s0) {
@@ -577,30 +589,68 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         if constexpr (PAGED) {
             if (rows_differ) {
                 // A key that only some rows see must not reach the others as
-                // 0 * NaN or 0 * inf.  Rows that do see it have it in their
-                // scores already, so its value may be taken as 0.
+                // 0 * NaN or 0 * inf: what is not finite is noted and taken as
+                // 0 in the product, and the rows that see it get their NaN
+                // (a score of -inf, the weight 0) by the notes.
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
                 constexpr int kEach = kTile * DL * 2 / 16 / kAttendBlock;
+                static_assert(kEach == DL / 64, "a thread has its key's chunk of every column");
+                const int key = tid >> 3;
+                char* const note = flaws + key * (DL / 8) + ((tid & 7) ^ chunk_xor(key));
                 i32x4* x16 = reinterpret_cast<i32x4*>(lds_memory + (j & (kStages - 1)) * kStageB) + tid;
                 i32x4 x[kEach];
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) x[i] = x16[i * kAttendBlock];
+                bool noted = false;
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) {
-                    bool bad = false;
+                    int bad = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const bool lo = (x[i][e] & 0x7F80) == 0x7F80, hi = (x[i][e] & 0x7F800000) == 0x7F800000;
                         x[i][e] &= (lo ? 0xFFFF0000 : ~0u) & (hi ? 0xFFFF : ~0u);
-                        bad |= lo | hi;
+                        bad |= (int)lo << (2 * e) | (int)hi << (2 * e + 1);
                     }
-                    if (bad) x16[i * kAttendBlock] = x[i];
+                    if (bad) {
+                        x16[i * kAttendBlock] = x[i];
+                        note[i * 8] = (char)bad;
+                        noted = true;
+                    }
                 }
+                if (noted) atomicOr(flawed_keys, (int)(1u << key));
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
+                const uint32_t flawed = __builtin_amdgcn_readfirstlane(*flawed_keys);
+                if (flawed) {
+                    uint32_t nan_at[NT] = {};
+                    for (uint32_t keys = flawed; keys; keys &= keys - 1) {
+                        const int k = __builtin_ctz(keys);
+                        const uint32_t* bits = reinterpret_cast<const uint32_t*>(flaws + k * (DL / 8)) + dp * NT;
+                        const uint32_t mine = see >> k & 1 ? ~0u : 0u;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) nan_at[t] |= bits[t] & mine;
+                    }
+                    sums_ready(o);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t at = nan_at[t] >> (4 * half);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (at >> ((r & 3) + 8 * (r >> 2)) & 1) o[t][r] = __builtin_nanf("");
+                        pin(o[t]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    // Cleared before the next stage's first barrier.
+                    if (noted)
+                        for (int i = 0; i < kEach; ++i) note[i * 8] = 0;
+                    if (tid == 0) *flawed_keys = 0;
+                }
                 first_v();
             }
         }
@@ -634,16 +684,17 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     const int64_t rh = token * a.heads + head;
     const float lse = l == 0.f ? -INFINITY : m * fabsf(a.scale) + __builtin_amdgcn_logf(l) * kLn2;
     const int64_t part = (int64_t)split * a.rows * a.heads + rh;
+    const bool empty = l == 0.f && m == kNoMax;  // nothing was seen
     if (dp == 0 && half == 0) {
         if (splits > 1) {
-            part_lse[part] = lse;
+            part_lse[part] = l == 0.f && !empty ? kNoMax : lse;  // the join reads its zeros and NaN
             if (split == 0)  // the join sees `splits` parts of every row
                 for (int p = pieces; p < splits; ++p) part_lse[(int64_t)p * a.rows * a.heads + rh] = -INFINITY;
         } else if (a.lse)
             a.lse[rh] = lse;
     }
     if (splits > 1) {
-        if (lse == -INFINITY) return;  // the join reads no values of an empty part
+        if (empty) return;  // the join reads no values of an empty part
         float* dst = part_out + part * DL + dp * NT * 32 + 4 * half;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -738,13 +789,14 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& plan, void* work
     const int64_t n = a.rows * a.heads;
     float* part_out = static_cast<float*>(workspace);
     float* part_lse = part_out ? part_out + (int64_t)plan.splits * n * DL : nullptr;
-    constexpr size_t lds = kStages * stage_bytes<DL>() + kAttendWaves * kEntryStages * 256;
+    constexpr size_t lds = kStages * stage_bytes<DL>() + kAttendWaves * kEntryStages * 256 +
+                           (PAGED ? flaw_bytes<DL>() : 0);
     hipLaunchKernelGGL((latent_attend_kernel<DL, HG, PAGED>), dim3((unsigned)grid), dim3(kAttendBlock), lds, s, a,
                        plan.splits, plan.target, part_out, part_lse);
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;
     if (plan.splits == 1) return RTS_OK;
     return launch_merge_attend(part_out, RTS_F32, part_lse, plan.splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
-                               PAGED ? a.query_starts + a.reqs : nullptr, s);
+                               PAGED ? a.query_starts + a.reqs : nullptr, true, s);
 }
 
 template <int DL, bool PAGED>
@@ -808,12 +860,13 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
 // a (row, head) from the caches.  kMergeAhead parts are on their way while as
 // many are added, the first also while the maximum is still being found.  Bound
 // by the bytes: 8 ranks x 1000 x 128 x 512 in bf16 take 207 us, 5.7 TB/s.
+// Where no part's lse is above `none` the lse is -inf.
 constexpr int kMergeAhead = 4;
 
 template <typename In, typename Out>
 __global__ __launch_bounds__(256) void merge_attend_kernel(
     const In* __restrict__ parts, const float* __restrict__ part_lse, int world, int64_t n, int dim8,
-    int heads, const int32_t* __restrict__ row_limit, Out* __restrict__ out, float* __restrict__ lse) {
+    int heads, const int32_t* __restrict__ row_limit, float none, Out* __restrict__ out, float* __restrict__ lse) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n * dim8) return;
     const int64_t rh = i / dim8;
@@ -867,12 +920,13 @@ __global__ __launch_bounds__(256) void merge_attend_kernel(
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
     }
     store8(out + rh * dim8 * 8 + d, acc);
-    if (lse && d == 0) lse[rh] = m != -INFINITY ? m + __builtin_amdgcn_logf(total) * kLn2 : m;
+    if (lse && d == 0) lse[rh] = m <= none ? -INFINITY : m + __builtin_amdgcn_logf(total) * kLn2;
 }
 
 int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
                         int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
-                        const int32_t* row_limit, hipStream_t s) {
+                        const int32_t* row_limit, bool pieces, hipStream_t s) {
+    const float none = pieces ? kNoMax : -INFINITY;
     const int64_t n = rows * heads, blocks = (n * (dim / 8) + 255) / 256;
     if (blocks > kMaxThreads / 256) return RTS_EUNSUPPORTED;
     const dim3 g((unsigned)blocks), b(256);
@@ -882,13 +936,13 @@ int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int
     float* of = static_cast<float*>(out);
     uint16_t* oh = static_cast<uint16_t*>(out);
     if (dtype == RTS_F32 && out_dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<float, float>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, of, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<float, float>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, of, lse);
     else if (dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<float, uint16_t>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, oh, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<float, uint16_t>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, oh, lse);
     else if (out_dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, float>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, of, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, float>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, of, lse);
     else
-        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, uint16_t>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, oh, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, uint16_t>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, oh, lse);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 

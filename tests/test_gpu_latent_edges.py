@@ -69,3 +69,112 @@ def test_scores_of_any_size(rts, power, sign):
                 ref.assert_close(out[0], want.expand(16, 512), bound.expand(16, 512), what)
                 lse_want = torch.logsumexp(z, 0).expand(16)
                 ref.assert_close(lse[0], lse_want, 4 * ref.U * (lse_want.abs() + 8), what)
+
+
+def attend_inf(q, kv, scale, latent):
+    """ref.attend of one token where some rows of kv are not finite: a score that is NaN or +inf makes the head
+    NaN; one of -inf has the weight 0, which its values that are not finite turn into NaN."""
+    z = scale * (q.double() @ kv.double().T)
+    out, bound = torch.zeros(q.shape[0], latent, dtype=torch.float64), torch.zeros(q.shape[0], latent, dtype=torch.float64)
+    lse, lse_bound = torch.full((q.shape[0],), -math.inf, dtype=torch.float64), torch.zeros(q.shape[0], dtype=torch.float64)
+    for h in range(q.shape[0]):
+        if bool((torch.isnan(z[h]) | (z[h] == math.inf)).any()):
+            out[h], lse[h] = math.nan, math.nan
+            continue
+        none = z[h] == -math.inf
+        o, l, ob, lb = ref.attend(q[h:h + 1], kv[~none], scale, latent)
+        out[h], bound[h], lse[h], lse_bound[h] = o[0], ob[0], l[0], lb[0]
+        out[h, (~torch.isfinite(kv[none][:, :latent])).any(0)] = math.nan
+    return out, lse, bound, lse_bound
+
+
+def check_seen(rts, seed, ctx, new, heads, latent, flaws, tree, block=16, all_low=False):
+    """A paged batch where flaws: {(request, position): columns} of keys hold +inf, and every key too (column 0)
+    with all_low; half of the heads have queries that turn them into -inf, the others into +inf."""
+    g = gen(seed)
+    reqs, tokens = len(ctx), sum(new)
+    cols = -(-max(c + n for c, n in zip(ctx, new)) // block)
+    table = torch.randperm(reqs * cols, generator=g).int().view(reqs, cols)
+    cache = torch.randn(reqs * cols * block, latent + 64, generator=g).bfloat16()
+    q = torch.randn(tokens, heads, latent + 64, generator=g).bfloat16()
+    starts = [0]
+    for n in new:
+        starts.append(starts[-1] + n)
+
+    def row(r, p):
+        return int(table[r, p // block]) * block + p % block
+
+    touched = sorted({c for cs in flaws.values() for c in cs} | ({0} if all_low else set()))
+    low = torch.arange(heads) % 2 == 0
+    for c in touched:
+        q[:, low, c] = -q[:, low, c].abs() - 0.5
+        q[:, ~low, c] = -q[:, ~low, c].abs() - 0.5 if all_low else q[:, ~low, c].abs() + 0.5
+    for (r, p), cs in flaws.items():
+        cache[row(r, p), cs] = math.inf
+    if all_low:
+        cache[:, 0] = math.inf
+    td = None if tree is None else torch.tensor([x - (1 << 64) if x >> 63 else x for x in tree], device=DEV)
+    results = []
+    for workspace in ("auto", None):
+        out, lse = rts.latent_attend_paged(q.to(DEV), cache.to(DEV), i32(starts), i32(ctx), table.to(DEV), block, 0.07,
+                                           d_latent=latent, tree=td, workspace=workspace)
+        out, lse = out.cpu(), lse.cpu()
+        results.append((out, lse))
+        for r in range(reqs):
+            for t in range(starts[r], starts[r + 1]):
+                j = t - starts[r]
+                mine = range(j + 1) if tree is None else [b for b in range(min(new[r], 64)) if tree[t] >> b & 1]
+                at = torch.tensor([row(r, p) for p in [*range(ctx[r]), *(ctx[r] + b for b in mine)]], dtype=torch.int64)
+                o, l, ob, lb = attend_inf(q[t], cache[at], 0.07, latent)
+                ref.assert_close(out[t], o, ob, f"out of token {t} (request {r}), {workspace}")
+                ref.assert_close(lse[t], l, lb, f"lse of token {t} (request {r}), {workspace}")
+    return results
+
+
+FLAWS = {(0, 3): [5], (0, 72): [0, 63, 64], (0, 74): [130, 255], (1, 2): [9], (1, 3): [9, 31]}
+
+
+@pytest.mark.parametrize("latent", [512, 256])
+@pytest.mark.parametrize("heads", [1, 2, 16, 70, 128])
+def test_seen_infinities(rts, heads, latent):
+    """Keys with infinities in stages where rows see different keys and in others: every row that sees one has its
+    NaN, every row that does not has none."""
+    say("latent paged: infinities that are seen", heads, latent)
+    ctx, new = [70, 0, 300], [6, 5, 2]
+    check_seen(rts, heads, ctx, new, heads, latent, {**FLAWS, (2, 301): [7], (2, 130): [200]}, None)
+    tree = [1 << j | (1 << (j // 2)) for n in new for j in range(n)]
+    tree[1] = 0
+    check_seen(rts, heads + 1, ctx, new, heads, latent, {**FLAWS, (2, 301): [7]}, tree)
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_seen_infinities_in_many_stages(rts, heads):
+    """More drafted tokens than a stage has keys: several stages with masks, flaws in each."""
+    say("latent paged: infinities in several masked stages", heads)
+    flaws = {(0, p): [p % 512, 511 - p % 100] for p in range(20, 130, 7)}
+    check_seen(rts, 7, [40], [100], heads, 512, flaws, None)
+
+
+@pytest.mark.parametrize("latent", [512, 256])
+def test_all_scores_minus_infinity(rts, latent):
+    """Every key's score is -inf: weights 0, lse -inf, NaN where the values are not finite; in one piece and in
+    several alike, and over listed rows too."""
+    say("latent: all scores -inf", latent)
+    a, b = check_seen(rts, 3, [900, 10, 0], [2, 3, 1], 16, latent, {}, None, all_low=True)
+    for x, y in zip(a, b):
+        assert torch.equal(torch.isnan(x), torch.isnan(y))
+    assert torch.isnan(a[0][..., 0]).all() and (a[0][..., 1:] == 0).all() and (a[1] == -math.inf).all()
+    q = -torch.rand(2, 16, latent + 64, generator=gen(4)).bfloat16() - 0.5
+    cache = torch.randn(700, latent + 64, generator=gen(5)).bfloat16()
+    cache[:, 2] = math.inf
+    cache[600:, 2] = 1.0
+    ids = torch.arange(600).int().repeat(2, 1)
+    for extra in (0, 40):                        # all of weight 0; some ordinary keys behind them
+        ids2 = torch.cat([ids, 600 + torch.arange(extra).int().repeat(2, 1)], 1)
+        for workspace in ("auto", None):
+            out, lse = rts.latent_attend_rows(q.to(DEV), cache.to(DEV), ids2.to(DEV), 0.07, d_latent=latent,
+                                              workspace=workspace)
+            for t in range(2):
+                o, l, ob, lb = attend_inf(q[t], cache[ids2[t].long()], 0.07, latent)
+                ref.assert_close(out[t], o, ob, f"out {t} {extra} {workspace}")
+                ref.assert_close(lse[t], l, lb, f"lse {t} {extra} {workspace}")
