@@ -88,9 +88,10 @@ struct LogitsShape {
 // D elements a row; tb tokens a workgroup, head_tiles tiles of 32 heads, `span`
 // columns a workgroup, `stages` (1 or 2) of the waves' rings.
 //
-// The heads that fill up the last tile are copies of the last head, and its
-// weight is dealt out to it and them in halves (w/2, w/4, ..), which is exact.
-// Zeros in their place would turn a key's infinity into NaN.
+// The heads that fill up the last tile are copies of the last head with 2^-64
+// of its weight (never 0 unless the weight is): their 31 parts at most are lost
+// in the first rounding of the last head's, and a key's infinity stays one,
+// which zeros in the queries or in the weights would turn into NaN.
 //
 // Both operands of product step i cover the same 16 elements of a row in the
 // same order, which is all that the sum needs: bf16 step i, half h has chunk
@@ -136,8 +137,8 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
     for (int i = tid; i < n_tok * hp; i += kBlock) {
         const int t = i / hp, h = i - t * hp, last = a.heads - 1;
         const float w = a.weights[(t0 + t) * a.ld_weights + (h < last ? h : last)];
-        const int halvings = h < last ? 0 : h < hp - 1 ? h - last + 1 : h - last;
-        lw[i] = ldexpf(w, -halvings);
+        const float part = ldexpf(w, -64);
+        lw[i] = h <= last ? w : part != 0.f || w == 0.f ? part : copysignf(1e-45f, w);
     }
     if (tid < n_tok) {
         const int64_t e = a.row_ends ? a.row_ends[t0 + tid] : a.cols;
