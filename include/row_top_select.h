@@ -430,6 +430,17 @@ int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, 
                          int64_t ld_logits, hipStream_t stream);
 
 /*
+ * indexer_logits_plan -- how indexer_logits (table_rows -1) or
+ * indexer_logits_paged would cut a call into workgroups, to read a profile or
+ * to choose the sizes of a test by: plan[0] tokens a workgroup, plan[1] steps
+ * of plan[2] columns each a workgroup, plan[3] stages of its rings of keys.
+ * Host only; rows and cols at least 1.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED as those calls.
+ */
+int indexer_logits_plan(int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t cols, int64_t table_rows,
+                        int64_t* plan);
+
+/*
  * latent_attend_rows -- attention over selected rows of a latent cache: one
  * vector c of d_latent + d_rope elements a cached token, shared by all heads,
  * is the key, and its first d_latent elements are the value (the queries come

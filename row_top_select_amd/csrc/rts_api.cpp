@@ -351,6 +351,17 @@ int indexer_logits_paged(const void* q, int dtype, int64_t rows, int32_t heads, 
     return rts::launch_indexer_logits(a, stream);
 }
 
+int indexer_logits_plan(int dtype, int64_t rows, int32_t heads, int32_t dim, int64_t cols, int64_t table_rows,
+                        int64_t* plan) {
+    if ((dtype != RTS_BF16 && dtype != RTS_E4M3) || rows < 1 || cols < 1 || heads < 1 || table_rows < -1 || !plan)
+        return RTS_EINVAL;
+    if (heads > 128 || (dim != 64 && dim != 128) || cols > 0x7FFFFFFFll || rows > 0x7FFFFFFFll)
+        return RTS_EUNSUPPORTED;
+    const rts::LogitsPlan p = rts::plan_indexer_logits(dtype, rows, cols, heads, dim, table_rows);
+    plan[0] = p.tokens, plan[1] = p.steps, plan[2] = p.step, plan[3] = p.stages;
+    return RTS_OK;
+}
+
 namespace {
 // What latent_attend_rows and latent_attend_paged check alike.
 int attend_args(const rts::AttendArgs& a, int32_t d_rope) {

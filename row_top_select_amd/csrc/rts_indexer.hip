@@ -375,24 +375,25 @@ __global__ __launch_bounds__((LogitsShape<D, E4M3>::kWaves * kWave), 1) void ind
     }
 }
 
-template <int D, bool E4M3, bool PAGED, typename Out>
-static int launch_logits(const LogitsArgs& a, hipStream_t s) {
+// `reqs`: requests of the paged form, or -1.
+template <int D, bool E4M3>
+static LogitsPlan plan_logits(int64_t rows, int64_t cols, int32_t heads, int64_t reqs) {
     using S = LogitsShape<D, E4M3>;
     constexpr int kLds = 160 << 10;
-    const int head_tiles = (a.heads + 31) / 32;
+    const int head_tiles = (heads + 31) / 32;
     const int per_token = head_tiles * D * 64 + head_tiles * 32 * 4 + 8;
     // Tokens that share keys: all, or about those of one request.
-    int64_t want = a.rows;
-    if (PAGED) {
-        const int64_t reqs = a.pages.table_rows < a.rows ? a.pages.table_rows : a.rows;
-        want = reqs > 0 ? (a.rows + reqs - 1) / reqs : 1;
+    int64_t want = rows;
+    if (reqs >= 0) {
+        reqs = reqs < rows ? reqs : rows;
+        want = reqs > 0 ? (rows + reqs - 1) / reqs : 1;
     }
     // Two stages of keys where few tokens leave little time for the next one
     // (decode of 64 x 32768 e4m3 keys: 52.4 us, 54.1 us with one).
     const int stages = S::ring_bytes(2) + per_token * want <= kLds ? 2 : 1;
     const int64_t fit = (kLds - S::ring_bytes(stages)) / per_token;
     const int64_t most = want < 16 ? (want < fit ? want : fit) : (fit < 16 ? fit : 16);
-    const int64_t steps = (a.cols + S::kStep - 1) / S::kStep;
+    const int64_t steps = (cols + S::kStep - 1) / S::kStep;
     // Tokens a workgroup and columns a workgroup by estimated time: a workgroup
     // takes a CU, 6 us around its steps, 0.5 us a step and kItemUs a head tile
     // of a token in a step (64 keys a wave through the matrix unit).  What
@@ -403,7 +404,7 @@ static int launch_logits(const LogitsArgs& a, hipStream_t s) {
     int64_t tb = 1, per = steps;
     double best = 1e300;
     for (int64_t t = 1; t <= most; ++t) {
-        const int64_t bx = (a.rows + t - 1) / t;
+        const int64_t bx = (rows + t - 1) / t;
         for (int round = 1; round <= 4; ++round) {
             int64_t parts = 256 * round / bx;
             parts = parts < 1 ? 1 : parts > steps ? steps : parts;
@@ -413,11 +414,25 @@ static int launch_logits(const LogitsArgs& a, hipStream_t s) {
             if (us < best) best = us, tb = t, per = p;
         }
     }
-    const int64_t blocks_x = (a.rows + tb - 1) / tb, parts = (steps + per - 1) / per;
+    return LogitsPlan{(int)tb, stages, S::kStep, per, S::ring_bytes(stages) + per_token * tb};
+}
+
+LogitsPlan plan_indexer_logits(int dtype, int64_t rows, int64_t cols, int32_t heads, int32_t dim, int64_t reqs) {
+    if (dtype == RTS_BF16)
+        return dim == 128 ? plan_logits<128, false>(rows, cols, heads, reqs) : plan_logits<64, false>(rows, cols, heads, reqs);
+    return dim == 128 ? plan_logits<128, true>(rows, cols, heads, reqs) : plan_logits<64, true>(rows, cols, heads, reqs);
+}
+
+template <int D, bool E4M3, bool PAGED, typename Out>
+static int launch_logits(const LogitsArgs& a, hipStream_t s) {
+    using S = LogitsShape<D, E4M3>;
+    const LogitsPlan p = plan_logits<D, E4M3>(a.rows, a.cols, a.heads, PAGED ? a.pages.table_rows : -1);
+    const int64_t span = p.steps * S::kStep;
+    const int64_t blocks_x = (a.rows + p.tokens - 1) / p.tokens, parts = (a.cols + span - 1) / span;
     if (blocks_x > kMaxThreads / (S::kWaves * kWave)) return RTS_EUNSUPPORTED;
     hipLaunchKernelGGL((indexer_logits_kernel<D, E4M3, PAGED, Out>),
-                       dim3((unsigned)blocks_x, (unsigned)parts), dim3(S::kWaves * kWave),
-                       S::ring_bytes(stages) + per_token * tb, s, a, (int)tb, head_tiles, per * S::kStep, stages);
+                       dim3((unsigned)blocks_x, (unsigned)parts), dim3(S::kWaves * kWave), (size_t)p.lds, s, a, p.tokens,
+                       (a.heads + 31) / 32, span, p.stages);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 

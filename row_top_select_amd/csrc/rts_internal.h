@@ -120,6 +120,17 @@ struct LogitsArgs {
 };
 int launch_indexer_logits(const LogitsArgs& a, hipStream_t stream);
 
+// How a call is cut into workgroups.
+struct LogitsPlan {
+    int tokens;         // of a workgroup
+    int stages;         // of its waves' rings of keys
+    int step;           // columns that all its waves take at a time
+    int64_t steps;      // of a workgroup
+    int64_t lds;        // bytes
+};
+// `reqs`: requests of the paged form, or -1.
+LogitsPlan plan_indexer_logits(int dtype, int64_t rows, int64_t cols, int32_t heads, int32_t dim, int64_t reqs);
+
 // The arguments of latent_attend_rows and latent_attend_paged.
 struct AttendArgs {
     bool paged;  // which of the two (ids may be null in the rows form: k == 0)
