@@ -518,6 +518,18 @@ int latent_attend_paged(const void* q, int64_t tokens, int32_t heads, int32_t d_
                         hipStream_t stream);
 
 /*
+ * latent_attend_rows_plan, latent_attend_paged_plan -- how those calls would be
+ * cut into workgroups, to read a profile or to choose the sizes of a test by:
+ * plan[0] groups of 32 query rows a workgroup (1, 2 or 4), plan[1] pieces of a
+ * row's keys at most.  split: whether the call has a workspace.  Host only;
+ * rows and tokens and requests at least 1.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED as those calls.
+ */
+int latent_attend_rows_plan(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, int split, int32_t* plan);
+int latent_attend_paged_plan(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent, int64_t max_len,
+                             int split, int32_t* plan);
+
+/*
  * merge_attend_rank_major -- joins the partial attentions of world ranks that
  * each own a part of the rows (emit_rows per dcp_rank, then
  * latent_attend_rows), read in place from the rank-major all-gather buffers:

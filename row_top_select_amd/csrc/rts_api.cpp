@@ -414,6 +414,23 @@ int latent_attend_rows(const void* q, int64_t rows, int32_t heads, int32_t d_lat
                           workspace, workspace_bytes, stream);
 }
 
+int latent_attend_rows_plan(int64_t rows, int32_t heads, int32_t d_latent, int32_t k, int split, int32_t* plan) {
+    if (rows < 1 || heads < 1 || k < 0 || !plan) return RTS_EINVAL;
+    if (heads > 1024 || rows > 0x7FFFFFFFll / heads || (d_latent != 256 && d_latent != 512)) return RTS_EUNSUPPORTED;
+    const rts::AttendPlan p = rts::plan_attend_rows(rows, heads, d_latent, k, split != 0);
+    plan[0] = p.groups, plan[1] = p.splits;
+    return RTS_OK;
+}
+
+int latent_attend_paged_plan(int64_t tokens, int64_t reqs, int32_t heads, int32_t d_latent, int64_t max_len,
+                             int split, int32_t* plan) {
+    if (tokens < 1 || reqs < 1 || heads < 1 || max_len < 0 || !plan) return RTS_EINVAL;
+    if (heads > 1024 || tokens > 0x7FFFFFFFll / heads || (d_latent != 256 && d_latent != 512)) return RTS_EUNSUPPORTED;
+    const rts::AttendPlan p = rts::plan_attend_paged(tokens, reqs, heads, d_latent, max_len, split != 0);
+    plan[0] = p.groups, plan[1] = p.splits;
+    return RTS_OK;
+}
+
 size_t latent_attend_paged_workspace_size(int64_t tokens, int64_t reqs, int32_t heads,
                                           int32_t d_latent, int64_t max_len) {
     if (tokens < 1 || reqs < 1 || heads < 1 || heads > 1024 || tokens > 0x7FFFFFFFll / heads ||

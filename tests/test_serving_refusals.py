@@ -24,3 +24,20 @@ def test_indexer_logits_plan():
     assert f(1, i64(3), 8, 128, i64(64), i64(-1), p) == 0
     tokens, steps, step, stages = p
     assert 1 <= tokens <= 3 and steps >= 1 and step in (256, 512) and stages in (1, 2)
+
+
+def test_latent_plans():
+    rows, paged, p = lib.latent_attend_rows_plan, lib.latent_attend_paged_plan, (ctypes.c_int32 * 2)()
+    for bad in ((i64(0), 16, 512, 64, 1, p), (i64(4), 0, 512, 64, 1, p), (i64(4), 16, 512, -1, 1, p),
+                (i64(4), 16, 512, 64, 1, None)):
+        assert rows(*bad) == -1, bad
+    for bad in ((i64(0), i64(2), 16, 512, i64(64), 1, p), (i64(4), i64(0), 16, 512, i64(64), 1, p),
+                (i64(4), i64(2), 0, 512, i64(64), 1, p), (i64(4), i64(2), 16, 512, i64(-1), 1, p),
+                (i64(4), i64(2), 16, 512, i64(64), 1, None)):
+        assert paged(*bad) == -1, bad
+    assert rows(i64(4), 1025, 512, 64, 1, p) == -2 and rows(i64(1 << 31), 16, 512, 64, 1, p) == -2
+    assert rows(i64(4), 16, 128, 64, 1, p) == -2 and paged(i64(4), i64(2), 16, 128, i64(64), 1, p) == -2
+    assert paged(i64(1 << 31), i64(2), 16, 512, i64(64), 1, p) == -2
+    for f, a in ((rows, (i64(2), 16, 512, 2048)), (paged, (i64(2), i64(2), 16, 512, i64(4096)))):
+        assert f(*a, 0, p) == 0 and p[0] in (1, 2, 4) and p[1] == 1
+        assert f(*a, 1, p) == 0 and p[0] in (1, 2, 4) and p[1] > 1
