@@ -527,6 +527,14 @@ def _launch(fn, where: str, device: torch.device, stream, *args) -> None:
         raise RtsError(status, where)
 
 
+def _no_grad(where: str, *tensors) -> None:
+    """Refuses inputs whose gradients a caller would wait for in vain."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError(f"{where} has no backward pass: call it under torch.no_grad(), or detach its inputs")
+
+
 def _on(device: torch.device, *tensors) -> None:
     for t in tensors:
         if t is not None and t.device != device:
@@ -624,6 +632,7 @@ _FLOAT_DTYPES = {torch.float32: RTS_F32, torch.bfloat16: RTS_BF16}
 
 def _logits_inputs(q, keys, weights, key_scales, row_ends, out, out_dtype, cols, stream):
     """What indexer_logits and indexer_logits_paged check alike."""
+    _no_grad("indexer_logits", q, keys, weights, key_scales)
     device = _gpu(q, "q")
     if q.dtype not in _INDEX_DTYPES or keys.dtype != q.dtype:
         raise TypeError("q and keys must both be bfloat16 or both float8_e4m3fn")
@@ -669,7 +678,8 @@ def indexer_logits(q: torch.Tensor, keys: torch.Tensor, weights: torch.Tensor,
                    out: torch.Tensor | None = None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """The logits [rows, cols] that topk_rows selects from: for ``q`` [rows, heads, dim], ``keys``
     [cols, dim] and ``weights`` [rows, heads], the weighted sum over heads of relu(q . k), times the
-    key's scale; see indexer_logits in the header.  Columns at or past a row's end are not written."""
+    key's scale; see indexer_logits in the header.  Columns at or past a row's end are not written.
+    Without a backward pass: inputs that require gradients are refused."""
     cols = keys.shape[0]
     device, rows, heads, dim, ld_q, _, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
         q, keys, weights, key_scales, row_ends, out, out_dtype, cols, stream)
@@ -686,7 +696,8 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
                          stride_rows: int | None = None, out: torch.Tensor | None = None,
                          out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """indexer_logits over the paged ``key_cache`` [cache_rows, dim] of each token's request (the
-    ``req_id`` and ``row_ends`` of assign_slots); see indexer_logits_paged in the header."""
+    ``req_id`` and ``row_ends`` of assign_slots); see indexer_logits_paged in the header.  Without a
+    backward pass, as indexer_logits."""
     if cols < 0:
         raise ValueError("cols must not be negative")
     device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
@@ -707,6 +718,7 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
 
 def _attend_inputs(q, cache, d_latent, out, lse, stream):
     """What latent_attend_rows and latent_attend_paged check alike."""
+    _no_grad("latent attention", q, cache)
     device = _gpu(q, "q")
     if q.dtype != torch.bfloat16 or cache.dtype != torch.bfloat16:
         raise TypeError("q and cache must be bfloat16")
@@ -737,7 +749,8 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, 
     """Attention of ``q`` [rows, heads, d] over the rows ``ids`` [rows, k] of the latent ``cache``
     [cache_rows, d], whose first ``d_latent`` elements are the values; ``ids`` and ``counts`` as emit_rows
     writes them (rows_out, valid_out).  Returns (out [rows, heads, d_latent], lse [rows, heads]); see
-    latent_attend_rows in the header.  ``workspace`` as in topk_rows."""
+    latent_attend_rows in the header.  ``workspace`` as in topk_rows.  Without a backward pass: inputs that
+    require gradients are refused."""
     device, rows, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
         q, cache, d_latent, out, lse, stream)
     if ids.dtype != torch.int32:
@@ -772,7 +785,8 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
     latent cache, causal or by the ancestor masks ``tree`` (int64 or uint64 [tokens], bit j: draft j of the
     request is seen); ``query_starts`` as assign_slots writes it.  ``max_len`` bounds the requests' lengths
     and only steers the split (default: what the table holds).  Returns (out, lse); see
-    latent_attend_paged in the header.  ``workspace`` as in topk_rows."""
+    latent_attend_paged in the header.  ``workspace`` as in topk_rows.  Without a backward pass, as
+    latent_attend_rows."""
     device, tokens, heads, d, cache_rows, ld_cache, ld_q, ld_head, out, lse = _attend_inputs(
         q, cache, d_latent, out, lse, stream)
     table_rows, table_cols, ld_table = _table(block_table)
@@ -801,7 +815,8 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
                             out_dtype=None, out_lse: torch.Tensor | None = None, stream=None):
     """Joins the partial attentions ``parts`` [W, rows, heads, dim] of W ranks by their ``lse``
     [W, rows, heads]; returns (out [rows, heads, dim], lse [rows, heads]); see merge_attend_rank_major in
-    the header.  ``out_dtype`` defaults to the parts' type."""
+    the header.  ``out_dtype`` defaults to the parts' type.  Without a backward pass."""
+    _no_grad("merge_attend_rank_major", parts, lse)
     device = _gpu(parts, "parts")
     if parts.dtype not in _FLOAT_DTYPES:
         raise TypeError("parts must be float32 or bfloat16")

@@ -41,3 +41,28 @@ def test_latent_plans():
     for f, a in ((rows, (i64(2), 16, 512, 2048)), (paged, (i64(2), i64(2), 16, 512, i64(4096)))):
         assert f(*a, 0, p) == 0 and p[0] in (1, 2, 4) and p[1] == 1
         assert f(*a, 1, p) == 0 and p[0] in (1, 2, 4) and p[1] > 1
+
+
+def test_inputs_that_require_gradients_are_refused():
+    """The operators have no backward pass: a result without a graph would lose the gradients silently."""
+    z = torch.zeros
+    i = dict(dtype=torch.int32)
+    b = dict(dtype=torch.bfloat16)
+    q_i, keys, w, ks = z(2, 8, 128, **b), z(4, 128, **b), z(2, 8), z(4)
+    q, cache = z(2, 8, 576, **b), z(4, 576, **b)
+    parts, lse = z(2, 3, 8, 512), z(2, 3, 8)
+    table = z(2, 1, **i)
+    calls = [(lambda: rts.indexer_logits(q_i, keys, w, key_scales=ks), (q_i, keys, w, ks)),
+             (lambda: rts.indexer_logits_paged(q_i, keys, w, z(2, **i), z(2, **i), table, 2, 2, key_scales=ks),
+              (q_i, keys, w, ks)),
+             (lambda: rts.latent_attend_rows(q, cache, z(2, 3, **i), 0.1), (q, cache)),
+             (lambda: rts.latent_attend_paged(q, cache, z(3, **i), z(2, **i), table, 2, 0.1), (q, cache)),
+             (lambda: rts.merge_attend_rank_major(parts, lse), (parts, lse))]
+    for call, inputs in calls:
+        for t in inputs:
+            t.requires_grad_(True)
+            with pytest.raises(ValueError, match="backward"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="GPU tensor"):  # as far as this goes without a GPU
+                call()
+            t.requires_grad_(False)
