@@ -93,6 +93,9 @@ inline Pages make_pages(const int32_t* table, int64_t table_rows, int32_t cols, 
     int32_t shift = -1;
     for (int32_t i = 0; i < 31; ++i)
         if (block_size == (1 << i)) shift = i;
+    // A cache has fewer than 2^31 rows: with a stride of 2^31 or more only block 0 has any, and the
+    // products of block ids and such strides could pass 64 bits.
+    if (stride_rows > (1ll << 31)) stride_rows = 1ll << 31;
     return Pages{table, table_rows, ld, stride_rows, cache_rows, cols, block_size, shift};
 }
 

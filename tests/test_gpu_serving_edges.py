@@ -1,0 +1,50 @@
+"""The operators around the select at the ends of their arguments' ranges."""
+
+import math
+
+import pytest
+
+from gpu_common import say
+
+torch = pytest.importorskip("torch")
+import serving_reference as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def rts():
+    import row_top_select_amd
+    return row_top_select_amd
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("stride,block", [(1 << 34, 1 << 30), ((1 << 62) + 8, 4), ((1 << 63) - 1, 2), (1 << 31, 1)])
+def test_block_strides_past_the_cache(rts, stride, block):
+    """block id * stride passes 64 bits: a physical row that does not exist, whatever its low bits are."""
+    say("paged: a block stride of", stride)
+    q = torch.randn(1, 8, 128, generator=gen(1)).bfloat16()
+    keys = torch.randn(64, 128, generator=gen(2)).bfloat16()
+    w = torch.randn(1, 8, generator=gen(3))
+    table = i32([[0, block, 0]])
+    got = rts.indexer_logits_paged(q.to(DEV), keys.to(DEV), w.to(DEV), i32([0]), i32([48]), table, 16, 48,
+                                   stride_rows=stride).cpu()
+    want, bound = ref.logits(q[0], keys[:16], w[0], None)
+    ref.assert_close(got[0, :16], want, bound, "block 0")
+    assert torch.isnan(got[0, 16:32]).all() and torch.equal(got[0, 32:], got[0, :16])
+    lq = torch.randn(1, 16, 576, generator=gen(4)).bfloat16()
+    cache = torch.randn(64, 576, generator=gen(5)).bfloat16()
+    out, lse = rts.latent_attend_paged(lq.to(DEV), cache.to(DEV), i32([0, 1]), i32([47]), table, 16, 0.07,
+                                       stride_rows=stride)
+    o, l, ob, lb = ref.attend(lq[0], torch.cat([cache[:16], cache[:16]]), 0.07, 512)
+    ref.assert_close(out[0], o, ob, "out")
+    ref.assert_close(lse[0], l, lb, "lse")
