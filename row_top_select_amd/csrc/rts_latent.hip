@@ -311,7 +311,7 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
         w.list = a.pages.table + req * a.pages.ld;
     }
 
-    const int all = (w.n + kTile - 1) / kTile;   // stages
+    const int all = w.n / kTile + (w.n % kTile != 0);   // stages
     const int per = (all + pieces - 1) / pieces;
     const int s0 = split * per;
     const int s1 = s0 + per < all ? s0 + per : all;

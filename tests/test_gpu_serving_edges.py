@@ -48,3 +48,21 @@ def test_block_strides_past_the_cache(rts, stride, block):
     o, l, ob, lb = ref.attend(lq[0], torch.cat([cache[:16], cache[:16]]), 0.07, 512)
     ref.assert_close(out[0], o, ob, "out")
     ref.assert_close(lse[0], l, lb, "lse")
+
+
+def test_the_longest_list(rts):
+    """2^31 - 1 entries, almost all -1; the few that are not lie at both ends and between."""
+    say("latent rows: a list of 2^31 - 1 entries")
+    k = (1 << 31) - 1
+    ids = torch.full((1, k), -1, dtype=torch.int32, device=DEV)
+    at = torch.tensor([0, 31, 32, 10 ** 9, k - 33, k - 2, k - 1], device=DEV)
+    ids[0, at] = torch.arange(7, dtype=torch.int32, device=DEV)
+    q = torch.randn(1, 16, 576, generator=gen(6)).bfloat16()
+    cache = torch.randn(9, 576, generator=gen(7)).bfloat16()
+    out, lse = rts.latent_attend_rows(q.to(DEV), cache.to(DEV), ids, 0.07)
+    o, l, ob, lb = ref.attend(q[0], cache[:7], 0.07, 512)
+    ref.assert_close(out[0], o, ob, "out")
+    ref.assert_close(lse[0], l, lb, "lse")
+    out, lse = rts.latent_attend_rows(q.to(DEV), cache.to(DEV), ids, 0.07, counts=i32([k - 1]))
+    o, l, ob, lb = ref.attend(q[0], cache[:6], 0.07, 512)
+    ref.assert_close(out[0], o, ob, "out of all but the last")
