@@ -456,6 +456,7 @@ int indexer_logits_plan(int dtype, int64_t rows, int32_t heads, int32_t dim, int
  *
  * q          bf16 [rows, heads, d_latent + d_rope]: row t, head h at
  *            q + t * ld_q + h * ld_head (elements).
+ * scale      any number from -2^127 to 2^127.
  * d_latent   256 or 512; d_rope 64.
  * cache      bf16 [cache_rows, ld_cache].
  * ids        int32 [rows, ld_ids], first k columns used.

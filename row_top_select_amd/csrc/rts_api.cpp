@@ -6,6 +6,8 @@
 
 #include <stdint.h>
 
+#include <cmath>
+
 #include "rts_internal.h"
 
 namespace {
@@ -367,7 +369,7 @@ namespace {
 int attend_args(const rts::AttendArgs& a, int32_t d_rope) {
     if (a.rows < 0 || a.heads < 1 || a.d_latent < 1 || d_rope < 0 || a.cache_rows < 0) return RTS_EINVAL;
     const int64_t d = (int64_t)a.d_latent + d_rope;
-    if (a.ld_cache < d || a.ld_head < d || a.ld_q < 0) return RTS_EINVAL;
+    if (a.ld_cache < d || a.ld_head < d || a.ld_q < 0 || !(std::fabs(a.scale) <= 0x1p127f)) return RTS_EINVAL;
     if ((a.d_latent != 256 && a.d_latent != 512) || d_rope != 64 || a.heads > 1024 ||
         a.rows > 0x7FFFFFFFll / a.heads || a.cache_rows > 0x7FFFFFFFll)
         return RTS_EUNSUPPORTED;

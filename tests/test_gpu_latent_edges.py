@@ -178,3 +178,21 @@ def test_all_scores_minus_infinity(rts, latent):
                 o, l, ob, lb = attend_inf(q[t], cache[ids2[t].long()], 0.07, latent)
                 ref.assert_close(out[t], o, ob, f"out {t} {extra} {workspace}")
                 ref.assert_close(lse[t], l, lb, f"lse {t} {extra} {workspace}")
+
+
+@pytest.mark.parametrize("scale,power", [(2.0 ** 127, -60), (-(2.0 ** 127), -60), (1e-38, 0), (-3e-39, 0), (1e-45, 0),
+                                         (1e-36, 50)])
+def test_scales_at_the_ends(rts, scale, power):
+    """Scales from the largest that is taken to the smallest there is; queries and keys make up for them."""
+    say("latent: a scale of", scale)
+    n = 300
+    q = (torch.randn(1, 16, 576, generator=gen(8)) * 2.0 ** power).bfloat16()
+    cache = torch.randn(n, 576, generator=gen(9)).bfloat16()
+    cache[:, 512:] = (cache[:, 512:].float() * 2.0 ** power).bfloat16()
+    q[..., :512] = 0                                     # the scores come from the positional part
+    scale32 = float(torch.tensor(scale, dtype=torch.float32))
+    for workspace in ("auto", None):
+        for form, (out, lse) in both_forms(rts, q, cache, scale, workspace=workspace):
+            o, l, ob, lb = ref.attend(q[0], cache, scale32, 512)
+            ref.assert_close(out[0], o, ob, (form, workspace))
+            ref.assert_close(lse[0], l, lb, (form, workspace))

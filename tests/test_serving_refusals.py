@@ -66,3 +66,12 @@ def test_inputs_that_require_gradients_are_refused():
             with torch.no_grad(), pytest.raises(ValueError, match="GPU tensor"):  # as far as this goes without a GPU
                 call()
             t.requires_grad_(False)
+
+
+def test_scales_that_are_not_numbers_are_refused():
+    p = ctypes.c_void_p(0x10000)  # never dereferenced
+    for scale in (float("nan"), float("inf"), float("-inf"), 1.8e38, -3e38):
+        assert lib.latent_attend_rows(p, 4, 16, 512, 64, 16 * 576, 576, p, 64, 576, p, 32, 32, p, scale, p, p, None, 0,
+                                      None) == -1, scale
+        assert lib.latent_attend_paged(p, 4, 16, 512, 64, 16 * 576, 576, p, 64, 576, p, p, 2, None, p, 4, 4, 16, 16, 64,
+                                       scale, p, p, None, 0, None) == -1, scale
