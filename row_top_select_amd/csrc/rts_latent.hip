@@ -80,6 +80,14 @@ constexpr int stage_bytes() { return kTile * (DL + kRope) * 2; }
 template <int DL>
 constexpr int flaw_bytes() { return kTile * DL / 8 + 16; }
 
+// 0 times 8 bf16: 0, or NaN for what is not finite.
+__device__ __forceinline__ i32x4 times_zero(i32x4 v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = ((v[e] & 0x7F80) == 0x7F80 ? 0x7FC0 : 0) | ((v[e] & 0x7F800000) == 0x7F800000 ? 0x7FC00000 : 0);
+    return v;
+}
+
 __device__ __forceinline__ uint16_t f32_bf16(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);  // round to nearest even
 }
@@ -397,7 +405,8 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             i32x4 v = {};
-            if (row_ok && a.scale != 0.f) v = *reinterpret_cast<const i32x4*>(qp + i * 16);
+            if (row_ok) v = *reinterpret_cast<const i32x4*>(qp + i * 16);
+            if (a.scale == 0.f) v = times_zero(v);
             q[i] = __builtin_bit_cast(bf16x8, v ^ (int)flip);
         }
     }

@@ -196,3 +196,24 @@ def test_scales_at_the_ends(rts, scale, power):
             o, l, ob, lb = ref.attend(q[0], cache, scale32, 512)
             ref.assert_close(out[0], o, ob, (form, workspace))
             ref.assert_close(lse[0], l, lb, (form, workspace))
+
+
+@pytest.mark.parametrize("latent", [512, 256])
+def test_scale_zero(rts, latent):
+    """0 times a product: the mean of the values; NaN where the product is not finite, whichever side it comes from."""
+    say("latent: a scale of 0")
+    n = 150
+    q = torch.randn(1, 16, latent + 64, generator=gen(10)).bfloat16()
+    cache = torch.randn(n, latent + 64, generator=gen(11)).bfloat16()
+    q[0, 3, latent + 5], q[0, 8, 2], q[0, 15, 0] = math.nan, math.inf, -math.inf
+    for scale in (0.0, -0.0):
+        for form, (out, lse) in both_forms(rts, q, cache, scale, latent):
+            bad = torch.zeros(16, dtype=torch.bool)
+            bad[[3, 8, 15]] = True
+            assert torch.isnan(out[0, bad]).all() and torch.isnan(lse[0, bad]).all(), form
+            o, l, ob, lb = ref.attend(q[0, ~bad], cache, 0.0, latent)
+            ref.assert_close(out[0, ~bad], o, ob, form)
+            ref.assert_close(lse[0, ~bad], l, lb, form)
+    cache[70, latent + 1] = math.inf
+    for form, (out, lse) in both_forms(rts, q, cache, 0.0, latent):
+        assert torch.isnan(out).all() and torch.isnan(lse).all(), form
