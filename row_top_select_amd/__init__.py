@@ -529,10 +529,9 @@ def _launch(fn, where: str, device: torch.device, stream, *args) -> None:
 
 def _no_grad(where: str, *tensors) -> None:
     """Refuses inputs whose gradients a caller would wait for in vain."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if getattr(t, "requires_grad", False):
-                raise ValueError(f"{where} has no backward pass: call it under torch.no_grad(), or detach its inputs")
+    for t in tensors:
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+            raise ValueError(f"{where} has no backward pass: call it under torch.no_grad(), or detach its inputs")
 
 
 def _on(device: torch.device, *tensors) -> None:
@@ -550,6 +549,8 @@ def _gpu(t, name: str) -> torch.device:
 def _out(t, shape, dtype, device, name: str, stream) -> torch.Tensor:
     """A caller's output tensor, checked, or a new one."""
     if t is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
         t = _new(shape, dtype, device, stream)
     elif t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {device}")
@@ -572,12 +573,30 @@ def _scratch(workspace, need: int, device, stream):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _too_large(name: str, bits: int):
+    """For numbers that ctypes would cut to their low bits."""
+    return ValueError(f"{name} must be below 2^{bits - 1}")
+
+
+def _pages(block_size: int, stride_rows) -> tuple:
+    """(tokens, physical rows) of a block."""
+    if not -0x80000000 <= block_size <= 0x7FFFFFFF:
+        raise _too_large("block_size", 32)
+    if stride_rows is None:
+        return block_size, block_size
+    if not -2 ** 63 <= stride_rows < 2 ** 63:
+        raise _too_large("stride_rows", 64)
+    return block_size, stride_rows
+
+
 def _table(block_table: torch.Tensor):
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [Q, B_max] with unit column stride")
     (rows, cols), (ld, step) = block_table.shape, block_table.stride()
     if cols > 1 and rows > 0 and step != 1:
         raise ValueError("block_table must be int32 [Q, B_max] with unit column stride")
+    if cols > 0x7FFFFFFF:
+        raise _too_large("the width of block_table", 32)
     return rows, cols, (ld if rows > 1 and cols > 0 else cols)
 
 
@@ -619,7 +638,7 @@ def assign_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, tokens: int, bl
         for name, t, n in zip(SlotMap._fields, out, (reqs + 1, tokens, tokens, tokens, 1)):
             _out(t, (n,), torch.int32, device, name, stream)
     _launch(_lib.assign_slots, "assign_slots", device, stream, ctx_lens.data_ptr(),
-            new_lens.data_ptr(), reqs, tokens, block_size, block_size if stride_rows is None else stride_rows,
+            new_lens.data_ptr(), reqs, tokens, *_pages(block_size, stride_rows),
             free_blocks.data_ptr(), n_free, block_table.data_ptr(), table_cols, ld_table,
             out.query_starts.data_ptr(), out.req_id.data_ptr(), out.row_ends.data_ptr(),
             out.slots.data_ptr(), out.used.data_ptr())
@@ -698,8 +717,8 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
     """indexer_logits over the paged ``key_cache`` [cache_rows, dim] of each token's request (the
     ``req_id`` and ``row_ends`` of assign_slots); see indexer_logits_paged in the header.  Without a
     backward pass, as indexer_logits."""
-    if cols < 0:
-        raise ValueError("cols must not be negative")
+    if not 0 <= cols < 2 ** 63:
+        raise ValueError("cols must not be negative, and below 2^63")
     device, rows, heads, dim, ld_q, n_keys, ld_keys, ld_w, row_ends, out, ld_out = _logits_inputs(
         q, key_cache, weights, key_scales, row_ends, out, out_dtype, cols, stream)
     req_id = _int32_vec(req_id, rows, "req_id")
@@ -710,8 +729,8 @@ def indexer_logits_paged(q: torch.Tensor, key_cache: torch.Tensor, weights: torc
     _launch(_lib.indexer_logits_paged, "indexer_logits_paged", device, stream, q.data_ptr(),
             _INDEX_DTYPES[q.dtype], rows, heads, dim, ld_q, key_cache.data_ptr(), n_keys, ld_keys,
             weights.data_ptr(), ld_w, _ptr(key_scales), req_id.data_ptr(), row_ends.data_ptr(),
-            block_table.data_ptr(), table_rows, table_cols, ld_table, block_size,
-            block_size if stride_rows is None else stride_rows, cols, out.data_ptr(),
+            block_table.data_ptr(), table_rows, table_cols, ld_table,
+            *_pages(block_size, stride_rows), cols, out.data_ptr(),
             _FLOAT_DTYPES[out.dtype], ld_out)
     return out
 
@@ -756,6 +775,8 @@ def latent_attend_rows(q: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, 
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
     id_rows, k, ld_ids = _rows_ld(ids, "ids")
+    if k > 0x7FFFFFFF:
+        raise _too_large("the width of ids", 32)
     if id_rows != rows:
         raise ValueError("ids must have one row per query row")
     if rows <= 1:
@@ -797,8 +818,11 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
     if tree is not None and (tree.dtype not in (torch.int64, torch.uint64) or tree.dim() != 1 or
                              tree.shape[0] < tokens or not tree.is_contiguous()):
         raise ValueError(f"tree must be a contiguous 64-bit vector of >= {tokens} entries")
+    pages = _pages(block_size, stride_rows)
     if max_len is None:
         max_len = table_cols * block_size
+    elif max_len >= 2 ** 63:
+        raise _too_large("max_len", 64)
     _on(device, query_starts, ctx_lens, block_table, tree)
     ws, ws_bytes = _scratch(workspace,
                             latent_attend_paged_workspace_size(tokens, table_rows, heads, d_latent, max_len)
@@ -806,8 +830,7 @@ def latent_attend_paged(q: torch.Tensor, cache: torch.Tensor, query_starts: torc
     _launch(_lib.latent_attend_paged, "latent_attend_paged", device, stream, q.data_ptr(), tokens,
             heads, d_latent, d - d_latent, ld_q, ld_head, cache.data_ptr(), cache_rows, ld_cache,
             query_starts.data_ptr(), ctx_lens.data_ptr(), table_rows, _ptr(tree), block_table.data_ptr(),
-            table_cols, ld_table, block_size, block_size if stride_rows is None else stride_rows, max_len,
-            scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
+            table_cols, ld_table, *pages, max_len, scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
     return out, lse
 
 

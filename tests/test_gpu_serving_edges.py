@@ -66,3 +66,30 @@ def test_the_longest_list(rts):
     out, lse = rts.latent_attend_rows(q.to(DEV), cache.to(DEV), ids, 0.07, counts=i32([k - 1]))
     o, l, ob, lb = ref.attend(q[0], cache[:6], 0.07, 512)
     ref.assert_close(out[0], o, ob, "out of all but the last")
+
+
+def test_numbers_that_do_not_fit_the_library_are_refused(rts):
+    """A block size of 2^32 + 16 is not one of 16."""
+    say("numbers past 32 and 64 bits")
+    q = torch.zeros(1, 8, 128, dtype=torch.bfloat16, device=DEV)
+    keys = torch.zeros(64, 128, dtype=torch.bfloat16, device=DEV)
+    w, table = torch.zeros(1, 8, device=DEV), i32([[0, 1, 2]])
+    lq = torch.zeros(1, 16, 576, dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros(64, 576, dtype=torch.bfloat16, device=DEV)
+    calls = [lambda b, s: rts.assign_slots(i32([3]), i32([2]), 4, table.clone(), i32([5, 6]), b, stride_rows=s),
+             lambda b, s: rts.indexer_logits_paged(q, keys, w, i32([0]), i32([5]), table, b, 16, stride_rows=s),
+             lambda b, s: rts.latent_attend_paged(lq, cache, i32([0, 1]), i32([5]), table, b, 0.1, stride_rows=s)]
+    for call in calls:
+        call(16, 16)
+        for b, s in (((1 << 32) + 16, None), (16 - (1 << 32), None), (1 << 31, None), (16, (1 << 64) + 16), (16, 1 << 63)):
+            with pytest.raises(ValueError, match="below"):
+                call(b, s)
+    with pytest.raises(ValueError, match="below"):
+        rts.latent_attend_paged(lq, cache, i32([0, 1]), i32([5]), table, 16, 0.1, max_len=1 << 64)
+    with pytest.raises(ValueError, match="below"):
+        rts.indexer_logits_paged(q, keys, w, i32([0]), i32([5]), table, 16, 1 << 64)
+    wide = torch.empty(0, 1 << 32, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="below"):
+        rts.latent_attend_rows(lq[:0], cache, wide, 0.1)
+    with pytest.raises(ValueError, match="below"):
+        rts.assign_slots(i32([]), i32([]), 4, wide, i32([5, 6]), 16)
