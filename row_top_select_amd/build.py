@@ -33,7 +33,8 @@ COMMON = [
 # registers and move to accumulation registers only under pressure.  The other
 # way round the indexer spends 2 of 6 vector instructions a product on copying
 # results back, and the latent kernels, which hold 256 registers of sums beside
-# 16 of scores, push sums out to scratch.
+# 16 of scores, push sums out to scratch (with it the widest one over listed rows
+# still keeps one other register there).
 _VECTOR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 EXTRA = {"rts_latent.hip": _VECTOR_RESULTS, "rts_indexer.hip": _VECTOR_RESULTS}
 

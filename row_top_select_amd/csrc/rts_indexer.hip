@@ -19,7 +19,7 @@
 // number of heads.  16-byte chunks are XOR-ed by the key's number so that the
 // reads do not meet in a bank.  Waves wait for their own loads only.
 //
-// What bounds it: 1024 x 16384 x 64 heads x 128 take 200 to 210 us, 1300
+// What bounds it: 1024 x 16384 x 64 heads x 128 take 206 us, 1300
 // TFLOP/s, more than a large library product reaches; decode of 64 requests
 // with 16384 to 32768 e4m3 keys takes 52 us, 4.1 TB/s.
 //
@@ -389,7 +389,7 @@ static LogitsPlan plan_logits(int64_t rows, int64_t cols, int32_t heads, int64_t
         want = reqs > 0 ? (rows + reqs - 1) / reqs : 1;
     }
     // Two stages of keys where few tokens leave little time for the next one
-    // (decode of 64 x 32768 e4m3 keys: 52.4 us, 54.1 us with one).
+    // (decode of 64 x 32768 e4m3 keys: 51.9 us, 52.5 us with one).
     const int stages = S::ring_bytes(2) + per_token * want <= kLds ? 2 : 1;
     const int64_t fit = (kLds - S::ring_bytes(stages)) / per_token;
     const int64_t most = want < 16 ? (want < fit ? want : fit) : (fit < 16 ? fit : 16);
@@ -398,8 +398,9 @@ static LogitsPlan plan_logits(int64_t rows, int64_t cols, int32_t heads, int64_t
     // takes a CU, 6 us around its steps, 0.5 us a step and kItemUs a head tile
     // of a token in a step (64 keys a wave through the matrix unit).  What
     // matters is that the last round of the 256 CUs is full: 333 x 8191 x 32
-    // bf16 takes 33 us with 11 tokens a workgroup (248 workgroups), 63 us with
-    // 5 (268 workgroups); 1024 x 16384 x 64 e4m3 212 us with 4, 237 us with 5.
+    // bf16 takes 28.8 us with 11 tokens a workgroup (248 workgroups), 50.0 us
+    // with 5 (268 workgroups); 1024 x 16384 x 64 e4m3 209 us with 4 (256
+    // workgroups), 229 us with 2 (512).
     constexpr double kItemUs = (D / 128.0) * (S::kWaves / 4) * 0.25;
     int64_t tb = 1, per = steps;
     double best = 1e300;

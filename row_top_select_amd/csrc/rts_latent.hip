@@ -33,10 +33,15 @@
 // neither the row reads of the first product nor the transposed reads of the
 // second meet in a bank.
 //
-// What bounds it: 1024 tokens x 128 heads x 2048 rows take 552 us, 1060 TFLOP/s
-// with the matrix units 52% busy (a large library product reaches 1200); LDS is
-// a quarter busy, and deeper read-ahead of either operand changes nothing.  With
-// 16 heads the rows' bytes bound it: 256 CUs take a stage each 1.5 us, 6 TB/s.
+// What bounds it: 1024 tokens x 128 heads x 2048 rows take 565 us, 1040 TFLOP/s
+// with the matrix units 52% busy (a large library product reaches 1200 to 1250);
+// deeper read-ahead of either operand changes nothing.  A stage takes a CU that
+// has the chip for itself 1.12, 1.25 or 1.50 us with one, two or four row groups,
+// wherever its rows lie (one row over and over: 1.13 us with one group), and
+// 1.44, 1.62 or 1.95 us beside 255 busy CUs (one row over and over: 1.18 us).
+// So with few rows three quarters of a stage are the CU's own: every wave reads
+// all keys and forms the same scores, 36 of its 44 matrix instructions.  Prompts
+// pay that for every token: 1024 x 16 heads x 2048 rows take 406 us.
 //
 // The maximum m is one of products, before the scale: the difference is taken
 // first, so that the greatest weight is 1 for scores of any size (S c - m with
@@ -554,10 +559,18 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
 
         bf16x8 p[2];
         float sum = 0.f;
+        // The weights are rounded to bf16 because the matrix instructions take both
+        // operands in one 16-bit type, and the values' range is bf16's; their sum
+        // keeps 32 bits.  A result is then 1.8e-3 to 2.1e-3 from 64 bits (relative,
+        // over all elements), of which 1.65e-3 is its own rounding to bf16.  Weights in
+        // two terms, the rounded one and its remainder, gave 1.65e-3 and cost a second
+        // product: 64 tokens x 16 heads x 2048 rows 42.4 us for 40.2, 1024 x 128 heads
+        // 731 for 567, dense decode 207 for 152, a causal chunk of 1024 tokens x 128
+        // heads 1457 for 1021.
         auto weigh = [&](int r) {
             const float x = __builtin_amdgcn_exp2f((s[r] - m) * c);
             sum += x;
-            p[r >> 3][r & 7] = (__bf16)x;  // rounded to 8 bits for the product; the sum keeps 32
+            p[r >> 3][r & 7] = (__bf16)x;
         };
         bf16x8 v[VB][2];
         uint32_t v_at[2][2];
@@ -736,14 +749,14 @@ constexpr int kCus = 256;
 
 // How a call is cut: the row groups of a workgroup (1, 2 or 4 of 32 query
 // rows) and the pieces of the keys that take the least estimated time.  A
-// workgroup has a CU for itself.  Measured on 256 busy CUs, a stage takes 1.5,
-// 1.75 or 2.05 us with 1, 2 or 4 groups (1.15 to 1.5 us on one CU) and what
-// lies around the stages 7, 11 or 16 us; pieces cost a second launch and the
-// way of their 32-bit results out and back at 4 TB/s.  Measured (groups/pieces:
-// us), the rule's choice first: 64 tokens x 128 heads x 2048 keys 4/4: 69, 2/2:
-// 82, 2/1: 100, 1/1: 120; 8 tokens 1/7: 31, 1/8: 37, 4/8: 41, 4/4: 49; 64 tokens
-// x 16 heads 1/4: 40, 1/2: 55, 1/8: 53; 1024 tokens x 128 heads x 512 keys 4/1:
-// 186, 2/1: 295, 4/2: 431.
+// workgroup has a CU for itself.  On 256 busy CUs a stage takes 1.44, 1.62 or
+// 1.95 us with 1, 2 or 4 groups and what lies around the stages, the launch
+// included, 9, 12 or 17 us; the rule has 5% more for a stage and 1 to 2 us less
+// around.  Pieces cost a second launch and the way of their 32-bit results out
+// and back at 4 TB/s.  Measured (groups/pieces: us), the rule's choice first: 64
+// tokens x 128 heads x 2048 keys 4/4: 65, 2/2: 77, 2/1: 93, 1/1: 101; 8 tokens
+// 1/7: 31, 1/8: 30, 4/8: 38, 4/4: 46; 64 tokens x 16 heads 1/4: 36, 1/8: 46, 1/2:
+// 49; 1024 tokens x 128 heads x 512 keys 4/1: 195, 2/1: 294, 4/2: 429.
 static AttendPlan plan_pieces(int64_t units, int64_t rows_each, int64_t stages, int64_t out_rows,
                               int32_t d_latent, bool allow) {
     constexpr float kStageUs[3] = {1.5f, 1.75f, 2.05f}, kAroundUs[3] = {7.f, 11.f, 16.f};
