@@ -160,3 +160,31 @@ def test_results_read_on_the_current_stream_are_kept_for_it(rts):
     later = [rts.merge_attend_rank_major(parts[1], lse, stream=side)[0] for _ in range(3)]
     torch.cuda.synchronize()
     assert (copy == 3).all() and all((x == 5).all() for x in later)
+
+
+@pytest.mark.parametrize("name", ["assign_slots", "indexer_logits_paged", "latent_attend_rows", "latent_attend_paged",
+                                  "merge_attend_rank_major", "topk_rows"])
+def test_captured_beside_a_call_on_another_stream(rts, name):
+    """A graph with the same call on its own stream and on one that joins it, replayed with eager calls between."""
+    say("captured on two streams:", name)
+    call = calls(rts)[name]
+    want = [t.clone() for t in flat(call(None))]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        on_side = flat(call(side))
+        if name != "assign_slots":       # which writes one table
+            here = flat(call(None))
+        torch.cuda.current_stream().wait_stream(side)
+        if name == "assign_slots":
+            here = flat(call(None))
+    for _ in range(4):
+        for t in on_side + here:
+            t.view(torch.uint8).fill_(0x33)
+        graph.replay()
+        eager = flat(call(None))
+        torch.cuda.synchronize()
+        for x, y, z, w in zip(on_side, here, eager, want):
+            assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8)) for t in (x, y, z))
