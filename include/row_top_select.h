@@ -502,6 +502,8 @@ int latent_attend_rows(const void* q, int64_t rows, int32_t heads, int32_t d_lat
  * q, out, lse as in latent_attend_rows, over tokens rows (tokens bounds
  * query_starts).  query_starts int32 [reqs + 1], non-decreasing from 0.
  * tree       uint64 [tokens] or NULL.
+ * ctx_lens   int32 [reqs], negative ones count as 0; positions from 2^31 - 64 on
+ *            are not seen.
  * max_len    an upper bound of ctx_lens[i] + new tokens; it sets how the keys
  *            are split, results hold for any value >= 0.
  * workspace  as in latent_attend_rows, latent_attend_paged_workspace_size bytes.

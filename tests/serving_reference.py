@@ -54,9 +54,9 @@ def logits(q, keys, w, ks):
     x = torch.clamp(q @ keys.T, min=0)
     x = torch.where(torch.isnan(q @ keys.T), torch.full_like(x, math.nan), x)
     out = w @ x
-    # dim steps in a dot product, then one for each head (whole tiles of 32: the
-    # last head's weight is dealt out over the rest of its tile), one for the
-    # halves' sum and one for the scale; every step relative to the sum of the
+    # dim steps in a dot product, then one for each head (of whole tiles of 32,
+    # more than the kernels need: the heads that fill up a tile add none), one for
+    # the halves' sum and one for the scale; every step relative to the sum of the
     # magnitudes.
     size = w.abs() @ (q.abs() @ keys.abs().T)
     bound = (dim + -(-heads // 32) * 32 + 2) * U * size

@@ -93,3 +93,58 @@ def test_numbers_that_do_not_fit_the_library_are_refused(rts):
         rts.latent_attend_rows(lq[:0], cache, wide, 0.1)
     with pytest.raises(ValueError, match="below"):
         rts.assign_slots(i32([]), i32([]), 4, wide, i32([5, 6]), 16)
+
+
+def test_the_longest_contexts(rts):
+    """Contexts of almost 2^31 positions, almost all on missing pages; a few tokens at the end of them."""
+    say("latent paged: contexts of almost 2^31 tokens")
+    block = 1 << 20
+    cols = (1 << 31) // block
+    table = torch.full((2, cols), -1, dtype=torch.int32)
+    # Block 0 of a cache of 48 rows: positions 0..47 of a page.
+    table[0, [0, 1000, cols - 2]] = 0
+    table[1, [5, cols - 1]] = 0
+    ctx = [(1 << 31) - 100 - 30, 3 * block + 7]
+    q = torch.randn(5, 16, 576, generator=gen(12)).bfloat16()
+    cache = torch.randn(48, 576, generator=gen(13)).bfloat16()
+    out, lse = rts.latent_attend_paged(q.to(DEV), cache.to(DEV), i32([0, 3, 5]), i32(ctx), table.to(DEV), block, 0.07)
+    for t in range(3):
+        o, l, ob, lb = ref.attend(q[t], cache.repeat(3, 1), 0.07, 512)
+        ref.assert_close(out[t], o, ob, f"out of token {t}")
+        ref.assert_close(lse[t], l, lb, f"lse of token {t}")
+    assert (out[3:] == 0).all() and (lse[3:] == -math.inf).all()   # page 5 lies behind the second request
+    # The new tokens' own page, at the end of the range.
+    table[0, cols - 1] = 0
+    ctx[0] = (1 << 31) - block + 40
+    out, lse = rts.latent_attend_paged(q.to(DEV), cache.to(DEV), i32([0, 3, 5]), i32(ctx), table.to(DEV), block, 0.07)
+    for t in range(3):
+        kv = torch.cat([cache.repeat(3, 1), cache[:41 + t]])
+        o, l, ob, lb = ref.attend(q[t], kv, 0.07, 512)
+        ref.assert_close(out[t], o, ob, f"out of token {t}")
+        ref.assert_close(lse[t], l, lb, f"lse of token {t}")
+
+
+def test_logits_of_the_longest_context(rts):
+    """2^31 - 1 columns, almost all of them keys without a physical row."""
+    say("logits paged: 2^31 - 1 columns")
+    block, cols = 1 << 20, (1 << 31) - 1
+    table = torch.full((1, (1 << 31) // block), -1, dtype=torch.int32)
+    table[0, [0, 1000, -1]] = 0
+    q = torch.randn(2, 8, 64, generator=gen(14)).bfloat16()
+    keys = torch.randn(block, 64, generator=gen(15)).bfloat16()
+    w = torch.randn(2, 8, generator=gen(16))
+    out = torch.full((2, cols + 1), 77.0, dtype=torch.bfloat16, device=DEV)
+    rts.indexer_logits_paged(q.to(DEV), keys.to(DEV), w.to(DEV), i32([0, 0]), i32([cols, cols - 70]), table.to(DEV), block,
+                             cols, out=out)
+    for t, end in ((0, cols), (1, cols - 70)):
+        want, bound = ref.logits(q[t], keys, w[t], None)
+        want, bound = want.to(DEV), (bound * (1 + ref.BF16) + want.abs() * ref.BF16).to(DEV)
+        for page in (0, 1000, (1 << 31) // block - 1):
+            n = min(block, end - page * block)
+            ref.assert_close(out[t, page * block:page * block + n], want[:n], bound[:n], f"row {t}, page {page}")
+        assert bool((out[t, end:] == 77.0).all())
+        for a in range(0, end, 1 << 28):       # all other pages, a part at a time
+            part = out[t, a:min(a + (1 << 28), end)].clone()
+            for page in (0, 1000, (1 << 31) // block - 1):
+                part[max(0, page * block - a):max(0, (page + 1) * block - a)] = math.nan
+            assert bool(torch.isnan(part).all()), f"row {t}, columns from {a}"
