@@ -367,9 +367,8 @@ int merge_select_pairs_row_major(const int32_t* gathered_pairs, int32_t world, i
  * req_id, row_ends, slots  int32 [tokens]: for token t of request i at
  *            position p = ctx + t - query_starts[i]: i, p + 1 and
  *            block_table[i, p / block_size] * stride_rows + p % block_size
- *            (computed in 64 bits, stored as its low 32 bits; -1 where the
- *            entry is negative or past the table).  Tokens behind the last
- *            request get -1, 0 and -1.
+ *            (its low 32 bits; -1 where the entry is negative or past the
+ *            table).  Tokens behind the last request get -1, 0 and -1.
  * used       int32 [1]: blocks taken; more than free_count means that the
  *            list was too short.
  * No output may overlap an input or another output.

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kSlotBlock) void assign_slots_kernel(
         else if (b < have) id = table[lo * ld_table + b];
         req_id[t] = lo;
         row_ends[t] = (int32_t)(pos + 1 < 0x7FFFFFFFll ? pos + 1 : 0x7FFFFFFFll);
-        slots[t] = id < 0 ? -1 : (int32_t)(uint32_t)((int64_t)id * stride_rows + in);
+        slots[t] = id < 0 ? -1 : (int32_t)((uint32_t)id * (uint32_t)stride_rows + (uint32_t)in);  // the low 32 bits
     }
 }
 

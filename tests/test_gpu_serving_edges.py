@@ -148,3 +148,14 @@ def test_logits_of_the_longest_context(rts):
             for page in (0, 1000, (1 << 31) // block - 1):
                 part[max(0, page * block - a):max(0, (page + 1) * block - a)] = math.nan
             assert bool(torch.isnan(part).all()), f"row {t}, columns from {a}"
+
+
+@pytest.mark.parametrize("stride", [(1 << 33) + 3, (1 << 62) + 8, (1 << 63) - 1])
+def test_slots_of_strides_past_32_bits(rts, stride):
+    """A slot is the low 32 bits of id * stride + offset, whatever the stride is."""
+    say("slots: a block stride of", stride)
+    free = [5, (1 << 31) - 1, 1 << 20]
+    m = rts.assign_slots(i32([0]), i32([9]), 9, torch.zeros(1, 3, dtype=torch.int32, device=DEV), i32(free), 3,
+                         stride_rows=stride)
+    low = [(free[t // 3] * stride + t % 3) & 0xFFFFFFFF for t in range(9)]
+    assert m.slots.tolist() == [x - (1 << 32) if x >> 31 else x for x in low]
