@@ -101,16 +101,34 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _new(shape, dtype, device: torch.device, stream) -> torch.Tensor:
+# torch.cuda.current_stream(device).cuda_stream without the Stream object,
+# which costs as much as a small call's launch; where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(device: torch.device) -> int:
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+
+
+def _new(shape, dtype, device: torch.device, stream, returned: bool = True) -> torch.Tensor:
     """Memory for a call on ``stream`` (None: the current stream).  A freed block of one stream's pool
     may still be in use by what that stream has yet to run, so a call on another stream takes
-    memory from its own; it is given back when the current stream, which may read the
-    results, is done with it too."""
-    if stream is None or device.type != "cuda":
+    memory from its own.  What is returned is given back when the current stream, which may
+    read it, is done with it too."""
+    if stream is None or device.type != "cuda" or stream.cuda_stream == _current(device):
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+    reader = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device() and device == stream.device:
+        torch.cuda.set_stream(stream)  # a third of the context manager's time
+        try:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        finally:
+            torch.cuda.set_stream(reader)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(reader)
     return t
 
 
@@ -176,7 +194,7 @@ def topk_rows(logits: torch.Tensor, k: int, row_ends: torch.Tensor | None = None
     if isinstance(workspace, str) and workspace == "auto":
         need = topk_rows_workspace_size(dt, rows, cols, k)
         if need:
-            ws = _new(need, torch.uint8, logits.device, stream)
+            ws = _new(need, torch.uint8, logits.device, stream, returned=False)
             ws_bytes = need
     elif workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.device != logits.device or \
@@ -505,15 +523,10 @@ def merge_select_pairs_rank_major(gathered_pairs: torch.Tensor, k: int,
     return out
 
 
-# torch.cuda.current_stream(device).cuda_stream without the Stream object,
-# which costs as much as a small call's launch; where torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _launch(fn, where: str, device: torch.device, stream, *args) -> None:
     """Calls ``fn(*args, stream)`` with ``device`` current."""
     if stream is None:
-        s = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        s = _current(device)
     else:
         if stream.device != device:
             raise ValueError(f"{where}: stream must belong to the device of the tensors")
@@ -564,7 +577,7 @@ def _scratch(workspace, need: int, device, stream):
             raise ValueError('workspace must be "auto", None or a GPU tensor')
         if not need:
             return None, 0
-        return _new(need, torch.uint8, device, stream), need
+        return _new(need, torch.uint8, device, stream, returned=False), need
     if workspace is None:
         return None, 0
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or \
