@@ -551,6 +551,188 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
                             int64_t rows, int32_t heads, int32_t dim, void* out, int out_dtype,
                             float* lse, hipStream_t stream);
 
+/*
+ * beam_select -- beam search's selection over beams and vocabulary.  A group is
+ * the beams of one request.  Beam b of group i has the score scores[i, b] and
+ * the logits x of row i * beams + b; token v continues it with the value
+ *   value(b, v) = scores[i, b] + x[v] - lse,   lse = log sum_v exp x[v]
+ * and each group keeps the k best of all its beams' tokens.  Order: value
+ * desc (in 64 bits, so that beams are told apart below the last bit of a
+ * 32-bit score), then beam asc, then logit desc, token asc; within a beam it
+ * is that of its logits.
+ *
+ * Not candidates: the token eos, tokens with a logit of -inf, beams whose score
+ * is not finite (-inf marks a beam that is not in use, such as all but the
+ * first at a search's first step) or whose logits hold a NaN, +inf or -inf only.
+ *
+ * logits     [groups * beams, ld_logits] of dtype RTS_F32 or RTS_BF16, vocab columns.
+ * beams      1..64.   k  1..64.
+ * scores     float [groups, beams].
+ * eos        a token that ends a hypothesis, or -1 for none.
+ * out_scores, parents, tokens  [groups, k], best first: the value (rounded to
+ *            32 bits), the row i * beams + b of the beam and the token; then
+ *            -inf, -1 and -1 where there are fewer candidates.  parents are
+ *            what fork_blocks takes.
+ * ended      float [groups, beams]: value(b, eos), -inf for beams that have no
+ *            candidates.  NULL exactly where eos is -1.
+ * workspace  device scratch, 16-byte aligned, of at least
+ *            beam_select_workspace_size bytes.  Calls in flight at the same time
+ *            need workspaces of their own.
+ * Maxima, sums and values are held in 32 bits or more (sums over a row's parts
+ * and values in 64).
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (beams, k, vocab >= 2^31, groups * beams
+ *         >= 2^31), RTS_EWORKSPACE, RTS_EHIP.
+ */
+size_t beam_select_workspace_size(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k);
+int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, int64_t vocab, int64_t ld_logits,
+                const float* scores, int32_t k, int32_t eos, float* out_scores, int32_t* parents, int32_t* tokens,
+                float* ended, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * fork_blocks -- the block table after rows were reordered, duplicated and
+ * dropped: row i of the new table continues row parents[i] of the old one.
+ * Rows share their parents' blocks; a block that more than one row would go on
+ * writing into is given out anew, and is the caller's to copy (copy_blocks);
+ * blocks that no row names any more are free.  Nothing is counted between
+ * calls: which blocks are in use follows from the new rows and `held` alone.
+ *
+ * With len = max(0, ctx_lens[p]) of row i's parent p, the row has the parent's
+ * first ceil(len / block_size) entries (of table_cols at most); the last of them
+ * is being written if len is no multiple of block_size.  Row i keeps it if i is the first row of
+ * p and the block is not held, not a whole block of any row and not
+ * the last of another parent's rows; otherwise the r-th row that wants a
+ * block of its own takes the r-th lowest free one and copies[r] = (the parent's
+ * block, the new one).  Free are blocks that are neither held nor named by any
+ * of these entries.  Where the pool is exhausted the entry is -1 and there is
+ * no copy.  Other entries of the row are -1, as are entries outside [0, pool_blocks).
+ *
+ * block_table int32 [rows_in, ld_table], table_cols columns used.
+ * ctx_lens   int32 [rows_in].
+ * parents    int32 [rows_out]; outside [0, rows_in): an empty row, of length 0.
+ *            A request ends when no row continues it.
+ * pool_blocks blocks of the pool, at most 2^19; rows_in and rows_out at most 4096.
+ * held       bytes [pool_blocks] or NULL: blocks that something else uses where
+ *            not 0; they are never free and never kept for writing.
+ * out_table  int32 [rows_out, ld_out]: table_cols columns are written.
+ * out_lens   int32 [rows_out].
+ * copies     int32 [rows_out, 2], 8-byte aligned, (-1, -1) behind the last; no
+ *            block is both a source and a destination.
+ * free_blocks int32 [n_free]: the ids that are free afterwards, ascending, then
+ *            -1: a list for assign_slots.
+ * counts     int32 [2]: how many are free afterwards (more than n_free, perhaps)
+ *            and how many blocks the rows wanted (more than there are copies
+ *            means that the pool was exhausted).
+ * No output may overlap an input or another output.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks), RTS_EHIP.
+ */
+int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols, int64_t ld_table,
+                const int32_t* ctx_lens, const int32_t* parents, int64_t rows_out, int32_t block_size,
+                int32_t pool_blocks, const uint8_t* held, int32_t* out_table, int64_t ld_out, int32_t* out_lens,
+                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, hipStream_t stream);
+
+/*
+ * compact_blocks -- moves that bring a pool's blocks in use to the lowest ids.
+ * In use are the first ceil(ctx_lens / block_size) entries of each row; those that are
+ * held stay where they are.  With n blocks in use that are not held, and T the
+ * smallest bound below which n blocks are not held, the blocks in use at or past T move, in
+ * ascending order, to the free ones below it.  A block that several rows share
+ * moves once.  The caller copies the blocks (copy_blocks) before the new
+ * table is used.
+ *
+ * max_moves  of the moves the first max_moves are made, the others left for
+ *            another call.
+ * out_table  int32 [rows, ld_out]: the table after the moves; entries past a
+ *            row's length and outside [0, pool_blocks) become -1.
+ * moves      int32 [max_moves, 2], 8-byte aligned: (from, to), then (-1, -1); no
+ *            block is both.
+ * free_blocks int32 [n_free]: the ids that are free after the moves, ascending, then -1.
+ * counts     int32 [2]: how many are free, and how many moves there are in all.
+ * Other arguments as in fork_blocks (rows < 2^31).
+ * No output may overlap an input or another output.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EHIP.
+ */
+int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols, int64_t ld_table,
+                   const int32_t* ctx_lens, int32_t block_size, int32_t pool_blocks, const uint8_t* held,
+                   int32_t* out_table, int64_t ld_out, int32_t* moves, int64_t max_moves, int32_t* free_blocks,
+                   int64_t n_free, int32_t* counts, hipStream_t stream);
+
+/* A paged cache of any element type: rows of row_bytes bytes, ld_bytes apart. */
+typedef struct {
+    void* data;
+    int64_t rows, row_bytes, ld_bytes;
+} rts_cache;
+
+/*
+ * copy_blocks -- copies blocks within each of a number of caches (keys, values,
+ * scales; the layers of a model): block b is the rows b * stride_rows .. +
+ * block_size.
+ *
+ * caches     n_caches of them, at most 64; this array is on the HOST and is read
+ *            before the call returns.
+ * pairs      int32 [n_pairs, 2], 8-byte aligned: (from, to).  A pair with a
+ *            negative id, of one block twice, or (in a cache) of a block that
+ *            does not lie in it, is skipped.  No block may be the destination
+ *            of two pairs, or of one and the source of another: what it then
+ *            holds is not specified.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (n_caches, rows, row_bytes or ld_bytes >=
+ *         2^31), RTS_EHIP.
+ */
+int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs, int64_t n_pairs, int32_t block_size,
+                int64_t stride_rows, hipStream_t stream);
+
+/*
+ * kv_attend_paged -- attention of new tokens over their requests' paged cache of
+ * keys and values.  The heads are in kv_heads groups of heads / kv_heads that
+ * share a key head.  Token t sees the positions p < row_ends[t] of request
+ * req_id[t] (its own is already in the cache) and, with a window, p >=
+ * row_ends[t] - window.  For head h, of key head j, over what is seen:
+ *   z_p = scale * k_scales[j] * q[t, h, :] . k[p, j, :],   lse[t, h] = log sum_p exp z_p
+ *   out[t, h, :] = v_scales[j] * sum_p exp(z_p - lse) v[p, j, :]
+ * Position p lies at physical row
+ *   block_table[req_id[t], p / block_size] * stride_rows + p % block_size
+ * of both caches; one without a physical row (as in indexer_logits_paged) is not
+ * seen.  What is not seen never reaches a result, NaN and infinities included.
+ * A token that sees nothing (a req_id outside [0, table_rows), such as a padded batch's,
+ * among them) gives zeros and -inf.  A score of -inf has the weight 0 (and 0
+ * times a value that is not finite is NaN); where all are -inf, all weights are 0 and lse is -inf.
+ * req_id and row_ends are what assign_slots writes.
+ *
+ * q          bf16 [rows, heads, dim]: row t, head h at q + t * ld_q + h * ld_qhead (elements).
+ * k_cache, v_cache  [cache_rows, kv_heads, dim] of dtype RTS_BF16 or RTS_E4M3: row r,
+ *            head j at + r * ld_cache + j * ld_head (elements).
+ * dim        64, 128 or 256.
+ * k_scales, v_scales  float [kv_heads] or NULL (= 1).
+ * window     positions seen at most, 0 for all.
+ * max_len    an upper bound of row_ends; it sets how the keys are split, results
+ *            hold for any value >= 0.
+ * scale      any number from -2^127 to 2^127, and so its products with k_scales.
+ * out        bf16 [rows, heads, dim], contiguous.   lse  float [rows, heads] or NULL.
+ * workspace  as in latent_attend_rows, kv_attend_paged_workspace_size bytes.
+ * q, the caches, out and their strides must be multiples of 16 bytes.
+ * Scores, softmax statistics and sums are held in 32 bits; the weights are
+ * rounded to bf16 for the products with the values.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 1024, cache_rows >= 2^31,
+ *         ld_cache > 2^30), RTS_EWORKSPACE, RTS_EHIP.
+ */
+size_t kv_attend_paged_workspace_size(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype,
+                                      int64_t max_len, int64_t window);
+int kv_attend_paged(const void* q, int64_t rows, int32_t heads, int64_t ld_q, int64_t ld_qhead, const void* k_cache,
+                    const void* v_cache, int dtype, int32_t kv_heads, int32_t dim, int64_t cache_rows,
+                    int64_t ld_cache, int64_t ld_head, const float* k_scales, const float* v_scales,
+                    const int32_t* req_id, const int32_t* row_ends, const int32_t* block_table, int64_t table_rows,
+                    int32_t table_cols, int64_t ld_table, int32_t block_size, int64_t stride_rows, int64_t window,
+                    int64_t max_len, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/*
+ * kv_attend_paged_plan -- how that call would be cut, to read a profile or to choose
+ * the sizes of a test by: plan[0] pieces of a row's keys at most, plan[1] keys of a
+ * piece.  split: whether the call has a workspace.  Host only; rows at least 1.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED as that call.
+ */
+int kv_attend_paged_plan(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
+                         int64_t window, int split, int64_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,7 +63,18 @@ _lib.latent_attend_paged_workspace_size.restype = _sz
 _lib.latent_attend_paged.argtypes = [_p, _i64, _i32, _i32, _i32, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _p,
                                      _p, _i32, _i64, _i32, _i64, _i64, _f32, _p, _p, _p, _sz, _p]
 _lib.merge_attend_rank_major.argtypes = [_p, ctypes.c_int, _p, _i32, _i64, _i32, _i32, _p, ctypes.c_int, _p, _p]
-for _f in (_lib.assign_slots, _lib.indexer_logits, _lib.indexer_logits_paged, _lib.latent_attend_rows,
+_lib.beam_select_workspace_size.argtypes = [ctypes.c_int, _i64, _i32, _i64, _i32]
+_lib.beam_select_workspace_size.restype = _sz
+_lib.beam_select.argtypes = [_p, ctypes.c_int, _i64, _i32, _i64, _i64, _p, _i32, _i32, _p, _p, _p, _p, _p, _sz, _p]
+_lib.fork_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _i64, _p, _p, _p, _i64, _p, _p]
+_lib.compact_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _i32, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p]
+_lib.copy_blocks.argtypes = [_p, _i32, _p, _i64, _i32, _i64, _p]
+_lib.kv_attend_paged_workspace_size.argtypes = [_i64, _i32, _i32, _i32, ctypes.c_int, _i64, _i64]
+_lib.kv_attend_paged_workspace_size.restype = _sz
+_lib.kv_attend_paged.argtypes = [_p, _i64, _i32, _i64, _i64, _p, _p, ctypes.c_int, _i32, _i32, _i64, _i64, _i64, _p, _p,
+                                 _p, _p, _p, _i64, _i32, _i64, _i32, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p]
+for _f in (_lib.beam_select, _lib.fork_blocks, _lib.compact_blocks, _lib.copy_blocks, _lib.kv_attend_paged,
+           _lib.assign_slots, _lib.indexer_logits, _lib.indexer_logits_paged, _lib.latent_attend_rows,
            _lib.latent_attend_paged, _lib.merge_attend_rank_major, _lib.topk_rows, _lib.topk_rows_noalloc, _lib.pack_candidates, _lib.merge_select_rank_major, _lib.pack_pairs,
            _lib.merge_select_pairs_rank_major, _lib.rescue_push, _lib.merge_rescue_rank_major,
            _lib.merge_select_row_major, _lib.merge_select_pairs_row_major, _lib.emit_rows,
@@ -79,6 +90,12 @@ class _KvRows(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("stride_rows", ctypes.c_int64),
                 ("rows_out", ctypes.c_void_p), ("out_cols", ctypes.c_int32),
                 ("valid_out", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    """rts_cache of include/row_top_select.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("row_bytes", ctypes.c_int64),
+                ("ld_bytes", ctypes.c_int64)]
 
 
 class RtsError(RuntimeError):
@@ -872,6 +889,258 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
             _FLOAT_DTYPES[parts.dtype], lse.data_ptr(), world, rows, heads, dim, out.data_ptr(),
             _FLOAT_DTYPES[out.dtype], out_lse.data_ptr())
     return out, out_lse
+
+
+class BeamStep(NamedTuple):
+    """What beam_select returns; see beam_select in the header."""
+    scores: torch.Tensor        # float32 [G, k]
+    parents: torch.Tensor       # int32 [G, k]
+    tokens: torch.Tensor        # int32 [G, k]
+    ended: torch.Tensor | None  # float32 [G, beams], None without an eos
+
+
+def beam_select_workspace_size(dtype, groups: int, beams: int, vocab: int, k: int) -> int:
+    dt = RTS_BF16 if dtype in (torch.bfloat16, RTS_BF16) else RTS_F32
+    return int(_lib.beam_select_workspace_size(dt, groups, beams, vocab, k))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int, eos: int = -1, out: BeamStep | None = None,
+                workspace="auto", stream=None) -> BeamStep:
+    """The k best continuations of each group's beams by ``scores`` [G, beams] plus the log-softmax of the beams'
+    ``logits`` [G * beams, vocab] (float32 or bfloat16), the token ``eos`` apart (-1: none); see beam_select in the
+    header.  ``workspace``: "auto" (allocated here) or a GPU tensor.  Without a backward pass: inputs that require
+    gradients are refused."""
+    _no_grad("beam_select", logits, scores)
+    device = _gpu(logits, "logits")
+    if logits.dtype not in _FLOAT_DTYPES:
+        raise TypeError("logits must be float32 or bfloat16")
+    rows, vocab, ld = _rows_ld(logits, "logits")
+    if scores.dtype != torch.float32 or scores.dim() != 2 or not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [G, beams]")
+    groups, beams = scores.shape
+    if groups * beams != rows:
+        raise ValueError("logits must have one row per score")
+    if not -0x80000000 <= k <= 0x7FFFFFFF or not -0x80000000 <= eos <= 0x7FFFFFFF:
+        raise _too_large("k and eos", 32)
+    _on(device, scores)
+    dt = _FLOAT_DTYPES[logits.dtype]
+    if out is None:
+        if k < 1 or beams < 1:
+            raise RtsError(RTS_EINVAL, "beam_select")
+        n = groups * k
+        flat = _new(3 * n + (rows if eos >= 0 else 0), torch.int32, device, stream)
+        out = BeamStep(flat[:n].view(torch.float32).view(groups, k), flat[n:2 * n].view(groups, k),
+                       flat[2 * n:3 * n].view(groups, k),
+                       flat[3 * n:].view(torch.float32).view(groups, beams) if eos >= 0 else None)
+    else:
+        for name, t, d in zip(BeamStep._fields, out, (torch.float32, torch.int32, torch.int32)):
+            _out(t, (groups, k), d, device, name, stream)
+        if eos >= 0:
+            _out(out.ended, (groups, beams), torch.float32, device, "ended", stream)
+        elif out.ended is not None:
+            raise ValueError("ended is written only with an eos")
+    if workspace is None:
+        raise ValueError('workspace must be "auto" or a GPU tensor')
+    ws, ws_bytes = _scratch(workspace, int(_lib.beam_select_workspace_size(dt, groups, beams, vocab, k))
+                            if isinstance(workspace, str) else 0, device, stream)
+    _launch(_lib.beam_select, "beam_select", device, stream, logits.data_ptr(), dt, groups, beams, vocab, ld,
+            scores.data_ptr(), k, eos, out.scores.data_ptr(), out.parents.data_ptr(), out.tokens.data_ptr(),
+            _ptr(out.ended), _ptr(ws), ws_bytes)
+    return out
+
+
+class Fork(NamedTuple):
+    """What fork_blocks returns, int32 each; see fork_blocks in the header."""
+    block_table: torch.Tensor  # [rows, B_max]
+    ctx_lens: torch.Tensor     # [rows]
+    copies: torch.Tensor       # [rows, 2]: pairs for copy_blocks, then -1
+    free_blocks: torch.Tensor  # [n_free]: a list for assign_slots, then -1
+    counts: torch.Tensor       # [2]: free blocks, blocks wanted
+
+
+class Compaction(NamedTuple):
+    """What compact_blocks returns, int32 each; see compact_blocks in the header."""
+    block_table: torch.Tensor  # [rows, B_max]
+    moves: torch.Tensor        # [max_moves, 2]: pairs for copy_blocks, then -1
+    free_blocks: torch.Tensor  # [n_free], then -1
+    counts: torch.Tensor       # [2]: free blocks, moves in all
+
+
+def _pool(pool_blocks: int, held, n_free, block_size: int):
+    """(n_free, pointer to held, block size) of a pool, checked."""
+    if not 0 <= pool_blocks <= 0x7FFFFFFF:
+        raise ValueError("pool_blocks must not be negative, and below 2^31")
+    if held is not None and (held.dtype not in (torch.bool, torch.uint8) or held.shape != (pool_blocks,) or
+                             not held.is_contiguous()):
+        raise ValueError(f"held must be a contiguous bool or uint8 vector of {pool_blocks} entries")
+    if n_free is None:
+        n_free = pool_blocks
+    if not 0 <= n_free < 2 ** 31:
+        raise ValueError("n_free must not be negative, and below 2^31")
+    return n_free, _ptr(held), _pages(block_size, None)[0]
+
+
+def _named_out(out, shapes, device, stream):
+    """The int32 outputs of a block call: a caller's, checked, or new ones from one allocation."""
+    for name, t, shape in zip(out._fields, out, shapes):
+        _out(t, shape, torch.int32, device, name, stream)
+    return out
+
+
+def _new_flat(kind, shapes, device, stream):
+    sizes, at, parts = [], 0, []
+    for shape in shapes:
+        n = 1
+        for d in shape:
+            n *= d
+        sizes.append((at, n, shape))
+        at += n + (n & 1)  # pairs start on 8 bytes
+    flat = _new(at, torch.int32, device, stream)
+    for a, n, shape in sizes:
+        parts.append(flat[a:a + n].view(shape))
+    return kind(*parts)
+
+
+def fork_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, parents: torch.Tensor, block_size: int,
+                pool_blocks: int, held: torch.Tensor | None = None, n_free: int | None = None,
+                out: Fork | None = None, stream=None) -> Fork:
+    """The block table whose row i continues row ``parents[i]`` of ``block_table`` (the parents of beam_select; -1:
+    an empty row), with fresh blocks where rows would write into the same one; see fork_blocks in the header.
+    ``copies`` are the caller's to make (copy_blocks).  ``n_free``: length of the list of free blocks (default: the
+    pool's)."""
+    device = _gpu(block_table, "block_table")
+    rows_in, cols, ld = _table(block_table)
+    if _int32_all(ctx_lens, "ctx_lens") != rows_in:
+        raise ValueError("ctx_lens must have one entry per row of block_table")
+    rows = _int32_all(parents, "parents")
+    n_free, held_ptr, block_size = _pool(pool_blocks, held, n_free, block_size)
+    _on(device, ctx_lens, parents, held)
+    shapes = ((rows, cols), (rows,), (rows, 2), (n_free,), (2,))
+    out = _new_flat(Fork, shapes, device, stream) if out is None else _named_out(out, shapes, device, stream)
+    _launch(_lib.fork_blocks, "fork_blocks", device, stream, block_table.data_ptr(), rows_in, cols, ld,
+            ctx_lens.data_ptr(), parents.data_ptr(), rows, block_size, pool_blocks, held_ptr,
+            out.block_table.data_ptr(), cols, out.ctx_lens.data_ptr(), out.copies.data_ptr(),
+            out.free_blocks.data_ptr(), n_free, out.counts.data_ptr())
+    return out
+
+
+def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size: int, pool_blocks: int,
+                   held: torch.Tensor | None = None, max_moves: int | None = None, n_free: int | None = None,
+                   out: Compaction | None = None, stream=None) -> Compaction:
+    """Moves (pairs for copy_blocks) that bring the blocks in use to the lowest ids, and the block table after
+    them; see compact_blocks in the header.  ``max_moves`` defaults to half of the pool, which is always enough."""
+    device = _gpu(block_table, "block_table")
+    rows, cols, ld = _table(block_table)
+    if _int32_all(ctx_lens, "ctx_lens") != rows:
+        raise ValueError("ctx_lens must have one entry per row of block_table")
+    n_free, held_ptr, block_size = _pool(pool_blocks, held, n_free, block_size)
+    if max_moves is None:
+        max_moves = pool_blocks // 2
+    if not 0 <= max_moves < 2 ** 31:
+        raise ValueError("max_moves must not be negative, and below 2^31")
+    _on(device, ctx_lens, held)
+    shapes = ((rows, cols), (max_moves, 2), (n_free,), (2,))
+    out = _new_flat(Compaction, shapes, device, stream) if out is None else _named_out(out, shapes, device, stream)
+    _launch(_lib.compact_blocks, "compact_blocks", device, stream, block_table.data_ptr(), rows, cols, ld,
+            ctx_lens.data_ptr(), block_size, pool_blocks, held_ptr, out.block_table.data_ptr(), cols,
+            out.moves.data_ptr(), max_moves, out.free_blocks.data_ptr(), n_free, out.counts.data_ptr())
+    return out
+
+
+def copy_blocks(caches, pairs: torch.Tensor, block_size: int, stride_rows: int | None = None, stream=None) -> None:
+    """Copies blocks within each of ``caches`` (tensors [cache_rows, ...] of any type, a row contiguous) by the
+    ``pairs`` int32 [n, 2] of (from, to), -1 skipped, in place; see copy_blocks in the header.  ``stride_rows``
+    defaults to ``block_size``."""
+    device = _gpu(pairs, "pairs")
+    if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or not pairs.is_contiguous():
+        raise ValueError("pairs must be contiguous int32 [n, 2]")
+    pages = _pages(block_size, stride_rows)
+    _on(device, *caches)
+    _no_grad("copy_blocks", *caches)
+    described = []
+    for t in caches:
+        if t.dim() < 1:
+            raise ValueError("a cache must be [cache_rows, ...]")
+        n, esz = 1, t.element_size()
+        for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            if size != 1 and step != n:
+                raise ValueError("a cache's rows must be contiguous")
+            n *= size
+        ld = t.stride(0) if t.shape[0] > 1 else n
+        if ld < n:
+            raise ValueError("a cache's rows must not overlap")
+        if n > 0:
+            described.append((t.data_ptr(), t.shape[0], n * esz, ld * esz))
+    n_pairs, where = pairs.shape[0], pairs.data_ptr()
+    for at in range(0, len(described), 64):
+        some = described[at:at + 64]
+        _launch(_lib.copy_blocks, "copy_blocks", device, stream, (_Cache * len(some))(*some), len(some), where, n_pairs,
+                *pages)
+
+
+def kv_attend_paged_workspace_size(dtype, rows: int, heads: int, kv_heads: int, dim: int, max_len: int,
+                                   window: int = 0) -> int:
+    dt = RTS_E4M3 if dtype in (torch.float8_e4m3fn, RTS_E4M3) else RTS_BF16
+    return int(_lib.kv_attend_paged_workspace_size(rows, heads, kv_heads, dim, dt, max_len, window))
+
+
+def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, req_id: torch.Tensor,
+                    row_ends: torch.Tensor, block_table: torch.Tensor, block_size: int, scale: float,
+                    k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None, window: int = 0,
+                    stride_rows: int | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace="auto", stream=None):
+    """Attention of new tokens ``q`` [rows, heads, dim] over their requests' paged ``k_cache`` and ``v_cache``
+    [cache_rows, kv_heads, dim] (bfloat16, or float8_e4m3fn with ``k_scales`` and ``v_scales`` [kv_heads]), a token
+    seeing the positions below its ``row_ends``, the last ``window`` of them where that is not 0; ``req_id`` and
+    ``row_ends`` as assign_slots writes them.  ``max_len`` bounds row_ends and only steers the split (default: what
+    the table holds).  Returns (out, lse); see kv_attend_paged in the header.  ``workspace`` as in topk_rows.
+    Without a backward pass: inputs that require gradients are refused."""
+    _no_grad("kv_attend_paged", q, k_cache, v_cache, k_scales, v_scales)
+    device = _gpu(q, "q")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if k_cache.dtype not in _INDEX_DTYPES or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
+    if q.dim() != 3 or k_cache.dim() != 3 or q.stride(2) != 1 or k_cache.stride(2) != 1:
+        raise ValueError("q must be [rows, heads, dim], the caches [cache_rows, kv_heads, dim], with unit element stride")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    (rows, heads, dim), (ld_q, ld_qhead, _) = q.shape, q.stride()
+    (cache_rows, kv_heads, cdim), (ld_cache, ld_head, _) = k_cache.shape, k_cache.stride()
+    if cdim != dim:
+        raise ValueError("q and the caches must have the same last dimension")
+    if heads > 0x7FFFFFFF or dim > 0x7FFFFFFF:
+        raise _too_large("the sizes of q", 32)
+    if kv_heads < 1 or heads % kv_heads != 0:
+        raise ValueError("heads must be a multiple of kv_heads")
+    ld_qhead = ld_qhead if heads > 1 else dim
+    ld_q = ld_q if rows > 1 else heads * dim
+    ld_head = ld_head if kv_heads > 1 else dim
+    ld_cache = ld_cache if cache_rows > 1 else kv_heads * dim
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (kv_heads,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 vector of {kv_heads} entries")
+    req_id, row_ends = _int32_vec(req_id, rows, "req_id"), _int32_vec(row_ends, rows, "row_ends")
+    if req_id is None or row_ends is None:
+        raise ValueError("req_id and row_ends are required")
+    table_rows, table_cols, ld_table = _table(block_table)
+    pages = _pages(block_size, stride_rows)
+    if max_len is None:
+        max_len = table_cols * block_size
+    if not 0 <= window < 2 ** 63 or max_len >= 2 ** 63:
+        raise ValueError("window must not be negative, and window and max_len below 2^63")
+    out = _out(out, (rows, heads, dim), torch.bfloat16, device, "out", stream)
+    lse = _out(lse, (rows, heads), torch.float32, device, "lse", stream)
+    _on(device, k_cache, v_cache, k_scales, v_scales, req_id, row_ends, block_table)
+    dt = _INDEX_DTYPES[k_cache.dtype]
+    ws, ws_bytes = _scratch(workspace,
+                            int(_lib.kv_attend_paged_workspace_size(rows, heads, kv_heads, dim, dt, max_len, window))
+                            if isinstance(workspace, str) else 0, device, stream)
+    _launch(_lib.kv_attend_paged, "kv_attend_paged", device, stream, q.data_ptr(), rows, heads, ld_q, ld_qhead,
+            k_cache.data_ptr(), v_cache.data_ptr(), dt, kv_heads, dim, cache_rows, ld_cache, ld_head, _ptr(k_scales),
+            _ptr(v_scales), req_id.data_ptr(), row_ends.data_ptr(), block_table.data_ptr(), table_rows, table_cols,
+            ld_table, *pages, window, max_len, scale, out.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes)
+    return out, lse
 
 
 def raw_library() -> ctypes.CDLL:

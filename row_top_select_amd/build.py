@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librow_top_select.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["rts_api.cpp", "rts_topk_rows.hip", "rts_merge.hip", "rts_slots.hip",
-           "rts_indexer.hip", "rts_latent.hip"]
+           "rts_indexer.hip", "rts_latent.hip", "rts_blocks.hip", "rts_beam.hip", "rts_kv.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -36,7 +36,7 @@ COMMON = [
 # 16 of scores, push sums out to scratch (with it the widest one over listed rows
 # still keeps one other register there).
 _VECTOR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA = {"rts_latent.hip": _VECTOR_RESULTS, "rts_indexer.hip": _VECTOR_RESULTS}
+EXTRA = {"rts_latent.hip": _VECTOR_RESULTS, "rts_indexer.hip": _VECTOR_RESULTS, "rts_kv.hip": _VECTOR_RESULTS}
 
 
 def _compile(src: str) -> str:

@@ -487,4 +487,187 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
                                     nullptr, false, stream);
 }
 
+namespace {
+int beam_args(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k) {
+    if ((dtype != RTS_F32 && dtype != RTS_BF16) || groups < 0 || beams < 1 || vocab < 1 || k < 1) return RTS_EINVAL;
+    if (beams > rts::kMaxBeams || k > rts::kMaxBeamK || vocab > 0x7FFFFFFFll || groups > 0x7FFFFFFFll / beams)
+        return RTS_EUNSUPPORTED;
+    return RTS_OK;
+}
+}  // namespace
+
+size_t beam_select_workspace_size(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k) {
+    if (beam_args(dtype, groups, beams, vocab, k) != RTS_OK || groups == 0) return 0;
+    return rts::plan_beam_select(dtype, groups, beams, vocab, k).ws_bytes;
+}
+
+int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, int64_t vocab, int64_t ld_logits,
+                const float* scores, int32_t k, int32_t eos, float* out_scores, int32_t* parents, int32_t* tokens,
+                float* ended, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const int rc = beam_args(dtype, groups, beams, vocab, k);
+    if (rc == RTS_EINVAL || ld_logits < vocab || eos < -1 || eos >= vocab)
+        return RTS_EINVAL;
+    if (rc != RTS_OK) return rc;
+    if (groups == 0) return RTS_OK;
+    if (!logits || !scores || !out_scores || !parents || !tokens || !workspace || (eos < 0) != (ended == nullptr))
+        return RTS_EINVAL;
+    if (!aligned(logits, dtype == RTS_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
+        !aligned(parents, 4) || !aligned(tokens, 4) || !aligned(ended, 4) || !aligned(workspace, 16))
+        return RTS_EINVAL;
+    const rts::BeamPlan plan = rts::plan_beam_select(dtype, groups, beams, vocab, k);
+    if (workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
+    if (groups * beams * plan.pieces > rts::kMaxThreads / 64 - 4 || groups > rts::kMaxThreads / 256)
+        return RTS_EUNSUPPORTED;
+    rts::BeamArgs a{};
+    a.logits = logits, a.scores = scores, a.out_scores = out_scores, a.ended = ended, a.parents = parents;
+    a.tokens = tokens, a.groups = groups, a.vocab = vocab, a.ld = ld_logits, a.beams = beams, a.k = k, a.eos = eos;
+    a.dtype = dtype;
+    return rts::launch_beam_select(a, plan, workspace, stream);
+}
+
+int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols, int64_t ld_table,
+                const int32_t* ctx_lens, const int32_t* parents, int64_t rows_out, int32_t block_size,
+                int32_t pool_blocks, const uint8_t* held, int32_t* out_table, int64_t ld_out, int32_t* out_lens,
+                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, hipStream_t stream) {
+    if (rows_in < 0 || table_cols < 0 || ld_table < table_cols || rows_out < 0 || block_size < 1 ||
+        pool_blocks < 0 || ld_out < table_cols || n_free < 0)
+        return RTS_EINVAL;
+    if (rows_in > rts::kMaxForkRows || rows_out > rts::kMaxForkRows || pool_blocks > rts::kMaxPool)
+        return RTS_EUNSUPPORTED;
+    if (!counts || (rows_in > 0 && !ctx_lens) || (rows_in > 0 && table_cols > 0 && !block_table) ||
+        (rows_out > 0 && (!parents || !out_lens || !copies)) || (rows_out > 0 && table_cols > 0 && !out_table) ||
+        (n_free > 0 && !free_blocks))
+        return RTS_EINVAL;
+    if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(parents, 4) || !aligned(out_table, 4) ||
+        !aligned(out_lens, 4) || !aligned(copies, 8) || !aligned(free_blocks, 4) || !aligned(counts, 4))
+        return RTS_EINVAL;
+    rts::ForkArgs a{};
+    a.table = block_table, a.ctx_lens = ctx_lens, a.parents = parents, a.held = held, a.out_table = out_table;
+    a.out_ctx = out_lens, a.copies = copies, a.free_blocks = free_blocks, a.counts = counts, a.rows_in = rows_in;
+    a.ld_table = ld_table, a.rows_out = rows_out, a.ld_out = ld_out, a.n_free = n_free, a.cols = table_cols;
+    a.block_size = block_size, a.pool = pool_blocks;
+    return rts::launch_fork_blocks(a, stream);
+}
+
+int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols, int64_t ld_table,
+                   const int32_t* ctx_lens, int32_t block_size, int32_t pool_blocks, const uint8_t* held,
+                   int32_t* out_table, int64_t ld_out, int32_t* moves, int64_t max_moves, int32_t* free_blocks,
+                   int64_t n_free, int32_t* counts, hipStream_t stream) {
+    if (rows < 0 || table_cols < 0 || ld_table < table_cols || block_size < 1 || pool_blocks < 0 ||
+        ld_out < table_cols || max_moves < 0 || n_free < 0)
+        return RTS_EINVAL;
+    if (rows > 0x7FFFFFFFll || pool_blocks > rts::kMaxPool) return RTS_EUNSUPPORTED;
+    if (!counts || (rows > 0 && !ctx_lens) || (rows > 0 && table_cols > 0 && (!block_table || !out_table)) ||
+        (max_moves > 0 && !moves) || (n_free > 0 && !free_blocks))
+        return RTS_EINVAL;
+    if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(out_table, 4) || !aligned(moves, 8) ||
+        !aligned(free_blocks, 4) || !aligned(counts, 4))
+        return RTS_EINVAL;
+    rts::CompactArgs a{};
+    a.table = block_table, a.ctx_lens = ctx_lens, a.held = held, a.out_table = out_table, a.moves = moves;
+    a.free_blocks = free_blocks, a.counts = counts, a.rows = rows, a.ld_table = ld_table, a.ld_out = ld_out;
+    a.n_free = n_free, a.max_moves = max_moves, a.cols = table_cols, a.block_size = block_size, a.pool = pool_blocks;
+    return rts::launch_compact_blocks(a, stream);
+}
+
+int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs, int64_t n_pairs, int32_t block_size,
+                int64_t stride_rows, hipStream_t stream) {
+    if (n_caches < 0 || n_pairs < 0 || block_size < 1 || stride_rows < 0 || (n_caches > 0 && !caches))
+        return RTS_EINVAL;
+    if (n_caches > rts::kMaxCopyCaches || n_pairs > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
+    if (n_pairs > 0 && (!pairs || !aligned(pairs, 8))) return RTS_EINVAL;
+    rts::CopyArgs a{};
+    a.pairs = pairs, a.n_pairs = n_pairs, a.block_size = block_size;
+    // A cache has fewer than 2^31 rows: with a stride of 2^31 or more only block 0 has any.
+    a.stride_rows = stride_rows < (1ll << 31) ? stride_rows : 1ll << 31;
+    for (int32_t i = 0; i < n_caches; ++i) {
+        const rts_cache& from = caches[i];
+        if (from.rows < 0 || from.row_bytes < 1 || from.ld_bytes < from.row_bytes || (from.rows > 0 && !from.data))
+            return RTS_EINVAL;
+        if (from.rows > 0x7FFFFFFFll || from.row_bytes > 0x7FFFFFFFll || from.ld_bytes > 0x7FFFFFFFll)
+            return RTS_EUNSUPPORTED;
+        const bool one = from.ld_bytes == from.row_bytes;
+        const int64_t bytes = one ? from.row_bytes * block_size : from.row_bytes;
+        const uintptr_t all = reinterpret_cast<uintptr_t>(from.data) | (uintptr_t)from.ld_bytes | (uintptr_t)from.row_bytes;
+        rts::CopyCache& to = a.cache[a.n_caches];
+        to.data = static_cast<char*>(from.data), to.rows = from.rows, to.ld = from.ld_bytes;
+        to.word = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+        to.row_words = bytes / to.word;
+        to.words = from.row_bytes / to.word * block_size;
+        if (from.rows >= block_size) ++a.n_caches;  // else no block lies in it
+    }
+    if (a.n_caches == 0 || n_pairs == 0) return RTS_OK;
+    return rts::launch_copy_blocks(a, stream);
+}
+
+namespace {
+int kv_args(const rts::KvArgs& a) {
+    if (a.dtype != RTS_BF16 && a.dtype != RTS_E4M3) return RTS_EINVAL;
+    if (a.rows < 0 || a.heads < 1 || a.kv_heads < 1 || a.heads % a.kv_heads != 0 || a.dim < 1 || a.cache_rows < 0 ||
+        a.window < 0 || a.max_len < 0)
+        return RTS_EINVAL;
+    if (a.ld_q < 0 || a.ld_qhead < a.dim || a.ld_cache < 0 || a.ld_head < a.dim || !(std::fabs(a.scale) <= 0x1p127f))
+        return RTS_EINVAL;
+    if ((a.dim != 64 && a.dim != 128 && a.dim != 256) || a.heads > 1024 || a.rows > 0x7FFFFFFFll / a.heads ||
+        a.cache_rows > 0x7FFFFFFFll || a.ld_cache > (1ll << 30) || a.ld_head > (1ll << 40))
+        return RTS_EUNSUPPORTED;
+    if (a.rows == 0) return RTS_OK;
+    const int64_t unit = a.dtype == RTS_E4M3 ? 16 : 8;  // elements of 16 bytes
+    if (!a.q || !a.out || !a.req_id || !a.row_ends || (a.cache_rows > 0 && (!a.k || !a.v))) return RTS_EINVAL;
+    if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) || !aligned(a.lse, 4) ||
+        !aligned(a.k_scales, 4) || !aligned(a.v_scales, 4) || !aligned(a.req_id, 4) || !aligned(a.row_ends, 4) ||
+        a.ld_q % 8 != 0 || a.ld_qhead % 8 != 0 || a.ld_cache % unit != 0 || a.ld_head % unit != 0)
+        return RTS_EINVAL;
+    return RTS_OK;
+}
+int64_t kv_longest(int64_t max_len, int64_t window) { return window > 0 && window < max_len ? window : max_len; }
+}  // namespace
+
+size_t kv_attend_paged_workspace_size(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype,
+                                      int64_t max_len, int64_t window) {
+    if (rows < 1 || heads < 1 || heads > 1024 || kv_heads < 1 || heads % kv_heads != 0 || rows > 0x7FFFFFFFll / heads ||
+        (dim != 64 && dim != 128 && dim != 256) || (dtype != RTS_BF16 && dtype != RTS_E4M3) || max_len < 0 || window < 0)
+        return 0;
+    return rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), true).ws_bytes;
+}
+
+int kv_attend_paged_plan(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
+                         int64_t window, int split, int64_t* plan) {
+    if (rows < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dtype != RTS_BF16 && dtype != RTS_E4M3) ||
+        max_len < 0 || window < 0 || !plan)
+        return RTS_EINVAL;
+    if (heads > 1024 || rows > 0x7FFFFFFFll / heads || (dim != 64 && dim != 128 && dim != 256)) return RTS_EUNSUPPORTED;
+    const rts::KvPlan p = rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), split != 0);
+    plan[0] = p.splits, plan[1] = p.piece;
+    return RTS_OK;
+}
+
+int kv_attend_paged(const void* q, int64_t rows, int32_t heads, int64_t ld_q, int64_t ld_qhead, const void* k_cache,
+                    const void* v_cache, int dtype, int32_t kv_heads, int32_t dim, int64_t cache_rows,
+                    int64_t ld_cache, int64_t ld_head, const float* k_scales, const float* v_scales,
+                    const int32_t* req_id, const int32_t* row_ends, const int32_t* block_table, int64_t table_rows,
+                    int32_t table_cols, int64_t ld_table, int32_t block_size, int64_t stride_rows, int64_t window,
+                    int64_t max_len, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream) {
+    rts::KvArgs a{};
+    a.q = static_cast<const uint16_t*>(q), a.k = k_cache, a.v = v_cache, a.k_scales = k_scales, a.v_scales = v_scales;
+    a.out = static_cast<uint16_t*>(out), a.lse = lse, a.req_id = req_id, a.row_ends = row_ends, a.rows = rows;
+    a.ld_q = ld_q, a.ld_qhead = ld_qhead, a.cache_rows = cache_rows, a.ld_cache = ld_cache, a.ld_head = ld_head;
+    a.window = window, a.max_len = max_len, a.heads = heads, a.kv_heads = kv_heads, a.dim = dim, a.dtype = dtype;
+    a.scale = scale;
+    int rc = kv_args(a);
+    if (rc != RTS_OK) return rc;
+    rc = pages_args(block_table, table_rows, table_cols, ld_table, block_size, stride_rows, cache_rows);
+    if (rc != RTS_OK) return rc;
+    if (workspace_bytes > 0 && !workspace) return RTS_EINVAL;
+    if (table_rows > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
+    if (rows == 0) return RTS_OK;
+    a.pages = rts::make_pages(block_table, table_rows, table_cols, ld_table, block_size, stride_rows, cache_rows);
+    const rts::KvPlan plan =
+        rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), workspace != nullptr);
+    if (workspace && workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
+    if (workspace && !aligned(workspace, 16)) return RTS_EINVAL;
+    return rts::launch_kv_attend(a, plan, workspace, stream);
+}
+
 }  // extern "C"

@@ -170,4 +170,89 @@ int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int
                         int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
                         const int32_t* row_limit, bool pieces, hipStream_t stream);
 
+// ------------------------------------------------------------ a beam-search step
+
+constexpr int kMaxBeams = 64;
+constexpr int kMaxBeamK = 64;
+
+struct BeamArgs {
+    const void* logits;
+    const float* scores;
+    float *out_scores, *ended;   // ended: or nullptr
+    int32_t *parents, *tokens;
+    int64_t groups, vocab, ld;   // ld in elements
+    int32_t beams, k, eos;       // eos: -1 for none
+    int dtype;
+};
+
+// How a call is cut: `pieces` of a row, each of `chunks` chunks of a wave's loads.
+struct BeamPlan {
+    int64_t pieces;
+    int chunks;
+    size_t ws_bytes;
+};
+BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k);
+int launch_beam_select(const BeamArgs& a, const BeamPlan& plan, void* workspace, hipStream_t stream);
+
+// The block calls hold two bits a block of the pool, and fork_blocks two words a row, in LDS.
+constexpr int32_t kMaxPool = 1 << 19;
+constexpr int64_t kMaxForkRows = 4096;
+
+struct ForkArgs {
+    const int32_t *table, *ctx_lens, *parents;
+    const uint8_t* held;  // or nullptr
+    int32_t *out_table, *out_ctx, *copies, *free_blocks, *counts;
+    int64_t rows_in, ld_table, rows_out, ld_out, n_free;
+    int32_t cols, block_size, pool;
+};
+int launch_fork_blocks(const ForkArgs& a, hipStream_t stream);
+
+struct CompactArgs {
+    const int32_t *table, *ctx_lens;
+    const uint8_t* held;  // or nullptr
+    int32_t *out_table, *moves, *free_blocks, *counts;
+    int64_t rows, ld_table, ld_out, n_free, max_moves;
+    int32_t cols, block_size, pool;
+};
+int launch_compact_blocks(const CompactArgs& a, hipStream_t stream);
+
+constexpr int kMaxCopyCaches = 64;  // they travel as kernel arguments
+struct CopyCache {
+    char* data;
+    int64_t rows, ld;          // ld in bytes
+    int64_t words, row_words;  // of `word` bytes: of a block, and of a row (as many as a block's where rows follow each other)
+    int64_t slice0;            // set by the launch
+    int32_t word;
+};
+struct CopyArgs {
+    const int32_t* pairs;
+    int64_t n_pairs, stride_rows, slices;
+    int32_t n_caches, block_size;
+    CopyCache cache[kMaxCopyCaches];
+};
+int launch_copy_blocks(CopyArgs& a, hipStream_t stream);
+
+struct KvArgs {
+    const uint16_t* q;
+    const void *k, *v;
+    const float *k_scales, *v_scales;  // a kv head, or nullptr
+    uint16_t* out;
+    float* lse;  // or nullptr
+    const int32_t *req_id, *row_ends;
+    int64_t rows, ld_q, ld_qhead, cache_rows, ld_cache, ld_head, window, max_len;  // window: 0 for none
+    int32_t heads, kv_heads, dim;
+    int dtype;
+    float scale;
+    Pages pages;
+};
+
+struct KvPlan {
+    int splits;   // pieces of a row's keys, joined by a second kernel when > 1
+    int64_t piece;  // keys of a piece
+    size_t ws_bytes;
+};
+KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
+                      bool allow_split);
+int launch_kv_attend(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t stream);
+
 }  // namespace rts
