@@ -557,9 +557,9 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * the logits x of row i * beams + b; token v continues it with the value
  *   value(b, v) = scores[i, b] + x[v] - lse,   lse = log sum_v exp x[v]
  * and each group keeps the k best of all its beams' tokens.  Order: value
- * desc (in 64 bits, so that beams are told apart below the last bit of a
- * 32-bit score), then beam asc, then logit desc, token asc; within a beam it
- * is that of its logits.
+ * desc (in 64 bits, to 2^-40 of its size, so that beams are told apart below the
+ * last bit of a 32-bit score), then beam asc, then logit desc, token asc; within
+ * a beam it is that of its logits.
  *
  * Not candidates: the token eos, tokens with a logit of -inf, beams whose score
  * is not finite (-inf marks a beam that is not in use, such as all but the

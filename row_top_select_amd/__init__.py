@@ -927,11 +927,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int, eos: int = -
     if out is None:
         if k < 1 or beams < 1:
             raise RtsError(RTS_EINVAL, "beam_select")
-        n = groups * k
-        flat = _new(3 * n + (rows if eos >= 0 else 0), torch.int32, device, stream)
-        out = BeamStep(flat[:n].view(torch.float32).view(groups, k), flat[n:2 * n].view(groups, k),
-                       flat[2 * n:3 * n].view(groups, k),
-                       flat[3 * n:].view(torch.float32).view(groups, beams) if eos >= 0 else None)
+        best, parents, tokens = _new((3, groups, k), torch.int32, device, stream).unbind(0)
+        out = BeamStep(best.view(torch.float32), parents, tokens,
+                       _new((groups, beams), torch.float32, device, stream) if eos >= 0 else None)
     else:
         for name, t, d in zip(BeamStep._fields, out, (torch.float32, torch.int32, torch.int32)):
             _out(t, (groups, k), d, device, name, stream)

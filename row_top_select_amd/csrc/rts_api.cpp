@@ -516,7 +516,7 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
         return RTS_EINVAL;
     const rts::BeamPlan plan = rts::plan_beam_select(dtype, groups, beams, vocab, k);
     if (workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
-    if (groups * beams * plan.pieces > rts::kMaxThreads / 64 - 4 || groups > rts::kMaxThreads / 256)
+    if (groups * beams * plan.pieces > rts::kMaxThreads / 256 || groups > rts::kMaxThreads / 1024)
         return RTS_EUNSUPPORTED;
     rts::BeamArgs a{};
     a.logits = logits, a.scores = scores, a.out_scores = out_scores, a.ended = ended, a.parents = parents;

@@ -4,13 +4,14 @@
 //   s_b + x_b[v] - lse_b,   lse_b = log sum_v exp x_b[v]
 // in two launches.
 //
-// 1. A wave streams a piece of a row once, in chunks of 512 elements, with the
-//    running maximum and sum of the softmax.  A row's order is that of its logits
-//    whatever lse_b is, so the piece's k best are found beside it without it: the
-//    wave keeps every lane's and every chunk's maximum.  At least k elements reach
-//    the k-th largest of the 64 lanes' maxima, so only chunks whose maximum reaches it can
-//    hold one of the k best: they are read once more (a few, from the caches)
-//    and what reaches the bound is sorted, 64 at a time, into a list of k.
+// 1. The four waves of a workgroup stream a row (or a piece of one), each every
+//    fourth group of 4 KB, with a running maximum and sum of the softmax.  A
+//    row's order is that of its logits whatever lse_b is, so its k best are
+//    collected beside it: at least j elements of a wave reach the j-th largest of its 64
+//    lanes' maxima, so the k best reach that of j = k, and the least of the four
+//    waves' with j = k / 4.  Few elements reach this bound once some groups have
+//    passed (k / n of the n-th element's kind); they are kept in LDS, and the
+//    waves' lists are sorted and merged at the end.
 // 2. A workgroup a group joins its rows' pieces and ranks the rows' candidates
 //    against each other by their values in 64 bits.
 #include <type_traits>
@@ -21,16 +22,30 @@
 
 namespace rts {
 
-constexpr int kBeamBlock = 256;
-constexpr int kBeamWaves = kBeamBlock / kWave;
+constexpr int kBeamWaves = 4;
+constexpr int kBeamBlock = kBeamWaves * kWave;
 constexpr int kChunk = 512;       // elements: 8 a lane
-constexpr int kMaxChunks = 64;    // of a piece: a lane keeps one's maximum
+template <typename T>
+constexpr int group_chunks() { return 8 / (int)sizeof(T); }  // that a wave loads at a time: 4 KB
+template <typename T>
+constexpr int group_elements() { return kChunk * group_chunks<T>(); }
+constexpr int kStaged = 1024;     // candidates that a wave holds
+constexpr int kMaxJoinWaves = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = -3.402823466e38f;  // the lowest finite number
 
+// A wave's part of a row's sum: sum e^ref.
 struct PieceStat {
-    float m, sum;
+    double ref, sum;
 };
+
+template <typename Op>
+__device__ __forceinline__ double wave_reduce(double x, Op op) {
+    const uint64_t r = wave_reduce64((uint64_t)__double_as_longlong(x), [&](uint64_t a, uint64_t b) {
+        return (uint64_t)__double_as_longlong(op(__longlong_as_double((long long)a), __longlong_as_double((long long)b)));
+    });
+    return __longlong_as_double((long long)r);
+}
 
 __device__ __forceinline__ float wave_max(float x) {
     auto step = [](float a, uint32_t b) { return fmaxf(a, __uint_as_float(b)); };
@@ -90,23 +105,17 @@ struct RowReader {
         }
         return r;
     }
-    // The last chunk: what lies behind the row is -inf.
+    // The last chunks: what lies behind the row is -inf.
     __device__ __forceinline__ void load_edge(int64_t c, float (&v)[8]) const {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int64_t at = element(c, e);
-            v[e] = -INFINITY;
-            if (at < vocab) {
-                if constexpr (sizeof(T) == 4) v[e] = row[at];
-                else v[e] = __uint_as_float((uint32_t)row[at] << 16);
-            }
+            const T x = row[at < vocab ? at : vocab - 1];
+            float f;
+            if constexpr (sizeof(T) == 4) f = x;
+            else f = __uint_as_float((uint32_t)x << 16);
+            v[e] = at < vocab ? f : -INFINITY;
         }
-    }
-    __device__ __forceinline__ void load_any(int64_t c, float (&v)[8]) const {
-        if (!inside(c)) return load_edge(c, v);
-        const Chunk8<T> x = load(c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = x.get(e);
     }
 };
 
@@ -120,216 +129,314 @@ __device__ __forceinline__ void merge_sorted(uint64_t& best, uint64_t more) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64_t pieces, int chunks,
+__global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64_t piece_groups,
                                                                uint64_t* __restrict__ lists,
                                                                PieceStat* __restrict__ stats) {
-    __shared__ uint64_t stage_memory[kBeamWaves][2 * kWave];
+    constexpr int kGroup = group_chunks<T>();
+    __shared__ uint64_t stage_memory[kBeamWaves][kStaged];
+    __shared__ __align__(16) float published[kBeamWaves];  // a bound that enough of the wave's elements reach
+    __shared__ int kept_by[kBeamWaves];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t unit = (int64_t)blockIdx.x * kBeamWaves + wave;
-    const int64_t rows = a.groups * a.beams;
-    if (unit >= rows * pieces) return;
-    const int64_t r = unit / pieces, piece = unit - r * pieces;
+    const int64_t r = blockIdx.x, unit = r * gridDim.y + blockIdx.y;
     const RowReader<T> in{static_cast<const T*>(a.logits) + r * a.ld, a.vocab};
-    const int64_t c0 = piece * chunks, all = (a.vocab + kChunk - 1) / kChunk;
-    const int n = (int)(all - c0 < chunks ? all - c0 : chunks);
-
-    float m = kLeast, sum = 0.f, lane_most = -INFINITY, chunk_most = -INFINITY;
-    auto take = [&](const float (&v)[8], int i) {
-        float top = v[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
-        lane_most = fmaxf(lane_most, top);
-        const float most = wave_max(top);
-        if (lane == i) chunk_most = most;
-        if (most > m) {
-            sum *= __builtin_amdgcn_exp2f((m - most) * kLog2e);
-            m = most;
-        }
-        // The differences are taken first: a rounded m log2(e) would be the same
-        // error in every term of a row.
-        float part = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) part += __builtin_amdgcn_exp2f((v[e] - m) * kLog2e);
-        sum += part;
-    };
-    constexpr int kAhead = 4;
-    for (int i = 0; i < n; i += kAhead) {
-        if (i + kAhead <= n && in.inside(c0 + i + kAhead - 1)) {
-            Chunk8<T> x[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) x[u] = in.load(c0 + i + u);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = x[u].get(e);
-                take(v, i + u);
-            }
-        } else {
-            for (int u = i; u < n && u < i + kAhead; ++u) {
-                float v[8];
-                in.load_any(c0 + u, v);
-                take(v, u);
-            }
-        }
-    }
-    {
-        double total = sum;
-        for (int d = 1; d < kWave; d <<= 1) total += __shfl_xor(total, d);
-        if (lane == 0) stats[unit] = PieceStat{m, (float)total};
-    }
+    const int64_t g0 = blockIdx.y * piece_groups, all = (a.vocab + group_elements<T>() - 1) / group_elements<T>();
+    const int64_t in_piece = all - g0 < piece_groups ? all - g0 : piece_groups;
+    const int busy = in_piece < kBeamWaves ? (int)in_piece : kBeamWaves;  // waves that have a group
+    const int64_t n = (in_piece - wave + kBeamWaves - 1) / kBeamWaves;    // this wave's
 
     // One more than k where the end token may be among them.
-    const int need = a.k + (a.eos >= 0 ? 1 : 0);
-    uint32_t key[1] = {key32_of_bits(__float_as_uint(lane_most))};
-    wave_bitonic_sort<1, true>(key);
-    // -inf is no candidate.
-    float bound = kLeast;
-    if (need <= kWave)
-        bound = fmaxf(bound, float_of_key32(__builtin_amdgcn_readlane(key[0], need <= kWave ? need - 1 : 0)));
-    uint64_t best = 0;
+    const int need = a.k + (a.eos >= 0 ? 1 : 0), share = (need + busy - 1) / busy;
+    if (threadIdx.x < kBeamWaves) published[threadIdx.x] = (int)threadIdx.x < busy ? -INFINITY : INFINITY;
+    __syncthreads();
+
+    float m = kLeast, sum = 0.f, lane_most = -INFINITY;
+    // Terms are 2^(x log2(e) - c2) with c2 = m log2(e): its rounding does not
+    // matter, because c2 itself is what the sum is taken to be relative to.
+    // Where it could overflow (a maximum past 1e38) they are e^(x - m).
+    float c2;
+    bool huge;
+    auto set_reference = [&] {
+        c2 = fminf(fmaxf(m * kLog2e, kLeast), -kLeast);
+        huge = fabsf(m) > 1e38f;
+    };
+    set_reference();
+    float bound = kLeast;  // elements from here on are candidates; -inf is none
+    uint64_t best = 0;     // what was sorted, where the stage ran over
     uint64_t* const stage = stage_memory[wave];
     int held = 0;
-    bool ties = true;  // elements equal to the bound count (they lie before all that set it, or it is no element's)
-    auto flush = [&](int count) {  // the first `count` staged entries, 64 at most
+    bool best_any = false;
+    // Sorts the last 64 (or fewer) staged entries into the best.
+    auto flush = [&] {
+        const int count = held < kWave ? held : kWave;
+        held -= count;
         wave_lds_sync();
-        uint64_t v[1] = {lane < count ? stage[lane] : 0};
-        const uint64_t rest = stage[kWave + lane];
+        uint64_t v[1] = {lane < count ? stage[held + lane] : 0};
         wave_lds_sync();
-        stage[lane] = rest;
         wave_bitonic_sort<1, true>(v);
         merge_sorted(best, v[0]);
-        held -= count;
+        best_any = true;
     };
-    for (uint64_t left = __ballot(lane < n && chunk_most >= bound); left; left &= left - 1) {
-        const int i = __builtin_ctzll(left);
-        const float most = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(chunk_most), i));
-        if (ties ? most < bound : most <= bound) continue;
-        float v[8];
-        in.load_any(c0 + i, v);
+    auto raise = [&](float to) { bound = to > bound ? to : bound; };
+    // A bound that n of the lanes' maxima reach, and few more: their keys' common
+    // bits, then a bit a step.
+    auto reached_by = [&](int n) {
+        const uint32_t key = key32_of_bits(__float_as_uint(lane_most));
+        const uint32_t least = wave_min32(key), most = key32_of_bits(__float_as_uint(m));
+        if (n == kWave || least >= most) return float_of_key32(least);
+        int bit = 31 - __builtin_clz(least ^ most);
+        const int last = bit > 24 ? 16 : bit > 8 ? bit - 8 : 0;
+        uint32_t to = most & ~1u << bit;
+        for (; bit >= last; --bit) {
+            const uint32_t with = to | 1u << bit;
+            const int count = __popcll(__ballot(key >= with));
+            if (count >= n) to = with;
+            if (count == n) break;
+        }
+        return float_of_key32(to > least ? to : least);
+    };
+    auto refresh = [&] {
+        if (share > kWave) return;
+        const float x = reached_by(share);
+        if (lane == 0) __hip_atomic_store(&published[wave], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    };
+    auto heed = [&] {  // the other waves
+        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        const f32x4 p = *reinterpret_cast<volatile f32x4*>(published);
+        const float least = fminf(fminf(p[0], p[1]), fminf(p[2], p[3]));
+        raise(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(least))));
+    };
+    // Looks at the wave's i-th group, chunks c .. + kGroup.
+    auto take = [&](int64_t c, int64_t i, const float (&v)[kGroup][8]) __attribute__((always_inline)) {
+        float top[kGroup], most = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t at = in.element(c0 + i, e);
-            const bool in_list = (ties ? v[e] >= bound : v[e] > bound) && at != a.eos;
-            const uint64_t mask = __ballot(in_list);
-            if (!mask) continue;
-            if (in_list) stage[held + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v[e])), (uint32_t)at);
-            held += __popcll(mask);
-            if (held >= kWave) flush(kWave);
+        for (int u = 0; u < kGroup; ++u) {
+            top[u] = v[u][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top[u] = fmaxf(top[u], v[u][e]);
+            most = fmaxf(most, top[u]);
         }
-        // Later chunks' elements come after all of this one's: they count if they
-        // are larger than the k-th so far.
-        const uint64_t kth = readlane64(best, a.k - 1);
-        if (kth) {
-            const float v_kth = float_of_key32((uint32_t)(kth >> 32));
-            if (v_kth >= bound) bound = v_kth, ties = false;
+        lane_most = fmaxf(lane_most, most);
+        most = wave_max(most);
+        if (most > m) {
+            const float from = c2;
+            m = most;
+            set_reference();
+            sum *= __builtin_amdgcn_exp2f(from - c2);
         }
+        if (huge) {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                float part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part += __builtin_amdgcn_exp2f((v[u][e] - m) * kLog2e);
+                sum += part;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                float part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part += __builtin_amdgcn_exp2f(fmaf(v[u][e], kLog2e, -c2));
+                sum += part;
+            }
+        }
+        if ((i & (i + 1)) == 0) refresh();  // groups 0, 1, 3, 7, ..
+        if (i == 0 && need <= kWave) raise(reached_by(need));
+        heed();
+        if (most < bound) return;
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            if (!__any(top[u] >= bound)) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!__any(v[u][e] >= bound)) continue;
+                const uint32_t at = (uint32_t)in.element(c + u, e);
+                const bool in_list = v[u][e] >= bound && at != (uint32_t)a.eos;
+                const uint64_t mask = __ballot(in_list);
+                if (in_list) stage[held + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v[u][e])), at);
+                held += __popcll(mask);
+            }
+            if (held > kStaged - kChunk) {
+                while (held > 0) flush();
+                // Later chunks of this wave lie behind what it has sorted: they
+                // count if they are larger than the k-th of that.
+                const uint64_t kth = readlane64(best, a.k - 1);
+                if (kth) raise(float_of_key32((uint32_t)(kth >> 32) + 1));
+            }
+        }
+    };
+
+    // The next group is on its way while one is looked at.
+    Chunk8<T> x[kGroup];
+    auto chunk_of = [&](int64_t i) { return (g0 + wave + i * kBeamWaves) * kGroup; };
+    auto load = [&](int64_t i) __attribute__((always_inline)) {
+        if (i < n && in.inside(chunk_of(i) + kGroup - 1))
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) x[u] = in.load(chunk_of(i) + u);
+    };
+    load(0);
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t c = chunk_of(i);
+        float v[kGroup][8];
+        if (in.inside(c + kGroup - 1)) {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[u][e] = x[u].get(e);
+        } else
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) in.load_edge(c + u, v[u]);
+        load(i + 1);
+        take(c, i, v);
     }
-    if (held > 0) flush(held);
+
+    {
+        const double total = wave_reduce(sum, [](double x, double y) { return x + y; });
+        // kLog2e is log2(e) (1 + d): the terms are those of logits times 1 + d,
+        // and their sum's logarithm is off by d times the softmax's mean logit, which lies near m.
+        constexpr double kOff = (double)kLog2e * 0.69314718055994530942 - 1.;
+        if (lane == 0)
+            stats[unit * kBeamWaves + wave] =
+                PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total};
+    }
+    refresh();
+    __syncthreads();
+    heed();
+    // What still reaches the bound, to the front of the stage.
+    {
+        const uint64_t least = (uint64_t)key32_of_bits(__float_as_uint(bound)) << 32;
+        int kept = 0;
+        for (int i = 0; i < held; i += kWave) {
+            wave_lds_sync();
+            const uint64_t v = i + lane < held ? stage[i + lane] : 0;
+            const bool keep = v >= least && v != 0;
+            const uint64_t mask = __ballot(keep);
+            wave_lds_sync();
+            if (keep) stage[kept + mbcnt64(mask)] = v;
+            kept += __popcll(mask);
+        }
+        held = kept;
+    }
+    if (best_any) {
+        while (held > 0) flush();
+        wave_lds_sync();
+        const uint64_t mask = __ballot(best != 0);  // the first lanes
+        stage[lane] = best;
+        held = __popcll(mask);
+    }
+    if (lane == 0) kept_by[wave] = held;
+    __syncthreads();
+    if (wave > 0) return;
+    // All waves' together, 64 at a time: most often there are no more.
+    int upto[kBeamWaves], count = 0;
+#pragma unroll
+    for (int w = 0; w < kBeamWaves; ++w) upto[w] = count += kept_by[w];
+    best = 0;
+    for (int i = 0; i < count; i += kWave) {
+        const int at = i + lane;
+        int w = 0, before = 0;
+#pragma unroll
+        for (int u = 0; u + 1 < kBeamWaves; ++u)
+            if (at >= upto[u]) w = u + 1, before = upto[u];
+        uint64_t v[1] = {at < count ? stage_memory[w][at - before] : 0};
+        wave_bitonic_sort<1, true>(v);
+        if (i == 0) best = v[0];
+        else merge_sorted(best, v[0]);
+    }
     if (lane < a.k) lists[unit * a.k + lane] = best;
 }
 
-// The key of a 64-bit value that orders like it; 0 is below all.
-__device__ __forceinline__ uint64_t key64(double v) {
+// A candidate among those of other beams: the upper 52 bits of its value's
+// key, so that values closer than 2^-40 of their size count as equal, and below them its beam and
+// its rank there, ascending.  0 is below all.
+static_assert(kMaxBeams <= 64 && kMaxBeamK <= 64, "12 bits");
+__device__ __forceinline__ uint64_t entry(double v, int beam, int rank) {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
-    return u >> 63 ? ~u : u | 1ull << 63;
+    return ((u >> 63 ? ~u : u | 1ull << 63) | 0xFFF) - (uint32_t)(beam * 64 + rank);
 }
 
 template <typename T>
-__global__ __launch_bounds__(kBeamBlock) void beam_join_kernel(BeamArgs a, int64_t pieces,
-                                                               const uint64_t* __restrict__ lists,
-                                                               const PieceStat* __restrict__ stats) {
-    extern __shared__ uint64_t keys[];  // [beams][k] values by rank in their beam, 0: none
-    uint32_t* const cols = reinterpret_cast<uint32_t*>(keys + a.beams * a.k);
-    float* const values = reinterpret_cast<float*>(cols + a.beams * a.k);
-    __shared__ int total;
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_join_kernel(BeamArgs a, int pieces,
+                                                                         const uint64_t* __restrict__ lists,
+                                                                         const PieceStat* __restrict__ stats) {
+    extern __shared__ uint64_t merged[];  // [waves][64]
+    const int lane = lane_id(), waves = blockDim.x / kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    float* const values = reinterpret_cast<float*>(merged + waves * kWave);    // [beams][64] by rank in their beam
+    uint32_t* const cols = reinterpret_cast<uint32_t*>(values + a.beams * 64);
     const int64_t group = blockIdx.x;
-    if (threadIdx.x == 0) total = 0;
-    for (int b = wave; b < a.beams; b += kBeamWaves) {
+    uint64_t mine = 0;
+    for (int b = wave; b < a.beams; b += waves) {
         const int64_t r = group * a.beams + b;
-        // The row's sum: a piece a lane.
-        float m = kLeast;
-        bool bad = false;
-        for (int64_t p = lane; p < pieces; p += kWave) m = fmaxf(m, stats[r * pieces + p].m);
-        m = wave_max(m);
-        double sum = 0;
-        for (int64_t p = lane; p < pieces; p += kWave) {
-            const PieceStat s = stats[r * pieces + p];
-            sum += (double)s.sum * exp((double)s.m - (double)m);
-            bad |= !(s.sum <= 3e38f);
-        }
-        for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+        const uint64_t* const list = lists + r * pieces * a.k + lane;
+        const PieceStat* const stat = stats + r * pieces * kBeamWaves;
+        const int parts = pieces * kBeamWaves;
+        constexpr int kAhead = 4;
+        uint64_t some[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) some[u] = lane < a.k && u < pieces ? list[u * a.k] : 0;
+        const PieceStat first = lane < parts ? stat[lane] : PieceStat{-1e300, 0.};
         const float score = a.scores[r];
+        float end_logit = 0.f;
+        if (a.ended) {
+            const T x = static_cast<const T*>(a.logits)[r * a.ld + a.eos];
+            if constexpr (sizeof(T) == 4) end_logit = x;
+            else end_logit = __uint_as_float((uint32_t)x << 16);
+        }
+        uint64_t best = some[0];
+        for (int p0 = 0; p0 < pieces; p0 += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (p0 + u >= pieces) break;
+                if (p0 + u > 0) merge_sorted(best, some[u]);
+                some[u] = lane < a.k && p0 + u + kAhead < pieces ? list[(int64_t)(p0 + u + kAhead) * a.k] : 0;
+            }
+        }
+        // The row's sum: a wave's part of a piece a lane.
+        auto sums = [](double x, double y) { return x + y; };
+        double m = first.ref;
+        for (int p = lane + kWave; p < parts; p += kWave) m = fmax(m, stat[p].ref);
+        m = wave_reduce(m, [](double x, double y) { return fmax(x, y); });
+        double sum = first.sum * exp(first.ref - m);
+        for (int p = lane + kWave; p < parts; p += kWave) sum += stat[p].sum * exp(stat[p].ref - m);
+        sum = wave_reduce(sum, sums);
         // A row without a finite sum (NaN or +inf in it, or -inf only) and a beam
         // without a finite score have no candidates.
-        const bool takes_part = !__any(bad) && sum > 0 && fabsf(score) <= 3.402823466e38f;
-        const double shift = (double)score - ((double)m + log(sum));
-        uint64_t best = lane < a.k ? lists[r * pieces * a.k + lane] : 0;
-        for (int64_t p = 1; p < pieces; ++p)
-            merge_sorted(best, lane < a.k ? lists[(r * pieces + p) * a.k + lane] : 0);
-        const bool there = takes_part && best != 0;
-        if (lane < a.k) {
-            const double v = shift + (double)float_of_key32((uint32_t)(best >> 32));
-            keys[b * a.k + lane] = there ? key64(v) : 0;
-            cols[b * a.k + lane] = composite_id(best);
-            values[b * a.k + lane] = (float)v;
-        }
-        if (a.ended && lane == 0) {
-            const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-            float x;
-            if constexpr (sizeof(T) == 4) x = row[a.eos];
-            else x = __uint_as_float((uint32_t)row[a.eos] << 16);
-            a.ended[r] = takes_part ? (float)(shift + (double)x) : -INFINITY;
-        }
-        const int n = __popcll(__ballot(there && lane < a.k));
-        if (lane == 0) atomicAdd(&total, n);
+        const bool takes_part = sum > 0 && sum <= 1e300 && fabs(m) <= 1e300 && fabsf(score) <= 3.402823466e38f;
+        const double shift = (double)score - (m + log(sum));
+        const double v = shift + (double)float_of_key32((uint32_t)(best >> 32));
+        values[b * 64 + lane] = (float)v;
+        cols[b * 64 + lane] = composite_id(best);
+        const uint64_t here = takes_part && best != 0 && lane < a.k ? entry(v, b, lane) : 0;
+        if (b == wave) mine = here;
+        else merge_sorted(mine, here);
+        if (a.ended && lane == 0) a.ended[r] = takes_part ? (float)(shift + (double)end_logit) : -INFINITY;
     }
-    __syncthreads();
-    // An entry's place: its own rank and, in every other beam, the entries ahead of it.
-    for (int e = threadIdx.x; e < a.beams * a.k; e += kBeamBlock) {
-        const int b = e / a.k;
-        const uint64_t mine = keys[e];
-        if (mine == 0) continue;
-        int place = e - b * a.k;
-        for (int o = 0; o < a.beams && place < a.k; ++o) {
-            if (o == b) continue;
-            const uint64_t* list = keys + o * a.k;
-            const uint64_t ahead = o < b ? mine : mine + 1;  // equal values by ascending beam
-            int lo = 0, hi = a.k;  // entries >= ahead
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (list[mid] >= ahead) lo = mid + 1; else hi = mid;
-            }
-            place += lo;
-        }
-        if (place < a.k) {
-            const int64_t at = group * a.k + place;
-            a.out_scores[at] = values[e];
-            a.parents[at] = (int32_t)(group * a.beams + b);
-            a.tokens[at] = (int32_t)cols[e];
-        }
+    // The waves' lists, two by two.
+    for (int step = 1; step < waves; step <<= 1) {
+        if ((wave & (2 * step - 1)) == step) merged[wave * kWave + lane] = mine;
+        __syncthreads();
+        if ((wave & (2 * step - 1)) == 0 && wave + step < waves) merge_sorted(mine, merged[(wave + step) * kWave + lane]);
     }
-    for (int i = threadIdx.x; i < a.k; i += kBeamBlock)
-        if (i >= total) {
-            const int64_t at = group * a.k + i;
-            a.out_scores[at] = -INFINITY;
-            a.parents[at] = -1;
-            a.tokens[at] = -1;
-        }
+    if (wave > 0 || lane >= a.k) return;
+    const int64_t at = group * a.k + lane;
+    const int from = 0xFFF - (int)(mine & 0xFFF);
+    a.out_scores[at] = mine ? values[from] : -INFINITY;
+    a.parents[at] = mine ? (int32_t)(group * a.beams + from / 64) : -1;
+    a.tokens[at] = mine ? (int32_t)cols[from] : -1;
 }
 
 BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k) {
-    const int64_t rows = groups * beams, all = (vocab + kChunk - 1) / kChunk;
-    int64_t pieces = (2048 + rows - 1) / rows;
-    const int64_t most = (all + 3) / 4, least = (all + kMaxChunks - 1) / kMaxChunks;
+    const int64_t each = dtype == RTS_F32 ? group_elements<float>() : group_elements<uint16_t>();
+    const int64_t rows = groups * beams, all = (vocab + each - 1) / each;
+    int64_t pieces = (768 + rows - 1) / rows;
+    const int64_t most = (all + kBeamWaves - 1) / kBeamWaves;
     pieces = pieces < most ? pieces : most;
-    pieces = pieces > least ? pieces : least;
     BeamPlan p;
-    p.chunks = (int)((all + pieces - 1) / pieces);
-    p.pieces = (all + p.chunks - 1) / p.chunks;
-    p.ws_bytes = (size_t)(rows * p.pieces) * ((size_t)k * sizeof(uint64_t) + sizeof(PieceStat));
+    p.piece_groups = (all + pieces - 1) / pieces;
+    p.pieces = (int)((all + p.piece_groups - 1) / p.piece_groups);
+    p.ws_bytes = (size_t)(rows * p.pieces) * ((size_t)k * sizeof(uint64_t) + kBeamWaves * sizeof(PieceStat));
     return p;
 }
 
@@ -338,11 +445,12 @@ static int launch_beam(const BeamArgs& a, const BeamPlan& plan, void* workspace,
     const int64_t units = a.groups * a.beams * plan.pieces;
     uint64_t* lists = static_cast<uint64_t*>(workspace);
     PieceStat* stats = reinterpret_cast<PieceStat*>(lists + units * a.k);
-    hipLaunchKernelGGL(beam_scan_kernel<T>, dim3((unsigned)((units + kBeamWaves - 1) / kBeamWaves)), dim3(kBeamBlock), 0,
-                       s, a, plan.pieces, plan.chunks, lists, stats);
+    hipLaunchKernelGGL(beam_scan_kernel<T>, dim3((unsigned)(a.groups * a.beams), plan.pieces),
+                       dim3(kBeamBlock), 0, s, a, plan.piece_groups, lists, stats);
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;
-    hipLaunchKernelGGL(beam_join_kernel<T>, dim3((unsigned)a.groups), dim3(kBeamBlock), (size_t)a.beams * a.k * 16, s, a,
-                       plan.pieces, lists, stats);
+    const int waves = a.beams < kMaxJoinWaves ? a.beams : kMaxJoinWaves;
+    hipLaunchKernelGGL(beam_join_kernel<T>, dim3((unsigned)a.groups), dim3(waves * kWave), (size_t)(waves + a.beams) * 64 * 8, s,
+                       a, plan.pieces, lists, stats);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 

@@ -185,10 +185,10 @@ struct BeamArgs {
     int dtype;
 };
 
-// How a call is cut: `pieces` of a row, each of `chunks` chunks of a wave's loads.
+// How a call is cut: `pieces` of a row, a workgroup each, of `piece_groups` groups of 4 KB.
 struct BeamPlan {
-    int64_t pieces;
-    int chunks;
+    int64_t piece_groups;
+    int pieces;
     size_t ws_bytes;
 };
 BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k);
