@@ -622,13 +622,20 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
  * counts     int32 [2]: how many are free afterwards (more than n_free, perhaps)
  *            and how many blocks the rows wanted (more than there are copies
  *            means that the pool was exhausted).
+ * workspace  optional device scratch, 16-byte aligned, of at least
+ *            fork_blocks_workspace_size bytes (0 where none is of use): lets several
+ *            workgroups read a large table.  Calls in flight at the same time need
+ *            workspaces of their own.
  * No output may overlap an input or another output.
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks), RTS_EHIP.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks), RTS_EWORKSPACE,
+ *         RTS_EHIP.
  */
+size_t fork_blocks_workspace_size(int64_t rows_in, int32_t table_cols, int32_t pool_blocks);
 int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols, int64_t ld_table,
                 const int32_t* ctx_lens, const int32_t* parents, int64_t rows_out, int32_t block_size,
                 int32_t pool_blocks, const uint8_t* held, int32_t* out_table, int64_t ld_out, int32_t* out_lens,
-                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, hipStream_t stream);
+                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, void* workspace,
+                size_t workspace_bytes, hipStream_t stream);
 
 /*
  * compact_blocks -- moves that bring a pool's blocks in use to the lowest ids.
@@ -647,14 +654,16 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
  *            block is both.
  * free_blocks int32 [n_free]: the ids that are free after the moves, ascending, then -1.
  * counts     int32 [2]: how many are free, and how many moves there are in all.
- * Other arguments as in fork_blocks (rows < 2^31).
+ * Other arguments as in fork_blocks (rows < 2^31), workspace with
+ * compact_blocks_workspace_size bytes.
  * No output may overlap an input or another output.
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EHIP.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EWORKSPACE, RTS_EHIP.
  */
+size_t compact_blocks_workspace_size(int64_t rows, int32_t table_cols, int32_t pool_blocks);
 int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols, int64_t ld_table,
                    const int32_t* ctx_lens, int32_t block_size, int32_t pool_blocks, const uint8_t* held,
                    int32_t* out_table, int64_t ld_out, int32_t* moves, int64_t max_moves, int32_t* free_blocks,
-                   int64_t n_free, int32_t* counts, hipStream_t stream);
+                   int64_t n_free, int32_t* counts, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* A paged cache of any element type: rows of row_bytes bytes, ld_bytes apart. */
 typedef struct {

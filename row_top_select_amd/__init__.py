@@ -66,8 +66,14 @@ _lib.merge_attend_rank_major.argtypes = [_p, ctypes.c_int, _p, _i32, _i64, _i32,
 _lib.beam_select_workspace_size.argtypes = [ctypes.c_int, _i64, _i32, _i64, _i32]
 _lib.beam_select_workspace_size.restype = _sz
 _lib.beam_select.argtypes = [_p, ctypes.c_int, _i64, _i32, _i64, _i64, _p, _i32, _i32, _p, _p, _p, _p, _p, _sz, _p]
-_lib.fork_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _i64, _p, _p, _p, _i64, _p, _p]
-_lib.compact_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _i32, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p]
+_lib.fork_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _i64, _p, _p, _p, _i64, _p, _p, _sz,
+                             _p]
+_lib.fork_blocks_workspace_size.argtypes = [_i64, _i32, _i32]
+_lib.fork_blocks_workspace_size.restype = _sz
+_lib.compact_blocks_workspace_size.argtypes = [_i64, _i32, _i32]
+_lib.compact_blocks_workspace_size.restype = _sz
+_lib.compact_blocks.argtypes = [_p, _i64, _i32, _i64, _p, _i32, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _sz,
+                                _p]
 _lib.copy_blocks.argtypes = [_p, _i32, _p, _i64, _i32, _i64, _p]
 _lib.kv_attend_paged_workspace_size.argtypes = [_i64, _i32, _i32, _i32, ctypes.c_int, _i64, _i64]
 _lib.kv_attend_paged_workspace_size.restype = _sz
@@ -979,33 +985,19 @@ def _pool(pool_blocks: int, held, n_free, block_size: int):
 
 
 def _named_out(out, shapes, device, stream):
-    """The int32 outputs of a block call: a caller's, checked, or new ones from one allocation."""
+    """A caller's int32 outputs of a block call, checked."""
     for name, t, shape in zip(out._fields, out, shapes):
         _out(t, shape, torch.int32, device, name, stream)
     return out
 
 
-def _new_flat(kind, shapes, device, stream):
-    sizes, at, parts = [], 0, []
-    for shape in shapes:
-        n = 1
-        for d in shape:
-            n *= d
-        sizes.append((at, n, shape))
-        at += n + (n & 1)  # pairs start on 8 bytes
-    flat = _new(at, torch.int32, device, stream)
-    for a, n, shape in sizes:
-        parts.append(flat[a:a + n].view(shape))
-    return kind(*parts)
-
-
 def fork_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, parents: torch.Tensor, block_size: int,
                 pool_blocks: int, held: torch.Tensor | None = None, n_free: int | None = None,
-                out: Fork | None = None, stream=None) -> Fork:
+                out: Fork | None = None, workspace="auto", stream=None) -> Fork:
     """The block table whose row i continues row ``parents[i]`` of ``block_table`` (the parents of beam_select; -1:
     an empty row), with fresh blocks where rows would write into the same one; see fork_blocks in the header.
     ``copies`` are the caller's to make (copy_blocks).  ``n_free``: length of the list of free blocks (default: the
-    pool's)."""
+    pool's).  ``workspace`` as in topk_rows."""
     device = _gpu(block_table, "block_table")
     rows_in, cols, ld = _table(block_table)
     if _int32_all(ctx_lens, "ctx_lens") != rows_in:
@@ -1013,20 +1005,28 @@ def fork_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, parents: torc
     rows = _int32_all(parents, "parents")
     n_free, held_ptr, block_size = _pool(pool_blocks, held, n_free, block_size)
     _on(device, ctx_lens, parents, held)
-    shapes = ((rows, cols), (rows,), (rows, 2), (n_free,), (2,))
-    out = _new_flat(Fork, shapes, device, stream) if out is None else _named_out(out, shapes, device, stream)
+    if out is None:
+        copies, counts, table, lens, free = torch.split_with_sizes(
+            _new(rows * (cols + 3) + n_free + 2, torch.int32, device, stream),
+            (rows * 2, 2, rows * cols, rows, n_free))
+        out = Fork(table.view(rows, cols), lens, copies.view(rows, 2), free, counts)
+    else:
+        _named_out(out, ((rows, cols), (rows,), (rows, 2), (n_free,), (2,)), device, stream)
+    ws, ws_bytes = _scratch(workspace, int(_lib.fork_blocks_workspace_size(rows_in, cols, pool_blocks))
+                            if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.fork_blocks, "fork_blocks", device, stream, block_table.data_ptr(), rows_in, cols, ld,
             ctx_lens.data_ptr(), parents.data_ptr(), rows, block_size, pool_blocks, held_ptr,
             out.block_table.data_ptr(), cols, out.ctx_lens.data_ptr(), out.copies.data_ptr(),
-            out.free_blocks.data_ptr(), n_free, out.counts.data_ptr())
+            out.free_blocks.data_ptr(), n_free, out.counts.data_ptr(), _ptr(ws), ws_bytes)
     return out
 
 
 def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size: int, pool_blocks: int,
                    held: torch.Tensor | None = None, max_moves: int | None = None, n_free: int | None = None,
-                   out: Compaction | None = None, stream=None) -> Compaction:
+                   out: Compaction | None = None, workspace="auto", stream=None) -> Compaction:
     """Moves (pairs for copy_blocks) that bring the blocks in use to the lowest ids, and the block table after
-    them; see compact_blocks in the header.  ``max_moves`` defaults to half of the pool, which is always enough."""
+    them; see compact_blocks in the header.  ``max_moves`` defaults to half of the pool, which is always enough;
+    ``workspace`` as in topk_rows."""
     device = _gpu(block_table, "block_table")
     rows, cols, ld = _table(block_table)
     if _int32_all(ctx_lens, "ctx_lens") != rows:
@@ -1037,11 +1037,18 @@ def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size
     if not 0 <= max_moves < 2 ** 31:
         raise ValueError("max_moves must not be negative, and below 2^31")
     _on(device, ctx_lens, held)
-    shapes = ((rows, cols), (max_moves, 2), (n_free,), (2,))
-    out = _new_flat(Compaction, shapes, device, stream) if out is None else _named_out(out, shapes, device, stream)
+    if out is None:
+        moves, counts, table, free = torch.split_with_sizes(
+            _new(rows * cols + max_moves * 2 + n_free + 2, torch.int32, device, stream),
+            (max_moves * 2, 2, rows * cols, n_free))
+        out = Compaction(table.view(rows, cols), moves.view(max_moves, 2), free, counts)
+    else:
+        _named_out(out, ((rows, cols), (max_moves, 2), (n_free,), (2,)), device, stream)
+    ws, ws_bytes = _scratch(workspace, int(_lib.compact_blocks_workspace_size(rows, cols, pool_blocks))
+                            if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.compact_blocks, "compact_blocks", device, stream, block_table.data_ptr(), rows, cols, ld,
             ctx_lens.data_ptr(), block_size, pool_blocks, held_ptr, out.block_table.data_ptr(), cols,
-            out.moves.data_ptr(), max_moves, out.free_blocks.data_ptr(), n_free, out.counts.data_ptr())
+            out.moves.data_ptr(), max_moves, out.free_blocks.data_ptr(), n_free, out.counts.data_ptr(), _ptr(ws), ws_bytes)
     return out
 
 

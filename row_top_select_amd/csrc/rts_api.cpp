@@ -525,10 +525,17 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
     return rts::launch_beam_select(a, plan, workspace, stream);
 }
 
+size_t fork_blocks_workspace_size(int64_t rows_in, int32_t table_cols, int32_t pool_blocks) {
+    if (rows_in < 0 || rows_in > rts::kMaxForkRows || table_cols < 0 || pool_blocks < 0 || pool_blocks > rts::kMaxPool)
+        return 0;
+    return rts::fork_blocks_bytes(rows_in, table_cols, pool_blocks);
+}
+
 int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols, int64_t ld_table,
                 const int32_t* ctx_lens, const int32_t* parents, int64_t rows_out, int32_t block_size,
                 int32_t pool_blocks, const uint8_t* held, int32_t* out_table, int64_t ld_out, int32_t* out_lens,
-                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, hipStream_t stream) {
+                int32_t* copies, int32_t* free_blocks, int64_t n_free, int32_t* counts, void* workspace,
+                size_t workspace_bytes, hipStream_t stream) {
     if (rows_in < 0 || table_cols < 0 || ld_table < table_cols || rows_out < 0 || block_size < 1 ||
         pool_blocks < 0 || ld_out < table_cols || n_free < 0)
         return RTS_EINVAL;
@@ -541,18 +548,25 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
     if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(parents, 4) || !aligned(out_table, 4) ||
         !aligned(out_lens, 4) || !aligned(copies, 8) || !aligned(free_blocks, 4) || !aligned(counts, 4))
         return RTS_EINVAL;
+    if ((workspace_bytes > 0 && !workspace) || !aligned(workspace, 16)) return RTS_EINVAL;
+    if (workspace && workspace_bytes < rts::fork_blocks_bytes(rows_in, table_cols, pool_blocks)) return RTS_EWORKSPACE;
     rts::ForkArgs a{};
     a.table = block_table, a.ctx_lens = ctx_lens, a.parents = parents, a.held = held, a.out_table = out_table;
     a.out_ctx = out_lens, a.copies = copies, a.free_blocks = free_blocks, a.counts = counts, a.rows_in = rows_in;
     a.ld_table = ld_table, a.rows_out = rows_out, a.ld_out = ld_out, a.n_free = n_free, a.cols = table_cols;
     a.block_size = block_size, a.pool = pool_blocks;
-    return rts::launch_fork_blocks(a, stream);
+    return rts::launch_fork_blocks(a, workspace, stream);
+}
+
+size_t compact_blocks_workspace_size(int64_t rows, int32_t table_cols, int32_t pool_blocks) {
+    if (rows < 0 || rows > 0x7FFFFFFFll || table_cols < 0 || pool_blocks < 0 || pool_blocks > rts::kMaxPool) return 0;
+    return rts::compact_blocks_bytes(rows, table_cols, pool_blocks);
 }
 
 int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols, int64_t ld_table,
                    const int32_t* ctx_lens, int32_t block_size, int32_t pool_blocks, const uint8_t* held,
                    int32_t* out_table, int64_t ld_out, int32_t* moves, int64_t max_moves, int32_t* free_blocks,
-                   int64_t n_free, int32_t* counts, hipStream_t stream) {
+                   int64_t n_free, int32_t* counts, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (rows < 0 || table_cols < 0 || ld_table < table_cols || block_size < 1 || pool_blocks < 0 ||
         ld_out < table_cols || max_moves < 0 || n_free < 0)
         return RTS_EINVAL;
@@ -563,11 +577,13 @@ int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols,
     if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(out_table, 4) || !aligned(moves, 8) ||
         !aligned(free_blocks, 4) || !aligned(counts, 4))
         return RTS_EINVAL;
+    if ((workspace_bytes > 0 && !workspace) || !aligned(workspace, 16)) return RTS_EINVAL;
+    if (workspace && workspace_bytes < rts::compact_blocks_bytes(rows, table_cols, pool_blocks)) return RTS_EWORKSPACE;
     rts::CompactArgs a{};
     a.table = block_table, a.ctx_lens = ctx_lens, a.held = held, a.out_table = out_table, a.moves = moves;
     a.free_blocks = free_blocks, a.counts = counts, a.rows = rows, a.ld_table = ld_table, a.ld_out = ld_out;
     a.n_free = n_free, a.max_moves = max_moves, a.cols = table_cols, a.block_size = block_size, a.pool = pool_blocks;
-    return rts::launch_compact_blocks(a, stream);
+    return rts::launch_compact_blocks(a, workspace, stream);
 }
 
 int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs, int64_t n_pairs, int32_t block_size,
@@ -576,7 +592,7 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
         return RTS_EINVAL;
     if (n_caches > rts::kMaxCopyCaches || n_pairs > 0x7FFFFFFFll) return RTS_EUNSUPPORTED;
     if (n_pairs > 0 && (!pairs || !aligned(pairs, 8))) return RTS_EINVAL;
-    rts::CopyArgs a{};
+    rts::CopyArgs<rts::kMaxCopyCaches> a{};
     a.pairs = pairs, a.n_pairs = n_pairs, a.block_size = block_size;
     // A cache has fewer than 2^31 rows: with a stride of 2^31 or more only block 0 has any.
     a.stride_rows = stride_rows < (1ll << 31) ? stride_rows : 1ll << 31;

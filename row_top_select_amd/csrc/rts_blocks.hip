@@ -16,6 +16,9 @@ namespace rts {
 constexpr int kPoolBlock = 1024;
 constexpr int kPoolWaves = kPoolBlock / kWave;
 
+// Words of a bit a block, in whole 16 bytes.
+__host__ __device__ __forceinline__ int words_of(int32_t pool) { return (pool + 127) / 128 * 4; }
+
 // The exclusive sum of x over the workgroup's threads; total: the whole sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wave_sum, uint32_t& total) {
     const int lane = lane_id(), wave = threadIdx.x / kWave;
@@ -33,88 +36,174 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wave_sum, u
 __device__ __forceinline__ void set_bit(uint32_t* bits, uint32_t i) { atomicOr(&bits[i >> 5], 1u << (i & 31)); }
 __device__ __forceinline__ bool get_bit(const uint32_t* bits, uint32_t i) { return bits[i >> 5] >> (i & 31) & 1; }
 
-// Bit b of word w: held[32 w + b] is set, or the pool has no such block and `past` is set.
-__device__ __forceinline__ uint32_t held_word(const uint8_t* held, int pool, int w, bool past) {
-    const int left = pool - w * 32;
-    uint32_t bits = 0;
-    if (held) {
-        if (left >= 32 && ((uintptr_t)held & 15) == 0) {
-            const uint4* p = reinterpret_cast<const uint4*>(held + (int64_t)w * 32);
-            const uint4 x[2] = {p[0], p[1]};
-            const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+// Which of four bytes are not 0.
+__device__ __forceinline__ uint32_t set_bytes(uint32_t v) {
+    const uint32_t high = (((v & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | v) & 0x80808080u;
+    return (high >> 7) * 0x10204080u >> 28;
+}
+// put(w, bits) for words [lo, hi) of `held`, bit b of word w: held[32 w + b] is not 0.
+template <typename Put>
+__device__ __forceinline__ void held_words(const uint8_t* held, int pool, int lo, int hi, Put&& put) {
+    if (!held) return;
+    constexpr int kAhead = 4;
+    const bool whole = ((uintptr_t)held & 15) == 0;
+    for (int w0 = lo + threadIdx.x; w0 < hi; w0 += kPoolBlock * kAhead) {
+        uint4 x[kAhead][2] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+        for (int u = 0; u < kAhead; ++u) {
+            const int w = w0 + u * kPoolBlock;
+            if (whole && w < hi && w * 32 + 32 <= pool) {
+                const uint4* p = reinterpret_cast<const uint4*>(held + (int64_t)w * 32);
+                x[u][0] = p[0], x[u][1] = p[1];
+            }
+        }
 #pragma unroll
-                for (int b = 0; b < 4; ++b) bits |= (uint32_t)((v[i] >> (8 * b) & 0xFF) != 0) << (4 * i + b);
-        } else
-            for (int b = 0; b < 32 && b < left; ++b) bits |= (uint32_t)(held[(int64_t)w * 32 + b] != 0) << b;
+        for (int u = 0; u < kAhead; ++u) {
+            const int w = w0 + u * kPoolBlock, left = pool - w * 32;
+            if (w >= hi) break;
+            uint32_t bits = 0;
+            if (!whole || left < 32) {
+                for (int b = 0; b < 32 && b < left; ++b) bits |= (uint32_t)(held[(int64_t)w * 32 + b] != 0) << b;
+            } else {
+                const uint32_t v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bits |= set_bytes(v[i]) << 4 * i;
+            }
+            put(w, bits);
+        }
     }
-    if (past && left < 32) bits |= left <= 0 ? ~0u : ~0u << left;
-    return bits;
+}
+// Words [0, words) of LDS, 16 bytes at a time.
+__device__ __forceinline__ void clear(uint32_t* bits, int words) {
+    for (int w = threadIdx.x * 4; w < words; w += kPoolBlock * 4) *reinterpret_cast<uint4*>(bits + w) = uint4{0, 0, 0, 0};
+}
+__device__ __forceinline__ void store_field(uint32_t* to, const uint32_t* bits, int words) {
+    for (int w = threadIdx.x * 4; w < words; w += kPoolBlock * 4)
+        *reinterpret_cast<uint4*>(to + w) = *reinterpret_cast<const uint4*>(bits + w);
+}
+// The bits of word w that are no block's.
+__device__ __forceinline__ uint32_t behind(int pool, int w) {
+    const int left = pool - w * 32;
+    return left >= 32 ? 0 : left <= 0 ? ~0u : ~0u << left;
 }
 
-// Sets the bits of the first n(row) entries of each row of a table.  A wave
-// takes 64 rows' lengths at a time and reads four rows' entries side by side.
+// Four entries of a table row at any address, and what of them lies inside of it.
+typedef int ids4 __attribute__((ext_vector_type(4)));
+typedef int ids4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ ids4 four_entries(const int32_t* row, int j, int n) {
+    ids4 x = {-1, -1, -1, -1};
+    if (j + 4 <= n)
+        x = *reinterpret_cast<const ids4_at4*>(row + j);
+    else if (j < n) {
+        x[0] = row[j];
+        if (j + 1 < n) x[1] = row[j + 1];
+        if (j + 2 < n) x[2] = row[j + 2];
+    }
+    return x;
+}
+
+// Sets the bits (from that of block `least` on, `pool` of them) of the first
+// n(row) entries of rows [lo, hi) of a table.  A wave takes 64 rows' lengths at a time and reads eight rows side by side, 256 entries each.
 template <typename Count>
-__device__ __forceinline__ void mark_rows(const int32_t* table, int64_t ld, int64_t rows, int pool, uint32_t* bits,
-                                          Count&& n) {
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const int64_t per = (rows + kPoolWaves - 1) / kPoolWaves;
-    const int64_t lo = wave * per, hi = lo + per < rows ? lo + per : rows;
+__device__ __forceinline__ void mark_rows(const int32_t* table, int64_t ld, int64_t lo, int64_t hi, int least,
+                                          int pool, uint32_t* bits, Count&& n) {
+    constexpr int kRows = 8;
+    const int lane = lane_id();
     for (int64_t r0 = lo; r0 < hi; r0 += kWave) {
         const int count = r0 + lane < hi ? n(r0 + lane) : 0;
-        const int here = (int)(hi - r0 < kWave ? hi - r0 : kWave);
-        for (int r = 0; r < here; r += 4) {
-            int c[4], most = 0;
+        uint64_t todo = __ballot(count > 0);
+        while (todo) {
+            int row[kRows], c[kRows], most = 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                c[u] = r + u < here ? __builtin_amdgcn_readlane(count, r + u) : 0;
+            for (int u = 0; u < kRows; ++u) {
+                row[u] = todo ? __builtin_ctzll(todo) : 0;
+                c[u] = todo ? __builtin_amdgcn_readlane(count, row[u]) : 0;
                 most = c[u] > most ? c[u] : most;
+                todo &= todo - 1;
             }
-            for (int j0 = 0; j0 < most; j0 += 2 * kWave) {
-                int id[4][2];
+            for (int j = lane * 4; j - lane * 4 < most; j += 4 * kWave) {
+                ids4 id[kRows];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < kRows; ++u) id[u] = four_entries(table + (r0 + row[u]) * ld, j, c[u]);
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int j = j0 + v * kWave + lane;
-                        id[u][v] = j < c[u] ? table[(r0 + r + u) * ld + j] : -1;
-                    }
+                for (int u = 0; u < kRows; ++u)
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-                        if ((uint32_t)id[u][v] < (uint32_t)pool) set_bit(bits, id[u][v]);
+                    for (int v = 0; v < 4; ++v)
+                        if ((uint32_t)(id[u][v] - least) < (uint32_t)pool) set_bit(bits, id[u][v] - least);
             }
         }
     }
 }
-
-// The position of the n-th set bit of x, from 0.
-__device__ __forceinline__ int nth_bit(uint32_t x, uint32_t n) {
-    for (; n > 0; --n) x &= x - 1;
-    return __builtin_ctz(x);
+// A wave's share of rows.
+__device__ __forceinline__ void rows_of(int64_t part, int64_t parts, int64_t rows, int64_t& lo, int64_t& hi) {
+    const int64_t per = (rows + parts - 1) / parts;
+    lo = part * per < rows ? part * per : rows;
+    hi = lo + per < rows ? lo + per : rows;
 }
 
-// Writes the ids of bits set in word(w), ascending, to out[rank - skip] for
-// ranks in [skip, skip + n): a wave takes a run of words, two at a time, a lane
-// an id.  before(w): the rank of word w's first.  `part` of `parts` waves.
-template <typename Word, typename Before>
-__device__ __forceinline__ void list_bits(int words, int unit, uint32_t part, uint32_t parts, uint32_t skip, int64_t n,
-                                          int32_t* out, Word&& word, Before&& before) {
+// Words of LDS bits a thread counts: twice an odd number, so that the lanes'
+// 8-byte reads lie in different banks.
+__device__ __forceinline__ int unit_of(int words) { return (((words + 2 * kPoolBlock - 1) / (2 * kPoolBlock)) | 1) * 2; }
+constexpr int kMaxUnitPairs = ((kMaxPool / 32 + 2 * kPoolBlock - 1) / (2 * kPoolBlock)) | 1;
+
+// The position of the n-th set bit of x, from 0.
+__device__ __forceinline__ int nth_bit(uint64_t x, uint32_t n) {
+    int at = 0;
+#pragma unroll
+    for (int w = 32; w > 0; w >>= 1) {
+        const uint32_t c = __popcll(x & ((1ull << w) - 1));
+        if (n >= c) n -= c, x >>= w, at += w;
+    }
+    return at;
+}
+
+// The block of rank r among the bits of pair(p), the p-th 64 of them, before(u) the
+// rank of unit u's first and `pairs` words' pairs a unit.
+template <typename Pair, typename Before>
+__device__ __forceinline__ int find_rank(uint32_t r, int pairs, int all_pairs, Pair&& pair, Before&& before) {
+    int lo = 0, hi = (all_pairs + pairs - 1) / pairs;  // the last unit with at most r bits before it
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before(mid) <= r) lo = mid; else hi = mid;
+    }
+    r -= before(lo);
+    uint64_t bits = 0, x[kMaxUnitPairs];
+    const int p0 = lo * pairs;
+    int at = p0;
+    uint32_t passed = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxUnitPairs; ++i) x[i] = i < pairs && p0 + i < all_pairs ? pair(p0 + i) : 0;
+#pragma unroll
+    for (int i = 0; i < kMaxUnitPairs; ++i) {
+        if (r >= sum) at = p0 + i, bits = x[i], passed = sum;
+        sum += __popcll(x[i]);
+    }
+    return at * 64 + nth_bit(bits, r - passed);
+}
+
+// Writes the ids of the bits set in pair(p), ascending, to out[rank - skip] for ranks
+// in [skip, skip + n): a wave takes a run of units, four pairs at a time, a lane an id.
+template <typename Pair, typename Before>
+__device__ __forceinline__ void list_bits(int all_pairs, int pairs, uint32_t part, uint32_t parts, uint32_t skip,
+                                          int64_t n, int32_t* out, Pair&& pair, Before&& before) {
+    constexpr int kAhead = 4;
     const int lane = lane_id();
-    const int units = (words + unit - 1) / unit;
+    const int units = (all_pairs + pairs - 1) / pairs;
     const int per = (units + parts - 1) / parts;
     const int u0 = part * per, u1 = u0 + per < units ? u0 + per : units;
     if (u0 >= u1) return;
     uint32_t rank = before(u0);
-    const int w1 = u1 * unit < words ? u1 * unit : words;
-    for (int w = u0 * unit; w < w1; w += 2) {
-        const uint32_t lo = word(w), hi = w + 1 < w1 ? word(w + 1) : 0;
-        const uint64_t both = (uint64_t)hi << 32 | lo;
-        const uint32_t r = rank + mbcnt64(both);
-        if ((both >> lane & 1) && r >= skip && (int64_t)(r - skip) < n) out[r - skip] = w * 32 + lane;
-        rank += __popcll(both);
+    const int end = u1 * pairs < all_pairs ? u1 * pairs : all_pairs;
+    for (int p = u0 * pairs; p < end; p += kAhead) {
+        uint64_t x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = p + i < end ? pair(p + i) : 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t r = rank + mbcnt64(x[i]);
+            if ((x[i] >> lane & 1) && r >= skip && (int64_t)(r - skip) < n) out[r - skip] = (p + i) * 64 + lane;
+            rank += __popcll(x[i]);
+        }
     }
 }
 
@@ -127,11 +216,139 @@ __device__ __forceinline__ Lengths lengths(int32_t ctx, int32_t block_size, int3
     return {full < cols ? full : cols, need < cols ? need : cols};
 }
 
-__global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a) {
-    extern __shared__ uint32_t lds[];
+// Columns [0, cols) of a row: edit(j, entry) of the first `need` entries, then -1.
+template <typename Edit>
+__device__ __forceinline__ void write_row(const int32_t* from, int32_t* to, int need, int cols, Edit&& edit) {
+    constexpr int kAhead = 2;
+    const int lane = lane_id();
+    for (int j0 = lane * 4; j0 - lane * 4 < cols; j0 += kAhead * 4 * kWave) {
+        ids4 id[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) id[u] = four_entries(from, j0 + u * 4 * kWave, need);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = j0 + u * 4 * kWave;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) id[u][v] = edit(j + v, id[u][v]);
+            if (j + 4 <= cols)
+                *reinterpret_cast<ids4_at4*>(to + j) = id[u];
+            else
+#pragma unroll
+                for (int v = 0; v < 3; ++v)
+                    if (j + v < cols) to[j + v] = id[u][v];
+        }
+    }
+}
+
+constexpr int kForkRowsEach = kMaxForkRows / kPoolBlock;  // rows of a thread
+constexpr int kNoRow = 0x7FFFFFFF;
+// Clears `first` and finds each parent's first row.  Ends behind a barrier.
+__device__ __forceinline__ void first_rows(const ForkArgs& a, int* first, const int (&par)[kForkRowsEach]) {
+    for (int p = threadIdx.x; p < a.rows_in; p += kPoolBlock) first[p] = kNoRow;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u)
+        if (par[u] >= 0) atomicMin(&first[par[u]], (int)threadIdx.x * kForkRowsEach + u);
+    __syncthreads();
+}
+// The parents of a thread's neighbouring rows, -1 where there is none.
+__device__ __forceinline__ void load_parents(const ForkArgs& a, int (&par)[kForkRowsEach]) {
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const int i = threadIdx.x * kForkRowsEach + u;
+        par[u] = i < a.rows_out ? a.parents[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u)
+        if ((uint32_t)par[u] >= (uint32_t)a.rows_in) par[u] = -1;
+}
+
+// Where tables are large, the bits of their entries are formed by several
+// workgroups, into bit fields that the call's workgroups join: one takes a part of the rows
+// and a quarter of the pool.  A wave's 64 atomic operations in LDS take 16
+// cycles, so they and not the reads bound this: the quarters read the same rows.
+constexpr int kQuarters = 4;
+struct MarkShare {
+    int first_word, words, least, blocks;  // of the pool
+    int64_t part, parts;                   // of the rows, a wave
+    int field;
+    __device__ __forceinline__ explicit MarkShare(int32_t pool) {
+        const int all = words_of(pool), per = (all / 4 + kQuarters - 1) / kQuarters * 4, q = blockIdx.x % kQuarters;
+        first_word = q * per < all ? q * per : all;
+        words = first_word + per < all ? per : all - first_word;
+        least = first_word * 32;
+        blocks = pool - least < words * 32 ? pool - least : words * 32;
+        if (blocks < 0) blocks = 0;
+        field = blockIdx.x / kQuarters;
+        part = field * kPoolWaves + threadIdx.x / kWave;
+        parts = (int64_t)(gridDim.x / kQuarters) * kPoolWaves;
+    }
+    // The held blocks' words of the quarter, this part's of them.
+    template <typename Put>
+    __device__ __forceinline__ void held(const uint8_t* held, int pool, Put&& put) const {
+        const int n = gridDim.x / kQuarters, per = (words + n - 1) / n;
+        const int lo = field * per < words ? field * per : words, hi = lo + per < words ? lo + per : words;
+        held_words(held, pool, first_word + lo, first_word + hi, put);
+    }
+};
+
+__global__ __launch_bounds__(kPoolBlock) void mark_fork_kernel(ForkArgs a, uint32_t* __restrict__ fields) {
+    extern __shared__ __align__(16) uint32_t lds[];
+    const MarkShare my(a.pool);
+    uint32_t* const used = lds;
+    int* const first = reinterpret_cast<int*>(used + my.words);
+    int par[kForkRowsEach];
+    load_parents(a, par);
+    clear(used, my.words);
+    first_rows(a, first, par);
+    my.held(a.held, a.pool, [&](int w, uint32_t bits) { atomicOr(&used[w - my.first_word], bits); });
+    int64_t lo, hi;
+    rows_of(my.part, my.parts, a.rows_in, lo, hi);
+    mark_rows(a.table, a.ld_table, lo, hi, my.least, my.blocks, used,
+              [&](int64_t p) { return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full; });
+    __syncthreads();
+    store_field(fields + (int64_t)my.field * words_of(a.pool) + my.first_word, used, my.words);
+}
+__global__ __launch_bounds__(kPoolBlock) void mark_compact_kernel(CompactArgs a, uint32_t* __restrict__ fields) {
+    extern __shared__ __align__(16) uint32_t lds[];
+    const MarkShare my(a.pool);
+    clear(lds, my.words);
+    __syncthreads();
+    const int64_t n = gridDim.x / kQuarters, words = words_of(a.pool);
+    my.held(a.held, a.pool, [&](int w, uint32_t bits) { fields[n * words + w] = bits; });  // a field of their own
+    int64_t lo, hi;
+    rows_of(my.part, my.parts, a.rows, lo, hi);
+    mark_rows(a.table, a.ld_table, lo, hi, my.least, my.blocks, lds,
+              [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
+    __syncthreads();
+    store_field(fields + (int64_t)my.field * words + my.first_word, lds, my.words);
+}
+// dst[w] |= word w of all fields (`words` a multiple of 4), four loads of 16 bytes on their way.
+__device__ __forceinline__ void join_fields(const uint32_t* fields, int n, int words, uint32_t* dst) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kFields = 4;
+    for (int w = threadIdx.x * 4; w < words; w += kPoolBlock * 4) {
+        u32x4 bits = *reinterpret_cast<u32x4*>(dst + w);
+        for (int f = 0; f < n; f += kFields) {
+            u32x4 x[kFields];
+#pragma unroll
+            for (int u = 0; u < kFields; ++u) {
+                x[u] = u32x4{0, 0, 0, 0};
+                if (f + u < n) x[u] = *reinterpret_cast<const u32x4*>(fields + (int64_t)(f + u) * words + w);
+            }
+#pragma unroll
+            for (int u = 0; u < kFields; ++u) bits |= x[u];
+        }
+        *reinterpret_cast<u32x4*>(dst + w) = bits;
+    }
+}
+
+__global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, const uint32_t* __restrict__ fields,
+                                                                 int n_fields) {
+    extern __shared__ __align__(16) uint32_t lds[];
     __shared__ uint32_t wave_sum[kPoolWaves];
     __shared__ uint32_t free_before[kPoolBlock];
-    const int words = (a.pool + 31) / 32;
+    const int words = words_of(a.pool);
     const int rows_in = (int)a.rows_in, rows = (int)a.rows_out;
     uint32_t* const used = lds;                                      // a bit a block
     uint32_t* const twice = used + words;                            // last blocks that no row may keep
@@ -140,69 +357,91 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a) {
     int* const fresh = first;                                        // afterwards: the fresh blocks
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
 
-    for (int w = tid; w < words; w += kPoolBlock) {
-        used[w] = held_word(a.held, a.pool, w, true);
-        twice[w] = 0;
+    // Every parent's last block, where it is being written, beside the rest.
+    int par[kForkRowsEach], ctx[kForkRowsEach], last[kForkRowsEach];
+    load_parents(a, par);
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const int p = tid + u * kPoolBlock;
+        ctx[u] = p < rows_in ? a.ctx_lens[p] : 0;
     }
-    for (int p = tid; p < rows_in; p += kPoolBlock) first[p] = 0x7FFFFFFF;
-    __syncthreads();
-    auto parent = [&](int i) {
-        const int p = a.parents[i];
-        return (uint32_t)p < (uint32_t)rows_in ? p : -1;
-    };
-    for (int i = tid; i < rows; i += kPoolBlock) {
-        const int p = parent(i);
-        if (p >= 0) atomicMin(&first[p], i);
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const Lengths n = lengths(ctx[u], a.block_size, a.cols);
+        last[u] = n.full < n.need ? a.table[(tid + u * kPoolBlock) * a.ld_table + n.full] : -1;
+        if ((uint32_t)last[u] >= (uint32_t)a.pool) last[u] = -1;
     }
+    clear(used, 2 * words);
+    first_rows(a, first, par);
+    if (n_fields)
+        join_fields(fields, n_fields, words, used);
+    else
+        held_words(a.held, a.pool, 0, words, [&](int w, uint32_t bits) { atomicOr(&used[w], bits); });
     __syncthreads();
-    auto shape = [&](int p) { return lengths(a.ctx_lens[p], a.block_size, a.cols); };
-    mark_rows(a.table, a.ld_table, rows_in, a.pool, used,
-              [&](int64_t p) { return first[p] == 0x7FFFFFFF ? 0 : shape((int)p).full; });
-    __syncthreads();
-    for (int p = tid; p < rows_in; p += kPoolBlock) {
-        if (first[p] == 0x7FFFFFFF) continue;
-        const Lengths n = shape(p);
-        if (n.full >= n.need) continue;
-        const uint32_t id = a.table[p * a.ld_table + n.full];
-        if (id >= (uint32_t)a.pool) continue;
-        const uint32_t bit = 1u << (id & 31);
-        if (atomicOr(&used[id >> 5], bit) & bit) atomicOr(&twice[id >> 5], bit);
+    if (tid < 4 && words > 0) atomicOr(&used[words - 4 + tid], behind(a.pool, words - 4 + tid));
+    if (n_fields == 0) {
+        int64_t lo, hi;
+        rows_of(wave, kPoolWaves, rows_in, lo, hi);
+        mark_rows(a.table, a.ld_table, lo, hi, 0, a.pool, used, [&](int64_t p) {
+            return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full;
+        });
+        __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const int p = tid + u * kPoolBlock;
+        if (p >= rows_in || first[p] == kNoRow) continue;
+        const uint32_t id = last[u];
+        if (last[u] >= 0) {
+            const uint32_t bit = 1u << (id & 31);
+            if (atomicOr(&used[id >> 5], bit) & bit) atomicOr(&twice[id >> 5], bit);
+        }
+        // Its first row and its last block in one word.
+        static_assert(kMaxForkRows <= 1 << 12 && kMaxPool <= 1 << 19, "31 bits");
+        first[p] = last[u] < 0 ? -1 : (int)(id | (uint32_t)first[p] << 19);
     }
     __syncthreads();
 
-    // The rows that want a fresh block, four neighbouring ones a thread.
-    constexpr int kRows = kMaxForkRows / kPoolBlock;
-    int last[kRows];  // the block to copy, or -1
+    // The rows that want a fresh block, neighbouring ones a thread.
     uint32_t own = 0;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const int i = tid * kRows + u;
-        last[u] = -1;
-        const int p = i < rows ? parent(i) : -1;
-        if (p < 0) continue;
-        const Lengths n = shape(p);
-        if (n.full >= n.need) continue;
-        const uint32_t id = a.table[p * a.ld_table + n.full];
-        if (id >= (uint32_t)a.pool || (first[p] == i && !get_bit(twice, id))) continue;
-        last[u] = (int)id;
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const int i = tid * kForkRowsEach + u;
+        last[u] = -1;  // from here on: the block to copy
+        const int x = par[u] >= 0 ? first[par[u]] : -1;
+        if (x < 0) continue;
+        const int id = x & ((1 << 19) - 1);
+        if (x >> 19 == i && !get_bit(twice, id)) continue;
+        last[u] = id;
         ++own;
     }
     uint32_t wanted, all_free;
     uint32_t rank = block_scan(own, wave_sum, wanted);
     // Free blocks before each thread's words.
-    const int unit = ((words + kPoolBlock - 1) / kPoolBlock + 1) & ~1;  // words a thread, even
+    const int pairs = unit_of(words) / 2;
+    const uint64_t* const used2 = reinterpret_cast<const uint64_t*>(used);
+    auto free_pair = [&](int p) { return ~used2[p]; };
     uint32_t mine = 0;
-    for (int w = tid * unit; w < (tid + 1) * unit && w < words; ++w) mine += __popc(~used[w]);
-    uint32_t before = block_scan(mine, wave_sum, all_free);
-    free_before[tid] = before;
-    for (int w = tid * unit; w < (tid + 1) * unit && w < words && before < wanted; ++w)
-        for (uint32_t x = ~used[w]; x && before < wanted; x &= x - 1) fresh[before++] = w * 32 + __builtin_ctz(x);
+    for (int p = tid * pairs; p < (tid + 1) * pairs && p < words / 2; ++p) mine += __popcll(free_pair(p));
+    free_before[tid] = block_scan(mine, wave_sum, all_free);
+    __syncthreads();
+    auto before = [&](int u) { return free_before[u]; };
+    // The lowest of them for the rows that want one, a unit a wave.
+    for (int u = wave; u * pairs < words / 2 && free_before[u] < wanted; u += kPoolWaves) {
+        uint32_t r = free_before[u];
+        for (int p = u * pairs; p < (u + 1) * pairs && p < words / 2; ++p) {
+            const uint64_t x = free_pair(p);
+            const uint32_t mine = r + mbcnt64(x);
+            if ((x >> lane & 1) && mine < wanted) fresh[mine] = p * 64 + lane;
+            r += __popcll(x);
+        }
+    }
     __syncthreads();
     const uint32_t taken = wanted < all_free ? wanted : all_free;
     const bool lead = blockIdx.x == 0;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-        const int i = tid * kRows + u;
+    for (int u = 0; u < kForkRowsEach; ++u) {
+        const int i = tid * kForkRowsEach + u;
         if (i >= rows) break;
         got[i] = -2;  // keeps what its parent has
         if (last[u] < 0) continue;
@@ -217,32 +456,53 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a) {
     if (at == 0) a.counts[0] = (int32_t)(all_free - taken), a.counts[1] = (int32_t)wanted;
     for (int64_t r = taken + at; r < rows; r += step) reinterpret_cast<int2*>(a.copies)[r] = int2{-1, -1};
     for (int64_t r = (int64_t)(all_free - taken) + at; r < a.n_free; r += step) a.free_blocks[r] = -1;
-    list_bits(words, unit, part, parts, taken, a.n_free, a.free_blocks, [&](int w) { return ~used[w]; },
-              [&](int u) { return free_before[u]; });
-    for (int i = part; i < rows; i += parts) {
-        const int p = parent(i);
-        int32_t* const out = a.out_table + i * a.ld_out;
-        const int ctx = p < 0 ? 0 : a.ctx_lens[p];
-        const Lengths n = lengths(ctx, a.block_size, a.cols);
-        if (lane == 0) a.out_ctx[i] = ctx > 0 ? ctx : 0;
-        const int own_block = got[i];
-        for (int j = lane; j < a.cols; j += kWave) {
-            int id = -1;
-            if (j < n.need) id = a.table[p * a.ld_table + j];
-            if ((uint32_t)id >= (uint32_t)a.pool) id = -1;
-            if (j == n.full && own_block != -2) id = own_block;
-            out[j] = id;
+    list_bits(words / 2, pairs, part, parts, taken, a.n_free, a.free_blocks, free_pair, before);
+    // Rows part, part + parts, ..; a lane has one's parent and length.
+    for (int i0 = part; i0 < rows; i0 += parts * kWave) {
+        const int i = i0 + lane * (int)parts;
+        int p = i < rows ? a.parents[i] : -1;
+        if ((uint32_t)p >= (uint32_t)rows_in) p = -1;
+        int len = p < 0 ? 0 : a.ctx_lens[p];
+        len = len > 0 ? len : 0;
+        if (i < rows) a.out_ctx[i] = len;
+        for (int r = 0; r < kWave && i0 + r * (int)parts < rows; ++r) {
+            const int row = i0 + r * (int)parts, from = __builtin_amdgcn_readlane(p, r);
+            const Lengths n = lengths(__builtin_amdgcn_readlane(len, r), a.block_size, a.cols);
+            const int own_block = got[row];
+            write_row(a.table + (from < 0 ? 0 : from) * a.ld_table, a.out_table + row * a.ld_out, n.need, a.cols,
+                      [&](int j, int id) {
+                          if ((uint32_t)id >= (uint32_t)a.pool) id = -1;
+                          return j == n.full && own_block != -2 ? own_block : id;
+                      });
         }
     }
 }
 
-int launch_fork_blocks(const ForkArgs& a, hipStream_t s) {
-    const int64_t work = a.rows_out * (int64_t)a.cols + a.n_free;
-    const int64_t grid = work / 16384 < 1 ? 1 : work / 16384 < 64 ? work / 16384 : 64;
-    const int64_t words = (a.pool + 31) / 32;
-    const size_t lds = (size_t)(words + (words > a.rows_out ? words : a.rows_out) +
-                                (a.rows_in > a.rows_out ? a.rows_in : a.rows_out)) * 4;
-    hipLaunchKernelGGL(fork_blocks_kernel, dim3((unsigned)grid), dim3(kPoolBlock), lds, s, a);
+// Bit fields of large tables: none where one workgroup reads the tables in
+// about the time that a launch takes.
+static int mark_parts(int64_t rows, int32_t cols) {
+    const int64_t entries = rows * (int64_t)cols;
+    return entries <= 65536 ? 0 : entries < 4 * 32768 ? 2 : 4;
+}
+static size_t mark_lds(int32_t pool) { return (size_t)(words_of(pool) / 4 + kQuarters - 1) / kQuarters * 16; }
+size_t fork_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
+    return (size_t)mark_parts(rows, cols) * words_of(pool) * 4;
+}
+
+static int64_t pool_grid(int64_t work) { return work / 4096 < 1 ? 1 : work / 4096 < 256 ? work / 4096 : 256; }
+
+int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t s) {
+    const size_t words = words_of(a.pool);
+    const int parts = workspace ? mark_parts(a.rows_in, a.cols) : 0;
+    uint32_t* fields = static_cast<uint32_t*>(workspace);
+    if (parts) {
+        hipLaunchKernelGGL(mark_fork_kernel, dim3(parts * kQuarters), dim3(kPoolBlock), mark_lds(a.pool) + a.rows_in * 4, s,
+                           a, fields);
+        if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+    }
+    const size_t rows = a.rows_out, most = a.rows_in > a.rows_out ? a.rows_in : a.rows_out;
+    hipLaunchKernelGGL(fork_blocks_kernel, dim3((unsigned)pool_grid(a.rows_out * (int64_t)a.cols + a.n_free)),
+                       dim3(kPoolBlock), (words + (words > rows ? words : rows) + most) * 4, s, a, fields, parts);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
@@ -250,31 +510,42 @@ int launch_fork_blocks(const ForkArgs& a, hipStream_t s) {
 // smallest bound below which there are n blocks that are not held.  Live ones at
 // or past T move, in ascending order, to the free ones below it: there are as
 // many of one as of the other, and no block is both left and taken.
-__global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs a) {
-    extern __shared__ uint32_t lds[];
+__global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs a, const uint32_t* __restrict__ fields,
+                                                                    int n_fields) {
+    extern __shared__ __align__(16) uint32_t lds[];
     __shared__ uint32_t wave_sum[kPoolWaves];
     __shared__ uint32_t open_before[kPoolBlock];  // blocks that are not held
     __shared__ uint32_t live_before[kPoolBlock];  // of those, live ones
     __shared__ uint32_t limit[2];                 // T, and the live ones below it
-    const int words = (a.pool + 31) / 32;
+    const int words = words_of(a.pool);
     uint32_t* const live = lds;           // not held, in a table
     uint32_t* const open = live + words;  // not held
+    const uint64_t *const live2 = reinterpret_cast<const uint64_t*>(live), *const open2 = reinterpret_cast<const uint64_t*>(open);
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-    for (int w = tid; w < words; w += kPoolBlock) {
-        live[w] = 0;
-        open[w] = ~held_word(a.held, a.pool, w, true);
+    clear(live, 2 * words);
+    __syncthreads();
+    if (tid < 4 && words > 0) open[words - 4 + tid] = behind(a.pool, words - 4 + tid);
+    __syncthreads();
+    if (n_fields) {
+        join_fields(fields, n_fields, words, live);
+        if (a.held) join_fields(fields + (int64_t)n_fields * words, 1, words, open);
+    } else {
+        held_words(a.held, a.pool, 0, words, [&](int w, uint32_t bits) { atomicOr(&open[w], bits); });
+        int64_t lo, hi;
+        rows_of(wave, kPoolWaves, a.rows, lo, hi);
+        mark_rows(a.table, a.ld_table, lo, hi, 0, a.pool, live,
+                  [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
     }
     __syncthreads();
-    mark_rows(a.table, a.ld_table, a.rows, a.pool, live,
-              [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
-    __syncthreads();
-    const int unit = ((words + kPoolBlock - 1) / kPoolBlock + 1) & ~1;
-    const int w0 = tid * unit < words ? tid * unit : words, w1 = w0 + unit < words ? w0 + unit : words;
+    const int all_pairs = words / 2, pairs = unit_of(words) / 2;
+    const int p0 = tid * pairs < all_pairs ? tid * pairs : all_pairs, p1 = p0 + pairs < all_pairs ? p0 + pairs : all_pairs;
     uint32_t n_open = 0, n_live = 0;
-    for (int w = w0; w < w1; ++w) {
-        live[w] &= open[w];
-        n_open += __popc(open[w]);
-        n_live += __popc(live[w]);
+    for (int p = p0; p < p1; ++p) {
+        const uint64_t o = ~open2[p], l = live2[p] & o;  // held until here
+        reinterpret_cast<uint64_t*>(open)[p] = o;
+        reinterpret_cast<uint64_t*>(live)[p] = l;
+        n_open += __popcll(o);
+        n_live += __popcll(l);
     }
     uint32_t all_open, all_live;
     const uint32_t before_open = block_scan(n_open, wave_sum, all_open);
@@ -284,49 +555,39 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
     if (tid == 0 && all_live == 0) limit[0] = limit[1] = 0;
     if (before_open < all_live && before_open + n_open >= all_live) {  // the n-th open block is among this thread's
         uint32_t o = before_open, l = before_live;
-        for (int w = w0; w < w1; ++w) {
-            const uint32_t c = __popc(open[w]);
+        for (int p = p0; p < p1; ++p) {
+            const uint32_t c = __popcll(open2[p]);
             if (o + c >= all_live) {
-                const int b = nth_bit(open[w], all_live - o - 1);
-                limit[0] = w * 32 + b + 1;
-                limit[1] = l + __popc(live[w] & (~0u >> (31 - b)));
+                const int b = nth_bit(open2[p], all_live - o - 1);
+                limit[0] = p * 64 + b + 1;
+                limit[1] = l + __popcll(live2[p] & (~0ull >> (63 - b)));
                 break;
             }
             o += c;
-            l += __popc(live[w]);
+            l += __popcll(live2[p]);
         }
     }
     __syncthreads();
     const uint32_t bound = limit[0], below = limit[1], wanted = all_live - below;
     const uint32_t moved = (int64_t)wanted < a.max_moves ? wanted : (uint32_t)a.max_moves;
 
-    // Bits of word w at or past the bound.
-    auto past = [&](int w) {
-        const int d = (int)bound - w * 32;
-        return d <= 0 ? ~0u : d >= 32 ? 0u : ~0u << d;
+    // Bits of pair p at or past the bound.
+    auto past = [&](int p) {
+        const int d = (int)bound - p * 64;
+        return d <= 0 ? ~0ull : d >= 64 ? 0ull : ~0ull << d;
     };
     // The live blocks before block b.
     auto live_rank = [&](uint32_t b) {
-        const int w = b >> 5, u = w / unit;
+        const int p = b >> 6, u = p / pairs, q = u * pairs;
         uint32_t r = live_before[u];
-        for (int v = u * unit; v < w; ++v) r += __popc(live[v]);
-        return r + __popc(live[w] & ~(~0u << (b & 31)));
+#pragma unroll
+        for (int i = 0; i < kMaxUnitPairs; ++i) r += q + i < p ? __popcll(live2[q + i]) : 0;
+        return r + __popcll(live2[p] & ~(~0ull << (b & 63)));
     };
     // The r-th free block (r below `wanted`: it lies below the bound).
     auto free_block = [&](uint32_t r) {
-        int lo = 0, hi = (words + unit - 1) / unit;  // the last unit with at most r free blocks before it
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (open_before[mid] - live_before[mid] <= r) lo = mid; else hi = mid;
-        }
-        r -= open_before[lo] - live_before[lo];
-        int w = lo * unit;
-        for (;; ++w) {
-            const uint32_t c = __popc(open[w] & ~live[w]);
-            if (r < c) break;
-            r -= c;
-        }
-        return w * 32 + nth_bit(open[w] & ~live[w], r);
+        return find_rank(r, pairs, all_pairs, [&](int p) { return open2[p] & ~live2[p]; },
+                         [&](int u) { return open_before[u] - live_before[u]; });
     };
 
     const int64_t at = (int64_t)blockIdx.x * kPoolBlock + tid, step = (int64_t)gridDim.x * kPoolBlock;
@@ -337,19 +598,16 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
     for (int64_t r = all_free + at; r < a.n_free; r += step) a.free_blocks[r] = -1;
     // Moves: sources by their rank past the bound, destinations by theirs below.
     {
-        const int units = (words + unit - 1) / unit, per = (units + parts - 1) / parts;
+        const int units = (all_pairs + pairs - 1) / pairs, per = (units + parts - 1) / parts;
         const int u0 = part * per, u1 = u0 + per < units ? u0 + per : units;
         if (u0 < u1) {
             uint32_t o = open_before[u0], l = live_before[u0];
-            const int e = u1 * unit < words ? u1 * unit : words;
-            for (int w = u0 * unit; w < e; w += 2) {
-                const bool two = w + 1 < e;
-                const uint64_t ob = (uint64_t)(two ? open[w + 1] : 0) << 32 | open[w];
-                const uint64_t lb = (uint64_t)(two ? live[w + 1] : 0) << 32 | live[w];
-                const uint64_t pb = (uint64_t)(two ? past(w + 1) : 0) << 32 | past(w);
+            const int e = u1 * pairs < all_pairs ? u1 * pairs : all_pairs;
+            for (int p = u0 * pairs; p < e; ++p) {
+                const uint64_t ob = open2[p], lb = live2[p], pb = past(p);
                 const uint32_t lr = l + mbcnt64(lb), fr = o + mbcnt64(ob) - lr;  // live and free ones before this lane's
                 const bool is_open = ob >> lane & 1, is_live = lb >> lane & 1, is_past = pb >> lane & 1;
-                const int id = w * 32 + lane;
+                const int id = p * 64 + lane;
                 if (is_live && is_past && lr - below < moved) a.moves[2 * (int64_t)(lr - below)] = id;
                 if (is_open && !is_live && !is_past && fr < moved) a.moves[2 * (int64_t)fr + 1] = id;
                 // Free afterwards: what was free and is not taken, and what was left.
@@ -366,85 +624,115 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
             }
         }
     }
-    for (int64_t i = part; i < a.rows; i += parts) {
-        const Lengths n = lengths(a.ctx_lens[i], a.block_size, a.cols);
-        for (int j = lane; j < a.cols; j += kWave) {
-            int id = -1;
-            if (j < n.need) id = a.table[i * a.ld_table + j];
-            if ((uint32_t)id >= (uint32_t)a.pool) id = -1;
-            if (id >= 0 && (uint32_t)id >= bound && get_bit(live, id)) {
-                const uint32_t r = live_rank(id) - below;
-                if (r < moved) id = free_block(r);
-            }
-            a.out_table[i * a.ld_out + j] = id;
+    // A lookup takes some hundred cycles, so a lane takes one entry at a time, a wave
+    // 64 neighbours of a row.
+    const int64_t segments = (a.cols + kWave - 1) / kWave;
+    for (int64_t u = part; u < a.rows * segments; u += parts) {
+        const int64_t row = u / segments;
+        const int j = (int)(u - row * segments) * kWave + lane;
+        if (j >= a.cols) continue;
+        int id = a.table[row * a.ld_table + j];
+        if (j >= lengths(a.ctx_lens[row], a.block_size, a.cols).need || (uint32_t)id >= (uint32_t)a.pool) id = -1;
+        if (id >= 0 && (uint32_t)id >= bound && get_bit(live, id)) {
+            const uint32_t k = live_rank(id) - below;
+            if (k < moved) id = free_block(k);
         }
+        a.out_table[row * a.ld_out + j] = id;
     }
 }
 
-int launch_compact_blocks(const CompactArgs& a, hipStream_t s) {
-    const int64_t work = a.rows * (int64_t)a.cols + a.n_free + 2 * a.max_moves;
-    const int64_t grid = work / 16384 < 1 ? 1 : work / 16384 < 64 ? work / 16384 : 64;
-    const size_t lds = (size_t)((a.pool + 31) / 32) * 8;
-    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)grid), dim3(kPoolBlock), lds, s, a);
+size_t compact_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
+    const int parts = mark_parts(rows, cols);
+    return parts ? (size_t)(parts + 1) * words_of(pool) * 4 : 0;  // one for the held blocks
+}
+
+int launch_compact_blocks(const CompactArgs& a, void* workspace, hipStream_t s) {
+    const size_t words = words_of(a.pool);
+    const int parts = workspace ? mark_parts(a.rows, a.cols) : 0;
+    uint32_t* fields = static_cast<uint32_t*>(workspace);
+    if (parts) {
+        hipLaunchKernelGGL(mark_compact_kernel, dim3(parts * kQuarters), dim3(kPoolBlock), mark_lds(a.pool), s, a, fields);
+        if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+    }
+    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)pool_grid(a.rows * (int64_t)a.cols + a.n_free + 2 * a.max_moves)),
+                       dim3(kPoolBlock), words * 8, s, a, fields, parts);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
-// Block copies.  A unit is up to kCopySlice bytes of one pair's block in one
-// cache; workgroups take units in turn.
+// Block copies.  A workgroup takes 16 KB (kCopySlice) of a pair's block in one
+// cache: four loads a thread, then four stores.
 constexpr int kCopyBlock = 256;
-constexpr int kCopySlice = 16384;
+constexpr int kCopyEach = 4;
+constexpr int kCopySlice = kCopyBlock * kCopyEach * 16;
 
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+
+// Words [first, last) of the block, row_words of them a row of ld bytes.
 template <typename T>
-__device__ __forceinline__ void copy_words(char* data, int64_t src, int64_t dst, int64_t ld, int64_t row_words, int64_t first,
+__device__ __forceinline__ void copy_words(const char* src, char* dst, int64_t ld, int64_t row_words, int64_t first,
                                            int64_t last) {
-    // Words [first, last) of the block, row_words of them a row of ld bytes.
-    constexpr int kAhead = 4;
-    for (int64_t i0 = first + threadIdx.x; i0 < last; i0 += kCopyBlock * kAhead) {
-        T v[kAhead] = {};
-        int64_t at[kAhead];
+    // Whole slices of rows that follow each other.
+    if (last <= row_words && last - first == kCopyBlock * kCopyEach) {
+        const int64_t at = (first + threadIdx.x) * (int64_t)sizeof(T);
+        T v[kCopyEach];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int64_t i = i0 + u * kCopyBlock;
-            at[u] = last <= row_words ? i * (int64_t)sizeof(T)  // one row: no division
-                                      : i / row_words * ld + i % row_words * (int64_t)sizeof(T);
-            if (i < last) v[u] = *reinterpret_cast<const T*>(data + src * ld + at[u]);
-        }
+        for (int u = 0; u < kCopyEach; ++u) v[u] = *reinterpret_cast<const T*>(src + at + u * kCopyBlock * (int64_t)sizeof(T));
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (i0 + u * kCopyBlock < last) *reinterpret_cast<T*>(data + dst * ld + at[u]) = v[u];
+        for (int u = 0; u < kCopyEach; ++u) *reinterpret_cast<T*>(dst + at + u * kCopyBlock * (int64_t)sizeof(T)) = v[u];
+        return;
+    }
+    for (int64_t i = first + threadIdx.x; i < last; i += kCopyBlock) {
+        const int64_t row = last <= row_words ? 0 : i / row_words, at = row * ld + (i - row * row_words) * (int64_t)sizeof(T);
+        *reinterpret_cast<T*>(dst + at) = *reinterpret_cast<const T*>(src + at);
     }
 }
 
-__global__ __launch_bounds__(kCopyBlock) void copy_blocks_kernel(CopyArgs a) {
-    const int64_t units = a.n_pairs * a.slices;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t s = u / a.n_pairs, pair = u - s * a.n_pairs;
-        const int2 p = reinterpret_cast<const int2*>(a.pairs)[pair];
-        if (p.x < 0 || p.y < 0 || p.x == p.y) continue;
+// blockIdx.x: pairs, blockIdx.y: slices of all caches' blocks, both in turn.
+// CACHES: how many the arguments have room for (a few hundred bytes of
+// arguments are read sooner than a few thousand).
+template <int CACHES>
+__global__ __launch_bounds__(kCopyBlock) void copy_blocks_kernel(CopyArgs<CACHES> a) {
+    for (int64_t s = blockIdx.y; s < a.slices; s += gridDim.y) {
         int c = 0;
         while (c + 1 < a.n_caches && s >= a.cache[c + 1].slice0) ++c;
-        const CopyCache& k = a.cache[c];
-        const int64_t src = p.x * a.stride_rows, dst = p.y * a.stride_rows;
-        if (src > k.rows - a.block_size || dst > k.rows - a.block_size) continue;
-        const int64_t all = k.words, per = kCopySlice / k.word;
-        const int64_t first = (s - k.slice0) * per, last = first + per < all ? first + per : all;
-        if (k.word == 16) copy_words<uint4>(k.data, src, dst, k.ld, k.row_words, first, last);
-        else if (k.word == 4) copy_words<uint32_t>(k.data, src, dst, k.ld, k.row_words, first, last);
-        else if (k.word == 2) copy_words<uint16_t>(k.data, src, dst, k.ld, k.row_words, first, last);
-        else copy_words<uint8_t>(k.data, src, dst, k.ld, k.row_words, first, last);
+        const CopyCache k = a.cache[c];
+        const int64_t per = kCopySlice / k.word, first = (s - k.slice0) * per;
+        const int64_t last = first + per < k.words ? first + per : k.words;
+        for (int64_t pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) {
+            const int2 p = reinterpret_cast<const int2*>(a.pairs)[pair];
+            if (p.x < 0 || p.y < 0 || p.x == p.y) continue;
+            const int64_t from = p.x * a.stride_rows, to = p.y * a.stride_rows;
+            if (from > k.rows - a.block_size || to > k.rows - a.block_size) continue;
+            const char* src = k.data + from * k.ld;
+            char* dst = k.data + to * k.ld;
+            if (k.word == 16) copy_words<words4>(src, dst, k.ld, k.row_words, first, last);
+            else if (k.word == 4) copy_words<uint32_t>(src, dst, k.ld, k.row_words, first, last);
+            else if (k.word == 2) copy_words<uint16_t>(src, dst, k.ld, k.row_words, first, last);
+            else copy_words<uint8_t>(src, dst, k.ld, k.row_words, first, last);
+        }
     }
 }
 
-int launch_copy_blocks(CopyArgs& a, hipStream_t s) {
+template <int CACHES>
+static int launch_copy(const CopyArgs<kMaxCopyCaches>& all, hipStream_t s) {
+    CopyArgs<CACHES> a;
+    a.pairs = all.pairs, a.n_pairs = all.n_pairs, a.stride_rows = all.stride_rows, a.slices = all.slices;
+    a.n_caches = all.n_caches, a.block_size = all.block_size;
+    for (int c = 0; c < all.n_caches; ++c) a.cache[c] = all.cache[c];
+    const unsigned y = a.slices < 4096 ? (unsigned)a.slices : 4096, most = 8192 / y > 1 ? 8192 / y : 1;
+    const unsigned x = a.n_pairs < most ? (unsigned)a.n_pairs : most;
+    hipLaunchKernelGGL(copy_blocks_kernel<CACHES>, dim3(x, y), dim3(kCopyBlock), 0, s, a);
+    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+}
+
+int launch_copy_blocks(CopyArgs<kMaxCopyCaches>& a, hipStream_t s) {
     a.slices = 0;
     for (int c = 0; c < a.n_caches; ++c) {
-        a.cache[c].slice0 = a.slices;
-        a.slices += (a.cache[c].words * a.cache[c].word + kCopySlice - 1) / kCopySlice;
+        CopyCache& k = a.cache[c];
+        k.slice0 = a.slices;
+        a.slices += (k.words * k.word + kCopySlice - 1) / kCopySlice;
     }
-    const int64_t units = a.n_pairs * a.slices;
-    const int64_t grid = units < 4096 ? units : 4096;
-    hipLaunchKernelGGL(copy_blocks_kernel, dim3((unsigned)grid), dim3(kCopyBlock), 0, s, a);
-    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+    return a.n_caches <= 4 ? launch_copy<4>(a, s) : launch_copy<kMaxCopyCaches>(a, s);
 }
 
 }  // namespace rts

@@ -205,7 +205,8 @@ struct ForkArgs {
     int64_t rows_in, ld_table, rows_out, ld_out, n_free;
     int32_t cols, block_size, pool;
 };
-int launch_fork_blocks(const ForkArgs& a, hipStream_t stream);
+size_t fork_blocks_bytes(int64_t rows_in, int32_t cols, int32_t pool);  // of a workspace; 0: takes none
+int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t stream);
 
 struct CompactArgs {
     const int32_t *table, *ctx_lens;
@@ -214,7 +215,8 @@ struct CompactArgs {
     int64_t rows, ld_table, ld_out, n_free, max_moves;
     int32_t cols, block_size, pool;
 };
-int launch_compact_blocks(const CompactArgs& a, hipStream_t stream);
+size_t compact_blocks_bytes(int64_t rows, int32_t cols, int32_t pool);
+int launch_compact_blocks(const CompactArgs& a, void* workspace, hipStream_t stream);
 
 constexpr int kMaxCopyCaches = 64;  // they travel as kernel arguments
 struct CopyCache {
@@ -224,13 +226,14 @@ struct CopyCache {
     int64_t slice0;            // set by the launch
     int32_t word;
 };
+template <int CACHES>
 struct CopyArgs {
     const int32_t* pairs;
     int64_t n_pairs, stride_rows, slices;
     int32_t n_caches, block_size;
-    CopyCache cache[kMaxCopyCaches];
+    CopyCache cache[CACHES];
 };
-int launch_copy_blocks(CopyArgs& a, hipStream_t stream);
+int launch_copy_blocks(CopyArgs<kMaxCopyCaches>& a, hipStream_t stream);
 
 struct KvArgs {
     const uint16_t* q;

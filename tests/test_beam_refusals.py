@@ -39,7 +39,7 @@ def test_beam_select():
 
 def fork(**kw):
     a = dict(table=P, rows_in=4, cols=8, ld=8, ctx=P, parents=P, rows_out=4, block=16, pool=100, held=P, out=P, ld_out=8,
-             lens=P, copies=P, free=P, n_free=10, counts=P)
+             lens=P, copies=P, free=P, n_free=10, counts=P, ws=None, ws_bytes=0)
     a.update(kw)
     return lib.fork_blocks(*a.values(), None)
 
@@ -53,11 +53,16 @@ def test_fork_blocks():
     assert fork(copies=ctypes.c_void_p(0x10004)) == EINVAL
     for kw in (dict(rows_in=4097), dict(rows_out=4097), dict(pool=(1 << 19) + 1)):
         assert fork(**kw) == EUNSUP, kw
+    assert fork(ws_bytes=4) == EINVAL and fork(ws=ODD, ws_bytes=4) == EINVAL
+    size = lib.fork_blocks_workspace_size
+    assert size(4, 8, 100) == 0 and size(4097, 8, 100) == 0 and size(4096, 800, (1 << 19) + 1) == 0
+    need = size(4096, 800, 5000)
+    assert need > 0 and fork(rows_in=4096, cols=800, ld=800, ld_out=800, pool=5000, ws=P, ws_bytes=need - 4) == EWS
 
 
 def compact(**kw):
     a = dict(table=P, rows=4, cols=8, ld=8, ctx=P, block=16, pool=100, held=P, out=P, ld_out=8, moves=P, max_moves=50,
-             free=P, n_free=10, counts=P)
+             free=P, n_free=10, counts=P, ws=None, ws_bytes=0)
     a.update(kw)
     return lib.compact_blocks(*a.values(), None)
 
@@ -71,6 +76,11 @@ def test_compact_blocks():
     assert compact(moves=ctypes.c_void_p(0x10004)) == EINVAL
     for kw in (dict(rows=1 << 31), dict(pool=(1 << 19) + 1)):
         assert compact(**kw) == EUNSUP, kw
+    assert compact(ws_bytes=4) == EINVAL and compact(ws=ODD, ws_bytes=4) == EINVAL
+    size = lib.compact_blocks_workspace_size
+    assert size(4, 8, 100) == 0 and size(1 << 31, 8, 100) == 0 and size(4096, 800, (1 << 19) + 1) == 0
+    need = size(10000, 800, 5000)
+    assert need > 0 and compact(rows=10000, cols=800, ld=800, ld_out=800, pool=5000, ws=P, ws_bytes=need - 4) == EWS
 
 
 def copy(caches=((0x10000, 64, 32, 32),), **kw):
