@@ -712,8 +712,8 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
  * dim        64, 128 or 256.
  * k_scales, v_scales  float [kv_heads] or NULL (= 1).
  * window     positions seen at most, 0 for all.
- * max_len    an upper bound of row_ends; it sets how the keys are split, results
- *            hold for any value >= 0.
+ * max_len    an upper bound of row_ends; it says whether the keys are worth
+ *            splitting, results hold for any value >= 0.
  * scale      any number from -2^127 to 2^127, and so its products with k_scales.
  * out        bf16 [rows, heads, dim], contiguous.   lse  float [rows, heads] or NULL.
  * workspace  as in latent_attend_rows, kv_attend_paged_workspace_size bytes.
@@ -721,7 +721,7 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
  * Scores, softmax statistics and sums are held in 32 bits; the weights are
  * rounded to bf16 for the products with the values.
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 1024, cache_rows >= 2^31,
- *         ld_cache > 2^30), RTS_EWORKSPACE, RTS_EHIP.
+ *         ld_cache > 2^30, a cache of 2^36 bytes or more), RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t kv_attend_paged_workspace_size(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype,
                                       int64_t max_len, int64_t window);
@@ -735,8 +735,10 @@ int kv_attend_paged(const void* q, int64_t rows, int32_t heads, int64_t ld_q, in
 
 /*
  * kv_attend_paged_plan -- how that call would be cut, to read a profile or to choose
- * the sizes of a test by: plan[0] pieces of a row's keys at most, plan[1] keys of a
- * piece.  split: whether the call has a workspace.  Host only; rows at least 1.
+ * the sizes of a test by: plan[0] pieces that the rows' keys are cut into, about (0: a
+ * row is one piece), plan[1] keys of a piece at least.  A call cuts all rows into
+ * pieces of one size, by the lengths that it finds on the device.  split: whether
+ * the call has a workspace.  Host only; rows at least 1.
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED as that call.
  */
 int kv_attend_paged_plan(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,

@@ -654,7 +654,7 @@ int kv_attend_paged_plan(int64_t rows, int32_t heads, int32_t kv_heads, int32_t 
         return RTS_EINVAL;
     if (heads > 1024 || rows > 0x7FFFFFFFll / heads || (dim != 64 && dim != 128 && dim != 256)) return RTS_EUNSUPPORTED;
     const rts::KvPlan p = rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), split != 0);
-    plan[0] = p.splits, plan[1] = p.piece;
+    plan[0] = p.target, plan[1] = rts::kKvLeastKeys;
     return RTS_OK;
 }
 

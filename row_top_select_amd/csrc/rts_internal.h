@@ -249,9 +249,10 @@ struct KvArgs {
     Pages pages;
 };
 
+constexpr int kKvLeastKeys = 128;  // of a piece
 struct KvPlan {
-    int splits;   // pieces of a row's keys, joined by a second kernel when > 1
-    int64_t piece;  // keys of a piece
+    int target;       // pieces that the rows' keys are to be cut into, joined by a second kernel; 0: a row is one
+    int rounds;       // as many times that, where they are long
     size_t ws_bytes;
 };
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,

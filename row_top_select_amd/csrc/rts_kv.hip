@@ -13,8 +13,8 @@
 // A wave has keys of its own, every kKvWaves-th tile of the workgroup's piece, and a
 // ring of two tiles in LDS, loaded straight from memory by whole rows; nothing
 // passes between waves until the end, where they join their sums through LDS.
-// Rows that a token does not see are read from a row of zeros, so that nothing of
-// theirs reaches a result.
+// Rows that a token does not see score -inf and their values are cleared in LDS,
+// so that nothing of theirs reaches a result.
 #include <type_traits>
 
 #include "rts_device.hpp"
@@ -35,6 +35,9 @@ constexpr int kKvStages = 2;
 constexpr int kKvWaves = 2;
 constexpr int kKvBlock = kKvWaves * kWave;
 constexpr int kKvHeads = 16;    // query heads of a workgroup
+constexpr int kKvLeast = kKvLeastKeys / kKvTile;  // tiles of a piece
+constexpr int kKvGoal = 48;
+constexpr int kKvRounds = 8;    // pieces a place at most
 constexpr int kKvEntries = 4;   // tiles of block-table entries that a wave holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -60,7 +63,30 @@ struct KvShape {
     }
 };
 
-__device__ const uint4 g_zero_kv[512 / 16] = {};  // where rows that are not seen are read from
+// The pieces' results: [part][heads][D], [part][heads], and each row's first part and number of pieces.
+struct KvParts {
+    float *out, *lse;
+    int2* rows;
+};
+
+__device__ __forceinline__ float wave_sum(float x) {
+    return __uint_as_float(wave_reduce32(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+__device__ const uint4 g_no_row[512 / 16] = {};  // stands in for a cache without rows
+
+// 16 bytes a lane from base + offset to LDS at `to` + 16 * lane; as load_to_lds
+// otherwise.  BIG: the offset counts 16 bytes.
+template <bool BIG>
+__device__ __forceinline__ void load_row(const char* base, uint32_t offset, uint32_t to) {
+    if constexpr (BIG) {
+        load_to_lds<16, 0>(base + ((uint64_t)offset << 4), to);
+    } else {
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(base) : "memory");
+    }
+}
 
 __device__ __forceinline__ int kv_widen2(int w, bool hi) {
     return hi ? __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
@@ -81,14 +107,16 @@ __device__ __forceinline__ float over_groups(float x, Op op) {
     return op(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
+__device__ __forceinline__ void lds_write(uint32_t at, i32x4 v) {
+    *(__attribute__((address_space(3))) i32x4*)(uintptr_t)at = v;
+}
+
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int splits, int64_t piece_keys,
-                                                             float* __restrict__ part_out,
-                                                             float* __restrict__ part_lse) {
+template <int D, bool E4M3, bool BIG>
+__global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int target, int rounds, KvParts parts) {
     using S = KvShape<D, E4M3>;
     constexpr int NK = D / 32, NT = D / 16;  // steps of the first product, tiles of the second
     extern __shared__ __align__(1024) char lds_memory[];
@@ -96,34 +124,103 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t ring = lds_address(lds_memory) + wave * S::kWaveB, entries = ring + kKvStages * S::kStageB;
 
-    // blockIdx: key heads, then blocks of 16 query heads, tokens, pieces.
+    // blockIdx: key heads, then blocks of 16 query heads, then pieces of tokens.
     const int group = a.heads / a.kv_heads, blocks = (group + kKvHeads - 1) / kKvHeads;
     uint32_t rest = blockIdx.x;
     const int kvh = rest % a.kv_heads;
     rest /= a.kv_heads;
     const int block = rest % blocks;
-    rest /= blocks;
-    const int64_t token = rest % (uint32_t)a.rows;
-    const int split = rest / (uint32_t)a.rows;
+    const int64_t unit = rest / blocks;
 
-    const int req = a.req_id[token];
-    int end = a.row_ends[token], begin = 0;
-    {
+    // What a token sees.
+    struct Row { int req, begin, end; };
+    auto row = [&](int64_t t) {
+        Row r{-1, 0, 0};
+        if (t >= a.rows) return r;
+        const int req = a.req_id[t];
+        int end = a.row_ends[t];
         const int64_t held = (int64_t)a.pages.cols * a.pages.block_size;
         if (end > held) end = (int)held;
         if (end < 0 || req < 0 || req >= a.pages.table_rows) end = 0;
-        if (a.window > 0 && end > a.window) begin = end - (int)a.window;
+        r.req = req;
+        r.end = end;
+        if (a.window > 0 && end > a.window) r.begin = end - (int)a.window;
+        return r;
+    };
+    int64_t token = unit;
+    Row seen;
+    int piece = 0, pieces = 1, part = 0;  // of the token's; its first part's place
+    int p0, p1;
+    if (target == 0) {
+        seen = row(unit);
+        p0 = seen.begin, p1 = seen.end;
+    } else {
+        // Lengths differ and are known here only, so the pieces are of one size for
+        // all tokens: one that gives the chip's places (`target` units) a piece each,
+        // or more of kKvGoal tiles each, up to `rounds` a place.  A running sum of
+        // the tokens' pieces, 64 tokens at a time, says which one this workgroup has.
+        const Row of_lane = row(lane);  // the first 64 are read once
+        auto rows = [&](int64_t t0) { return t0 == 0 ? of_lane : row(t0 + lane); };
+        auto tiles_of = [](const Row& r) { return (r.end - r.begin) / kKvTile + ((r.end - r.begin) % kKvTile != 0); };
+        auto count_of = [](int tiles, int chunk) {
+            return tiles > chunk ? (int)((uint32_t)(tiles + chunk - 1) / (uint32_t)chunk) : 1;
+        };
+        float total = 0.f;
+        for (int64_t t0 = 0; t0 < a.rows; t0 += kWave) total += wave_sum((float)tiles_of(rows(t0)));
+        const float most = total * 1.0001f / (float)(target * rounds);  // more pieces have no room
+        float size = total / (float)target;
+        size = fmaxf(fminf(size, (float)kKvGoal), fmaxf(most, (float)kKvLeast));
+        int chunk = __builtin_amdgcn_readfirstlane((int)fminf(size, 1e9f) + 1);
+        // Where a place has one piece, rounding must not leave a few for another round.
+        if (size * (float)target > total * 0.75f)
+            for (int tries = 0; tries < 4; ++tries) {
+                float sum = 0.f;
+                for (int64_t t0 = 0; t0 < a.rows; t0 += kWave) {
+                    const int tiles = tiles_of(rows(t0));
+                    sum += wave_sum(t0 + lane < a.rows ? (float)count_of(tiles, chunk) : 0.f);
+                }
+                if (sum <= (float)target) break;
+                chunk += chunk / 16 + 1;
+            }
+        uint32_t before = 0, part_before = 0;
+        token = -1;
+        for (int64_t t0 = 0; t0 < a.rows; t0 += kWave) {
+            const Row r = rows(t0);
+            const int tiles = tiles_of(r);
+            const uint32_t n = t0 + lane >= a.rows ? 0 : count_of(tiles, chunk);
+            const uint32_t several = n > 1 ? n : 0;
+            const uint32_t upto = wave_incl_scan32(n), part_upto = wave_incl_scan32(several);
+            const uint64_t past = __ballot(before + upto > unit);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                token = t0 + at;
+                seen = Row{__builtin_amdgcn_readlane(r.req, at), __builtin_amdgcn_readlane(r.begin, at),
+                           __builtin_amdgcn_readlane(r.end, at)};
+                pieces = __builtin_amdgcn_readlane(n, at);
+                piece = (int)(unit - before - __builtin_amdgcn_readlane(upto - n, at));
+                part = part_before + __builtin_amdgcn_readlane(part_upto - several, at);
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, kWave - 1);
+            part_before += __builtin_amdgcn_readlane(part_upto, kWave - 1);
+        }
+        if (token < 0) return;
+        // Even pieces, in whole tiles.
+        const int64_t each = (int64_t)((uint32_t)(tiles_of(seen) + pieces - 1) / (uint32_t)pieces) * kKvTile;
+        const int64_t from = seen.begin + piece * each, to = from + each;
+        p0 = (int)(from < seen.end ? from : seen.end);
+        p1 = (int)(to < seen.end ? to : seen.end);
+        if (piece == 0 && kvh == 0 && block == 0 && tid == 0) parts.rows[token] = int2{part, pieces};
     }
-    const int64_t seen = end - begin;
-    int pieces = 1;
-    if (splits > 1 && seen > piece_keys) {
-        const int64_t n = (seen + piece_keys - 1) / piece_keys;
-        pieces = n < splits ? (int)n : splits;
+    const int head = kvh * group + block * kKvHeads + col;
+    const bool head_ok = block * kKvHeads + col < group;
+    i32x4 raw_q[NK];  // under way beside what leads to the first tile
+    {
+        const uint16_t* qp = a.q + token * a.ld_q + (int64_t)(head_ok ? head : kvh * group) * a.ld_qhead + g * 8;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) raw_q[i] = *reinterpret_cast<const i32x4*>(qp + i * 32);
     }
-    if (split >= pieces) return;
-    const int p0 = begin + (int)(split * piece_keys);
-    const int p1 = split == pieces - 1 ? end : p0 + (int)piece_keys;  // the last has what is left, however much
-    const int32_t* const table = a.pages.table + (int64_t)(req < 0 ? 0 : req) * a.pages.ld;
+    const int32_t* const table = a.pages.table + (int64_t)(seen.req < 0 ? 0 : seen.req) * a.pages.ld;
     const int tiles = (p1 - p0) / kKvTile + ((p1 - p0) % kKvTile != 0);
     const int count = (tiles - wave + kKvWaves - 1) / kKvWaves;  // of this wave
 
@@ -145,25 +242,26 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
         const uint32_t e = tile_at(n) + (lane & 31);
         return n < count && e < (uint32_t)p1 ? phys_row(a.pages, entry, e) : -1;
     };
-    const int64_t esz = E4M3 ? 1 : 2, ldb = a.ld_cache * esz;
-    const char* const keys = static_cast<const char*>(a.k) + kvh * a.ld_head * esz;
-    const char* const values = static_cast<const char*>(a.v) + kvh * a.ld_head * esz;
-    // Loads tile n into its stage; row: what row_of(n) gives.
+    constexpr int kEsz = E4M3 ? 1 : 2;
+    const bool no_rows = a.pages.cache_rows == 0;
+    const char* const keys = no_rows ? reinterpret_cast<const char*>(g_no_row) : static_cast<const char*>(a.k) + kvh * a.ld_head * kEsz;
+    const char* const values = no_rows ? reinterpret_cast<const char*>(g_no_row) : static_cast<const char*>(a.v) + kvh * a.ld_head * kEsz;
+    const uint32_t row_step = (uint32_t)(a.ld_cache * kEsz / (BIG ? 16 : 1));
+    // Loads tile n into its stage; row: what row_of(n) gives.  In place of a row
+    // that is not seen comes the cache's first.
     auto fetch = [&](int n, int row) {
-        const uint32_t to = ring + (n & (kKvStages - 1)) * S::kStageB;
-        const char* from[2][S::kLoads];
+        const uint32_t to = ring + (n & (kKvStages - 1)) * S::kStageB, mine = row < 0 ? 0 : (uint32_t)row * row_step;
+        uint32_t at[S::kLoads];
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
             const int key = i * S::kRowsEach + lane / S::kChunks;
-            const int r = __builtin_amdgcn_ds_bpermute(key * 4, row);
-            const int chunk = ((lane % S::kChunks) ^ S::swizzle(key)) * 16;
-            from[0][i] = (r < 0 ? reinterpret_cast<const char*>(g_zero_kv) : keys + r * ldb) + chunk;
-            from[1][i] = (r < 0 ? reinterpret_cast<const char*>(g_zero_kv) : values + r * ldb) + chunk;
+            const uint32_t chunk = (lane % S::kChunks) ^ S::swizzle(key);
+            at[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(key * 4, mine) + chunk * (BIG ? 1 : 16);
         }
 #pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) load_to_lds<16, 0>(from[0][i], to + i * 1024);
+        for (int i = 0; i < S::kLoads; ++i) load_row<BIG>(keys, at[i], to + i * 1024);
 #pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) load_to_lds<16, 0>(from[1][i], to + S::kHalfB + i * 1024);
+        for (int i = 0; i < S::kLoads; ++i) load_row<BIG>(values, at[i], to + S::kHalfB + i * 1024);
     };
     auto exists = [&](int row) { return (uint32_t)__ballot(row >= 0); };
 
@@ -183,16 +281,12 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
     }
 
     // Lane group g holds elements 32 i + 8 g .. + 8 of its query head.
-    const int head = kvh * group + block * kKvHeads + col;
-    const bool head_ok = block * kKvHeads + col < group;
     bf16x8 q[NK];
     {
-        const uint16_t* qp = a.q + token * a.ld_q + (int64_t)head * a.ld_qhead + g * 8;
         const uint32_t flip = factor < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            i32x4 v = {};
-            if (head_ok) v = *reinterpret_cast<const i32x4*>(qp + i * 32);
+            i32x4 v = head_ok ? raw_q[i] : i32x4{};
             if (factor == 0.f) {  // 0, or NaN for what is not finite
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -227,9 +321,15 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
             }
         const uint32_t see = exist;
         if (see != ~0u) {
+            // What is not seen scores -inf, and its values, whatever they are, become 0.
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 if (!(see >> ((r >> 2) * 16 + 4 * g + (r & 3)) & 1)) s[r >> 2][r & 3] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < S::kLoads; ++i)
+                if (!(see >> (i * S::kRowsEach + lane / S::kChunks) & 1))
+                    lds_write(at + S::kHalfB + i * 1024 + lane * 16, i32x4{0, 0, 0, 0});
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
         float top = s[0][0];
 #pragma unroll
@@ -244,12 +344,13 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
             for (int t = 0; t < NT; ++t) o[t] *= f;
             m = to;
         }
-        bf16x8 p;
+        bf16x8 p, low;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
             const float x = __builtin_amdgcn_exp2f((s[r >> 2][r & 3] - m) * c);
             l += x;
             p[r] = (__bf16)x;
+            low[r] = (__bf16)(x - (float)p[r]);
         }
         const uint32_t v_at = at + S::kHalfB;
 #pragma unroll
@@ -276,6 +377,7 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
                 v = __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
             }
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, o[t], 0, 0, 0);
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, low, o[t], 0, 0, 0);
         }
         // The stage is read, and tile n + 2's entries have arrived.
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * S::kLoads) : "memory");
@@ -323,62 +425,153 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int split
         const float inv = total == 0.f ? 0.f : v_scale / total;
         const float lse = total == 0.f ? -INFINITY : most * fabsf(factor) + __builtin_amdgcn_logf(total) * kLn2;
         const int64_t rh = token * a.heads + kvh * group + block * kKvHeads + h;
-        if (splits == 1) {
+        if (pieces == 1) {
             if (d8 == 0 && a.lse) a.lse[rh] = lse;
             *reinterpret_cast<uint4*>(a.out + rh * D + d8 * 8) =
                 uint4{bf16_pair(sum[0][0] * inv, sum[0][1] * inv), bf16_pair(sum[0][2] * inv, sum[0][3] * inv),
                       bf16_pair(sum[1][0] * inv, sum[1][1] * inv), bf16_pair(sum[1][2] * inv, sum[1][3] * inv)};
             continue;
         }
-        const int64_t n = a.rows * a.heads, part = split * n + rh;
+        const int64_t at = (int64_t)(part + piece) * a.heads + kvh * group + block * kKvHeads + h;
         const bool empty = total == 0.f && most == kNoMax;  // nothing was seen
-        if (d8 == 0) {
-            part_lse[part] = total == 0.f && !empty ? kNoMax : lse;  // the join reads its zeros and NaN
-            if (split == 0)  // the join sees `splits` parts of every row
-                for (int p = pieces; p < splits; ++p) part_lse[p * n + rh] = -INFINITY;
-        }
+        if (d8 == 0) parts.lse[at] = total == 0.f && !empty ? kNoMax : lse;  // the join reads its zeros and NaN
         if (empty) continue;  // the join reads no values of an empty part
-        float* const to = part_out + part * D + d8 * 8;
+        float* const to = parts.out + at * D + d8 * 8;
         reinterpret_cast<f32x4*>(to)[0] = sum[0] * inv;
         reinterpret_cast<f32x4*>(to)[1] = sum[1] * inv;
     }
 }
 
+// The join of a row and head's pieces: out = sum_s e^(lse_s - lse) part_s.  A
+// workgroup takes W elements of one, its threads 4 of them each of every n-th piece,
+// with a running maximum: what they read does not wait for anything.  (64 pieces
+// of 192 (row, head) pairs, one after the other, took 15 us.)
+constexpr int kJoinBlock = 256;
+
+template <int D, int W>
+__global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int heads, uint16_t* __restrict__ out,
+                                                             float* __restrict__ lse) {
+    constexpr int kColumns = W / 4, kSide = kJoinBlock / kColumns;  // pieces side by side
+    __shared__ f32x4 sums[kSide][kColumns];
+    __shared__ float totals[kSide], tops[kSide];
+    const int64_t rh = blockIdx.x, row = rh / heads;
+    const int col = threadIdx.x % kColumns, side = threadIdx.x / kColumns, d = blockIdx.y * W + col * 4;
+    const int2 of_row = parts.rows[row];
+    const int splits = of_row.y;
+    if (splits == 1) return;  // written by its one workgroup
+    const int64_t first = (int64_t)of_row.x * heads + (rh - row * heads);
+    const float* const stat = parts.lse + first;
+    const float* const from = parts.out + first * D + d;
+    float m = -INFINITY, total = 0.f;  // m is NaN if any piece's is
+    f32x4 acc = {};
+    constexpr int kAhead = 4;
+    for (int s0 = side; s0 < splits; s0 += kSide * kAhead) {
+        float x[kAhead];
+        f32x4 v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t s = s0 + u * kSide < splits ? s0 + u * kSide : side;
+            x[u] = stat[s * heads];
+            v[u] = *reinterpret_cast<const f32x4*>(from + s * heads * D);
+            if (s0 + u * kSide >= splits) x[u] = -INFINITY;
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) top = __builtin_elementwise_maximum(top, x[u]);
+        if (top == -INFINITY) continue;
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * kLog2e);
+        total *= f;
+        acc *= f;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (x[u] == -INFINITY) continue;  // an empty piece has no values
+            const float w = __builtin_amdgcn_exp2f((x[u] - m) * kLog2e);
+            total += w;
+            acc += v[u] * w;
+        }
+    }
+    sums[side][col] = acc;
+    if (col == 0) totals[side] = total, tops[side] = m;
+    __syncthreads();
+    if (side > 0) return;
+    float most = m;
+#pragma unroll
+    for (int i = 1; i < kSide; ++i) most = __builtin_elementwise_maximum(most, tops[i]);
+    acc = f32x4{};
+    total = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSide; ++i) {
+        if (tops[i] == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f((tops[i] - most) * kLog2e);
+        acc += sums[i][col] * f;
+        total += totals[i] * f;
+    }
+    const float inv = most == -INFINITY ? 0.f : 1.f / total;
+    *reinterpret_cast<uint2*>(out + rh * D + d) =
+        uint2{bf16_pair(acc[0] * inv, acc[1] * inv), bf16_pair(acc[2] * inv, acc[3] * inv)};
+    // kNoMax: keys were seen, all with scores of -inf.
+    if (lse && d == 0) lse[rh] = most <= kNoMax ? -INFINITY : most + __builtin_amdgcn_logf(total) * kLn2;
+}
+
+// Workgroups that a CU has room for, by their LDS.
+static int kv_places(int32_t dim, int dtype) {
+    const int wave_bytes = kKvStages * 2 * kKvTile * dim * (dtype == RTS_E4M3 ? 1 : 2) + kKvEntries * 256;
+    const int n = 160 * 1024 / (kKvWaves * wave_bytes);
+    return n < 6 ? n : 6;
+}
+
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
                       bool allow_split) {
-    const int group = heads / kv_heads;
-    const int64_t blocks = rows * kv_heads * ((group + kKvHeads - 1) / kKvHeads);
-    const int64_t longest = max_len < 0x7FFFFFFF ? max_len : 0x7FFFFFFF;
-    KvPlan p{1, longest, 0};
-    if (!allow_split) return p;
-    // Pieces of about 1024 keys, or as many as it takes to have 1024 workgroups, of 128 keys at least.
-    int64_t n = (longest + 1023) / 1024;
-    const int64_t fill = (1024 + blocks - 1) / blocks, most = (longest + 127) / 128;
-    n = n > fill ? n : fill;
-    n = n < most ? n : most;
-    n = n < 64 ? n : 64;
-    if (n <= 1) return p;
-    p.piece = ((longest + n - 1) / n + 63) & ~63ll;
-    p.splits = (int)((longest + p.piece - 1) / p.piece);
-    if (p.splits <= 1) return KvPlan{1, longest, 0};
-    p.ws_bytes = ((size_t)p.splits * rows * heads * (dim + 1) * 4 + 15) & ~size_t(15);
+    const int64_t blocks = kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
+    // Every workgroup of a split call sums up the rows, so calls of very many are not.
+    if (!allow_split || max_len <= kKvLeastKeys || rows > 4096) return KvPlan{0, 0, 0};
+    // The grid has room for what max_len may need: workgroups without a piece take
+    // a place for 2 us each (8 times too many of them cost a call of 8 us another 7).
+    const int64_t tiles = max_len < (1ll << 31) ? (max_len + kKvTile - 1) / kKvTile : 1ll << 26, all = rows * tiles;
+    const int64_t places = (256 * kv_places(dim, dtype) + blocks - 1) / blocks, least = (all + kKvLeast - 1) / kKvLeast;
+    KvPlan p;
+    p.target = (int)(places < least ? places : least);
+    const int64_t rounds = (all + kKvGoal * p.target - 1) / (kKvGoal * p.target);
+    p.rounds = (int)(rounds < kKvRounds ? rounds : kKvRounds);
+    // Rows of several pieces have no more than twice the most of them.
+    p.ws_bytes = (size_t)(2 * p.rounds * p.target) * heads * (dim + 1) * 4 + (size_t)rows * 8;
+    p.ws_bytes = (p.ws_bytes + 15) & ~size_t(15);
     return p;
 }
 
+template <int D, bool E4M3, bool BIG>
+static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {
+    const int64_t group = a.heads / a.kv_heads, blocks = a.kv_heads * ((group + kKvHeads - 1) / kKvHeads);
+    const int64_t most = (int64_t)plan.target * plan.rounds, grid = (a.rows + (most ? most + 1 : 0)) * blocks;
+    if (grid > kMaxThreads / kKvBlock || a.rows * a.heads > kMaxThreads / kJoinBlock) return RTS_EUNSUPPORTED;
+    KvParts parts{};
+    if (plan.target) {
+        parts.out = static_cast<float*>(workspace);
+        parts.lse = parts.out + 2 * most * a.heads * D;
+        parts.rows = reinterpret_cast<int2*>(parts.lse + 2 * most * a.heads);
+    }
+    hipLaunchKernelGGL((kv_attend_kernel<D, E4M3, BIG>), dim3((unsigned)grid), dim3(kKvBlock),
+                       kKvWaves * (KvShape<D, E4M3>::kWaveB), s, a, plan.target, plan.rounds, parts);
+    if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+    if (plan.target == 0) return RTS_OK;
+    // Few of them are cut finer, to have more of the chip read the pieces.
+    const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);
+    if (a.rows * a.heads <= 512)
+        hipLaunchKernelGGL((kv_join_kernel<D, 32>), dim3(pairs.x, D / 32), block, 0, s, parts, a.heads, a.out, a.lse);
+    else
+        hipLaunchKernelGGL((kv_join_kernel<D, D>), pairs, block, 0, s, parts, a.heads, a.out, a.lse);
+    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+}
+
+// Offsets into a cache are held in 32 bits: of bytes, or of 16 bytes where it is
+// larger than 4 GB (two more vector instructions a load).
 template <int D, bool E4M3>
 static int launch_kv(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {
-    const int64_t group = a.heads / a.kv_heads;
-    const int64_t grid = a.rows * a.kv_heads * ((group + kKvHeads - 1) / kKvHeads) * plan.splits;
-    if (grid > kMaxThreads / kKvBlock) return RTS_EUNSUPPORTED;
-    const int64_t n = a.rows * a.heads;
-    float* part_out = static_cast<float*>(workspace);
-    float* part_lse = part_out ? part_out + (int64_t)plan.splits * n * D : nullptr;
-    hipLaunchKernelGGL((kv_attend_kernel<D, E4M3>), dim3((unsigned)grid), dim3(kKvBlock),
-                       kKvWaves * (KvShape<D, E4M3>::kWaveB), s, a, plan.splits, plan.piece, part_out, part_lse);
-    if (hipGetLastError() != hipSuccess) return RTS_EHIP;
-    if (plan.splits == 1) return RTS_OK;
-    return launch_merge_attend(part_out, RTS_F32, part_lse, plan.splits, a.rows, a.heads, D, a.out, RTS_BF16, a.lse,
-                               nullptr, true, s);
+    const int64_t bytes = a.cache_rows * a.ld_cache * (E4M3 ? 1 : 2);
+    if (bytes >> 4 > 0xFFFFFF00ll) return RTS_EUNSUPPORTED;
+    return bytes > 0xFFFFF000ll ? launch_kv_of<D, E4M3, true>(a, plan, workspace, s)
+                                : launch_kv_of<D, E4M3, false>(a, plan, workspace, s);
 }
 
 int launch_kv_attend(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {

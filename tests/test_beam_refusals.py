@@ -146,8 +146,9 @@ def test_kv_attend_paged_plan():
         assert f(**kw) == EINVAL, kw
     for kw in (dict(heads=1028), dict(dim=96), dict(rows=1 << 31)):
         assert f(**kw) == EUNSUP, kw
-    assert f(split=0) == 0 and p[0] == 1
-    assert f() == 0 and p[0] > 1 and p[0] * p[1] >= 4096
+    assert f(split=0) == 0 and p[0] == 0
+    assert f() == 0 and p[0] > 1 and p[1] >= 32
+    assert f(w=64) == 0 and p[0] == 0
 
 
 def test_binding():

@@ -111,15 +111,35 @@ def plan(rts, rows, heads, kv, dim, max_len, window=0):
 
 def test_pieces(rts):
     """Lengths at the borders of the pieces, and bounds on the lengths that are too low or too high."""
+    target, least = plan(rts, 6, 8, 1, 64, 4096)
+    assert target * least > 5000  # so all rows together are cut into the least pieces
     ctx = [4096] * 3
     a = list(setup(7, ctx, 8, 1, 64, 32))
-    splits, keys = plan(rts, 6, 8, 1, 64, 4096)
-    assert splits > 2
     a[0] = a[0].repeat(2, 1, 1)
     a[3] = [0, 1, 2, 0, 1, 2]
-    a[4] = [keys, keys + 1, 2 * keys - 1, 4096, keys - 1, 1]
-    for max_len in (None, 0, 1, keys, 5000, 1 << 40):
+    a[4] = [least, least + 1, 2 * least - 1, 4096, least - 1, 1]
+    for max_len in (None, 0, 1, least, 5000, 1 << 40):
         check(rts, *a, 32, 0.125, max_len=max_len)
+
+
+@pytest.mark.parametrize("rows", [1, 63, 64, 65, 130, 700])
+def test_pieces_of_many_and_very_ragged_rows(rts, rows):
+    """One long row among short and empty ones, at every place where the sums over the rows go on."""
+    g = torch.Generator().manual_seed(rows)
+    q, k, v, _, _, table = setup(12, [3000, 40], 2, 1, 64, 16)
+    q = rand(g, rows, 2, 64)
+    for at in {0, rows // 2, rows - 1}:
+        req, ends = [1] * rows, torch.randint(0, 41, (rows,), generator=g).tolist()
+        req[at], ends[at] = 0, 3000
+        check(rts, q, k, v, req, ends, table, 16, 0.125)
+
+
+def test_longer_pieces(rts):
+    """So many keys that the pieces are longer than the least."""
+    target, least = plan(rts, 40, 8, 8, 64, 1 << 20)
+    ctx = [3000 + 7 * i for i in range(40)]
+    assert sum(ctx) > 2 * target * least
+    check(rts, *setup(13, ctx, 8, 8, 64, 64), 64, 0.125)
 
 
 def test_padded_batch_and_bad_requests(rts):
