@@ -627,8 +627,8 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
  *            workgroups read a large table.  Calls in flight at the same time need
  *            workspaces of their own.
  * No output may overlap an input or another output.
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks), RTS_EWORKSPACE,
- *         RTS_EHIP.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks, table_cols >= 2^19),
+ *         RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t fork_blocks_workspace_size(int64_t rows_in, int32_t table_cols, int32_t pool_blocks);
 int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols, int64_t ld_table,
@@ -654,7 +654,7 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
  *            block is both.
  * free_blocks int32 [n_free]: the ids that are free after the moves, ascending, then -1.
  * counts     int32 [2]: how many are free, and how many moves there are in all.
- * Other arguments as in fork_blocks (rows < 2^31), workspace with
+ * Other arguments as in fork_blocks (rows * table_cols < 2^31), workspace with
  * compact_blocks_workspace_size bytes.
  * No output may overlap an input or another output.
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EWORKSPACE, RTS_EHIP.

@@ -539,7 +539,8 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
     if (rows_in < 0 || table_cols < 0 || ld_table < table_cols || rows_out < 0 || block_size < 1 ||
         pool_blocks < 0 || ld_out < table_cols || n_free < 0)
         return RTS_EINVAL;
-    if (rows_in > rts::kMaxForkRows || rows_out > rts::kMaxForkRows || pool_blocks > rts::kMaxPool)
+    if (rows_in > rts::kMaxForkRows || rows_out > rts::kMaxForkRows || pool_blocks > rts::kMaxPool ||
+        table_cols > 0x7FFFFFFF / rts::kMaxForkRows)
         return RTS_EUNSUPPORTED;
     if (!counts || (rows_in > 0 && !ctx_lens) || (rows_in > 0 && table_cols > 0 && !block_table) ||
         (rows_out > 0 && (!parents || !out_lens || !copies)) || (rows_out > 0 && table_cols > 0 && !out_table) ||
@@ -559,7 +560,9 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
 }
 
 size_t compact_blocks_workspace_size(int64_t rows, int32_t table_cols, int32_t pool_blocks) {
-    if (rows < 0 || rows > 0x7FFFFFFFll || table_cols < 0 || pool_blocks < 0 || pool_blocks > rts::kMaxPool) return 0;
+    if (rows < 0 || table_cols < 0 || rows > 0x7FFFFFFFll / (table_cols > 0 ? table_cols : 1) || pool_blocks < 0 ||
+        pool_blocks > rts::kMaxPool)
+        return 0;
     return rts::compact_blocks_bytes(rows, table_cols, pool_blocks);
 }
 
@@ -570,7 +573,7 @@ int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols,
     if (rows < 0 || table_cols < 0 || ld_table < table_cols || block_size < 1 || pool_blocks < 0 ||
         ld_out < table_cols || max_moves < 0 || n_free < 0)
         return RTS_EINVAL;
-    if (rows > 0x7FFFFFFFll || pool_blocks > rts::kMaxPool) return RTS_EUNSUPPORTED;
+    if (rows > 0x7FFFFFFFll / (table_cols > 0 ? table_cols : 1) || pool_blocks > rts::kMaxPool) return RTS_EUNSUPPORTED;
     if (!counts || (rows > 0 && !ctx_lens) || (rows > 0 && table_cols > 0 && (!block_table || !out_table)) ||
         (max_moves > 0 && !moves) || (n_free > 0 && !free_blocks))
         return RTS_EINVAL;

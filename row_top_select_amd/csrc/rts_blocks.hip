@@ -141,6 +141,41 @@ __device__ __forceinline__ void rows_of(int64_t part, int64_t parts, int64_t row
     hi = lo + per < rows ? lo + per : rows;
 }
 
+// The same of narrow tables, whose rows would leave most of a wave idle: a lane
+// takes an entry, eight on their way, of entries [lo, hi) of the table read row by row.
+template <typename Count>
+__device__ __forceinline__ void mark_entries(const int32_t* table, int64_t ld, uint32_t cols, uint32_t lo, uint32_t hi,
+                                             int least, int pool, uint32_t* bits, Count&& n) {
+    constexpr int kAhead = 8;
+    for (uint32_t e0 = lo + threadIdx.x; e0 < hi; e0 += kAhead * kPoolBlock) {
+        int id[kAhead];
+        bool inside[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint32_t e = e0 + u * kPoolBlock, at = e < hi ? e : lo, r = at / cols, j = at - r * cols;
+            id[u] = table[(int64_t)r * ld + j];
+            inside[u] = e < hi && (int)j < n(r);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (inside[u] && (uint32_t)(id[u] - least) < (uint32_t)pool) set_bit(bits, id[u] - least);
+    }
+}
+constexpr int kNarrow = 128;  // columns below which a table is
+template <typename Count>
+__device__ __forceinline__ void mark_table(const int32_t* table, int64_t ld, int cols, int64_t rows, int64_t part,
+                                           int64_t parts, int least, int pool, uint32_t* bits, Count&& n) {
+    if (cols < kNarrow) {
+        const uint32_t all = (uint32_t)rows * (uint32_t)cols, per = (all + (uint32_t)parts - 1) / (uint32_t)parts;
+        const uint32_t lo = (uint32_t)part * per < all ? (uint32_t)part * per : all;
+        mark_entries(table, ld, cols, lo, lo + per < all ? lo + per : all, least, pool, bits, n);
+    } else {
+        int64_t lo, hi;
+        rows_of(part * kPoolWaves + threadIdx.x / kWave, parts * kPoolWaves, rows, lo, hi);
+        mark_rows(table, ld, lo, hi, least, pool, bits, n);
+    }
+}
+
 // Words of LDS bits a thread counts: twice an odd number, so that the lanes'
 // 8-byte reads lie in different banks.
 __device__ __forceinline__ int unit_of(int words) { return (((words + 2 * kPoolBlock - 1) / (2 * kPoolBlock)) | 1) * 2; }
@@ -216,27 +251,23 @@ __device__ __forceinline__ Lengths lengths(int32_t ctx, int32_t block_size, int3
     return {full < cols ? full : cols, need < cols ? need : cols};
 }
 
-// Columns [0, cols) of a row: edit(j, entry) of the first `need` entries, then -1.
-template <typename Edit>
-__device__ __forceinline__ void write_row(const int32_t* from, int32_t* to, int need, int cols, Edit&& edit) {
-    constexpr int kAhead = 2;
-    const int lane = lane_id();
-    for (int j0 = lane * 4; j0 - lane * 4 < cols; j0 += kAhead * 4 * kWave) {
-        ids4 id[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) id[u] = four_entries(from, j0 + u * 4 * kWave, need);
+// Every entry of a table: entry(row, column), kAhead of a thread side by side.
+template <int kAhead, typename Entry>
+__device__ __forceinline__ void write_table(int32_t* table, int64_t ld, int cols, int64_t rows, int64_t at, int64_t step,
+                                            Entry&& entry) {
+    const uint32_t all = (uint32_t)rows * (uint32_t)cols;
+    for (int64_t e0 = at; e0 < all; e0 += kAhead * step) {
+        int32_t id[kAhead], *to[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int j = j0 + u * 4 * kWave;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) id[u][v] = edit(j + v, id[u][v]);
-            if (j + 4 <= cols)
-                *reinterpret_cast<ids4_at4*>(to + j) = id[u];
-            else
-#pragma unroll
-                for (int v = 0; v < 3; ++v)
-                    if (j + v < cols) to[j + v] = id[u][v];
+            const int64_t e = e0 + u * step;
+            const uint32_t i = (uint32_t)(e < all ? e : at) / (uint32_t)cols, j = (uint32_t)(e < all ? e : at) - i * cols;
+            to[u] = table + i * ld + j;
+            id[u] = entry(i, (int)j);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (e0 + u * step < all) *to[u] = id[u];
     }
 }
 
@@ -270,8 +301,7 @@ __device__ __forceinline__ void load_parents(const ForkArgs& a, int (&par)[kFork
 constexpr int kQuarters = 4;
 struct MarkShare {
     int first_word, words, least, blocks;  // of the pool
-    int64_t part, parts;                   // of the rows, a wave
-    int field;
+    int field, parts;                      // of the rows
     __device__ __forceinline__ explicit MarkShare(int32_t pool) {
         const int all = words_of(pool), per = (all / 4 + kQuarters - 1) / kQuarters * 4, q = blockIdx.x % kQuarters;
         first_word = q * per < all ? q * per : all;
@@ -280,13 +310,12 @@ struct MarkShare {
         blocks = pool - least < words * 32 ? pool - least : words * 32;
         if (blocks < 0) blocks = 0;
         field = blockIdx.x / kQuarters;
-        part = field * kPoolWaves + threadIdx.x / kWave;
-        parts = (int64_t)(gridDim.x / kQuarters) * kPoolWaves;
+        parts = gridDim.x / kQuarters;
     }
     // The held blocks' words of the quarter, this part's of them.
     template <typename Put>
     __device__ __forceinline__ void held(const uint8_t* held, int pool, Put&& put) const {
-        const int n = gridDim.x / kQuarters, per = (words + n - 1) / n;
+        const int per = (words + parts - 1) / parts;
         const int lo = field * per < words ? field * per : words, hi = lo + per < words ? lo + per : words;
         held_words(held, pool, first_word + lo, first_word + hi, put);
     }
@@ -302,10 +331,8 @@ __global__ __launch_bounds__(kPoolBlock) void mark_fork_kernel(ForkArgs a, uint3
     clear(used, my.words);
     first_rows(a, first, par);
     my.held(a.held, a.pool, [&](int w, uint32_t bits) { atomicOr(&used[w - my.first_word], bits); });
-    int64_t lo, hi;
-    rows_of(my.part, my.parts, a.rows_in, lo, hi);
-    mark_rows(a.table, a.ld_table, lo, hi, my.least, my.blocks, used,
-              [&](int64_t p) { return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full; });
+    mark_table(a.table, a.ld_table, a.cols, a.rows_in, my.field, my.parts, my.least, my.blocks, used,
+               [&](int64_t p) { return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full; });
     __syncthreads();
     store_field(fields + (int64_t)my.field * words_of(a.pool) + my.first_word, used, my.words);
 }
@@ -314,12 +341,10 @@ __global__ __launch_bounds__(kPoolBlock) void mark_compact_kernel(CompactArgs a,
     const MarkShare my(a.pool);
     clear(lds, my.words);
     __syncthreads();
-    const int64_t n = gridDim.x / kQuarters, words = words_of(a.pool);
-    my.held(a.held, a.pool, [&](int w, uint32_t bits) { fields[n * words + w] = bits; });  // a field of their own
-    int64_t lo, hi;
-    rows_of(my.part, my.parts, a.rows, lo, hi);
-    mark_rows(a.table, a.ld_table, lo, hi, my.least, my.blocks, lds,
-              [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
+    const int64_t words = words_of(a.pool);
+    my.held(a.held, a.pool, [&](int w, uint32_t bits) { fields[my.parts * words + w] = bits; });  // a field of their own
+    mark_table(a.table, a.ld_table, a.cols, a.rows, my.field, my.parts, my.least, my.blocks, lds,
+               [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
     __syncthreads();
     store_field(fields + (int64_t)my.field * words + my.first_word, lds, my.words);
 }
@@ -380,9 +405,7 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
     __syncthreads();
     if (tid < 4 && words > 0) atomicOr(&used[words - 4 + tid], behind(a.pool, words - 4 + tid));
     if (n_fields == 0) {
-        int64_t lo, hi;
-        rows_of(wave, kPoolWaves, rows_in, lo, hi);
-        mark_rows(a.table, a.ld_table, lo, hi, 0, a.pool, used, [&](int64_t p) {
+        mark_table(a.table, a.ld_table, a.cols, rows_in, 0, 1, 0, a.pool, used, [&](int64_t p) {
             return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full;
         });
         __syncthreads();
@@ -457,39 +480,33 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
     for (int64_t r = taken + at; r < rows; r += step) reinterpret_cast<int2*>(a.copies)[r] = int2{-1, -1};
     for (int64_t r = (int64_t)(all_free - taken) + at; r < a.n_free; r += step) a.free_blocks[r] = -1;
     list_bits(words / 2, pairs, part, parts, taken, a.n_free, a.free_blocks, free_pair, before);
-    // Rows part, part + parts, ..; a lane has one's parent and length.
-    for (int i0 = part; i0 < rows; i0 += parts * kWave) {
-        const int i = i0 + lane * (int)parts;
-        int p = i < rows ? a.parents[i] : -1;
-        if ((uint32_t)p >= (uint32_t)rows_in) p = -1;
-        int len = p < 0 ? 0 : a.ctx_lens[p];
-        len = len > 0 ? len : 0;
-        if (i < rows) a.out_ctx[i] = len;
-        for (int r = 0; r < kWave && i0 + r * (int)parts < rows; ++r) {
-            const int row = i0 + r * (int)parts, from = __builtin_amdgcn_readlane(p, r);
-            const Lengths n = lengths(__builtin_amdgcn_readlane(len, r), a.block_size, a.cols);
-            const int own_block = got[row];
-            write_row(a.table + (from < 0 ? 0 : from) * a.ld_table, a.out_table + row * a.ld_out, n.need, a.cols,
-                      [&](int j, int id) {
-                          if ((uint32_t)id >= (uint32_t)a.pool) id = -1;
-                          return j == n.full && own_block != -2 ? own_block : id;
-                      });
-        }
+    for (int i = at; i < rows; i += step) {
+        const uint32_t p = a.parents[i];
+        const int len = p < (uint32_t)rows_in ? a.ctx_lens[p] : 0;
+        a.out_ctx[i] = len > 0 ? len : 0;
     }
+    write_table<4>(a.out_table, a.ld_out, a.cols, rows, at, step, [&](uint32_t i, int j) {
+        const uint32_t p = a.parents[i];
+        if (p >= (uint32_t)rows_in) return -1;
+        const int len = a.ctx_lens[p], id = a.table[(int64_t)p * a.ld_table + j], own_block = got[i];
+        const Lengths n = lengths(len, a.block_size, a.cols);
+        if (j >= n.need || (uint32_t)id >= (uint32_t)a.pool) return j == n.full && own_block != -2 ? own_block : -1;
+        return j == n.full && own_block != -2 ? own_block : id;
+    });
 }
 
 // Bit fields of large tables: none where one workgroup reads the tables in
 // about the time that a launch takes.
 static int mark_parts(int64_t rows, int32_t cols) {
     const int64_t entries = rows * (int64_t)cols;
-    return entries <= 65536 ? 0 : entries < 4 * 32768 ? 2 : 4;
+    return entries <= 81920 ? 0 : entries < 4 * 32768 ? 2 : 4;
 }
 static size_t mark_lds(int32_t pool) { return (size_t)(words_of(pool) / 4 + kQuarters - 1) / kQuarters * 16; }
 size_t fork_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
     return (size_t)mark_parts(rows, cols) * words_of(pool) * 4;
 }
 
-static int64_t pool_grid(int64_t work) { return work / 4096 < 1 ? 1 : work / 4096 < 256 ? work / 4096 : 256; }
+static int64_t pool_grid(int64_t work) { return work / 2048 < 1 ? 1 : work / 2048 < 256 ? work / 2048 : 256; }
 
 int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t s) {
     const size_t words = words_of(a.pool);
@@ -531,10 +548,8 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
         if (a.held) join_fields(fields + (int64_t)n_fields * words, 1, words, open);
     } else {
         held_words(a.held, a.pool, 0, words, [&](int w, uint32_t bits) { atomicOr(&open[w], bits); });
-        int64_t lo, hi;
-        rows_of(wave, kPoolWaves, a.rows, lo, hi);
-        mark_rows(a.table, a.ld_table, lo, hi, 0, a.pool, live,
-                  [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
+        mark_table(a.table, a.ld_table, a.cols, a.rows, 0, 1, 0, a.pool, live,
+                   [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
     }
     __syncthreads();
     const int all_pairs = words / 2, pairs = unit_of(words) / 2;
@@ -624,21 +639,16 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
             }
         }
     }
-    // A lookup takes some hundred cycles, so a lane takes one entry at a time, a wave
-    // 64 neighbours of a row.
-    const int64_t segments = (a.cols + kWave - 1) / kWave;
-    for (int64_t u = part; u < a.rows * segments; u += parts) {
-        const int64_t row = u / segments;
-        const int j = (int)(u - row * segments) * kWave + lane;
-        if (j >= a.cols) continue;
-        int id = a.table[row * a.ld_table + j];
-        if (j >= lengths(a.ctx_lens[row], a.block_size, a.cols).need || (uint32_t)id >= (uint32_t)a.pool) id = -1;
-        if (id >= 0 && (uint32_t)id >= bound && get_bit(live, id)) {
+    // A lookup takes some hundred cycles, so there are threads for an entry each, up to the chip's.
+    write_table<1>(a.out_table, a.ld_out, a.cols, a.rows, at, step, [&](uint32_t i, int j) {
+        const int id = a.table[i * a.ld_table + j];
+        if (j >= lengths(a.ctx_lens[i], a.block_size, a.cols).need || (uint32_t)id >= (uint32_t)a.pool) return -1;
+        if ((uint32_t)id >= bound && get_bit(live, id)) {
             const uint32_t k = live_rank(id) - below;
-            if (k < moved) id = free_block(k);
+            if (k < moved) return free_block(k);
         }
-        a.out_table[row * a.ld_out + j] = id;
-    }
+        return id;
+    });
 }
 
 size_t compact_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
@@ -654,8 +664,8 @@ int launch_compact_blocks(const CompactArgs& a, void* workspace, hipStream_t s) 
         hipLaunchKernelGGL(mark_compact_kernel, dim3(parts * kQuarters), dim3(kPoolBlock), mark_lds(a.pool), s, a, fields);
         if (hipGetLastError() != hipSuccess) return RTS_EHIP;
     }
-    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)pool_grid(a.rows * (int64_t)a.cols + a.n_free + 2 * a.max_moves)),
-                       dim3(kPoolBlock), words * 8, s, a, fields, parts);
+    const int64_t grid = pool_grid(2 * a.rows * (int64_t)a.cols + a.n_free + 2 * a.max_moves);
+    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)grid), dim3(kPoolBlock), words * 8, s, a, fields, parts);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
