@@ -718,8 +718,8 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
  * out        bf16 [rows, heads, dim], contiguous.   lse  float [rows, heads] or NULL.
  * workspace  as in latent_attend_rows, kv_attend_paged_workspace_size bytes.
  * q, the caches, out and their strides must be multiples of 16 bytes.
- * Scores, softmax statistics and sums are held in 32 bits; the weights are
- * rounded to bf16 for the products with the values.
+ * Scores, softmax statistics and sums are held in 32 bits; the weights enter the
+ * products with the values as two bf16 terms (2^-16 of a weight is left out).
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 1024, cache_rows >= 2^31,
  *         ld_cache > 2^30, a cache of 2^36 bytes or more), RTS_EWORKSPACE, RTS_EHIP.
  */

@@ -9,6 +9,7 @@ the library has not been built (``python row_top_select_amd/build.py``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -897,6 +898,14 @@ def merge_attend_rank_major(parts: torch.Tensor, lse: torch.Tensor, out: torch.T
     return out, out_lse
 
 
+# Workspace sizes by the sizes of a call: a query costs a microsecond, a step's calls make the same ones.
+_sizes = functools.lru_cache(maxsize=1024)
+_beam_bytes = _sizes(lambda *a: int(_lib.beam_select_workspace_size(*a)))
+_fork_bytes = _sizes(lambda *a: int(_lib.fork_blocks_workspace_size(*a)))
+_compact_bytes = _sizes(lambda *a: int(_lib.compact_blocks_workspace_size(*a)))
+_kv_bytes = _sizes(lambda *a: int(_lib.kv_attend_paged_workspace_size(*a)))
+
+
 class BeamStep(NamedTuple):
     """What beam_select returns; see beam_select in the header."""
     scores: torch.Tensor        # float32 [G, k]
@@ -945,7 +954,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int, eos: int = -
             raise ValueError("ended is written only with an eos")
     if workspace is None:
         raise ValueError('workspace must be "auto" or a GPU tensor')
-    ws, ws_bytes = _scratch(workspace, int(_lib.beam_select_workspace_size(dt, groups, beams, vocab, k))
+    ws, ws_bytes = _scratch(workspace, _beam_bytes(dt, groups, beams, vocab, k)
                             if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.beam_select, "beam_select", device, stream, logits.data_ptr(), dt, groups, beams, vocab, ld,
             scores.data_ptr(), k, eos, out.scores.data_ptr(), out.parents.data_ptr(), out.tokens.data_ptr(),
@@ -1012,7 +1021,7 @@ def fork_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, parents: torc
         out = Fork(table.view(rows, cols), lens, copies.view(rows, 2), free, counts)
     else:
         _named_out(out, ((rows, cols), (rows,), (rows, 2), (n_free,), (2,)), device, stream)
-    ws, ws_bytes = _scratch(workspace, int(_lib.fork_blocks_workspace_size(rows_in, cols, pool_blocks))
+    ws, ws_bytes = _scratch(workspace, _fork_bytes(rows_in, cols, pool_blocks)
                             if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.fork_blocks, "fork_blocks", device, stream, block_table.data_ptr(), rows_in, cols, ld,
             ctx_lens.data_ptr(), parents.data_ptr(), rows, block_size, pool_blocks, held_ptr,
@@ -1044,7 +1053,7 @@ def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size
         out = Compaction(table.view(rows, cols), moves.view(max_moves, 2), free, counts)
     else:
         _named_out(out, ((rows, cols), (max_moves, 2), (n_free,), (2,)), device, stream)
-    ws, ws_bytes = _scratch(workspace, int(_lib.compact_blocks_workspace_size(rows, cols, pool_blocks))
+    ws, ws_bytes = _scratch(workspace, _compact_bytes(rows, cols, pool_blocks)
                             if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.compact_blocks, "compact_blocks", device, stream, block_table.data_ptr(), rows, cols, ld,
             ctx_lens.data_ptr(), block_size, pool_blocks, held_ptr, out.block_table.data_ptr(), cols,
@@ -1053,10 +1062,12 @@ def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size
 
 
 def copy_blocks(caches, pairs: torch.Tensor, block_size: int, stride_rows: int | None = None, stream=None) -> None:
-    """Copies blocks within each of ``caches`` (tensors [cache_rows, ...] of any type, a row contiguous) by the
+    """Copies blocks within each of ``caches`` (one tensor or several, [cache_rows, ...] of any type, a row contiguous) by the
     ``pairs`` int32 [n, 2] of (from, to), -1 skipped, in place; see copy_blocks in the header.  ``stride_rows``
     defaults to ``block_size``."""
     device = _gpu(pairs, "pairs")
+    if isinstance(caches, torch.Tensor):
+        caches = (caches,)
     if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or not pairs.is_contiguous():
         raise ValueError("pairs must be contiguous int32 [n, 2]")
     pages = _pages(block_size, stride_rows)
@@ -1108,7 +1119,8 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
     if q.dim() != 3 or k_cache.dim() != 3 or q.stride(2) != 1 or k_cache.stride(2) != 1:
         raise ValueError("q must be [rows, heads, dim], the caches [cache_rows, kv_heads, dim], with unit element stride")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() and any(
+            n > 1 and x != y for n, x, y in zip(k_cache.shape, k_cache.stride(), v_cache.stride())):
         raise ValueError("k_cache and v_cache must have the same shape and strides")
     (rows, heads, dim), (ld_q, ld_qhead, _) = q.shape, q.stride()
     (cache_rows, kv_heads, cdim), (ld_cache, ld_head, _) = k_cache.shape, k_cache.stride()
@@ -1139,7 +1151,7 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     _on(device, k_cache, v_cache, k_scales, v_scales, req_id, row_ends, block_table)
     dt = _INDEX_DTYPES[k_cache.dtype]
     ws, ws_bytes = _scratch(workspace,
-                            int(_lib.kv_attend_paged_workspace_size(rows, heads, kv_heads, dim, dt, max_len, window))
+                            _kv_bytes(rows, heads, kv_heads, dim, dt, max_len, window)
                             if isinstance(workspace, str) else 0, device, stream)
     _launch(_lib.kv_attend_paged, "kv_attend_paged", device, stream, q.data_ptr(), rows, heads, ld_q, ld_qhead,
             k_cache.data_ptr(), v_cache.data_ptr(), dt, kv_heads, dim, cache_rows, ld_cache, ld_head, _ptr(k_scales),

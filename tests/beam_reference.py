@@ -152,10 +152,10 @@ def kv_attend(q, k, v, scale):
     # exponent's argument by a step of the score and of the maximum; exp2 by 2 steps.
     dz = (dim + 3) * U * abs(scale) * (q.abs() @ k.abs().T).amax(1) + 4 * U * z.abs().amax(1) + 2 * U
     size = (p / total) @ v.abs()
-    # Relative: each weight by dz and its rounding to bf16, the weights' sum by dz and n steps, the products'
-    # sum by n steps (and as many for rescaling the running sums), the quotient and a value scale by 4.
-    # The result is rounded to bf16.
-    rel = 2 * dz + BF16 + (3 * n + 8) * U
+    # Relative: each weight by dz and what two bf16 terms leave of it, the weights' sum by dz and n steps, the
+    # products' sum by 2 n steps (and as many for rescaling the running sums), the quotient and a value scale
+    # by 4.  The result is rounded to bf16.
+    rel = 2 * dz + BF16 * BF16 + (5 * n + 8) * U
     return (out, lse, size * rel[:, None] * (1 + BF16) + out.abs() * BF16,
             dz + (2 * n + 4) * U + 4 * U * lse.abs())
 

@@ -200,6 +200,8 @@ def test_copy_many_caches_and_none(rts):
     rts.copy_blocks(caches, i32([[0, 3], [2, 1]]), 16)
     for c, b in zip(caches, before):
         assert torch.equal(c[48:], b[:16]) and torch.equal(c[16:32], b[32:48]) and torch.equal(c[32:48], b[32:48])
+    rts.copy_blocks(caches[0], i32([[0, 2]]), 16)  # one tensor
+    assert torch.equal(caches[0][32:48], before[0][:16])
     rts.copy_blocks([], i32([[0, 1]]), 16)
     rts.copy_blocks(caches, torch.empty(0, 2, dtype=torch.int32, device=DEV), 16)
 
@@ -240,3 +242,31 @@ def test_block_calls_captured(rts):
             if a >= 0:
                 before[b * block:(b + 1) * block] = before[a * block:(a + 1) * block]
         assert torch.equal(cache, before)
+
+
+def test_streams(rts):
+    """Calls on another stream take their memory from it, behind work that keeps the current stream busy."""
+    pool, block = 400, 16
+    table, ctx, _ = setup(6, 40, 4, 120, block, pool, 0)
+    parents = list(range(160))
+    cache = torch.randn(pool * block, 8, device=DEV)
+    before = cache.clone()
+    t, c, p = i32(table), i32(ctx), i32([x // 2 for x in parents])
+    want = ref.fork(table, ctx, p.tolist(), block, pool, None, pool)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        junk = torch.full((200_000,), 7, dtype=torch.int32, device=DEV)
+        torch.cuda._sleep(10_000_000)
+        junk.fill_(9)
+        del junk  # given back to the current stream, which is still to write it
+        f = rts.fork_blocks(t, c, p, block, pool, stream=side)
+        m = rts.compact_blocks(t, c, block, pool, stream=side)
+        rts.copy_blocks([cache], f.copies, block, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert_same(f, want, "fork")
+        assert_same(m, ref.compact(table, ctx, block, pool, None, pool // 2, pool), "compact")
+    for a, b in want["copies"]:
+        if a >= 0:
+            before[b * block:(b + 1) * block] = before[a * block:(a + 1) * block]
+    assert torch.equal(cache, before)

@@ -305,3 +305,42 @@ def test_streams_replay_and_calls_at_once(rts):
         eager, eager_lse = call(max_len=1300)
         assert torch.equal(out, eager) and torch.equal(lse, eager_lse)
         check(rts, q, k, v, req, lens, table, 16, 0.1)
+
+
+@pytest.mark.parametrize("heads,kv", [(128, 1), (34, 2), (3, 3)])
+def test_groups_of_heads(rts, heads, kv):
+    """Many query heads a key head, and numbers that leave a block of 16 partly empty."""
+    for ws in ("auto", None):
+        check(rts, *setup(heads, [150, 33, 2], heads, kv, 64, 16), 16, 0.125, workspace=ws)
+
+
+def test_more_rows_than_are_split(rts):
+    q, k, v, _, _, table = setup(14, [200], 1, 1, 64, 16)
+    rows = 4100
+    assert plan(rts, rows, 1, 1, 64, 200)[0] == 0 and plan(rts, 4096, 1, 1, 64, 200)[0] > 0
+    q = rand(torch.Generator().manual_seed(2), rows, 1, 64)
+    ends = [(7 * t) % 201 for t in range(rows)]
+    check(rts, q, k, v, [0] * rows, ends, table, 16, 0.125)
+
+
+def test_key_scales_of_any_sign(rts):
+    q, k, v, req, ends, table = setup(15, [60, 300], 8, 4, 64, 16, dtype=E4M3)
+    ks, vs = torch.tensor([-0.7, 0.0, 1e-3, 2.0]), torch.tensor([0.0, -1.5, 300.0, 1e-6])
+    for scale in (0.2, -0.2):
+        check(rts, q, k, v, req, ends, table, 16, scale, ks=ks, vs=vs)
+
+
+def test_longest_contexts(rts):
+    """Positions up to 2^31 - 1, few of which have a row: blocks of 2^30 tokens over a small cache."""
+    g = torch.Generator().manual_seed(16)
+    k, v, q = rand(g, 100, 1, 64), rand(g, 100, 1, 64), rand(g, 2, 2, 64)
+    end = 2 ** 31 - 1
+    for window in (0, 2 ** 30 + 40):
+        got, lse = rts.kv_attend_paged(q.to(DEV), k.to(DEV), v.to(DEV), i32([0, 0]), i32([end, 2 ** 30 + 7]), i32([[0, 0]]),
+                                       2 ** 30, 0.125, window=window)
+        for t, e in ((0, end), (1, 2 ** 30 + 7)):
+            seen = [p % 2 ** 30 for p in [*range(100), *range(2 ** 30, 2 ** 30 + 100)]
+                    if p < e and (not window or p >= e - window)]
+            o, l, ob, lb = ref.kv_attend(q[t], k[seen, 0], v[seen, 0], 0.125)
+            assert_close(got[t], o, ob, f"out {window} {t}")
+            assert_close(lse[t], l, lb, f"lse {window} {t}")
