@@ -25,7 +25,7 @@ def beam_values(logits, score):
     # rescaled by a factor that is off like a term.
     each = 3 * U24 * float((w * d.abs()).sum()) / total + 2 * U
     bound = each + (8 + 64 * 4) * U + 3 * U24 * float(-d.min() if d.min() > -200 else 200.0)
-    return score + (x - (m + math.log(total))), bound
+    return score + ((x - m) - math.log(total)), bound
 
 
 def check_beams(got, logits, scores, k, eos, what=""):

@@ -123,6 +123,41 @@ def test_far_scores(rts):
     assert got.tokens[0].tolist() == [5, 9] and float(got.scores[0, 0]) == 0.0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_far_logits(rts, dtype):
+    """Logits at both ends of the range, whose maxima grow from group to group, and small ones behind them: the sums
+    count what is equal to the largest, or near it."""
+    vocab = 40000
+    logits = torch.full((6, vocab), -math.inf)
+    logits[0, ::10] = torch.arange(vocab // 10) * 1e33 - 3.2e38       # a new maximum every ten tokens
+    logits[1, ::10] = torch.arange(vocab // 10) * 2e34 + 2.4e38
+    logits[2, :30000], logits[2, 30000:] = -3e38, -2.5e38              # 10000 equal ones
+    logits[3, :30000], logits[3, 30000:] = 2.5e38, 3e38
+    logits[4, :20000], logits[4, 20000:] = -3.3e38, torch.randn(20000, generator=torch.Generator().manual_seed(0))
+    logits[5, :20000], logits[5, 20000:39999] = 9e37, torch.randn(19999)
+    logits = logits.to(dtype)
+    scores = torch.zeros(6, 1)
+    got = run(rts, logits, scores, 9, -1)
+    check_beams(got, logits, scores, 9, -1)
+    assert abs(float(got.scores[2, 0]) + math.log(10000)) < 1e-5 and abs(float(got.scores[3, 0]) + math.log(10000)) < 1e-5
+    assert abs(float(got.scores[5, 0]) + math.log(20000)) < 1e-5
+
+
+def test_logits_around_a_million(rts):
+    """Maxima that cross the size at which the sums' terms change their form, upwards and from below."""
+    vocab = 30000
+    logits = torch.full((4, vocab), -math.inf)
+    logits[0, :15000], logits[0, 15000:] = 999999.5, 1000000.5
+    logits[1, :15000], logits[1, 15000:] = -1000000.5, -999999.5
+    logits[2, :15000], logits[2, 15000:] = 1000000.5, 999999.5
+    logits[3, :15000], logits[3, 15000:] = -999999.5, -1000000.5
+    scores = torch.zeros(4, 1)
+    got = run(rts, logits, scores, 5, -1)
+    check_beams(got, logits, scores, 5, -1)
+    want = -math.log(15000 * (1 + math.exp(-1)))
+    assert (got.scores[:, 0].double() - want).abs().max() < 1e-5
+
+
 def test_given_outputs_streams_and_replay(rts):
     logits, scores = inputs(5, 3, 4, 9000, torch.bfloat16)
     x, s = logits.to(DEV), scores.to(DEV)
