@@ -8,12 +8,21 @@
 //    fourth group of 4 KB, with a running maximum and sum of the softmax.  A
 //    row's order is that of its logits whatever lse_b is, so its k best are
 //    collected beside it: at least j elements of a wave reach the j-th largest of its 64
-//    lanes' maxima, so the k best reach that of j = k, and the least of the four
-//    waves' with j = k / 4.  Few elements reach this bound once some groups have
-//    passed (k / n of the n-th element's kind); they are kept in LDS, and the
-//    waves' lists are sorted and merged at the end.
+//    lanes' maxima, so the k best reach the least of the four waves' with
+//    j = k / 4.  Few elements reach this bound once some groups have passed (k / n
+//    of the n-th element's kind).  The 16-byte words that they lie in are kept in
+//    LDS as they are, three instructions and two stores a word; only at the end, when the bound is
+//    what the whole piece gave, are their elements looked at, a lane an element.
+//    What is left (some 20 for k = 8) is ranked by counting the larger ones.
 // 2. A workgroup a group joins its rows' pieces and ranks the rows' candidates
 //    against each other by their values in 64 bits.
+//
+// Bound by the reads.  Measured, the scan and the join: 256 x 102400 bf16, k = 8:
+// 15.3 + 4.9 us (3.4 TB/s); 1024 x 131072 bf16 and k = 32, the whole call: 62 us
+// (4.3 TB/s); 1024 x 131071 f32, k = 32: 95 + 6.5 us (5.6 TB/s).  On short rows it is
+// bound by the chain of steps that a piece is: 2000 clocks to the first group, 850 its
+// sum, 900 a bound, 2500 the end.  Elements appended one at a time as a row passes
+// took the first case 17.3 us.
 #include <type_traits>
 
 #include "rts_device.hpp"
@@ -24,12 +33,12 @@ namespace rts {
 
 constexpr int kBeamWaves = 4;
 constexpr int kBeamBlock = kBeamWaves * kWave;
-constexpr int kChunk = 512;       // elements: 8 a lane
+constexpr int kWords = 4;         // of 16 bytes that a lane loads at a time: a group of 4 KB a wave
 template <typename T>
-constexpr int group_chunks() { return 8 / (int)sizeof(T); }  // that a wave loads at a time: 4 KB
-template <typename T>
-constexpr int group_elements() { return kChunk * group_chunks<T>(); }
-constexpr int kStaged = 1024;     // candidates that a wave holds
+constexpr int group_elements() { return kWords * kWave * 16 / (int)sizeof(T); }
+constexpr int kStaged = 384;      // words with candidates that a wave holds
+constexpr int kListed = 2 * kWave;  // candidates
+constexpr int kAtOnce = 8;
 constexpr int kMaxJoinWaves = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = -3.402823466e38f;  // the lowest finite number
@@ -58,64 +67,44 @@ __device__ __forceinline__ float wave_max(float x) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), kWave - 1));
 }
 
-// A lane's 8 elements of a chunk, as they lie in memory.
+// An element of a 16-byte word.
 template <typename T>
-struct Chunk8;
-template <>
-struct Chunk8<uint16_t> {
-    uint4 w[1];
-    __device__ __forceinline__ float get(int e) const {
-        const uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-        return __uint_as_float(e & 1 ? x[e >> 1] & 0xFFFF0000u : x[e >> 1] << 16);
-    }
-};
-template <>
-struct Chunk8<float> {
-    uint4 w[2];
-    __device__ __forceinline__ float get(int e) const {
-        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        return __uint_as_float(x[e]);
-    }
-};
+__device__ __forceinline__ float element_of(const uint4& w, int e) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) return __uint_as_float(x[e]);
+    else return __uint_as_float(e & 1 ? x[e >> 1] & 0xFFFF0000u : x[e >> 1] << 16);
+}
 
 // 16 bytes at any multiple of 4, or of 2.
 typedef uint32_t words_at4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t words_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
-// Chunk c of a row holds its elements 512 c .. + 512 whatever the row's alignment
+// Word w of a row is its elements kEach w .. + kEach, whatever the row's alignment
 // is (loads of 16 bytes take any address), so that equal rows give equal sums.
-// Load j of a lane is elements (j * 64 + lane) * kEach .. + kEach of the chunk.
+// Word j of group g is the lanes' (g kWords + j) * 64 + lane.
 template <typename T>
 struct RowReader {
-    static constexpr int kEach = 16 / sizeof(T), G = kChunk / kWave / kEach;
+    static constexpr int kEach = 16 / sizeof(T);
     using words = std::conditional_t<sizeof(T) == 4, words_at4, words_at2>;
     const T* row;
     int64_t vocab;
-    // The element that a lane's e-th of chunk c is (it may lie behind the row).
-    __device__ __forceinline__ int64_t element(int64_t c, int e) const {
-        return c * kChunk + (e / kEach * kWave + lane_id()) * kEach + e % kEach;
+    __device__ __forceinline__ int64_t word_of(int64_t g, int j) const { return (g * kWords + j) * kWave + lane_id(); }
+    __device__ __forceinline__ bool inside(int64_t g) const { return (g + 1) * group_elements<T>() <= vocab; }
+    __device__ __forceinline__ uint4 load(int64_t g, int j) const {  // a group inside of the row
+        const words w = *reinterpret_cast<const words*>(row + word_of(g, j) * kEach);
+        return uint4{w[0], w[1], w[2], w[3]};
     }
-    __device__ __forceinline__ bool inside(int64_t c) const { return (c + 1) * kChunk <= vocab; }
-    __device__ __forceinline__ Chunk8<T> load(int64_t c) const {  // a chunk inside of the row
-        Chunk8<T> r;
+    // The last group: what lies behind the row is -inf.
+    __device__ __forceinline__ uint4 load_edge(int64_t g, int j) const {
+        uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const words w = *reinterpret_cast<const words*>(row + element(c, j * kEach));
-            r.w[j] = uint4{w[0], w[1], w[2], w[3]};
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t at = word_of(g, j) * kEach + e;
+            const T t = row[at < vocab ? at : vocab - 1];
+            if constexpr (sizeof(T) == 4) x[e] = at < vocab ? __float_as_uint(t) : 0xFF800000u;
+            else x[e / 2] |= (uint32_t)(at < vocab ? t : 0xFF80) << 16 * (e % 2);
         }
-        return r;
-    }
-    // The last chunks: what lies behind the row is -inf.
-    __device__ __forceinline__ void load_edge(int64_t c, float (&v)[8]) const {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t at = element(c, e);
-            const T x = row[at < vocab ? at : vocab - 1];
-            float f;
-            if constexpr (sizeof(T) == 4) f = x;
-            else f = __uint_as_float((uint32_t)x << 16);
-            v[e] = at < vocab ? f : -INFINITY;
-        }
+        return uint4{x[0], x[1], x[2], x[3]};
     }
 };
 
@@ -132,10 +121,13 @@ template <typename T>
 __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64_t piece_groups,
                                                                uint64_t* __restrict__ lists,
                                                                PieceStat* __restrict__ stats) {
-    constexpr int kGroup = group_chunks<T>();
-    __shared__ uint64_t stage_memory[kBeamWaves][kStaged];
+    constexpr int kEach = RowReader<T>::kEach;
+    static_assert(kStaged >= kWords * kWave && kListed >= kWave + kAtOnce, "a group; a full list and what follows it");
+    __shared__ __align__(16) uint4 staged_words[kBeamWaves][kStaged];
+    __shared__ uint32_t staged_at[kBeamWaves][kStaged];
+    __shared__ __align__(16) uint64_t listed[kBeamWaves][kListed];
     __shared__ __align__(16) float published[kBeamWaves];  // a bound that enough of the wave's elements reach
-    __shared__ int kept_by[kBeamWaves];
+    __shared__ int kept_by[kBeamWaves], places[kWave];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t r = blockIdx.x, unit = r * gridDim.y + blockIdx.y;
@@ -144,6 +136,16 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     const int64_t in_piece = all - g0 < piece_groups ? all - g0 : piece_groups;
     const int busy = in_piece < kBeamWaves ? (int)in_piece : kBeamWaves;  // waves that have a group
     const int64_t n = (in_piece - wave + kBeamWaves - 1) / kBeamWaves;    // this wave's
+
+    // The next group is on its way while one is looked at.
+    uint4 next[kWords];
+    auto group_of = [&](int64_t i) { return g0 + wave + i * kBeamWaves; };
+    auto load = [&](int64_t i) __attribute__((always_inline)) {
+        if (i < n && in.inside(group_of(i)))
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) next[j] = in.load(group_of(i), j);
+    };
+    load(0);
 
     // One more than k where the end token may be among them.
     const int need = a.k + (a.eos >= 0 ? 1 : 0), share = (need + busy - 1) / busy;
@@ -163,15 +165,14 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     set_reference();
     float bound = kLeast;  // elements from here on are candidates; -inf is none
     uint64_t best = 0;     // what was sorted, where the stage ran over
-    uint64_t* const stage = stage_memory[wave];
-    int held = 0;
+    int held = 0, in_list = 0;
     bool best_any = false;
-    // Sorts the last 64 (or fewer) staged entries into the best.
+    // Sorts the last 64 (or fewer) of the list into the best.
     auto flush = [&] {
-        const int count = held < kWave ? held : kWave;
-        held -= count;
+        const int count = in_list < kWave ? in_list : kWave;
+        in_list -= count;
         wave_lds_sync();
-        uint64_t v[1] = {lane < count ? stage[held + lane] : 0};
+        uint64_t v[1] = {lane < count ? listed[wave][in_list + lane] : 0};
         wave_lds_sync();
         wave_bitonic_sort<1, true>(v);
         merge_sorted(best, v[0]);
@@ -179,24 +180,31 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     };
     auto raise = [&](float to) { bound = to > bound ? to : bound; };
     // A bound that n of the lanes' maxima reach, and few more: their keys' common
-    // bits, then a bit a step.
+    // bits, then two bits a step.
     auto reached_by = [&](int n) {
         const uint32_t key = key32_of_bits(__float_as_uint(lane_most));
         const uint32_t least = wave_min32(key), most = key32_of_bits(__float_as_uint(m));
         if (n == kWave || least >= most) return float_of_key32(least);
-        int bit = 31 - __builtin_clz(least ^ most);
+        int bit = 31 - __builtin_clz(least ^ most) & ~1;
         const int last = bit > 24 ? 16 : bit > 8 ? bit - 8 : 0;
-        uint32_t to = most & ~1u << bit;
-        for (; bit >= last; --bit) {
-            const uint32_t with = to | 1u << bit;
-            const int count = __popcll(__ballot(key >= with));
-            if (count >= n) to = with;
-            if (count == n) break;
+        uint32_t to = most & ~3u << bit;
+        for (; bit >= last; bit -= 2) {
+            uint32_t with[3];
+            int count[3], chosen = 0;
+#pragma unroll
+            for (int d = 0; d < 3; ++d) {
+                with[d] = to | (uint32_t)(d + 1) << bit;
+                count[d] = __popcll(__ballot(key >= with[d]));
+            }
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+                if (count[d] >= n) to = with[d], chosen = count[d];
+            if (chosen == n) break;
         }
         return float_of_key32(to > least ? to : least);
     };
     auto refresh = [&] {
-        if (share > kWave) return;
+        if (n == 0 || share > kWave) return;
         const float x = reached_by(share);
         if (lane == 0) __hip_atomic_store(&published[wave], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
@@ -208,16 +216,9 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         const float least = fminf(fminf(p[0], p[1]), fminf(p[2], p[3]));
         raise(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(least))));
     };
-    // Looks at the wave's i-th group, chunks c .. + kGroup.
-    auto take = [&](int64_t c, int64_t i, const float (&v)[kGroup][8]) __attribute__((always_inline)) {
-        float top[kGroup], most = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            top[u] = v[u][0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) top[u] = fmaxf(top[u], v[u][e]);
-            most = fmaxf(most, top[u]);
-        }
+    // The maximum and the sum of a group.
+    auto add = [&](const uint4 (&x)[kWords], const float (&top)[kWords]) __attribute__((always_inline)) {
+        float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         lane_most = fmaxf(lane_most, most);
         most = wave_max(most);
         if (most > m) {
@@ -230,73 +231,111 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
             else if (huge) lower = -fmaf(m, kLog2e, -from);
             sum *= __builtin_amdgcn_exp2f(lower);
         }
-        if (huge) {
+        auto terms = [&](auto term) __attribute__((always_inline)) {
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
+            for (int j = 0; j < kWords; ++j) {
                 float part = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) part += __builtin_amdgcn_exp2f((v[u][e] - m) * kLog2e);
+                for (int e = 0; e < kEach; ++e) part += __builtin_amdgcn_exp2f(term(element_of<T>(x[j], e)));
                 sum += part;
             }
-        } else {
+        };
+        if (huge) terms([&](float v) { return (v - m) * kLog2e; });
+        else terms([&](float v) { return fmaf(v, kLog2e, -c2); });
+    };
+    // Stages the words of a group in which something reaches the bound.
+    auto collect = [&](int64_t g, const uint4 (&x)[kWords], const float (&top)[kWords]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                float part = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) part += __builtin_amdgcn_exp2f(fmaf(v[u][e], kLog2e, -c2));
-                sum += part;
+        for (int j = 0; j < kWords; ++j) {
+            const uint64_t mask = __ballot(top[j] >= bound);
+            if (!mask) continue;
+            if (top[j] >= bound) {
+                const int at = held + mbcnt64(mask);
+                staged_words[wave][at] = x[j];
+                staged_at[wave][at] = (uint32_t)in.word_of(g, j);
             }
+            held += __popcll(mask);
         }
-        if ((i & (i + 1)) == 0) refresh();  // groups 0, 1, 3, 7, ..
-        if (i == 0 && need <= kWave) raise(reached_by(need));
-        heed();
-        if (most < bound) return;
-#pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-            if (!__any(top[u] >= bound)) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!__any(v[u][e] >= bound)) continue;
-                const uint32_t at = (uint32_t)in.element(c + u, e);
-                const bool in_list = v[u][e] >= bound && at != (uint32_t)a.eos;
-                const uint64_t mask = __ballot(in_list);
-                if (in_list) stage[held + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v[u][e])), at);
-                held += __popcll(mask);
-            }
-            if (held > kStaged - kChunk) {
-                while (held > 0) flush();
-                // Later chunks of this wave lie behind what it has sorted: they
+    };
+    // Lists the elements of the staged words that reach the bound, a lane an element.
+    auto expand = [&] {
+        wave_lds_sync();
+        for (int i = 0; i < held; i += kWave / kEach) {
+            const int from = i + lane / kEach;
+            const uint32_t at = from < held ? staged_at[wave][from] * kEach + lane % kEach : 0;
+            const T t = reinterpret_cast<const T*>(&staged_words[wave][from < held ? from : 0])[lane % kEach];
+            float v;
+            if constexpr (sizeof(T) == 4) v = t;
+            else v = __uint_as_float((uint32_t)t << 16);
+            const bool hit = from < held && v >= bound && at != (uint32_t)a.eos;
+            const uint64_t mask = __ballot(hit);
+            if (hit) listed[wave][in_list + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v)), at);
+            in_list += __popcll(mask);
+            if (in_list > kWave) {
+                flush();
+                // Later elements of this wave lie behind what it has sorted: they
                 // count if they are larger than the k-th of that.
                 const uint64_t kth = readlane64(best, a.k - 1);
                 if (kth) raise(float_of_key32((uint32_t)(kth >> 32) + 1));
             }
         }
+        held = 0;
     };
 
-    // The next group is on its way while one is looked at.
-    Chunk8<T> x[kGroup];
-    auto chunk_of = [&](int64_t i) { return (g0 + wave + i * kBeamWaves) * kGroup; };
-    auto load = [&](int64_t i) __attribute__((always_inline)) {
-        if (i < n && in.inside(chunk_of(i) + kGroup - 1))
+    for (int64_t i = 0;; ++i) {
+        if (i < n) {
+            const int64_t g = group_of(i);
+            if (!in.inside(g))
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u) x[u] = in.load(chunk_of(i) + u);
-    };
-    load(0);
-    for (int64_t i = 0; i < n; ++i) {
-        const int64_t c = chunk_of(i);
-        float v[kGroup][8];
-        if (in.inside(c + kGroup - 1)) {
+                for (int j = 0; j < kWords; ++j) next[j] = in.load_edge(g, j);
+            uint4 x[kWords];
+            float top[kWords];
 #pragma unroll
-            for (int u = 0; u < kGroup; ++u)
+            for (int j = 0; j < kWords; ++j) {
+                x[j] = next[j];
+                top[j] = element_of<T>(x[j], 0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[u][e] = x[u].get(e);
-        } else
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u) in.load_edge(c + u, v[u]);
-        load(i + 1);
-        take(c, i, v);
+                for (int e = 1; e < kEach; ++e) top[j] = fmaxf(top[j], element_of<T>(x[j], e));
+            }
+            load(i + 1);
+            add(x, top);
+            if ((i & (i + 1)) == 0) refresh();  // groups 0, 1, 3, 7, ..
+            if (i == 0) __syncthreads();        // little is known of the first: all waves' together
+            heed();
+            collect(g, x, top);
+        } else {
+            if (n == 0) __syncthreads();
+            if ((n & (n - 1)) != 0) refresh();  // else it was after the last
+            __syncthreads();
+            heed();
+        }
+        if (held > kStaged - kWords * kWave || i >= n) expand();
+        if (i >= n) break;
     }
 
+    if (best_any) {
+        while (in_list > 0) flush();
+        wave_lds_sync();
+        const uint64_t mask = __ballot(best != 0);  // the first lanes
+        listed[wave][lane] = best;
+        in_list = __popcll(mask);
+    }
+    if (lane < kAtOnce) listed[wave][in_list + lane] = 0;
+    if (lane == 0) kept_by[wave] = in_list;
+    if (wave == 0) places[lane] = 0;
+    __syncthreads();
+    // All waves' together.
+    int upto[kBeamWaves], count = 0;
+#pragma unroll
+    for (int w = 0; w < kBeamWaves; ++w) upto[w] = count += kept_by[w];
+    auto entry_at = [&](int at) {
+        int w = 0, before = 0;
+#pragma unroll
+        for (int u = 0; u + 1 < kBeamWaves; ++u)
+            if (at >= upto[u]) w = u + 1, before = upto[u];
+        return at < count ? listed[w][at - before] : 0;
+    };
+    const uint64_t own = entry_at(lane);
     {
         const double total = wave_reduce(sum, [](double x, double y) { return x + y; });
         // kLog2e is log2(e) (1 + d): the terms are those of logits times 1 + d,
@@ -306,46 +345,25 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
             stats[unit * kBeamWaves + wave] =
                 PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total};
     }
-    refresh();
-    __syncthreads();
-    heed();
-    // What still reaches the bound, to the front of the stage.
-    {
-        const uint64_t least = (uint64_t)key32_of_bits(__float_as_uint(bound)) << 32;
-        int kept = 0;
-        for (int i = 0; i < held; i += kWave) {
-            wave_lds_sync();
-            const uint64_t v = i + lane < held ? stage[i + lane] : 0;
-            const bool keep = v >= least && v != 0;
-            const uint64_t mask = __ballot(keep);
-            wave_lds_sync();
-            if (keep) stage[kept + mbcnt64(mask)] = v;
-            kept += __popcll(mask);
-        }
-        held = kept;
-    }
-    if (best_any) {
-        while (held > 0) flush();
-        wave_lds_sync();
-        const uint64_t mask = __ballot(best != 0);  // the first lanes
-        stage[lane] = best;
-        held = __popcll(mask);
-    }
-    if (lane == 0) kept_by[wave] = held;
-    __syncthreads();
-    if (wave > 0) return;
-    // All waves' together, 64 at a time: most often there are no more.
-    int upto[kBeamWaves], count = 0;
+    if (count <= kWave) {  // most often: an entry's place is the number of larger ones, a wave counts its own
+        int larger = 0;
+        for (int i = 0; i < in_list; i += kAtOnce) {
+            uint64_t other[kAtOnce];
 #pragma unroll
-    for (int w = 0; w < kBeamWaves; ++w) upto[w] = count += kept_by[w];
+            for (int u = 0; u < kAtOnce; ++u) other[u] = listed[wave][i + u];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) larger += other[u] > own;
+        }
+        if (lane < count && larger) __hip_atomic_fetch_add(&places[lane], larger, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        __syncthreads();
+        const int place = lane < count ? places[lane] : lane;
+        if (wave == 0 && place < a.k) lists[unit * a.k + place] = own;
+        return;
+    }
+    if (wave > 0) return;
     best = 0;
     for (int i = 0; i < count; i += kWave) {
-        const int at = i + lane;
-        int w = 0, before = 0;
-#pragma unroll
-        for (int u = 0; u + 1 < kBeamWaves; ++u)
-            if (at >= upto[u]) w = u + 1, before = upto[u];
-        uint64_t v[1] = {at < count ? stage_memory[w][at - before] : 0};
+        uint64_t v[1] = {entry_at(i + lane)};
         wave_bitonic_sort<1, true>(v);
         if (i == 0) best = v[0];
         else merge_sorted(best, v[0]);
