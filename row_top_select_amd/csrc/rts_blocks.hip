@@ -73,6 +73,12 @@ __device__ __forceinline__ void held_words(const uint8_t* held, int pool, int lo
         }
     }
 }
+// The same for a workgroup's share of them.
+template <typename Put>
+__device__ __forceinline__ void held_share(const uint8_t* held, int pool, int words, Put&& put) {
+    const int per = (words + gridDim.x - 1) / gridDim.x, lo = blockIdx.x * per;
+    held_words(held, pool, lo, lo + per < words ? lo + per : words, put);
+}
 // Words [0, words) of LDS, 16 bytes at a time.
 __device__ __forceinline__ void clear(uint32_t* bits, int words) {
     for (int w = threadIdx.x * 4; w < words; w += kPoolBlock * 4) *reinterpret_cast<uint4*>(bits + w) = uint4{0, 0, 0, 0};
@@ -102,11 +108,10 @@ __device__ __forceinline__ ids4 four_entries(const int32_t* row, int j, int n) {
     return x;
 }
 
-// Sets the bits (from that of block `least` on, `pool` of them) of the first
-// n(row) entries of rows [lo, hi) of a table.  A wave takes 64 rows' lengths at a time and reads eight rows side by side, 256 entries each.
+// Sets the bits of the first n(row) entries of rows [lo, hi) of a table.  A wave takes 64 rows' lengths at a time and reads eight rows side by side, 256 entries each.
 template <typename Count>
-__device__ __forceinline__ void mark_rows(const int32_t* table, int64_t ld, int64_t lo, int64_t hi, int least,
-                                          int pool, uint32_t* bits, Count&& n) {
+__device__ __forceinline__ void mark_rows(const int32_t* table, int64_t ld, int64_t lo, int64_t hi, int pool,
+                                          uint32_t* bits, Count&& n) {
     constexpr int kRows = 8;
     const int lane = lane_id();
     for (int64_t r0 = lo; r0 < hi; r0 += kWave) {
@@ -129,7 +134,7 @@ __device__ __forceinline__ void mark_rows(const int32_t* table, int64_t ld, int6
                 for (int u = 0; u < kRows; ++u)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        if ((uint32_t)(id[u][v] - least) < (uint32_t)pool) set_bit(bits, id[u][v] - least);
+                        if ((uint32_t)id[u][v] < (uint32_t)pool) set_bit(bits, id[u][v]);
             }
         }
     }
@@ -145,7 +150,7 @@ __device__ __forceinline__ void rows_of(int64_t part, int64_t parts, int64_t row
 // takes an entry, eight on their way, of entries [lo, hi) of the table read row by row.
 template <typename Count>
 __device__ __forceinline__ void mark_entries(const int32_t* table, int64_t ld, uint32_t cols, uint32_t lo, uint32_t hi,
-                                             int least, int pool, uint32_t* bits, Count&& n) {
+                                             int pool, uint32_t* bits, Count&& n) {
     constexpr int kAhead = 8;
     for (uint32_t e0 = lo + threadIdx.x; e0 < hi; e0 += kAhead * kPoolBlock) {
         int id[kAhead];
@@ -158,21 +163,21 @@ __device__ __forceinline__ void mark_entries(const int32_t* table, int64_t ld, u
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (inside[u] && (uint32_t)(id[u] - least) < (uint32_t)pool) set_bit(bits, id[u] - least);
+            if (inside[u] && (uint32_t)id[u] < (uint32_t)pool) set_bit(bits, id[u]);
     }
 }
 constexpr int kNarrow = 128;  // columns below which a table is
 template <typename Count>
 __device__ __forceinline__ void mark_table(const int32_t* table, int64_t ld, int cols, int64_t rows, int64_t part,
-                                           int64_t parts, int least, int pool, uint32_t* bits, Count&& n) {
+                                           int64_t parts, int pool, uint32_t* bits, Count&& n) {
     if (cols < kNarrow) {
         const uint32_t all = (uint32_t)rows * (uint32_t)cols, per = (all + (uint32_t)parts - 1) / (uint32_t)parts;
         const uint32_t lo = (uint32_t)part * per < all ? (uint32_t)part * per : all;
-        mark_entries(table, ld, cols, lo, lo + per < all ? lo + per : all, least, pool, bits, n);
+        mark_entries(table, ld, cols, lo, lo + per < all ? lo + per : all, pool, bits, n);
     } else {
         int64_t lo, hi;
         rows_of(part * kPoolWaves + threadIdx.x / kWave, parts * kPoolWaves, rows, lo, hi);
-        mark_rows(table, ld, lo, hi, least, pool, bits, n);
+        mark_rows(table, ld, lo, hi, pool, bits, n);
     }
 }
 
@@ -295,81 +300,78 @@ __device__ __forceinline__ void load_parents(const ForkArgs& a, int (&par)[kFork
 }
 
 // Where tables are large, the bits of their entries are formed by several
-// workgroups, into bit fields that the call's workgroups join: one takes a part of the rows
-// and a quarter of the pool.  A wave's 64 atomic operations in LDS take 16
-// cycles, so they and not the reads bound this: the quarters read the same rows.
-constexpr int kQuarters = 4;
-struct MarkShare {
-    int first_word, words, least, blocks;  // of the pool
-    int field, parts;                      // of the rows
-    __device__ __forceinline__ explicit MarkShare(int32_t pool) {
-        const int all = words_of(pool), per = (all / 4 + kQuarters - 1) / kQuarters * 4, q = blockIdx.x % kQuarters;
-        first_word = q * per < all ? q * per : all;
-        words = first_word + per < all ? per : all - first_word;
-        least = first_word * 32;
-        blocks = pool - least < words * 32 ? pool - least : words * 32;
-        if (blocks < 0) blocks = 0;
-        field = blockIdx.x / kQuarters;
-        parts = gridDim.x / kQuarters;
-    }
-    // The held blocks' words of the quarter, this part's of them.
-    template <typename Put>
-    __device__ __forceinline__ void held(const uint8_t* held, int pool, Put&& put) const {
-        const int per = (words + parts - 1) / parts;
-        const int lo = field * per < words ? field * per : words, hi = lo + per < words ? lo + per : words;
-        held_words(held, pool, first_word + lo, first_word + hi, put);
-    }
-};
-
+// workgroups, each of a share of the rows and of the held blocks, into bit fields of the whole pool
+// that a further launch joins to one.
 __global__ __launch_bounds__(kPoolBlock) void mark_fork_kernel(ForkArgs a, uint32_t* __restrict__ fields) {
     extern __shared__ __align__(16) uint32_t lds[];
-    const MarkShare my(a.pool);
+    const int words = words_of(a.pool);
     uint32_t* const used = lds;
-    int* const first = reinterpret_cast<int*>(used + my.words);
+    int* const first = reinterpret_cast<int*>(used + words);
     int par[kForkRowsEach];
     load_parents(a, par);
-    clear(used, my.words);
+    clear(used, words);
     first_rows(a, first, par);
-    my.held(a.held, a.pool, [&](int w, uint32_t bits) { atomicOr(&used[w - my.first_word], bits); });
-    mark_table(a.table, a.ld_table, a.cols, a.rows_in, my.field, my.parts, my.least, my.blocks, used,
+    held_share(a.held, a.pool, words, [&](int w, uint32_t bits) { atomicOr(&used[w], bits); });
+    mark_table(a.table, a.ld_table, a.cols, a.rows_in, blockIdx.x, gridDim.x, a.pool, used,
                [&](int64_t p) { return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full; });
     __syncthreads();
-    store_field(fields + (int64_t)my.field * words_of(a.pool) + my.first_word, used, my.words);
+    store_field(fields + (int64_t)blockIdx.x * words, used, words);
 }
 __global__ __launch_bounds__(kPoolBlock) void mark_compact_kernel(CompactArgs a, uint32_t* __restrict__ fields) {
     extern __shared__ __align__(16) uint32_t lds[];
-    const MarkShare my(a.pool);
-    clear(lds, my.words);
+    const int words = words_of(a.pool);
+    clear(lds, words);
     __syncthreads();
-    const int64_t words = words_of(a.pool);
-    my.held(a.held, a.pool, [&](int w, uint32_t bits) { fields[my.parts * words + w] = bits; });  // a field of their own
-    mark_table(a.table, a.ld_table, a.cols, a.rows, my.field, my.parts, my.least, my.blocks, lds,
+    uint32_t* const held = fields + (int64_t)gridDim.x * words;  // a field of their own
+    held_share(a.held, a.pool, words, [&](int w, uint32_t bits) { held[w] = bits; });
+    mark_table(a.table, a.ld_table, a.cols, a.rows, blockIdx.x, gridDim.x, a.pool, lds,
                [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
     __syncthreads();
-    store_field(fields + (int64_t)my.field * words + my.first_word, lds, my.words);
+    store_field(fields + (int64_t)blockIdx.x * words, lds, words);
 }
-// dst[w] |= word w of all fields (`words` a multiple of 4), four loads of 16 bytes on their way.
-__device__ __forceinline__ void join_fields(const uint32_t* fields, int n, int words, uint32_t* dst) {
+// Field 0 becomes all n fields' bits, four words a thread.
+constexpr int kJoinBlock = 64;
+__global__ __launch_bounds__(kJoinBlock) void join_fields_kernel(uint32_t* fields, int n, int words) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    constexpr int kFields = 4;
-    for (int w = threadIdx.x * 4; w < words; w += kPoolBlock * 4) {
-        u32x4 bits = *reinterpret_cast<u32x4*>(dst + w);
-        for (int f = 0; f < n; f += kFields) {
-            u32x4 x[kFields];
+    constexpr int kAhead = 8;
+    const int w = (blockIdx.x * kJoinBlock + threadIdx.x) * 4;
+    if (w >= words) return;
+    u32x4 bits = {0, 0, 0, 0};
+    for (int f = 0; f < n; f += kAhead) {
+        u32x4 x[kAhead];
 #pragma unroll
-            for (int u = 0; u < kFields; ++u) {
-                x[u] = u32x4{0, 0, 0, 0};
-                if (f + u < n) x[u] = *reinterpret_cast<const u32x4*>(fields + (int64_t)(f + u) * words + w);
-            }
+        for (int u = 0; u < kAhead; ++u)
+            x[u] = *reinterpret_cast<const u32x4*>(fields + (int64_t)(f + u < n ? f + u : f) * words + w);
 #pragma unroll
-            for (int u = 0; u < kFields; ++u) bits |= x[u];
+        for (int u = 0; u < kAhead; ++u) bits |= x[u];
+    }
+    *reinterpret_cast<u32x4*>(fields + w) = bits;
+}
+static int launch_join_fields(uint32_t* fields, int n, int words, hipStream_t s) {
+    hipLaunchKernelGGL(join_fields_kernel, dim3((unsigned)(words / 4 + kJoinBlock - 1) / kJoinBlock), dim3(kJoinBlock), 0, s,
+                       fields, n, words);
+    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+}
+// dst = a field, four loads of 16 bytes of a thread on their way.
+__device__ __forceinline__ void load_field(const uint32_t* field, int words, uint32_t* dst) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kAhead = 4;
+    for (int w0 = threadIdx.x * 4; w0 < words; w0 += kPoolBlock * 4 * kAhead) {
+        u32x4 x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int w = w0 + u * kPoolBlock * 4;
+            x[u] = *reinterpret_cast<const u32x4*>(field + (w < words ? w : w0));
         }
-        *reinterpret_cast<u32x4*>(dst + w) = bits;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int w = w0 + u * kPoolBlock * 4;
+            if (w < words) *reinterpret_cast<u32x4*>(dst + w) = x[u];
+        }
     }
 }
 
-__global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, const uint32_t* __restrict__ fields,
-                                                                 int n_fields) {
+__global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, const uint32_t* __restrict__ field) {
     extern __shared__ __align__(16) uint32_t lds[];
     __shared__ uint32_t wave_sum[kPoolWaves];
     __shared__ uint32_t free_before[kPoolBlock];
@@ -396,16 +398,16 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
         last[u] = n.full < n.need ? a.table[(tid + u * kPoolBlock) * a.ld_table + n.full] : -1;
         if ((uint32_t)last[u] >= (uint32_t)a.pool) last[u] = -1;
     }
-    clear(used, 2 * words);
+    if (field) clear(twice, words);
+    else clear(used, 2 * words);
+    if (field) load_field(field, words, used);
     first_rows(a, first, par);
-    if (n_fields)
-        join_fields(fields, n_fields, words, used);
-    else
+    if (!field)
         held_words(a.held, a.pool, 0, words, [&](int w, uint32_t bits) { atomicOr(&used[w], bits); });
     __syncthreads();
     if (tid < 4 && words > 0) atomicOr(&used[words - 4 + tid], behind(a.pool, words - 4 + tid));
-    if (n_fields == 0) {
-        mark_table(a.table, a.ld_table, a.cols, rows_in, 0, 1, 0, a.pool, used, [&](int64_t p) {
+    if (!field) {
+        mark_table(a.table, a.ld_table, a.cols, rows_in, 0, 1, a.pool, used, [&](int64_t p) {
             return first[p] == kNoRow ? 0 : lengths(a.ctx_lens[p], a.block_size, a.cols).full;
         });
         __syncthreads();
@@ -495,13 +497,14 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
     });
 }
 
-// Bit fields of large tables: none where one workgroup reads the tables in
-// about the time that a launch takes.
+// Bit fields of large tables, one for 16384 entries (for 8192 nothing is gained): none where
+// every workgroup reads the table itself in about the time of two more launches.  Calls of
+// fork_blocks and compact_blocks, us, without and with fields: 160 x 256 entries 15 / 15 and
+// 19 / 18; 256 x 256 18 / 18 and 19 / 18; 512 x 256 23 / 27 and 19 / 19; 800 x 512 46 / 64 and 25 / 30.
 static int mark_parts(int64_t rows, int32_t cols) {
     const int64_t entries = rows * (int64_t)cols;
-    return entries <= 81920 ? 0 : entries < 4 * 32768 ? 2 : 4;
+    return entries <= 65536 ? 0 : entries < 32 * 16384 ? (int)((entries + 16383) / 16384) : 32;
 }
-static size_t mark_lds(int32_t pool) { return (size_t)(words_of(pool) / 4 + kQuarters - 1) / kQuarters * 16; }
 size_t fork_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
     return (size_t)mark_parts(rows, cols) * words_of(pool) * 4;
 }
@@ -510,16 +513,15 @@ static int64_t pool_grid(int64_t work) { return work / 2048 < 1 ? 1 : work / 204
 
 int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t s) {
     const size_t words = words_of(a.pool);
-    const int parts = workspace ? mark_parts(a.rows_in, a.cols) : 0;
+    const int parts = workspace && words ? mark_parts(a.rows_in, a.cols) : 0;
     uint32_t* fields = static_cast<uint32_t*>(workspace);
     if (parts) {
-        hipLaunchKernelGGL(mark_fork_kernel, dim3(parts * kQuarters), dim3(kPoolBlock), mark_lds(a.pool) + a.rows_in * 4, s,
-                           a, fields);
-        if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+        hipLaunchKernelGGL(mark_fork_kernel, dim3(parts), dim3(kPoolBlock), (words + a.rows_in) * 4, s, a, fields);
+        if (hipGetLastError() != hipSuccess || launch_join_fields(fields, parts, (int)words, s)) return RTS_EHIP;
     }
     const size_t rows = a.rows_out, most = a.rows_in > a.rows_out ? a.rows_in : a.rows_out;
     hipLaunchKernelGGL(fork_blocks_kernel, dim3((unsigned)pool_grid(a.rows_out * (int64_t)a.cols + a.n_free)),
-                       dim3(kPoolBlock), (words + (words > rows ? words : rows) + most) * 4, s, a, fields, parts);
+                       dim3(kPoolBlock), (words + (words > rows ? words : rows) + most) * 4, s, a, parts ? fields : nullptr);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
@@ -527,8 +529,8 @@ int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t s) {
 // smallest bound below which there are n blocks that are not held.  Live ones at
 // or past T move, in ascending order, to the free ones below it: there are as
 // many of one as of the other, and no block is both left and taken.
-__global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs a, const uint32_t* __restrict__ fields,
-                                                                    int n_fields) {
+__global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs a, const uint32_t* __restrict__ field,
+                                                                    const uint32_t* __restrict__ held) {
     extern __shared__ __align__(16) uint32_t lds[];
     __shared__ uint32_t wave_sum[kPoolWaves];
     __shared__ uint32_t open_before[kPoolBlock];  // blocks that are not held
@@ -539,18 +541,20 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
     uint32_t* const open = live + words;  // not held
     const uint64_t *const live2 = reinterpret_cast<const uint64_t*>(live), *const open2 = reinterpret_cast<const uint64_t*>(open);
     const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
-    clear(live, 2 * words);
-    __syncthreads();
-    if (tid < 4 && words > 0) open[words - 4 + tid] = behind(a.pool, words - 4 + tid);
-    __syncthreads();
-    if (n_fields) {
-        join_fields(fields, n_fields, words, live);
-        if (a.held) join_fields(fields + (int64_t)n_fields * words, 1, words, open);
+    if (field) {
+        load_field(field, words, live);
+        if (held) load_field(held, words, open);
+        else clear(open, words);
+        __syncthreads();
     } else {
+        clear(live, 2 * words);
+        __syncthreads();
         held_words(a.held, a.pool, 0, words, [&](int w, uint32_t bits) { atomicOr(&open[w], bits); });
-        mark_table(a.table, a.ld_table, a.cols, a.rows, 0, 1, 0, a.pool, live,
+        mark_table(a.table, a.ld_table, a.cols, a.rows, 0, 1, a.pool, live,
                    [&](int64_t r) { return lengths(a.ctx_lens[r], a.block_size, a.cols).need; });
+        __syncthreads();
     }
+    if (tid < 4 && words > 0) open[words - 4 + tid] |= behind(a.pool, words - 4 + tid);
     __syncthreads();
     const int all_pairs = words / 2, pairs = unit_of(words) / 2;
     const int p0 = tid * pairs < all_pairs ? tid * pairs : all_pairs, p1 = p0 + pairs < all_pairs ? p0 + pairs : all_pairs;
@@ -658,14 +662,15 @@ size_t compact_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
 
 int launch_compact_blocks(const CompactArgs& a, void* workspace, hipStream_t s) {
     const size_t words = words_of(a.pool);
-    const int parts = workspace ? mark_parts(a.rows, a.cols) : 0;
+    const int parts = workspace && words ? mark_parts(a.rows, a.cols) : 0;
     uint32_t* fields = static_cast<uint32_t*>(workspace);
     if (parts) {
-        hipLaunchKernelGGL(mark_compact_kernel, dim3(parts * kQuarters), dim3(kPoolBlock), mark_lds(a.pool), s, a, fields);
-        if (hipGetLastError() != hipSuccess) return RTS_EHIP;
+        hipLaunchKernelGGL(mark_compact_kernel, dim3(parts), dim3(kPoolBlock), words * 4, s, a, fields);
+        if (hipGetLastError() != hipSuccess || launch_join_fields(fields, parts, (int)words, s)) return RTS_EHIP;
     }
     const int64_t grid = pool_grid(2 * a.rows * (int64_t)a.cols + a.n_free + 2 * a.max_moves);
-    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)grid), dim3(kPoolBlock), words * 8, s, a, fields, parts);
+    hipLaunchKernelGGL(compact_blocks_kernel, dim3((unsigned)grid), dim3(kPoolBlock), words * 8, s, a,
+                       parts ? fields : nullptr, parts && a.held ? fields + (size_t)parts * words : nullptr);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
