@@ -500,10 +500,10 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
 // Bit fields of large tables, one for 16384 entries (for 8192 nothing is gained): none where
 // every workgroup reads the table itself in about the time of two more launches.  Calls of
 // fork_blocks and compact_blocks, us, without and with fields: 160 x 256 entries 15 / 15 and
-// 19 / 18; 256 x 256 18 / 18 and 19 / 18; 512 x 256 23 / 27 and 19 / 19; 800 x 512 46 / 64 and 25 / 30.
+// 19 / 18; 320 x 256 20 / 21 and 19 / 18; 512 x 256 23 / 27 and 19 / 19; 800 x 512 46 / 64 and 25 / 30.
 static int mark_parts(int64_t rows, int32_t cols) {
     const int64_t entries = rows * (int64_t)cols;
-    return entries <= 65536 ? 0 : entries < 32 * 16384 ? (int)((entries + 16383) / 16384) : 32;
+    return entries <= 81920 ? 0 : entries < 32 * 16384 ? (int)((entries + 16383) / 16384) : 32;
 }
 size_t fork_blocks_bytes(int64_t rows, int32_t cols, int32_t pool) {
     return (size_t)mark_parts(rows, cols) * words_of(pool) * 4;
