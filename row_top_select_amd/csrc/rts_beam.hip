@@ -127,14 +127,16 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     __shared__ uint32_t staged_at[kBeamWaves][kStaged];
     __shared__ __align__(16) uint64_t listed[kBeamWaves][kListed];
     __shared__ __align__(16) float published[kBeamWaves];  // a bound that enough of the wave's elements reach
-    __shared__ int kept_by[kBeamWaves], places[kWave];
+    __shared__ int kept_by[kBeamWaves], places[kBeamBlock];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t r = blockIdx.x, unit = r * gridDim.y + blockIdx.y;
     const RowReader<T> in{static_cast<const T*>(a.logits) + r * a.ld, a.vocab};
     const int64_t g0 = blockIdx.y * piece_groups, all = (a.vocab + group_elements<T>() - 1) / group_elements<T>();
     const int64_t in_piece = all - g0 < piece_groups ? all - g0 : piece_groups;
-    const int busy = in_piece < kBeamWaves ? (int)in_piece : kBeamWaves;  // waves that have a group
+    // Waves that have a whole group (the row's last one may have too few elements for a bound of use).
+    const int64_t whole = in_piece > 1 && !in.inside(g0 + in_piece - 1) ? in_piece - 1 : in_piece;
+    const int busy = whole < kBeamWaves ? (int)whole : kBeamWaves;
     const int64_t n = (in_piece - wave + kBeamWaves - 1) / kBeamWaves;    // this wave's
 
     // The next group is on its way while one is looked at.
@@ -204,7 +206,7 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         return float_of_key32(to > least ? to : least);
     };
     auto refresh = [&] {
-        if (n == 0 || share > kWave) return;
+        if (wave >= busy || share > kWave) return;
         const float x = reached_by(share);
         if (lane == 0) __hip_atomic_store(&published[wave], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
@@ -259,6 +261,10 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     };
     // Lists the elements of the staged words that reach the bound, a lane an element.
     auto expand = [&] {
+        // More than there should be: the other waves hold the bound down (their elements
+        // are masked, or rise), and this wave's own may be higher.  256 x 102400 bf16, the whole
+        // call: all but 2048 masked 24.5 us without it, 20.9 with it; rows in order 153 and 53.
+        if (held > kWave && need <= kWave) raise(reached_by(need));
         wave_lds_sync();
         for (int i = 0; i < held; i += kWave / kEach) {
             const int from = i + lane / kEach;
@@ -322,7 +328,7 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     }
     if (lane < kAtOnce) listed[wave][in_list + lane] = 0;
     if (lane == 0) kept_by[wave] = in_list;
-    if (wave == 0) places[lane] = 0;
+    places[threadIdx.x] = 0;
     __syncthreads();
     // All waves' together.
     int upto[kBeamWaves], count = 0;
@@ -335,7 +341,7 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
             if (at >= upto[u]) w = u + 1, before = upto[u];
         return at < count ? listed[w][at - before] : 0;
     };
-    const uint64_t own = entry_at(lane);
+    const uint64_t mine = entry_at(threadIdx.x);
     {
         const double total = wave_reduce(sum, [](double x, double y) { return x + y; });
         // kLog2e is log2(e) (1 + d): the terms are those of logits times 1 + d,
@@ -345,30 +351,22 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
             stats[unit * kBeamWaves + wave] =
                 PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total};
     }
-    if (count <= kWave) {  // most often: an entry's place is the number of larger ones, a wave counts its own
+    // An entry's place is the number of larger ones: a wave counts those of its own.
+    for (int at = lane; at - lane < count; at += kWave) {
+        const uint64_t v = entry_at(at);
         int larger = 0;
         for (int i = 0; i < in_list; i += kAtOnce) {
             uint64_t other[kAtOnce];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) other[u] = listed[wave][i + u];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) larger += other[u] > own;
+            for (int u = 0; u < kAtOnce; ++u) larger += other[u] > v;
         }
-        if (lane < count && larger) __hip_atomic_fetch_add(&places[lane], larger, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        __syncthreads();
-        const int place = lane < count ? places[lane] : lane;
-        if (wave == 0 && place < a.k) lists[unit * a.k + place] = own;
-        return;
+        if (at < count && larger) __hip_atomic_fetch_add(&places[at], larger, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
-    if (wave > 0) return;
-    best = 0;
-    for (int i = 0; i < count; i += kWave) {
-        uint64_t v[1] = {entry_at(i + lane)};
-        wave_bitonic_sort<1, true>(v);
-        if (i == 0) best = v[0];
-        else merge_sorted(best, v[0]);
-    }
-    if (lane < a.k) lists[unit * a.k + lane] = best;
+    __syncthreads();
+    const int place = (int)threadIdx.x < count ? places[threadIdx.x] : threadIdx.x;
+    if (place < a.k) lists[unit * a.k + place] = mine;
 }
 
 // A candidate among those of other beams: the upper 52 bits of its value's

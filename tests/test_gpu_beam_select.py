@@ -110,6 +110,31 @@ def test_masked_logits_and_beams(rts):
     assert (got.parents[3] == -1).all() and (got.scores[3] == -math.inf).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["start", "end", "few", "rising", "falling", "tail of large ones"])
+@pytest.mark.parametrize("vocab", [6253, 8200, 70001])
+def test_uneven_rows(rts, dtype, kind, vocab):
+    """Candidates in a few places of a row only, or all in its last elements."""
+    say("uneven", dtype, kind, vocab)
+    logits, scores = inputs(vocab, 2, 3, vocab, torch.float32)
+    if kind == "start":
+        logits[:, 900:] = -math.inf
+    elif kind == "end":
+        logits[:, :-70] = -math.inf
+    elif kind == "few":
+        keep = torch.rand(logits.shape, generator=torch.Generator().manual_seed(2)) < 40 / vocab
+        logits[~keep] = -math.inf
+    elif kind == "rising":
+        logits = logits.sort(dim=1).values
+    elif kind == "falling":
+        logits = logits.sort(dim=1, descending=True).values
+    else:
+        logits[:, -5:] += 30
+    logits = logits.to(dtype)
+    for k, eos in ((1, -1), (32, 0), (64, vocab - 1)):
+        check_beams(run(rts, logits, scores, k, eos), logits, scores, k, eos)
+
+
 def test_far_scores(rts):
     """Scores and logits at the ends of their range: the order is that of 64-bit values, then of the logits."""
     logits, scores = inputs(4, 1, 3, 900, torch.float32)
