@@ -578,6 +578,8 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * workspace  device scratch, 16-byte aligned, of at least
  *            beam_select_workspace_size bytes.  Calls in flight at the same time
  *            need workspaces of their own.
+ * out_scores may be scores where k is beams (refused otherwise); no other output may
+ * overlap an input or another output.
  * Maxima, sums and values are held in 32 bits or more (sums over a row's parts
  * and values in 64).
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (beams, k, vocab >= 2^31, groups * beams
@@ -626,7 +628,8 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
  *            fork_blocks_workspace_size bytes (0 where none is of use): lets several
  *            workgroups read a large table.  Calls in flight at the same time need
  *            workspaces of their own.
- * No output may overlap an input or another output.
+ * No output may overlap an input or another output (a table or lengths in place are
+ * refused).
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (rows, pool_blocks, table_cols >= 2^19),
  *         RTS_EWORKSPACE, RTS_EHIP.
  */
@@ -656,7 +659,7 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
  * counts     int32 [2]: how many are free, and how many moves there are in all.
  * Other arguments as in fork_blocks (rows * table_cols < 2^31), workspace with
  * compact_blocks_workspace_size bytes.
- * No output may overlap an input or another output.
+ * No output may overlap an input or another output (a table in place is refused).
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED, RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t compact_blocks_workspace_size(int64_t rows, int32_t table_cols, int32_t pool_blocks);

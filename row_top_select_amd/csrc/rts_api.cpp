@@ -518,6 +518,7 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
     if (workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
     if (groups * beams * plan.pieces > rts::kMaxThreads / 256 || groups > rts::kMaxThreads / 1024)
         return RTS_EUNSUPPORTED;
+    if (out_scores == scores && k != beams) return RTS_EINVAL;  // a group's would go over another's
     rts::BeamArgs a{};
     a.logits = logits, a.scores = scores, a.out_scores = out_scores, a.ended = ended, a.parents = parents;
     a.tokens = tokens, a.groups = groups, a.vocab = vocab, a.ld = ld_logits, a.beams = beams, a.k = k, a.eos = eos;
@@ -551,6 +552,8 @@ int fork_blocks(const int32_t* block_table, int64_t rows_in, int32_t table_cols,
         return RTS_EINVAL;
     if ((workspace_bytes > 0 && !workspace) || !aligned(workspace, 16)) return RTS_EINVAL;
     if (workspace && workspace_bytes < rts::fork_blocks_bytes(rows_in, table_cols, pool_blocks)) return RTS_EWORKSPACE;
+    if ((out_table && out_table == block_table) || (out_lens && (out_lens == ctx_lens || out_lens == parents)))
+        return RTS_EINVAL;  // not in place
     rts::ForkArgs a{};
     a.table = block_table, a.ctx_lens = ctx_lens, a.parents = parents, a.held = held, a.out_table = out_table;
     a.out_ctx = out_lens, a.copies = copies, a.free_blocks = free_blocks, a.counts = counts, a.rows_in = rows_in;
@@ -582,6 +585,7 @@ int compact_blocks(const int32_t* block_table, int64_t rows, int32_t table_cols,
         return RTS_EINVAL;
     if ((workspace_bytes > 0 && !workspace) || !aligned(workspace, 16)) return RTS_EINVAL;
     if (workspace && workspace_bytes < rts::compact_blocks_bytes(rows, table_cols, pool_blocks)) return RTS_EWORKSPACE;
+    if (out_table && out_table == block_table) return RTS_EINVAL;  // not in place
     rts::CompactArgs a{};
     a.table = block_table, a.ctx_lens = ctx_lens, a.held = held, a.out_table = out_table, a.moves = moves;
     a.free_blocks = free_blocks, a.counts = counts, a.rows = rows, a.ld_table = ld_table, a.ld_out = ld_out;

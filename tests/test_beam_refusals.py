@@ -151,6 +151,14 @@ def test_kv_attend_paged_plan():
     assert f(w=64) == 0 and p[0] == 0
 
 
+def test_outputs_in_place():
+    other = ctypes.c_void_p(0x20000)
+    assert beam(k=5) == EINVAL  # scores of 4 beams, 5 picks
+    assert fork(lens=other) == EINVAL and fork(out=other) == EINVAL
+    assert fork(out=other, lens=other, parents=other) == EINVAL
+    assert compact() == EINVAL
+
+
 def test_binding():
     z = torch.zeros
     i = dict(dtype=torch.int32)

@@ -211,6 +211,16 @@ def test_given_outputs_streams_and_replay(rts):
         assert all(torch.equal(a, b) for a, b in zip(eager, out))
 
 
+@pytest.mark.parametrize("beams", [1, 5, 64])
+def test_scores_in_place(rts, beams):
+    logits, scores = inputs(beams, 7, beams, 3001, torch.float32)
+    x, s = logits.to(DEV), scores.to(DEV)
+    want = rts.beam_select(x, s, beams, eos=3)
+    out = rts.BeamStep(s, torch.empty_like(want.parents), torch.empty_like(want.tokens), torch.empty_like(want.ended))
+    rts.beam_select(x, s, beams, eos=3, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_far_rows(rts):
     """Rows past 2^32 bytes."""
     vocab, ld = 1000, 300_000_000
