@@ -50,6 +50,7 @@ constexpr int kKvLeast = kKvLeastKeys / kKvTile;  // tiles of a piece
 // 16384, bf16, 569 us (24: 570, 96: 572, whose last pieces end later).
 constexpr int kKvGoal = 48;
 constexpr int kKvRounds = 8;    // pieces a place at most
+constexpr int kKvWhole = 1 << 17;
 constexpr int kKvEntries = 4;   // tiles of block-table entries that a wave holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -536,8 +537,12 @@ static int kv_places(int32_t dim, int dtype) {
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
                       bool allow_split) {
     const int64_t blocks = kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
-    // Every workgroup of a split call sums up the rows, so calls of very many are not.
-    if (!allow_split || max_len <= kKvLeastKeys || rows > 4096) return KvPlan{0, 0, 0};
+    // Rows that a workgroup each has done in the time of the second launch, some 4 us, are not
+    // split: a step of 64 keys takes 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements.  Calls of 4
+    // rows, split and whole, us: 128 elements 17.2 and 13.3 for 512 keys, 17.1 and 15.8 for 768, 17.1 and
+    // 19.6 for 1024; 64 elements 17.0 and 14.3 for 1024; 256 elements 18.1 and 15.7 for 384, 18.0 and 18.9 for
+    // 512.  Every workgroup of a split call sums up the rows, so calls of very many are not, either.
+    if (!allow_split || max_len <= kKvWhole / (dim + 48) || rows > 4096) return KvPlan{0, 0, 0};
     // The grid has room for what max_len may need: workgroups without a piece take
     // a place for 2 us each (8 times too many of them cost a call of 8 us another 7).
     const int64_t tiles = max_len < (1ll << 31) ? (max_len + kKvTile - 1) / kKvTile : 1ll << 26, all = rows * tiles;

@@ -32,15 +32,20 @@ def rand(g, *shape, dtype=torch.bfloat16, scale=1.0):
 
 def check(rts, q, k, v, req, ends, table, block, scale, stride=None, window=0, ks=None, vs=None, max_len=None,
           workspace="auto", kd=None, vd=None, qd=None):
-    """q, k, v on the CPU; kd, vd, qd: the tensors to hand over, where they differ."""
+    """q, k, v on the CPU; kd, vd, qd: the tensors to hand over, where they differ.  Calls that may be split are made
+    with a bound on the lengths too that has them split."""
     stride = block if stride is None else stride
     kd, vd = (k.to(DEV) if kd is None else kd), (v.to(DEV) if vd is None else vd)
     qd = q.to(DEV) if qd is None else qd
-    got, lse = rts.kv_attend_paged(
-        qd, kd, vd, i32(req), i32(ends), i32(table) if table and table[0] else torch.empty(
-            len(table), 0, dtype=torch.int32, device=DEV), block, scale, k_scales=None if ks is None else ks.to(DEV),
-        v_scales=None if vs is None else vs.to(DEV), window=window, stride_rows=stride, max_len=max_len,
-        workspace=workspace)
+    def call(max_len):
+        return rts.kv_attend_paged(
+            qd, kd, vd, i32(req), i32(ends), i32(table) if table and table[0] else torch.empty(
+                len(table), 0, dtype=torch.int32, device=DEV), block, scale, k_scales=None if ks is None else ks.to(DEV),
+            v_scales=None if vs is None else vs.to(DEV), window=window, stride_rows=stride, max_len=max_len,
+            workspace=workspace)
+
+    got, lse = call(max_len)
+    calls = [(got, lse)] + ([call(1 << 20)] if max_len is None and workspace == "auto" else [])
     torch.cuda.synchronize()
     rows, heads, dim = q.shape
     kv_heads = k.shape[1]
@@ -58,8 +63,9 @@ def check(rts, q, k, v, req, ends, table, block, scale, stride=None, window=0, k
                 x.append(y)
     o, ob = (torch.stack(want[i]).view(rows, heads, dim) for i in (0, 2))
     l, lb = (torch.stack(want[i]).view(rows, heads) for i in (1, 3))
-    assert_close(got, o, ob, "out")
-    assert_close(lse, l, lb, "lse")
+    for got, lse in reversed(calls):
+        assert_close(got, o, ob, "out")
+        assert_close(lse, l, lb, "lse")
     return got, lse
 
 
@@ -92,7 +98,7 @@ def test_kv_attend(rts, dtype, dim, ctx, heads, kv, block, stride):
         check(rts, *a, block, dim ** -0.5, stride=stride, ks=ks, vs=vs, workspace=ws)
 
 
-@pytest.mark.parametrize("window", [1, 31, 100, 5000])
+@pytest.mark.parametrize("window", [1, 31, 100, 777, 1001, 5000])
 @pytest.mark.parametrize("each", [1, 3])
 def test_window(rts, window, each):
     say("window", window, each)
@@ -317,7 +323,7 @@ def test_groups_of_heads(rts, heads, kv):
 def test_more_rows_than_are_split(rts):
     q, k, v, _, _, table = setup(14, [200], 1, 1, 64, 16)
     rows = 4100
-    assert plan(rts, rows, 1, 1, 64, 200)[0] == 0 and plan(rts, 4096, 1, 1, 64, 200)[0] > 0
+    assert plan(rts, rows, 1, 1, 64, 1 << 20)[0] == 0 and plan(rts, 4096, 1, 1, 64, 1 << 20)[0] > 0
     q = rand(torch.Generator().manual_seed(2), rows, 1, 64)
     ends = [(7 * t) % 201 for t in range(rows)]
     check(rts, q, k, v, [0] * rows, ends, table, 16, 0.125)
