@@ -270,3 +270,41 @@ def test_streams(rts):
         if a >= 0:
             before[b * block:(b + 1) * block] = before[a * block:(a + 1) * block]
     assert torch.equal(cache, before)
+
+
+def test_large_tables_captured_and_at_once(rts):
+    """Tables that several workgroups read first: replays on other inputs, and calls at the same time."""
+    pool, block, rows = 90_000, 16, 400
+    assert rts.raw_library().fork_blocks_workspace_size(rows, 251, pool) > 0
+    cases = []
+    for seed in (21, 22, 23):
+        table, ctx, held = setup(seed, 50, 8, 4000, block, pool, 0.02)
+        parents = torch.randint(-1, rows, (rows,), generator=torch.Generator().manual_seed(seed)).tolist()
+        assert len(table) == rows and len(table[0]) == 251
+        cases.append((table, ctx, held, parents, ref.fork(table, ctx, parents, block, pool, held, pool),
+                      ref.compact(table, ctx, block, pool, held, pool // 2, pool)))
+    t, c, p = i32(cases[0][0]), i32(cases[0][1]), i32(cases[0][3])
+    h = torch.tensor(cases[0][2], device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f = rts.fork_blocks(t, c, p, block, pool, held=h)
+        m = rts.compact_blocks(t, c, block, pool, held=h)
+    for table, ctx, held, parents, forked, compacted in cases:
+        t.copy_(torch.tensor(table))
+        c.copy_(torch.tensor(ctx))
+        p.copy_(torch.tensor(parents))
+        h.copy_(torch.tensor(held))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_same(f, forked, "fork")
+        assert_same(m, compacted, "compact")
+    streams = [torch.cuda.Stream() for _ in cases]
+    inputs = [(i32(x[0]), i32(x[1]), i32(x[3]), torch.tensor(x[2], device=DEV)) for x in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [(rts.fork_blocks(t, c, p, block, pool, held=h, stream=s), rts.compact_blocks(t, c, block, pool, held=h, stream=s))
+               for s, (t, c, p, h) in zip(streams, inputs)]
+        torch.cuda.synchronize()
+        for (f, m), x in zip(got, cases):
+            assert_same(f, x[4], "fork")
+            assert_same(m, x[5], "compact")
