@@ -50,7 +50,7 @@ constexpr int kKvLeast = kKvLeastKeys / kKvTile;  // tiles of a piece
 // 16384, bf16, 569 us (24: 570, 96: 572, whose last pieces end later).
 constexpr int kKvGoal = 48;
 constexpr int kKvRounds = 8;    // pieces a place at most
-constexpr int kKvWhole = 1 << 17;
+constexpr int kKvWhole = 9 << 14;
 constexpr int kKvEntries = 4;   // tiles of block-table entries that a wave holds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
     }
     const int32_t* const table = a.pages.table + (int64_t)(seen.req < 0 ? 0 : seen.req) * a.pages.ld;
     const int tiles = (p1 - p0) / kKvTile + ((p1 - p0) % kKvTile != 0);
-    const int count = (tiles - wave + kKvWaves - 1) / kKvWaves;  // of this wave
+    const int count = __builtin_amdgcn_readfirstlane((tiles - wave + kKvWaves - 1) / kKvWaves);  // of this wave
 
     const float factor = a.scale * (a.k_scales ? a.k_scales[kvh] : 1.f);
     const float c = factor == 0.f ? 1.f : fabsf(factor) * kLog2e;
@@ -278,8 +278,8 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
     };
     auto exists = [&](int row) { return (uint32_t)__ballot(row >= 0); };
 
-    // The ring is always filled (behind the last tile with zeros), so that the
-    // number of loads under way is the same at every tile.
+    // Behind tile n are under way, as long as there is a tile n + 1, the entries of
+    // tile n + 2 and the tile n + 1, in this order; behind the last tile nothing that matters.
     uint32_t exist = 0, exist_next = 0;  // which keys of tiles n and n + 1 are seen
     if (count > 0) {
         look(0);
@@ -287,8 +287,10 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const int first = row_of(0), second = row_of(1);
         fetch(0, first);
-        look(2);
-        fetch(1, second);
+        if (count > 1) {
+            look(2);
+            fetch(1, second);
+        }
         exist = exists(first);
         exist_next = exists(second);
     }
@@ -314,7 +316,10 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
     float m = kNoMax, l = 0.f;
     for (int n = 0; n < count; ++n) {
         // Tile n has arrived once only what was issued behind it is under way.
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::kLoads + 1) : "memory");
+        if (n + 1 < count)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::kLoads + 1) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const uint32_t at = ring + (n & (kKvStages - 1)) * S::kStageB;
         f32x4 s[2] = {};
 #pragma unroll
@@ -392,10 +397,11 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p, o[t], 0, 0, 0);
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, low, o[t], 0, 0, 0);
         }
+        exist = exist_next;
+        if (n + 2 >= count) continue;
         // The stage is read, and tile n + 2's entries have arrived.
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * S::kLoads) : "memory");
         const int next = row_of(n + 2);
-        exist = exist_next;
         exist_next = exists(next);
         look(n + 3);
         fetch(n + 2, next);
@@ -539,8 +545,8 @@ KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim
     const int64_t blocks = kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
     // Rows that a workgroup each has done in the time of the second launch, some 4 us, are not
     // split: a step of 64 keys takes 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements.  Calls of 4
-    // rows, split and whole, us: 128 elements 17.2 and 13.3 for 512 keys, 17.1 and 15.8 for 768, 17.1 and
-    // 19.6 for 1024; 64 elements 17.0 and 14.3 for 1024; 256 elements 18.1 and 15.7 for 384, 18.0 and 18.9 for
+    // rows, split and whole, us: 128 elements 17.2 and 13.3 for 512 keys, 17.8 and 15.7 for 768, 17.9 and
+    // 19.6 for 1024; 64 elements 17.0 and 14.5 for 1024; 256 elements 18.1 and 14.8 for 384, 18.0 and 18.1 for
     // 512.  Every workgroup of a split call sums up the rows, so calls of very many are not, either.
     if (!allow_split || max_len <= kKvWhole / (dim + 48) || rows > 4096) return KvPlan{0, 0, 0};
     // The grid has room for what max_len may need: workgroups without a piece take
