@@ -10,7 +10,7 @@
 // its terms in any order, so lane group g has keys 4 g + 0..3 and 16 + 4 g + 0..3,
 // which the transposing LDS reads deliver of V in the same order.
 //
-// A wave has keys of its own, every kKvWaves-th tile of the workgroup's piece, and a
+// A wave has keys of its own, every second (or fourth, or eighth) tile of the workgroup's piece, and a
 // ring of two tiles in LDS, loaded straight from memory by whole rows; nothing
 // passes between waves until the end, where they join their sums through LDS.
 // Rows that a token does not see score -inf and their values are cleared in LDS,
@@ -43,7 +43,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kKvTile = 32;     // keys of a stage
 constexpr int kKvStages = 2;
 constexpr int kKvWaves = 2;     // (1: 64 requests of 16384 positions 584 us for 569, 4 of 1000 10.2 for 8.6)
-constexpr int kKvBlock = kKvWaves * kWave;
 constexpr int kKvHeads = 16;    // query heads of a workgroup
 constexpr int kKvLeast = kKvLeastKeys / kKvTile;  // tiles of a piece
 // Tiles of a piece of long contexts.  3 requests of 131072 positions, e4m3, 63 us (24: 74, 96: 62); 64 of
@@ -128,8 +127,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16;
 }
 
-template <int D, bool E4M3, bool BIG>
-__global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int target, int rounds, KvParts parts) {
+template <int D, bool E4M3, bool BIG, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void kv_attend_kernel(KvArgs a, int target, int rounds, KvParts parts) {
     using S = KvShape<D, E4M3>;
     constexpr int NK = D / 32, NT = D / 16;  // steps of the first product, tiles of the second
     extern __shared__ __align__(1024) char lds_memory[];
@@ -235,14 +234,14 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
     }
     const int32_t* const table = a.pages.table + (int64_t)(seen.req < 0 ? 0 : seen.req) * a.pages.ld;
     const int tiles = (p1 - p0) / kKvTile + ((p1 - p0) % kKvTile != 0);
-    const int count = __builtin_amdgcn_readfirstlane((tiles - wave + kKvWaves - 1) / kKvWaves);  // of this wave
+    const int count = __builtin_amdgcn_readfirstlane((tiles - wave + WAVES - 1) / WAVES);  // of this wave
 
     const float factor = a.scale * (a.k_scales ? a.k_scales[kvh] : 1.f);
     const float c = factor == 0.f ? 1.f : fabsf(factor) * kLog2e;
     const float lazy = kLazy / c;
 
     // The first position of the wave's tile n.  Past the piece's end they may pass 2^31.
-    auto tile_at = [&](int n) { return (uint32_t)p0 + ((uint32_t)n * kKvWaves + wave) * kKvTile; };
+    auto tile_at = [&](int n) { return (uint32_t)p0 + ((uint32_t)n * WAVES + wave) * kKvTile; };
     auto look = [&](int n) {
         uint32_t e = tile_at(n) + (lane & 31);
         e = e < (uint32_t)p1 ? e : (uint32_t)(p1 - 1);
@@ -421,12 +420,12 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
     }
     __syncthreads();
     const float v_scale = a.v_scales ? a.v_scales[kvh] : 1.f;
-    for (int i = tid; i < kKvHeads * D / 8; i += kKvBlock) {
+    for (int i = tid; i < kKvHeads * D / 8; i += WAVES * kWave) {
         const int h = i / (D / 8), d8 = i % (D / 8);
         if (block * kKvHeads + h >= group) break;
-        float wm[kKvWaves], wl[kKvWaves], most = kNoMax, total = 0.f;
+        float wm[WAVES], wl[WAVES], most = kNoMax, total = 0.f;
 #pragma unroll
-        for (int w = 0; w < kKvWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const float* stat = reinterpret_cast<const float*>(lds_memory + w * S::kWaveB + kKvStages * S::kStageB);
             wm[w] = stat[h];
             wl[w] = stat[16 + h];
@@ -434,7 +433,7 @@ __global__ __launch_bounds__(kKvBlock) void kv_attend_kernel(KvArgs a, int targe
         }
         f32x4 sum[2] = {};
 #pragma unroll
-        for (int w = 0; w < kKvWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const float f = __builtin_amdgcn_exp2f((wm[w] - most) * c);
             total += wl[w] * f;
             const float* from = reinterpret_cast<const float*>(lds_memory + w * S::kWaveB) + h * D;
@@ -534,6 +533,17 @@ __global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int 
 }
 
 // Workgroups that a CU has room for, by their LDS.
+// Workgroups of a token.
+static int64_t kv_blocks(int32_t heads, int32_t kv_heads) {
+    return kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
+}
+// Waves of a workgroup that has whole rows: as many as have room in a CU where there
+// are no more workgroups than CUs.
+constexpr int kKvWideMost = 256;
+static constexpr int wide_waves(int row_bytes) { return row_bytes <= 128 ? 8 : row_bytes <= 256 ? 4 : kKvWaves; }
+static int kv_waves(int64_t workgroups, int row_bytes) {
+    return workgroups <= kKvWideMost ? wide_waves(row_bytes) : kKvWaves;
+}
 static int kv_places(int32_t dim, int dtype) {
     const int wave_bytes = kKvStages * 2 * kKvTile * dim * (dtype == RTS_E4M3 ? 1 : 2) + kKvEntries * 256;
     const int n = 160 * 1024 / (kKvWaves * wave_bytes);
@@ -542,13 +552,15 @@ static int kv_places(int32_t dim, int dtype) {
 
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
                       bool allow_split) {
-    const int64_t blocks = kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
+    const int64_t blocks = kv_blocks(heads, kv_heads);
     // Rows that a workgroup each has done in the time of the second launch, some 4 us, are not
-    // split: a step of 64 keys takes 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements.  Calls of 4
-    // rows, split and whole, us: 128 elements 17.2 and 13.3 for 512 keys, 17.8 and 15.7 for 768, 17.9 and
-    // 19.6 for 1024; 64 elements 17.0 and 14.5 for 1024; 256 elements 18.1 and 14.8 for 384, 18.0 and 18.1 for
-    // 512.  Every workgroup of a split call sums up the rows, so calls of very many are not, either.
-    if (!allow_split || max_len <= kKvWhole / (dim + 48) || rows > 4096) return KvPlan{0, 0, 0};
+    // split: a step of 64 keys takes two waves 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements, and
+    // more waves less.  Calls of 4 rows, split and whole, us: 128 elements, bf16, four waves 17 and 13.5
+    // for 1024 keys, 17 and 23 for 2048; e4m3, eight waves 18.5 and 15.6 for 2048; 64 elements, eight
+    // waves 17 and 13 for 2048; 256 elements, two waves 18 and 15 for 384, 18 and 18 for 512.
+    // Every workgroup of a split call sums up the rows, so calls of very many are not, either.
+    const int64_t waves = kv_waves(rows * blocks, dim * (dtype == RTS_E4M3 ? 1 : 2));
+    if (!allow_split || max_len <= kKvWhole * (waves + 2) / 4 / (dim + 48) || rows > 4096) return KvPlan{0, 0, 0};
     // The grid has room for what max_len may need: workgroups without a piece take
     // a place for 2 us each (8 times too many of them cost a call of 8 us another 7).
     const int64_t tiles = max_len < (1ll << 31) ? (max_len + kKvTile - 1) / kKvTile : 1ll << 26, all = rows * tiles;
@@ -563,21 +575,30 @@ KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim
     return p;
 }
 
+template <int D, bool E4M3, bool BIG, int WAVES>
+static int launch_kv_waves(const KvArgs& a, int64_t grid, const KvPlan& plan, const KvParts& parts, hipStream_t s) {
+    if (grid > kMaxThreads / (WAVES * kWave)) return RTS_EUNSUPPORTED;
+    hipLaunchKernelGGL((kv_attend_kernel<D, E4M3, BIG, WAVES>), dim3((unsigned)grid), dim3(WAVES * kWave),
+                       WAVES * (KvShape<D, E4M3>::kWaveB), s, a, plan.target, plan.rounds, parts);
+    return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+}
+
 template <int D, bool E4M3, bool BIG>
 static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {
-    const int64_t group = a.heads / a.kv_heads, blocks = a.kv_heads * ((group + kKvHeads - 1) / kKvHeads);
-    const int64_t most = (int64_t)plan.target * plan.rounds, grid = (a.rows + (most ? most + 1 : 0)) * blocks;
-    if (grid > kMaxThreads / kKvBlock || a.rows * a.heads > kMaxThreads / kJoinBlock) return RTS_EUNSUPPORTED;
-    KvParts parts{};
-    if (plan.target) {
-        parts.out = static_cast<float*>(workspace);
-        parts.lse = parts.out + 2 * most * a.heads * D;
-        parts.rows = reinterpret_cast<int2*>(parts.lse + 2 * most * a.heads);
+    const int64_t blocks = kv_blocks(a.heads, a.kv_heads);
+    if (a.rows * a.heads > kMaxThreads / kJoinBlock) return RTS_EUNSUPPORTED;
+    if (plan.target == 0) {
+        constexpr int kWide = wide_waves(KvShape<D, E4M3>::kRowB);
+        return a.rows * blocks <= kKvWideMost ? launch_kv_waves<D, E4M3, BIG, kWide>(a, a.rows * blocks, plan, KvParts{}, s)
+                                            : launch_kv_waves<D, E4M3, BIG, kKvWaves>(a, a.rows * blocks, plan, KvParts{}, s);
     }
-    hipLaunchKernelGGL((kv_attend_kernel<D, E4M3, BIG>), dim3((unsigned)grid), dim3(kKvBlock),
-                       kKvWaves * (KvShape<D, E4M3>::kWaveB), s, a, plan.target, plan.rounds, parts);
-    if (hipGetLastError() != hipSuccess) return RTS_EHIP;
-    if (plan.target == 0) return RTS_OK;
+    const int64_t most = (int64_t)plan.target * plan.rounds;
+    KvParts parts;
+    parts.out = static_cast<float*>(workspace);
+    parts.lse = parts.out + 2 * most * a.heads * D;
+    parts.rows = reinterpret_cast<int2*>(parts.lse + 2 * most * a.heads);
+    const int rc = launch_kv_waves<D, E4M3, BIG, kKvWaves>(a, (a.rows + most + 1) * blocks, plan, parts, s);
+    if (rc != RTS_OK) return rc;
     // Few of them are cut finer, to have more of the chip read the pieces: 8 heads of one
     // request of 131072 positions 7.3 us, 15.8 whole; 32 heads 5.6 both; 128 (4 requests of 1000) 4.0 and 3.7.
     const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);

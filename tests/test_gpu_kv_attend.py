@@ -98,7 +98,7 @@ def test_kv_attend(rts, dtype, dim, ctx, heads, kv, block, stride):
         check(rts, *a, block, dim ** -0.5, stride=stride, ks=ks, vs=vs, workspace=ws)
 
 
-@pytest.mark.parametrize("window", [1, 31, 100, 840, 1001, 5000])
+@pytest.mark.parametrize("window", [1, 31, 100, 840, 1300, 5000])
 @pytest.mark.parametrize("each", [1, 3])
 def test_window(rts, window, each):
     say("window", window, each)
