@@ -576,8 +576,8 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * ended      float [groups, beams]: value(b, eos), -inf for beams that have no
  *            candidates.  NULL exactly where eos is -1.
  * workspace  device scratch, 16-byte aligned, of at least
- *            beam_select_workspace_size bytes.  Calls in flight at the same time
- *            need workspaces of their own.
+ *            beam_select_workspace_size bytes; may be NULL where that is 0 (short rows of few
+ *            beams).  Calls in flight at the same time need workspaces of their own.
  * out_scores may be scores where k is beams (refused otherwise); no other output may
  * overlap an input or another output.
  * Maxima, sums and values are held in 32 bits or more (sums over a row's parts

@@ -509,12 +509,13 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
         return RTS_EINVAL;
     if (rc != RTS_OK) return rc;
     if (groups == 0) return RTS_OK;
-    if (!logits || !scores || !out_scores || !parents || !tokens || !workspace || (eos < 0) != (ended == nullptr))
+    if (!logits || !scores || !out_scores || !parents || !tokens || (eos < 0) != (ended == nullptr))
         return RTS_EINVAL;
     if (!aligned(logits, dtype == RTS_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
         !aligned(parents, 4) || !aligned(tokens, 4) || !aligned(ended, 4) || !aligned(workspace, 16))
         return RTS_EINVAL;
     const rts::BeamPlan plan = rts::plan_beam_select(dtype, groups, beams, vocab, k);
+    if (!workspace && (workspace_bytes > 0 || plan.ws_bytes > 0)) return RTS_EINVAL;
     if (workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
     if (groups * beams * plan.pieces > rts::kMaxThreads / 256 || groups > rts::kMaxThreads / 1024)
         return RTS_EUNSUPPORTED;

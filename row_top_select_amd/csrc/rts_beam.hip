@@ -2,7 +2,7 @@
 //
 // For a group of beams with scores s_b and rows of logits x_b, the k largest of
 //   s_b + x_b[v] - lse_b,   lse_b = log sum_v exp x_b[v]
-// in two launches.
+// in two launches, or one.
 //
 // 1. The four waves of a workgroup stream a row (or a piece of one), each every
 //    fourth group of 4 KB, with a running maximum and sum of the softmax.  A
@@ -16,6 +16,7 @@
 //    What is left (some 20 for k = 8) is ranked by counting the larger ones.
 // 2. A workgroup a group joins its rows' pieces and ranks the rows' candidates
 //    against each other by their values in 64 bits.
+// Where rows are short and beams few, one workgroup does both.
 //
 // Bound by the reads.  Measured, the scan and the join: 256 x 102400 bf16, k = 8:
 // 15.3 + 4.9 us (3.4 TB/s); 1024 x 131072 bf16 and k = 32, the whole call: 62 us
@@ -36,6 +37,10 @@ constexpr int kBeamBlock = kBeamWaves * kWave;
 constexpr int kWords = 4;         // of 16 bytes that a lane loads at a time: a group of 4 KB a wave
 template <typename T>
 constexpr int group_elements() { return kWords * kWave * 16 / (int)sizeof(T); }
+template <typename T>
+__host__ __device__ __forceinline__ int64_t row_groups(int64_t vocab) {
+    return (vocab + group_elements<T>() - 1) / group_elements<T>();
+}
 constexpr int kStaged = 384;      // words with candidates that a wave holds
 constexpr int kListed = 2 * kWave;  // candidates
 constexpr int kAtOnce = 8;
@@ -117,31 +122,39 @@ __device__ __forceinline__ void merge_sorted(uint64_t& best, uint64_t more) {
     best = v[0];
 }
 
-template <typename T>
-__global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64_t piece_groups,
-                                                               uint64_t* __restrict__ lists,
-                                                               PieceStat* __restrict__ stats) {
+template <int WAVES>
+struct ScanLds {
+    uint4 words[WAVES][kStaged];     // with candidates
+    uint64_t listed[WAVES][kListed];
+    float published[WAVES];          // a bound that enough of the wave's elements reach
+    uint32_t at[WAVES][kStaged];
+    int kept[WAVES], places[WAVES * kWave];
+};
+static_assert(kStaged >= kWords * kWave && kListed >= kWave + kAtOnce, "a group; a full list and what follows it");
+
+// The scan of `count` groups from g0 on of a row by EACH waves of a workgroup, whose other waves scan
+// other rows (or none: 0 groups): stat(part of the sum) by lane 0 of each, put(place, entry) for places 0..k-1
+// by any thread of theirs.
+template <typename T, int WAVES, int EACH, typename Stat, typename Put>
+__device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds, const RowReader<T>& in, int64_t g0,
+                                         int64_t groups, Stat&& stat, Put&& put) {
     constexpr int kEach = RowReader<T>::kEach;
-    static_assert(kStaged >= kWords * kWave && kListed >= kWave + kAtOnce, "a group; a full list and what follows it");
-    __shared__ __align__(16) uint4 staged_words[kBeamWaves][kStaged];
-    __shared__ uint32_t staged_at[kBeamWaves][kStaged];
-    __shared__ __align__(16) uint64_t listed[kBeamWaves][kListed];
-    __shared__ __align__(16) float published[kBeamWaves];  // a bound that enough of the wave's elements reach
-    __shared__ int kept_by[kBeamWaves], places[kBeamBlock];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t r = blockIdx.x, unit = r * gridDim.y + blockIdx.y;
-    const RowReader<T> in{static_cast<const T*>(a.logits) + r * a.ld, a.vocab};
-    const int64_t g0 = blockIdx.y * piece_groups, all = (a.vocab + group_elements<T>() - 1) / group_elements<T>();
-    const int64_t in_piece = all - g0 < piece_groups ? all - g0 : piece_groups;
+    const int side = EACH == WAVES ? wave : wave % EACH;  // the wave's number in its row
+    const int team = EACH == WAVES ? 0 : wave - side;     // the first of them
+    uint4* const staged_words = lds.words[wave];
+    uint32_t* const staged_at = lds.at[wave];
+    uint64_t* const listed = lds.listed[wave];
+    float* const published = lds.published + team;
     // Waves that have a whole group (the row's last one may have too few elements for a bound of use).
-    const int64_t whole = in_piece > 1 && !in.inside(g0 + in_piece - 1) ? in_piece - 1 : in_piece;
-    const int busy = whole < kBeamWaves ? (int)whole : kBeamWaves;
-    const int64_t n = (in_piece - wave + kBeamWaves - 1) / kBeamWaves;    // this wave's
+    const int64_t whole = groups > 1 && !in.inside(g0 + groups - 1) ? groups - 1 : groups;
+    const int busy = whole < EACH ? (int)whole : EACH;
+    const int64_t n = (groups - side + EACH - 1) / EACH;  // this wave's
 
     // The next group is on its way while one is looked at.
     uint4 next[kWords];
-    auto group_of = [&](int64_t i) { return g0 + wave + i * kBeamWaves; };
+    auto group_of = [&](int64_t i) { return g0 + side + i * EACH; };
     auto load = [&](int64_t i) __attribute__((always_inline)) {
         if (i < n && in.inside(group_of(i)))
 #pragma unroll
@@ -150,8 +163,8 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
     load(0);
 
     // One more than k where the end token may be among them.
-    const int need = a.k + (a.eos >= 0 ? 1 : 0), share = (need + busy - 1) / busy;
-    if (threadIdx.x < kBeamWaves) published[threadIdx.x] = (int)threadIdx.x < busy ? -INFINITY : INFINITY;
+    const int need = a.k + (a.eos >= 0 ? 1 : 0), share = (need + busy - 1) / (busy > 0 ? busy : 1);
+    if (lane == 0) published[side] = side < busy ? -INFINITY : INFINITY;
     __syncthreads();
 
     float m = kLeast, sum = 0.f, lane_most = -INFINITY;
@@ -174,7 +187,7 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         const int count = in_list < kWave ? in_list : kWave;
         in_list -= count;
         wave_lds_sync();
-        uint64_t v[1] = {lane < count ? listed[wave][in_list + lane] : 0};
+        uint64_t v[1] = {lane < count ? listed[in_list + lane] : 0};
         wave_lds_sync();
         wave_bitonic_sort<1, true>(v);
         merge_sorted(best, v[0]);
@@ -206,16 +219,18 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         return float_of_key32(to > least ? to : least);
     };
     auto refresh = [&] {
-        if (wave >= busy || share > kWave) return;
+        if (side >= busy || share > kWave) return;
         const float x = reached_by(share);
-        if (lane == 0) __hip_atomic_store(&published[wave], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (lane == 0) __hip_atomic_store(&published[side], x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
     auto heed = [&] {  // the other waves
-        typedef float f32x4 __attribute__((ext_vector_type(4)));
+        typedef float bounds __attribute__((ext_vector_type(EACH)));
         // Through a plain pointer the read waits for the group under way as well,
         // and that is faster: 1024 x 131072 bf16 65 us, read as LDS without that wait 74.
-        const f32x4 p = *reinterpret_cast<volatile f32x4*>(published);
-        const float least = fminf(fminf(p[0], p[1]), fminf(p[2], p[3]));
+        const bounds p = *reinterpret_cast<volatile bounds*>(published);
+        float least = p[0];
+#pragma unroll
+        for (int w = 1; w < EACH; ++w) least = fminf(least, p[w]);
         raise(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(least))));
     };
     // The maximum and the sum of a group.
@@ -253,8 +268,8 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
             if (!mask) continue;
             if (top[j] >= bound) {
                 const int at = held + mbcnt64(mask);
-                staged_words[wave][at] = x[j];
-                staged_at[wave][at] = (uint32_t)in.word_of(g, j);
+                staged_words[at] = x[j];
+                staged_at[at] = (uint32_t)in.word_of(g, j);
             }
             held += __popcll(mask);
         }
@@ -268,14 +283,14 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         wave_lds_sync();
         for (int i = 0; i < held; i += kWave / kEach) {
             const int from = i + lane / kEach;
-            const uint32_t at = from < held ? staged_at[wave][from] * kEach + lane % kEach : 0;
-            const T t = reinterpret_cast<const T*>(&staged_words[wave][from < held ? from : 0])[lane % kEach];
+            const uint32_t at = from < held ? staged_at[from] * kEach + lane % kEach : 0;
+            const T t = reinterpret_cast<const T*>(&staged_words[from < held ? from : 0])[lane % kEach];
             float v;
             if constexpr (sizeof(T) == 4) v = t;
             else v = __uint_as_float((uint32_t)t << 16);
             const bool hit = from < held && v >= bound && at != (uint32_t)a.eos;
             const uint64_t mask = __ballot(hit);
-            if (hit) listed[wave][in_list + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v)), at);
+            if (hit) listed[in_list + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v)), at);
             in_list += __popcll(mask);
             if (in_list > kWave) {
                 flush();
@@ -323,33 +338,34 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         while (in_list > 0) flush();
         wave_lds_sync();
         const uint64_t mask = __ballot(best != 0);  // the first lanes
-        listed[wave][lane] = best;
+        listed[lane] = best;
         in_list = __popcll(mask);
     }
-    if (lane < kAtOnce) listed[wave][in_list + lane] = 0;
-    if (lane == 0) kept_by[wave] = in_list;
-    places[threadIdx.x] = 0;
+    if (lane < kAtOnce) listed[in_list + lane] = 0;
+    if (lane == 0) lds.kept[wave] = in_list;
+    lds.places[threadIdx.x] = 0;
     __syncthreads();
-    // All waves' together.
-    int upto[kBeamWaves], count = 0;
+    // All of the row's waves' together.
+    int* const places = lds.places + team * kWave;
+    int upto[EACH], count = 0;
 #pragma unroll
-    for (int w = 0; w < kBeamWaves; ++w) upto[w] = count += kept_by[w];
+    for (int w = 0; w < EACH; ++w) upto[w] = count += lds.kept[team + w];
     auto entry_at = [&](int at) {
         int w = 0, before = 0;
 #pragma unroll
-        for (int u = 0; u + 1 < kBeamWaves; ++u)
+        for (int u = 0; u + 1 < EACH; ++u)
             if (at >= upto[u]) w = u + 1, before = upto[u];
-        return at < count ? listed[w][at - before] : 0;
+        return at < count ? lds.listed[team + w][at - before] : 0;
     };
-    const uint64_t mine = entry_at(threadIdx.x);
+    const int thread = side * kWave + lane;
+    const uint64_t mine = entry_at(thread);
     {
         const double total = wave_reduce(sum, [](double x, double y) { return x + y; });
         // kLog2e is log2(e) (1 + d): the terms are those of logits times 1 + d,
         // and their sum's logarithm is off by d times the softmax's mean logit, which lies near m.
         constexpr double kOff = (double)kLog2e * 0.69314718055994530942 - 1.;
         if (lane == 0)
-            stats[unit * kBeamWaves + wave] =
-                PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total};
+            stat(PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total});
     }
     // An entry's place is the number of larger ones: a wave counts those of its own.
     for (int at = lane; at - lane < count; at += kWave) {
@@ -358,15 +374,29 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
         for (int i = 0; i < in_list; i += kAtOnce) {
             uint64_t other[kAtOnce];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) other[u] = listed[wave][i + u];
+            for (int u = 0; u < kAtOnce; ++u) other[u] = listed[i + u];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) larger += other[u] > v;
         }
         if (at < count && larger) __hip_atomic_fetch_add(&places[at], larger, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     __syncthreads();
-    const int place = (int)threadIdx.x < count ? places[threadIdx.x] : threadIdx.x;
-    if (place < a.k) lists[unit * a.k + place] = mine;
+    const int place = thread < count ? places[thread] : thread;
+    if (place < a.k) put(place, mine);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64_t piece_groups,
+                                                               uint64_t* __restrict__ lists,
+                                                               PieceStat* __restrict__ stats) {
+    __shared__ __align__(16) ScanLds<kBeamWaves> lds;
+    const int64_t r = blockIdx.x, unit = r * gridDim.y + blockIdx.y;
+    const int64_t g0 = blockIdx.y * piece_groups, all = row_groups<T>(a.vocab);
+    scan_row<T, kBeamWaves, kBeamWaves>(
+        a, lds, RowReader<T>{static_cast<const T*>(a.logits) + r * a.ld, a.vocab}, g0,
+        all - g0 < piece_groups ? all - g0 : piece_groups,
+        [&](PieceStat x) { stats[unit * kBeamWaves + threadIdx.x / kWave] = x; },
+        [&](int place, uint64_t x) { lists[unit * a.k + place] = x; });
 }
 
 // A candidate among those of other beams: the upper 52 bits of its value's
@@ -379,49 +409,50 @@ __device__ __forceinline__ uint64_t entry(double v, int beam, int rank) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_join_kernel(BeamArgs a, int pieces,
-                                                                         const uint64_t* __restrict__ lists,
-                                                                         const PieceStat* __restrict__ stats) {
-    extern __shared__ uint64_t merged[];  // [waves][64]
-    const int lane = lane_id(), waves = blockDim.x / kWave;
+__device__ __forceinline__ float end_logit_of(const BeamArgs& a, int64_t r) {
+    const T x = static_cast<const T*>(a.logits)[r * a.ld + a.eos];
+    if constexpr (sizeof(T) == 4) return x;
+    else return __uint_as_float((uint32_t)x << 16);
+}
+
+// What joins a group: `waves` waves (others of the workgroup only keep step) that take a beam each in turn.
+struct JoinLds {
+    uint64_t* merged;  // [waves][64]
+    float* values;     // [beams][64] by rank in their beam
+    uint32_t* cols;
+};
+// list(r, u), of piece u of row r, this lane's entry; stat(r, p) of its part p.
+template <typename T, typename List, typename Stat, typename Score>
+__device__ __forceinline__ void join_group(const BeamArgs& a, int64_t group, int waves, const JoinLds& lds, int pieces,
+                                           int parts, List&& list, Stat&& stat, Score&& score_of) {
+    const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    float* const values = reinterpret_cast<float*>(merged + waves * kWave);    // [beams][64] by rank in their beam
-    uint32_t* const cols = reinterpret_cast<uint32_t*>(values + a.beams * 64);
-    const int64_t group = blockIdx.x;
     uint64_t mine = 0;
     for (int b = wave; b < a.beams; b += waves) {
         const int64_t r = group * a.beams + b;
-        const uint64_t* const list = lists + r * pieces * a.k + lane;
-        const PieceStat* const stat = stats + r * pieces * kBeamWaves;
-        const int parts = pieces * kBeamWaves;
         constexpr int kAhead = 4;
         uint64_t some[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) some[u] = lane < a.k && u < pieces ? list[u * a.k] : 0;
-        const PieceStat first = lane < parts ? stat[lane] : PieceStat{-1e300, 0.};
-        const float score = a.scores[r];
-        float end_logit = 0.f;
-        if (a.ended) {
-            const T x = static_cast<const T*>(a.logits)[r * a.ld + a.eos];
-            if constexpr (sizeof(T) == 4) end_logit = x;
-            else end_logit = __uint_as_float((uint32_t)x << 16);
-        }
+        for (int u = 0; u < kAhead; ++u) some[u] = lane < a.k && u < pieces ? list(r, u) : 0;
+        const PieceStat first = lane < parts ? stat(r, lane) : PieceStat{-1e300, 0.};
+        float end_logit;
+        const float score = score_of(r, end_logit);
         uint64_t best = some[0];
         for (int p0 = 0; p0 < pieces; p0 += kAhead) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (p0 + u >= pieces) break;
                 if (p0 + u > 0) merge_sorted(best, some[u]);
-                some[u] = lane < a.k && p0 + u + kAhead < pieces ? list[(int64_t)(p0 + u + kAhead) * a.k] : 0;
+                some[u] = lane < a.k && p0 + u + kAhead < pieces ? list(r, p0 + u + kAhead) : 0;
             }
         }
         // The row's sum: a wave's part of a piece a lane.
         auto sums = [](double x, double y) { return x + y; };
         double m = first.ref;
-        for (int p = lane + kWave; p < parts; p += kWave) m = fmax(m, stat[p].ref);
+        for (int p = lane + kWave; p < parts; p += kWave) m = fmax(m, stat(r, p).ref);
         m = wave_reduce(m, [](double x, double y) { return fmax(x, y); });
         double sum = first.sum * exp(first.ref - m);
-        for (int p = lane + kWave; p < parts; p += kWave) sum += stat[p].sum * exp(stat[p].ref - m);
+        for (int p = lane + kWave; p < parts; p += kWave) sum += stat(r, p).sum * exp(stat(r, p).ref - m);
         sum = wave_reduce(sum, sums);
         // A row without a finite sum (NaN or +inf in it, or -inf only) and a beam
         // without a finite score have no candidates.
@@ -430,8 +461,8 @@ __global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_join_kernel(BeamAr
         // The difference first: logits of any size keep what lies behind their last place.
         auto value = [&](float x) { return ((double)x - m) + shift; };
         const double v = value(float_of_key32((uint32_t)(best >> 32)));
-        values[b * 64 + lane] = (float)v;
-        cols[b * 64 + lane] = composite_id(best);
+        lds.values[b * 64 + lane] = (float)v;
+        lds.cols[b * 64 + lane] = composite_id(best);
         const uint64_t here = takes_part && best != 0 && lane < a.k ? entry(v, b, lane) : 0;
         if (b == wave) mine = here;
         else merge_sorted(mine, here);
@@ -439,25 +470,80 @@ __global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_join_kernel(BeamAr
     }
     // The waves' lists, two by two.
     for (int step = 1; step < waves; step <<= 1) {
-        if ((wave & (2 * step - 1)) == step) merged[wave * kWave + lane] = mine;
+        if ((wave & (2 * step - 1)) == step) lds.merged[wave * kWave + lane] = mine;
         __syncthreads();
-        if ((wave & (2 * step - 1)) == 0 && wave + step < waves) merge_sorted(mine, merged[(wave + step) * kWave + lane]);
+        if ((wave & (2 * step - 1)) == 0 && wave + step < waves) merge_sorted(mine, lds.merged[(wave + step) * kWave + lane]);
     }
     if (wave > 0 || lane >= a.k) return;
     const int64_t at = group * a.k + lane;
     const int from = 0xFFF - (int)(mine & 0xFFF);
-    a.out_scores[at] = mine ? values[from] : -INFINITY;
+    a.out_scores[at] = mine ? lds.values[from] : -INFINITY;
     a.parents[at] = mine ? (int32_t)(group * a.beams + from / 64) : -1;
-    a.tokens[at] = mine ? (int32_t)cols[from] : -1;
+    a.tokens[at] = mine ? (int32_t)lds.cols[from] : -1;
 }
 
+template <typename T>
+__global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_join_kernel(BeamArgs a, int pieces,
+                                                                         const uint64_t* __restrict__ lists,
+                                                                         const PieceStat* __restrict__ stats) {
+    extern __shared__ uint64_t memory[];
+    const int waves = blockDim.x / kWave, parts = pieces * kBeamWaves, lane = lane_id();
+    float* const values = reinterpret_cast<float*>(memory + waves * kWave);
+    join_group<T>(a, blockIdx.x, waves, JoinLds{memory, values, reinterpret_cast<uint32_t*>(values + a.beams * 64)}, pieces, parts,
+                  [&](int64_t r, int u) { return lists[(r * pieces + u) * a.k + lane]; },
+                  [&](int64_t r, int p) { return stats[r * parts + p]; },
+                  [&](int64_t r, float& end_logit) {
+                      end_logit = a.ended ? end_logit_of<T>(a, r) : 0.f;
+                      return a.scores[r];
+                  });
+}
+
+// Both at once, a workgroup a group: EACH waves a row.
+template <typename T, int EACH>
+__global__ __launch_bounds__(kMaxJoinWaves * kWave) void beam_group_kernel(BeamArgs a) {
+    constexpr int kWaves = kMaxJoinWaves, kRows = kWaves / EACH;
+    __shared__ __align__(16) ScanLds<kWaves> lds;
+    __shared__ PieceStat stats[kWaves];
+    // What the scan's waves have staged is gone when their lists are ranked.
+    static_assert(sizeof(lds.words) >= 3 * kWaves * kWave * sizeof(uint64_t), "lists, merged lists, values and tokens");
+    uint64_t* const lists = reinterpret_cast<uint64_t*>(lds.words);  // [beams][64]
+    uint64_t* const merged = lists + kRows * kWave;
+    float* const values = reinterpret_cast<float*>(merged + kWaves * kWave);
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), beam = wave / EACH;
+    const int64_t group = blockIdx.x, r = group * a.beams + (beam < a.beams ? beam : 0);
+    // Of the row that this wave joins.
+    const int64_t own = group * a.beams + (wave < a.beams ? wave : 0);
+    const float own_score = a.scores[own], own_end = a.ended ? end_logit_of<T>(a, own) : 0.f;
+    scan_row<T, kWaves, EACH>(
+        a, lds, RowReader<T>{static_cast<const T*>(a.logits) + r * a.ld, a.vocab}, 0, beam < a.beams ? row_groups<T>(a.vocab) : 0,
+        [&](PieceStat x) { stats[wave] = x; }, [&](int place, uint64_t x) { lists[beam * kWave + place] = x; });
+    __syncthreads();
+    join_group<T>(a, group, a.beams, JoinLds{merged, values, reinterpret_cast<uint32_t*>(values + kRows * kWave)}, 1, EACH,
+                  [&](int64_t row, int) { return lists[(row - group * a.beams) * kWave + lane]; },
+                  [&](int64_t row, int p) { return stats[(row - group * a.beams) * EACH + p]; },
+                  [&](int64_t, float& end_logit) {
+                      end_logit = own_end;
+                      return own_score;
+                  });
+}
+
+// Short rows of few beams are scanned and joined in one launch, a CU a group, as far as
+// that saves more than a second launch costs.  Calls, us, in one launch and in two: 16 x 4 beams fp32,
+// 4096 tokens 12.2 and 16.4, 16384 14.5 and 16.4, 32768 20.4 and 16.5; 16 x 8 beams bf16, 8192
+// tokens 13.0 and 16.4, 16384 18.1 and 16.4; 600 x 4 beams fp32, 8192 tokens 32 and 25.
+constexpr int64_t kWholeElements = 4096;  // of a wave
+constexpr int64_t kWholeGroups = 256;
 BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k) {
     const int64_t each = dtype == RTS_F32 ? group_elements<float>() : group_elements<uint16_t>();
     const int64_t rows = groups * beams, all = (vocab + each - 1) / each;
+    BeamPlan p;
+    p.each = beams <= 4 ? 4 : beams <= 8 ? 2 : beams <= 16 ? 1 : 0;
+    if (p.each && groups <= kWholeGroups && vocab <= kWholeElements * p.each) return BeamPlan{all, 1, 0, p.each};
+    p.each = 0;
     int64_t pieces = (768 + rows - 1) / rows;
     const int64_t most = (all + kBeamWaves - 1) / kBeamWaves;
     pieces = pieces < most ? pieces : most;
-    BeamPlan p;
     p.piece_groups = (all + pieces - 1) / pieces;
     p.pieces = (int)((all + p.piece_groups - 1) / p.piece_groups);
     p.ws_bytes = (size_t)(rows * p.pieces) * ((size_t)k * sizeof(uint64_t) + kBeamWaves * sizeof(PieceStat));
@@ -466,6 +552,13 @@ BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t voca
 
 template <typename T>
 static int launch_beam(const BeamArgs& a, const BeamPlan& plan, void* workspace, hipStream_t s) {
+    if (plan.each) {
+        const dim3 grid((unsigned)a.groups), block(kMaxJoinWaves * kWave);
+        if (plan.each == 4) hipLaunchKernelGGL((beam_group_kernel<T, 4>), grid, block, 0, s, a);
+        else if (plan.each == 2) hipLaunchKernelGGL((beam_group_kernel<T, 2>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((beam_group_kernel<T, 1>), grid, block, 0, s, a);
+        return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
+    }
     const int64_t units = a.groups * a.beams * plan.pieces;
     uint64_t* lists = static_cast<uint64_t*>(workspace);
     PieceStat* stats = reinterpret_cast<PieceStat*>(lists + units * a.k);

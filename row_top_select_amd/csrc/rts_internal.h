@@ -190,6 +190,7 @@ struct BeamPlan {
     int64_t piece_groups;
     int pieces;
     size_t ws_bytes;
+    int each;  // waves of a row, where a workgroup does a whole group; 0: two launches
 };
 BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k);
 int launch_beam_select(const BeamArgs& a, const BeamPlan& plan, void* workspace, hipStream_t stream);

@@ -16,23 +16,24 @@ lib = rts.raw_library()
 
 
 def beam(**kw):
-    a = dict(logits=P, dtype=0, groups=2, beams=4, vocab=1000, ld=1000, scores=P, k=4, eos=2, out=P, parents=P, tokens=P,
+    a = dict(logits=P, dtype=0, groups=2, beams=4, vocab=100000, ld=100000, scores=P, k=4, eos=2, out=P, parents=P, tokens=P,
              ended=P, ws=P, ws_bytes=1 << 20)
     a.update(kw)
     return lib.beam_select(*a.values(), None)
 
 
 def test_beam_select():
-    for kw in (dict(dtype=2), dict(groups=-1), dict(beams=0), dict(vocab=0), dict(ld=999), dict(k=0), dict(eos=-2),
-               dict(eos=1000), dict(eos=-1), dict(ended=None), dict(logits=None), dict(scores=None), dict(out=None),
+    for kw in (dict(dtype=2), dict(groups=-1), dict(beams=0), dict(vocab=0), dict(ld=99999), dict(k=0), dict(eos=-2),
+               dict(eos=100000), dict(eos=-1), dict(ended=None), dict(logits=None), dict(scores=None), dict(out=None),
                dict(parents=None), dict(tokens=None), dict(ws=None), dict(logits=ODD), dict(scores=ODD), dict(out=ODD),
                dict(parents=ODD), dict(tokens=ODD), dict(ended=ODD), dict(ws=ODD), dict(dtype=1, logits=ODD)):
         assert beam(**kw) == EINVAL, kw
     for kw in (dict(beams=65), dict(k=65), dict(vocab=1 << 31, ld=1 << 31), dict(groups=1 << 30)):
         assert beam(**kw) == EUNSUP, kw
     assert beam(groups=0) == 0
-    need = lib.beam_select_workspace_size(0, 2, 4, 1000, 4)
+    need = lib.beam_select_workspace_size(0, 2, 4, 100000, 4)
     assert need > 0 and beam(ws_bytes=need - 1) == EWS
+    assert lib.beam_select_workspace_size(0, 2, 4, 1000, 4) == 0 and beam(vocab=1000, ws=None) == EINVAL  # but a size
     for bad in ((2, 2, 4, 1000, 4), (0, 0, 4, 1000, 4), (0, 2, 65, 1000, 4), (0, 2, 4, 0, 4), (0, 2, 4, 1000, 65)):
         assert lib.beam_select_workspace_size(*bad) == 0, bad
 

@@ -41,7 +41,9 @@ def run(rts, logits, scores, k, eos, pad=0, shift=0):
     (1, 1, 1, 1, -1, 0, 0), (1, 1, 1, 1, 0, 0, 0), (1, 4, 65, 4, 2, 0, 0), (3, 5, 1000, 10, 999, 3, 1),
     (2, 8, 32000, 16, 7, 0, 0), (2, 3, 70001, 8, -1, 0, 3), (1, 2, 33000, 64, 5, 0, 0), (1, 64, 515, 64, -1, 5, 0),
     (5, 1, 20000, 63, 0, 0, 2), (300, 2, 2048, 2, 1, 0, 0), (1, 2, 200000, 7, -1, 1, 0), (1, 3, 512, 64, 511, 0, 0),
-    (2, 2, 20, 50, 3, 0, 0)])
+    (2, 2, 20, 50, 3, 0, 0), (2, 17, 6253, 32, 4, 0, 1), (3, 20, 70, 5, -1, 0, 0), (7, 4, 16384, 9, 1, 0, 0),
+    (7, 4, 16385, 9, 1, 0, 0), (5, 8, 8192, 8, 0, 3, 0), (3, 16, 4096, 64, 9, 0, 5), (256, 2, 500, 4, 0, 0, 0), (2, 13, 7000, 26, -1, 0, 0),
+    (2, 6, 300, 12, 7, 0, 0)])
 def test_beam_select(rts, dtype, groups, beams, vocab, k, eos, pad, shift):
     say("beam", dtype, groups, beams, vocab, k, eos, pad, shift)
     logits, scores = inputs(vocab + k, groups, beams, vocab, dtype)
@@ -112,11 +114,11 @@ def test_masked_logits_and_beams(rts):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["start", "end", "few", "rising", "falling", "tail of large ones"])
-@pytest.mark.parametrize("vocab", [6253, 8200, 70001])
-def test_uneven_rows(rts, dtype, kind, vocab):
+@pytest.mark.parametrize("beams,vocab", [(3, 6253), (3, 8200), (3, 70001), (7, 8000), (16, 4000), (17, 6253)])
+def test_uneven_rows(rts, dtype, kind, beams, vocab):
     """Candidates in a few places of a row only, or all in its last elements."""
-    say("uneven", dtype, kind, vocab)
-    logits, scores = inputs(vocab, 2, 3, vocab, torch.float32)
+    say("uneven", dtype, kind, beams, vocab)
+    logits, scores = inputs(vocab, 2, beams, vocab, torch.float32)
     if kind == "start":
         logits[:, 900:] = -math.inf
     elif kind == "end":
@@ -183,10 +185,11 @@ def test_logits_around_a_million(rts):
     assert (got.scores[:, 0].double() - want).abs().max() < 1e-5
 
 
-def test_given_outputs_streams_and_replay(rts):
-    logits, scores = inputs(5, 3, 4, 9000, torch.bfloat16)
+@pytest.mark.parametrize("vocab", [9000, 90000])
+def test_given_outputs_streams_and_replay(rts, vocab):
+    logits, scores = inputs(5, 3, 4, vocab, torch.bfloat16)
     x, s = logits.to(DEV), scores.to(DEV)
-    n = rts.beam_select_workspace_size(torch.bfloat16, 3, 4, 9000, 5)
+    n = rts.beam_select_workspace_size(torch.bfloat16, 3, 4, vocab, 5)
     ws = torch.empty(n, dtype=torch.uint8, device=DEV)
     out = rts.BeamStep(torch.empty(3, 5, device=DEV), torch.empty(3, 5, dtype=torch.int32, device=DEV),
                        torch.empty(3, 5, dtype=torch.int32, device=DEV), torch.empty(3, 4, device=DEV))
@@ -199,7 +202,7 @@ def test_given_outputs_streams_and_replay(rts):
     with torch.cuda.graph(graph):
         rts.beam_select(x, s, 5, eos=1, out=out, workspace=ws)
     for seed in (6, 7, 8):
-        logits, scores = inputs(seed, 3, 4, 9000, torch.bfloat16)
+        logits, scores = inputs(seed, 3, 4, vocab, torch.bfloat16)
         x.copy_(logits)
         s.copy_(scores)
         for t in out:
