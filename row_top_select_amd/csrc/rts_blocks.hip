@@ -25,18 +25,25 @@ constexpr int kPoolWaves = kPoolBlock / kWave;
 // Words of a bit a block, in whole 16 bytes.
 __host__ __device__ __forceinline__ int words_of(int32_t pool) { return (pool + 127) / 128 * 4; }
 
-// The exclusive sum of x over the workgroup's threads; total: the whole sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wave_sum, uint32_t& total) {
+// The exclusive sums of x and y over the workgroup's threads, and the whole sums.
+// Once in a kernel: nothing guards wave_sum from a scan before.
+struct Sums {
+    uint32_t x, y, all_x, all_y;
+};
+__device__ __forceinline__ Sums block_scan(uint32_t x, uint32_t y, uint2* wave_sum) {
     const int lane = lane_id(), wave = threadIdx.x / kWave;
-    const uint32_t inc = wave_incl_scan32(x);
-    __syncthreads();  // wave_sum may still be read from the scan before
-    if (lane == kWave - 1) wave_sum[wave] = inc;
+    const uint32_t inc_x = wave_incl_scan32(x), inc_y = wave_incl_scan32(y);
+    if (lane == kWave - 1) wave_sum[wave] = uint2{inc_x, inc_y};
     __syncthreads();
-    const uint32_t mine = lane < kPoolWaves ? wave_sum[lane] : 0;
-    const uint32_t upto = wave_incl_scan32(mine);
-    total = __builtin_amdgcn_readlane(upto, kPoolWaves - 1);
-    const uint32_t before = wave > 0 ? __builtin_amdgcn_readlane(upto, wave - 1) : 0;
-    return before + inc - x;
+    const uint2 of_lane = lane < kPoolWaves ? wave_sum[lane] : uint2{0, 0};
+    const uint32_t upto_x = wave_incl_scan32(of_lane.x), upto_y = wave_incl_scan32(of_lane.y);
+    const int w = __builtin_amdgcn_readfirstlane(wave);
+    Sums s;
+    s.x = inc_x - x + (w > 0 ? __builtin_amdgcn_readlane(upto_x, w - 1) : 0);
+    s.y = inc_y - y + (w > 0 ? __builtin_amdgcn_readlane(upto_y, w - 1) : 0);
+    s.all_x = __builtin_amdgcn_readlane(upto_x, kPoolWaves - 1);
+    s.all_y = __builtin_amdgcn_readlane(upto_y, kPoolWaves - 1);
+    return s;
 }
 
 __device__ __forceinline__ void set_bit(uint32_t* bits, uint32_t i) { atomicOr(&bits[i >> 5], 1u << (i & 31)); }
@@ -379,7 +386,7 @@ __device__ __forceinline__ void load_field(const uint32_t* field, int words, uin
 
 __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, const uint32_t* __restrict__ field) {
     extern __shared__ __align__(16) uint32_t lds[];
-    __shared__ uint32_t wave_sum[kPoolWaves];
+    __shared__ uint2 wave_sum[kPoolWaves];
     __shared__ uint32_t free_before[kPoolBlock];
     const int words = words_of(a.pool);
     const int rows_in = (int)a.rows_in, rows = (int)a.rows_out;
@@ -446,15 +453,16 @@ __global__ __launch_bounds__(kPoolBlock) void fork_blocks_kernel(ForkArgs a, con
         last[u] = id;
         ++own;
     }
-    uint32_t wanted, all_free;
-    uint32_t rank = block_scan(own, wave_sum, wanted);
-    // Free blocks before each thread's words.
+    // Free blocks in each thread's words.
     const int pairs = unit_of(words) / 2;
     const uint64_t* const used2 = reinterpret_cast<const uint64_t*>(used);
     auto free_pair = [&](int p) { return ~used2[p]; };
     uint32_t mine = 0;
     for (int p = tid * pairs; p < (tid + 1) * pairs && p < words / 2; ++p) mine += __popcll(free_pair(p));
-    free_before[tid] = block_scan(mine, wave_sum, all_free);
+    const Sums sums = block_scan(own, mine, wave_sum);
+    const uint32_t wanted = sums.all_x, all_free = sums.all_y;
+    uint32_t rank = sums.x;
+    free_before[tid] = sums.y;
     __syncthreads();
     auto before = [&](int u) { return free_before[u]; };
     // The lowest of them for the rows that want one, a unit a wave.
@@ -538,7 +546,7 @@ int launch_fork_blocks(const ForkArgs& a, void* workspace, hipStream_t s) {
 __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs a, const uint32_t* __restrict__ field,
                                                                     const uint32_t* __restrict__ held) {
     extern __shared__ __align__(16) uint32_t lds[];
-    __shared__ uint32_t wave_sum[kPoolWaves];
+    __shared__ uint2 wave_sum[kPoolWaves];
     __shared__ uint32_t open_before[kPoolBlock];  // blocks that are not held
     __shared__ uint32_t live_before[kPoolBlock];  // of those, live ones
     __shared__ uint32_t limit[2];                 // T, and the live ones below it
@@ -572,9 +580,8 @@ __global__ __launch_bounds__(kPoolBlock) void compact_blocks_kernel(CompactArgs 
         n_open += __popcll(o);
         n_live += __popcll(l);
     }
-    uint32_t all_open, all_live;
-    const uint32_t before_open = block_scan(n_open, wave_sum, all_open);
-    const uint32_t before_live = block_scan(n_live, wave_sum, all_live);
+    const Sums sums = block_scan(n_open, n_live, wave_sum);
+    const uint32_t all_open = sums.all_x, all_live = sums.all_y, before_open = sums.x, before_live = sums.y;
     open_before[tid] = before_open;
     live_before[tid] = before_live;
     if (tid == 0 && all_live == 0) limit[0] = limit[1] = 0;
