@@ -541,6 +541,8 @@ BeamPlan plan_beam_select(int dtype, int64_t groups, int32_t beams, int64_t voca
     p.each = beams <= 4 ? 4 : beams <= 8 ? 2 : beams <= 16 ? 1 : 0;
     if (p.each && groups <= kWholeGroups && vocab <= kWholeElements * p.each) return BeamPlan{all, 1, 0, p.each};
     p.each = 0;
+    // Three workgroups a CU: 256 x 102400 bf16 takes 19.7 us with 768 of them, 20.5 with 512, 21.3 with
+    // 1024 and 24 with 1536; 512 x 102400 fp32 45.8, 44.5, 45.9 and 48.
     int64_t pieces = (768 + rows - 1) / rows;
     const int64_t most = (all + kBeamWaves - 1) / kBeamWaves;
     pieces = pieces < most ? pieces : most;

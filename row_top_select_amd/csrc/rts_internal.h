@@ -250,7 +250,7 @@ struct KvArgs {
     Pages pages;
 };
 
-constexpr int kKvLeastKeys = 128;  // of a piece
+constexpr int kKvLeastKeys = 64;  // of a piece
 struct KvPlan {
     int target;       // pieces that the rows' keys are to be cut into, joined by a second kernel; 0: a row is one
     int rounds;       // as many times that, where they are long

@@ -44,7 +44,9 @@ constexpr int kKvTile = 32;     // keys of a stage
 constexpr int kKvStages = 2;
 constexpr int kKvWaves = 2;     // (1: 64 requests of 16384 positions 584 us for 569, 4 of 1000 10.2 for 8.6)
 constexpr int kKvHeads = 16;    // query heads of a workgroup
-constexpr int kKvLeast = kKvLeastKeys / kKvTile;  // tiles of a piece
+// Tiles of a piece at least: one a wave.  Kernels, us, with 2, 4 and 8: 4 requests of 2000 positions 9.0, 10.8
+// and 10.8; of 3800, 64 elements, 7.4, 9.1 and 9.8.
+constexpr int kKvLeast = kKvLeastKeys / kKvTile;
 // Tiles of a piece of long contexts.  3 requests of 131072 positions, e4m3, 63 us (24: 74, 96: 62); 64 of
 // 16384, bf16, 569 us (24: 570, 96: 572, whose last pieces end later).
 constexpr int kKvGoal = 48;
@@ -544,10 +546,10 @@ static constexpr int wide_waves(int row_bytes) { return row_bytes <= 128 ? 8 : r
 static int kv_waves(int64_t workgroups, int row_bytes) {
     return workgroups <= kKvWideMost ? wide_waves(row_bytes) : kKvWaves;
 }
+// Workgroups of a split call that a CU has room for.
 static int kv_places(int32_t dim, int dtype) {
     const int wave_bytes = kKvStages * 2 * kKvTile * dim * (dtype == RTS_E4M3 ? 1 : 2) + kKvEntries * 256;
-    const int n = 160 * 1024 / (kKvWaves * wave_bytes);
-    return n < 6 ? n : 6;
+    return 160 * 1024 / (kKvWaves * wave_bytes);  // by the LDS: 1 to 8
 }
 
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
