@@ -11,8 +11,8 @@
 // that each workgroup reads them.  Those are read by workgroups of their own first, see mark_parts.
 //
 // Measured, kernels: fork_blocks 256 x 257 entries, 74240 blocks: 15.7 us (marking 7, the
-// ranks 3, the tables 2); 800 x 513, 462400 blocks: 8.6 + 3.6 + 13.2; compact_blocks 64 x 129:
-// 10.4; 1000 x 257, 386000 blocks: 6.9 + 2.7 + 14.6.
+// ranks 3, the tables 2); 800 x 513, 462400 blocks: 8.6 + 3.3 + 12.8; compact_blocks 64 x 129:
+// 10.1; 1000 x 257, 386000 blocks: 7.0 + 2.7 + 14.5.
 #include "rts_device.hpp"
 #include "rts_internal.h"
 #include "../../include/row_top_select.h"
