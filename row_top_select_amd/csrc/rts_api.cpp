@@ -610,14 +610,16 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
             return RTS_EINVAL;
         if (from.rows > 0x7FFFFFFFll || from.row_bytes > 0x7FFFFFFFll || from.ld_bytes > 0x7FFFFFFFll)
             return RTS_EUNSUPPORTED;
+        // Rows that follow each other are one run: what counts is where blocks begin and end.
         const bool one = from.ld_bytes == from.row_bytes;
         const int64_t bytes = one ? from.row_bytes * block_size : from.row_bytes;
-        const uintptr_t all = reinterpret_cast<uintptr_t>(from.data) | (uintptr_t)from.ld_bytes | (uintptr_t)from.row_bytes;
+        const uintptr_t step = (uintptr_t)from.ld_bytes * (one ? (uintptr_t)a.stride_rows : 1);
+        const uintptr_t all = reinterpret_cast<uintptr_t>(from.data) | step | (uintptr_t)bytes;
         rts::CopyCache& to = a.cache[a.n_caches];
         to.data = static_cast<char*>(from.data), to.rows = from.rows, to.ld = from.ld_bytes;
         to.word = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
         to.row_words = bytes / to.word;
-        to.words = from.row_bytes / to.word * block_size;
+        to.words = to.row_words * (one ? 1 : block_size);
         if (from.rows >= block_size) ++a.n_caches;  // else no block lies in it
     }
     if (a.n_caches == 0 || n_pairs == 0) return RTS_OK;

@@ -688,21 +688,22 @@ int launch_compact_blocks(const CompactArgs& a, void* workspace, hipStream_t s) 
 }
 
 // Block copies.  A workgroup takes 16 KB (kCopySlice) of a pair's block in one
-// cache: four loads a thread, then four stores.  8000 pairs of 45 KB: 149 us (4.85 TB/s
+// cache: four loads a thread, then four stores.  8000 pairs of 45 KB: 150 us (4.8 TB/s
 // read and written, as a large copy reaches); 192 pairs of 64 KB 6.3 us.
-constexpr int kCopyBlock = 256;
+constexpr int kCopyBlock = 256;  // 1 << 8, as launch_copy_blocks counts
 constexpr int kCopyEach = 4;
 constexpr int kCopySlice = kCopyBlock * kCopyEach * 16;
 
 typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 
-// Words [first, last) of the block, row_words of them a row of ld bytes.
+// Words [first, last) of the block, row_words of them a row of ld bytes, by `lanes`
+// threads, of which this is the t-th.
 template <typename T>
 __device__ __forceinline__ void copy_words(const char* src, char* dst, int64_t ld, int64_t row_words, int64_t first,
-                                           int64_t last) {
+                                           int64_t last, int t, int lanes) {
     // Whole slices of rows that follow each other.
     if (last <= row_words && last - first == kCopyBlock * kCopyEach) {
-        const int64_t at = (first + threadIdx.x) * (int64_t)sizeof(T);
+        const int64_t at = (first + t) * (int64_t)sizeof(T);
         T v[kCopyEach];
 #pragma unroll
         for (int u = 0; u < kCopyEach; ++u) v[u] = *reinterpret_cast<const T*>(src + at + u * kCopyBlock * (int64_t)sizeof(T));
@@ -710,13 +711,15 @@ __device__ __forceinline__ void copy_words(const char* src, char* dst, int64_t l
         for (int u = 0; u < kCopyEach; ++u) *reinterpret_cast<T*>(dst + at + u * kCopyBlock * (int64_t)sizeof(T)) = v[u];
         return;
     }
-    for (int64_t i = first + threadIdx.x; i < last; i += kCopyBlock) {
+    for (int64_t i = first + t; i < last; i += lanes) {
         const int64_t row = last <= row_words ? 0 : i / row_words, at = row * ld + (i - row * row_words) * (int64_t)sizeof(T);
         *reinterpret_cast<T*>(dst + at) = *reinterpret_cast<const T*>(src + at);
     }
 }
 
-// blockIdx.x: pairs, blockIdx.y: slices of all caches' blocks, both in turn.
+// blockIdx.x: pairs, blockIdx.y: slices of all caches' blocks, both in turn.  Where a
+// block has fewer words than the workgroup threads, several pairs are copied side
+// by side (19542 pairs of blocks of 1584 and 240 bytes: 29 us one by one, 16 so).
 // CACHES: how many the arguments have room for (a few hundred bytes of
 // arguments are read sooner than a few thousand).
 template <int CACHES>
@@ -727,17 +730,19 @@ __global__ __launch_bounds__(kCopyBlock) void copy_blocks_kernel(CopyArgs<CACHES
         const CopyCache k = a.cache[c];
         const int64_t per = kCopySlice / k.word, first = (s - k.slice0) * per;
         const int64_t last = first + per < k.words ? first + per : k.words;
-        for (int64_t pair = blockIdx.x; pair < a.n_pairs; pair += gridDim.x) {
+        const int lanes = 1 << k.lanes_log2, beside = kCopyBlock >> k.lanes_log2, t = threadIdx.x & (lanes - 1);
+        for (int64_t pair = (int64_t)blockIdx.x * beside + (threadIdx.x >> k.lanes_log2); pair < a.n_pairs;
+             pair += (int64_t)gridDim.x * beside) {
             const int2 p = reinterpret_cast<const int2*>(a.pairs)[pair];
             if (p.x < 0 || p.y < 0 || p.x == p.y) continue;
             const int64_t from = p.x * a.stride_rows, to = p.y * a.stride_rows;
             if (from > k.rows - a.block_size || to > k.rows - a.block_size) continue;
             const char* src = k.data + from * k.ld;
             char* dst = k.data + to * k.ld;
-            if (k.word == 16) copy_words<words4>(src, dst, k.ld, k.row_words, first, last);
-            else if (k.word == 4) copy_words<uint32_t>(src, dst, k.ld, k.row_words, first, last);
-            else if (k.word == 2) copy_words<uint16_t>(src, dst, k.ld, k.row_words, first, last);
-            else copy_words<uint8_t>(src, dst, k.ld, k.row_words, first, last);
+            if (k.word == 16) copy_words<words4>(src, dst, k.ld, k.row_words, first, last, t, lanes);
+            else if (k.word == 4) copy_words<uint32_t>(src, dst, k.ld, k.row_words, first, last, t, lanes);
+            else if (k.word == 2) copy_words<uint16_t>(src, dst, k.ld, k.row_words, first, last, t, lanes);
+            else copy_words<uint8_t>(src, dst, k.ld, k.row_words, first, last, t, lanes);
         }
     }
 }
@@ -748,8 +753,11 @@ static int launch_copy(const CopyArgs<kMaxCopyCaches>& all, hipStream_t s) {
     a.pairs = all.pairs, a.n_pairs = all.n_pairs, a.stride_rows = all.stride_rows, a.slices = all.slices;
     a.n_caches = all.n_caches, a.block_size = all.block_size;
     for (int c = 0; c < all.n_caches; ++c) a.cache[c] = all.cache[c];
+    int widest = 0;
+    for (int c = 0; c < all.n_caches; ++c) widest = a.cache[c].lanes_log2 > widest ? a.cache[c].lanes_log2 : widest;
+    const int64_t beside = kCopyBlock >> widest, units = (a.n_pairs + beside - 1) / beside;
     const unsigned y = a.slices < 4096 ? (unsigned)a.slices : 4096, most = 8192 / y > 1 ? 8192 / y : 1;
-    const unsigned x = a.n_pairs < most ? (unsigned)a.n_pairs : most;
+    const unsigned x = units < most ? (unsigned)units : most;
     hipLaunchKernelGGL(copy_blocks_kernel<CACHES>, dim3(x, y), dim3(kCopyBlock), 0, s, a);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
@@ -760,6 +768,7 @@ int launch_copy_blocks(CopyArgs<kMaxCopyCaches>& a, hipStream_t s) {
         CopyCache& k = a.cache[c];
         k.slice0 = a.slices;
         a.slices += (k.words * k.word + kCopySlice - 1) / kCopySlice;
+        for (k.lanes_log2 = 8; k.lanes_log2 > 3 && 1 << (k.lanes_log2 - 1) >= k.words; --k.lanes_log2) {}
     }
     return a.n_caches <= 4 ? launch_copy<4>(a, s) : launch_copy<kMaxCopyCaches>(a, s);
 }

@@ -226,6 +226,7 @@ struct CopyCache {
     int64_t words, row_words;  // of `word` bytes: of a block, and of a row (as many as a block's where rows follow each other)
     int64_t slice0;            // set by the launch
     int32_t word;
+    int32_t lanes_log2;        // threads of a pair, set by the launch
 };
 template <int CACHES>
 struct CopyArgs {

@@ -171,6 +171,7 @@ def test_copy(rts, block, stride):
     caches = [torch.randn(rows, 8, 16, generator=g).bfloat16().to(DEV), wide[:, 4:68], wide.bfloat16()[:, 1:34],
               torch.randn(rows, generator=g).to(DEV), torch.randint(0, 256, (rows, 5), generator=g).byte().to(DEV),
               torch.randn(rows, 3, generator=g).bfloat16().to(DEV), torch.randn(rows - 1, 4, generator=g).to(DEV),
+              torch.randint(0, 256, (rows * 10 + 7,), generator=g).byte().to(DEV)[7:].view(rows, 10),
               torch.empty(rows, 0, device=DEV), torch.randn(rows + 3, 128, generator=g).to(torch.float8_e4m3fn).to(DEV)]
     ids = torch.randperm(pool, generator=g)[:40].view(20, 2)
     pairs = torch.cat([ids, torch.tensor([[-1, 3], [4, -1], [-1, -1], [pool + 9, 1], [1, pool + 9], [7, 7],
