@@ -179,11 +179,14 @@ __device__ __forceinline__ void mark_entries(const int32_t* table, int64_t ld, u
             if (inside[u] && (uint32_t)id[u] < (uint32_t)pool) set_bit(bits, id[u]);
     }
 }
+// Rows of a workgroup below which a table is read so too, us by rows and by entries: 6 x 7772 entries 38 and 27,
+// 64 x 8192 59 and 26; 16 x 4096 28 and 34.
+constexpr int kFew = kPoolWaves;
 constexpr int kNarrow = 128;  // columns below which a table is: 1568 rows of 4 columns 122 us by rows, 17 so
 template <typename Count>
 __device__ __forceinline__ void mark_table(const int32_t* table, int64_t ld, int cols, int64_t rows, int64_t part,
                                            int64_t parts, int pool, uint32_t* bits, Count&& n) {
-    if (cols < kNarrow) {
+    if (cols < kNarrow || rows < kFew * parts) {
         const uint32_t all = (uint32_t)rows * (uint32_t)cols, per = (all + (uint32_t)parts - 1) / (uint32_t)parts;
         const uint32_t lo = (uint32_t)part * per < all ? (uint32_t)part * per : all;
         mark_entries(table, ld, cols, lo, lo + per < all ? lo + per : all, pool, bits, n);

@@ -69,7 +69,8 @@ def check_fork(rts, table, ctx, parents, block, pool, held, n_free=None, pad=0):
     (1, 1, 1, 1, 1, 0, 0), (1, 4, 100, 16, 64, 0, 0), (8, 4, 300, 16, 4096, 0, 3), (8, 4, 300, 16, 700, 0.1, 0),
     (50, 8, 100, 1, 60000, 0, 0), (30, 5, 1000, 24, 9001, 0.05, 1), (512, 8, 200, 128, 30000, 0, 0),
     (4096, 1, 40, 16, 20000, 0.01, 0), (3, 2, 5000, 16, 1 << 19, 0, 0), (3, 2, 50, 16, 33, 0.3, 0),
-    (64, 8, 4000, 16, 90000, 0.02, 0), (1500, 2, 2000, 16, 400000, 0, 1)])
+    (64, 8, 4000, 16, 90000, 0.02, 0), (1500, 2, 2000, 16, 400000, 0, 1), (2, 2, 8000, 1, 50000, 0, 3),
+    (4, 4, 9000, 1, 200000, 0.1, 0)])
 def test_fork(rts, reqs, beams, ctx, block, pool, held, pad):
     say("fork", reqs, beams, ctx, block, pool, held, pad)
     g = torch.Generator().manual_seed(reqs)
@@ -137,7 +138,7 @@ def check_compact(rts, table, ctx, block, pool, held, max_moves=None, n_free=Non
     (1, 1, 1, 1, 1, 0, 0), (1, 4, 100, 16, 64, 0, 0), (8, 4, 300, 16, 4096, 0, 3), (8, 4, 300, 16, 700, 0.1, 0),
     (50, 8, 100, 1, 60000, 0, 0), (30, 5, 1000, 24, 9001, 0.05, 1), (5000, 1, 40, 16, 20000, 0.01, 0),
     (3, 2, 5000, 16, 1 << 19, 0.5, 0), (3, 2, 50, 16, 33, 0.3, 0), (64, 8, 4000, 16, 90000, 0.02, 0),
-    (1500, 2, 2000, 16, 400000, 0.1, 1)])
+    (1500, 2, 2000, 16, 400000, 0.1, 1), (2, 2, 8000, 1, 50000, 0, 3), (4, 4, 9000, 1, 200000, 0.1, 0)])
 def test_compact(rts, reqs, beams, ctx, block, pool, held, pad):
     say("compact", reqs, beams, ctx, block, pool, held, pad)
     table, lens, held = setup(reqs, reqs, beams, ctx, block, pool, held)
