@@ -943,8 +943,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int, eos: int = -
         if k < 1 or beams < 1:
             raise RtsError(RTS_EINVAL, "beam_select")
         best, parents, tokens = _new((3, groups, k), torch.int32, device, stream).unbind(0)
-        out = BeamStep(best.view(torch.float32), parents, tokens,
-                       _new((groups, beams), torch.float32, device, stream) if eos >= 0 else None)
+        ended = None
+        if eos >= 0:
+            ended = torch.empty_like(scores) if stream is None else _new((groups, beams), torch.float32, device, stream)
+        out = BeamStep(best.view(torch.float32), parents, tokens, ended)
     else:
         for name, t, d in zip(BeamStep._fields, out, (torch.float32, torch.int32, torch.int32)):
             _out(t, (groups, k), d, device, name, stream)
@@ -1117,13 +1119,14 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise TypeError("q must be bfloat16")
     if k_cache.dtype not in _INDEX_DTYPES or v_cache.dtype != k_cache.dtype:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
-    if q.dim() != 3 or k_cache.dim() != 3 or q.stride(2) != 1 or k_cache.stride(2) != 1:
+    shape, steps, cache, cache_steps = q.shape, q.stride(), k_cache.shape, k_cache.stride()
+    if len(shape) != 3 or len(cache) != 3 or steps[2] != 1 or cache_steps[2] != 1:
         raise ValueError("q must be [rows, heads, dim], the caches [cache_rows, kv_heads, dim], with unit element stride")
-    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride() and any(
-            n > 1 and x != y for n, x, y in zip(k_cache.shape, k_cache.stride(), v_cache.stride())):
+    if v_cache.shape != cache or v_cache.stride() != cache_steps and any(
+            n > 1 and x != y for n, x, y in zip(cache, cache_steps, v_cache.stride())):
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    (rows, heads, dim), (ld_q, ld_qhead, _) = q.shape, q.stride()
-    (cache_rows, kv_heads, cdim), (ld_cache, ld_head, _) = k_cache.shape, k_cache.stride()
+    (rows, heads, dim), (ld_q, ld_qhead, _) = shape, steps
+    (cache_rows, kv_heads, cdim), (ld_cache, ld_head, _) = cache, cache_steps
     if cdim != dim:
         raise ValueError("q and the caches must have the same last dimension")
     if heads > 0x7FFFFFFF or dim > 0x7FFFFFFF:
@@ -1134,9 +1137,10 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ld_q = ld_q if rows > 1 else heads * dim
     ld_head = ld_head if kv_heads > 1 else dim
     ld_cache = ld_cache if cache_rows > 1 else kv_heads * dim
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (kv_heads,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 vector of {kv_heads} entries")
+    if k_scales is not None or v_scales is not None:
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (kv_heads,) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous float32 vector of {kv_heads} entries")
     req_id, row_ends = _int32_vec(req_id, rows, "req_id"), _int32_vec(row_ends, rows, "row_ends")
     if req_id is None or row_ends is None:
         raise ValueError("req_id and row_ends are required")
@@ -1146,7 +1150,10 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         max_len = table_cols * block_size
     if not 0 <= window < 2 ** 63 or max_len >= 2 ** 63:
         raise ValueError("window must not be negative, and window and max_len below 2^63")
-    out = _out(out, (rows, heads, dim), torch.bfloat16, device, "out", stream)
+    if out is None and stream is None and q.is_contiguous():
+        out = torch.empty_like(q)  # two thirds of torch.empty's time
+    else:
+        out = _out(out, (rows, heads, dim), torch.bfloat16, device, "out", stream)
     lse = _out(lse, (rows, heads), torch.float32, device, "lse", stream)
     _on(device, k_cache, v_cache, k_scales, v_scales, req_id, row_ends, block_table)
     dt = _INDEX_DTYPES[k_cache.dtype]
