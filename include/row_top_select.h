@@ -697,7 +697,7 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
  * keys and values.  The heads are in kv_heads groups of heads / kv_heads that
  * share a key head.  Token t sees the positions p < row_ends[t] of request
  * req_id[t] (its own is already in the cache) and, with a window, p >=
- * row_ends[t] - window.  For head h, of key head j, over what is seen:
+ * row_ends[t] - window, wherever the table ends.  For head h, of key head j, over what is seen:
  *   z_p = scale * k_scales[j] * q[t, h, :] . k[p, j, :],   lse[t, h] = log sum_p exp z_p
  *   out[t, h, :] = v_scales[j] * sum_p exp(z_p - lse) v[p, j, :]
  * Position p lies at physical row

@@ -154,11 +154,13 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_attend_kernel(KvArgs a, int 
         const int req = a.req_id[t];
         int end = a.row_ends[t];
         const int64_t held = (int64_t)a.pages.cols * a.pages.block_size;
-        if (end > held) end = (int)held;
         if (end < 0 || req < 0 || req >= a.pages.table_rows) end = 0;
+        // A window counts back from the row's end, which may lie past its table.
+        if (a.window > 0 && end > a.window) r.begin = end - (int)a.window;
+        if (end > held) end = (int)held;
+        if (r.begin > end) r.begin = end;
         r.req = req;
         r.end = end;
-        if (a.window > 0 && end > a.window) r.begin = end - (int)a.window;
         return r;
     };
     int64_t token = unit;
