@@ -1064,12 +1064,11 @@ def compact_blocks(block_table: torch.Tensor, ctx_lens: torch.Tensor, block_size
 
 
 def copy_blocks(caches, pairs: torch.Tensor, block_size: int, stride_rows: int | None = None, stream=None) -> None:
-    """Copies blocks within each of ``caches`` (one tensor or several, [cache_rows, ...] of any type, a row contiguous) by the
+    """Copies blocks within each of ``caches`` (one tensor or any iterable of them, [cache_rows, ...] of any type, a row contiguous) by the
     ``pairs`` int32 [n, 2] of (from, to), -1 skipped, in place; see copy_blocks in the header.  ``stride_rows``
     defaults to ``block_size``."""
     device = _gpu(pairs, "pairs")
-    if isinstance(caches, torch.Tensor):
-        caches = (caches,)
+    caches = (caches,) if isinstance(caches, torch.Tensor) else tuple(caches)  # walked more than once
     if pairs.dtype != torch.int32 or pairs.dim() != 2 or pairs.shape[1] != 2 or not pairs.is_contiguous():
         raise ValueError("pairs must be contiguous int32 [n, 2]")
     pages = _pages(block_size, stride_rows)
