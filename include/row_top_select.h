@@ -559,7 +559,7 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * and each group keeps the k best of all its beams' tokens.  Order: value
  * desc (in 64 bits, to 2^-40 of its size, so that beams are told apart below the
  * last bit of a 32-bit score), then beam asc, then logit desc, token asc; within
- * a beam it is that of its logits.
+ * a beam it is that of its logits, of which -0 and 0 are equal.
  *
  * Not candidates: the token eos, tokens with a logit of -inf, beams whose score
  * is not finite (-inf marks a beam that is not in use, such as all but the

@@ -290,7 +290,8 @@ __device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds,
             else v = __uint_as_float((uint32_t)t << 16);
             const bool hit = from < held && v >= bound && at != (uint32_t)a.eos;
             const uint64_t mask = __ballot(hit);
-            if (hit) listed[in_list + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v)), at);
+            // -0 and 0 are one logit: the sum is 0 for both.
+            if (hit) listed[in_list + mbcnt64(mask)] = composite(key32_of_bits(__float_as_uint(v + 0.f)), at);
             in_list += __popcll(mask);
             if (in_list > kWave) {
                 flush();
