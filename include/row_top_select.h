@@ -557,9 +557,14 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * the logits x of row i * beams + b; token v continues it with the value
  *   value(b, v) = scores[i, b] + x[v] - lse,   lse = log sum_v exp x[v]
  * and each group keeps the k best of all its beams' tokens.  Order: value
- * desc (in 64 bits, to 2^-40 of its size, so that beams are told apart below the
- * last bit of a 32-bit score), then beam asc, then logit desc, token asc; within
- * a beam it is that of its logits, of which -0 and 0 are equal.
+ * desc, then beam asc, then logit desc, token asc; within a beam it is that of
+ * its logits, of which -0 and 0 are equal.
+ * Values are formed in 64 bits and told apart to 2^-40 of
+ * their size.  A row's sum has terms of 32 bits, so lse is off by up to
+ * 2^-20 + 2^-23 of the mean (by weight) distance of the logits from their maximum,
+ * some 1e-7 as a rule (for logits up to 1e6): beams whose values lie closer
+ * than that may change places.  It is exact where one token has all of the
+ * weight, and never below the largest logit: no value is above its beam's score.
  *
  * Not candidates: the token eos, tokens with a logit of -inf, beams whose score
  * is not finite (-inf marks a beam that is not in use, such as all but the
@@ -580,8 +585,8 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  *            beams).  Calls in flight at the same time need workspaces of their own.
  * out_scores may be scores where k is beams (refused otherwise); no other output may
  * overlap an input or another output.
- * Maxima, sums and values are held in 32 bits or more (sums over a row's parts
- * and values in 64).
+ * Maxima and a sum's terms are held in 32 bits, sums over more than 32 terms and
+ * values in 64.
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (beams, k, vocab >= 2^31, groups * beams
  *         >= 2^31), RTS_EWORKSPACE, RTS_EHIP.
  */

@@ -167,15 +167,19 @@ __device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds,
     if (lane == 0) published[side] = side < busy ? -INFINITY : INFINITY;
     __syncthreads();
 
-    float m = kLeast, sum = 0.f, lane_most = -INFINITY;
-    // Terms are 2^(x log2(e) - c2) with c2 = m log2(e): its rounding does not
-    // matter, because c2 itself is what the sum is taken to be relative to.
-    // Past 1e6 it would come near the range of an exponential, and they are e^(x - m).
+    float m = kLeast, lane_most = -INFINITY;
+    // Terms are 2^(x log2(e) - c2) in 32 bits, c2 the whole number next to m log2(e), so
+    // that sums go over to a new maximum without a rounding.  The sum is taken relative to the
+    // maximum's own term, what is computed for x = m: a row whose weight is all on one logit has
+    // its logarithm to the last bit, and none is below its largest logit.  A group's terms are added in
+    // 32 bits, groups in 64: 4 to 8 roundings of a row's sum are left, 1e-7 of it.
+    // Past 1e6 the difference would come near the range of an exponential, and they are e^(x - m).
+    double sum = 0.;
     float c2;
     bool huge;
     auto set_reference = [&] {
         huge = fabsf(m) > 1e6f;
-        c2 = huge ? 0.f : m * kLog2e;
+        c2 = huge ? 0.f : rintf(m * kLog2e);
     };
     set_reference();
     float bound = kLeast;  // elements from here on are candidates; -inf is none
@@ -243,19 +247,25 @@ __device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds,
             const bool was_huge = huge;
             m = most;
             set_reference();
-            float lower = from - c2;
-            if (was_huge) lower = huge ? (was - m) * kLog2e : fmaf(was, kLog2e, -c2);
-            else if (huge) lower = -fmaf(m, kLog2e, -from);
-            sum *= __builtin_amdgcn_exp2f(lower);
+            if (!huge && !was_huge) {
+                sum = ldexp(sum, (int)(from - c2));
+            } else {
+                const float lower = !huge      ? fmaf(was, kLog2e, -c2)
+                                    : was_huge ? (was - m) * kLog2e
+                                               : -fmaf(m, kLog2e, -from);
+                sum *= __builtin_amdgcn_exp2f(lower);
+            }
         }
         auto terms = [&](auto term) __attribute__((always_inline)) {
+            float all = 0.f;
 #pragma unroll
             for (int j = 0; j < kWords; ++j) {
                 float part = 0.f;
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) part += __builtin_amdgcn_exp2f(term(element_of<T>(x[j], e)));
-                sum += part;
+                all += part;
             }
+            sum += all;
         };
         if (huge) terms([&](float v) { return (v - m) * kLog2e; });
         else terms([&](float v) { return fmaf(v, kLog2e, -c2); });
@@ -362,11 +372,8 @@ __device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds,
     const uint64_t mine = entry_at(thread);
     {
         const double total = wave_reduce(sum, [](double x, double y) { return x + y; });
-        // kLog2e is log2(e) (1 + d): the terms are those of logits times 1 + d,
-        // and their sum's logarithm is off by d times the softmax's mean logit, which lies near m.
-        constexpr double kOff = (double)kLog2e * 0.69314718055994530942 - 1.;
-        if (lane == 0)
-            stat(PieceStat{huge ? (double)m : (double)c2 * 0.69314718055994530942 - kOff * (double)m, total});
+        const float own = __builtin_amdgcn_exp2f(huge ? (m - m) * kLog2e : fmaf(m, kLog2e, -c2));
+        if (lane == 0) stat(PieceStat{(double)m, total / own});
     }
     // An entry's place is the number of larger ones: a wave counts those of its own.
     for (int at = lane; at - lane < count; at += kWave) {
@@ -401,8 +408,8 @@ __global__ __launch_bounds__(kBeamBlock) void beam_scan_kernel(BeamArgs a, int64
 }
 
 // A candidate among those of other beams: the upper 52 bits of its value's
-// key, so that values closer than 2^-40 of their size count as equal, and below them its beam and
-// its rank there, ascending.  0 is below all.
+// key, so that values closer than 2^-40 of their size count as equal (a row's sum, of 32-bit terms,
+// puts all of its values some 1e-7 off), and below them its beam and its rank there, ascending.  0 is below all.
 static_assert(kMaxBeams <= 64 && kMaxBeamK <= 64, "12 bits");
 __device__ __forceinline__ uint64_t entry(double v, int beam, int rank) {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
