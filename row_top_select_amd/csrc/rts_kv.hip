@@ -77,11 +77,25 @@ struct KvShape {
     }
 };
 
-// The pieces' results: [part][heads][D], [part][heads], and each row's first part and number of pieces.
+// The pieces' results: [part][heads][D], [part][heads] maxima and sums of the softmax, and each row's
+// first part and number of pieces.  (Not the sum's logarithm: scores past 3.4e38 have none in 32 bits.)
 struct KvParts {
-    float *out, *lse;
+    float* out;
+    float2* stat;
     int2* rows;
 };
+
+// What turns a product of q and k into a score, and into an exponent of 2.
+struct KvFactor {
+    float factor, c;
+};
+__device__ __forceinline__ KvFactor factor_of(float scale, const float* k_scales, int kvh) {
+    const float f = scale * (k_scales ? k_scales[kvh] : 1.f);
+    return {f, f == 0.f ? 1.f : fabsf(f) * kLog2e};
+}
+__device__ __forceinline__ float lse_of(const KvFactor& f, float most, float total) {
+    return total == 0.f ? -INFINITY : most * fabsf(f.factor) + __builtin_amdgcn_logf(total) * kLn2;
+}
 
 __device__ __forceinline__ float wave_sum(float x) {
     return __uint_as_float(wave_reduce32(__float_as_uint(x), [](uint32_t a, uint32_t b) {
@@ -240,8 +254,8 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_attend_kernel(KvArgs a, int 
     const int tiles = (p1 - p0) / kKvTile + ((p1 - p0) % kKvTile != 0);
     const int count = __builtin_amdgcn_readfirstlane((tiles - wave + WAVES - 1) / WAVES);  // of this wave
 
-    const float factor = a.scale * (a.k_scales ? a.k_scales[kvh] : 1.f);
-    const float c = factor == 0.f ? 1.f : fabsf(factor) * kLog2e;
+    const KvFactor of = factor_of(a.scale, a.k_scales, kvh);
+    const float factor = of.factor, c = of.c;
     const float lazy = kLazy / c;
 
     // The first position of the wave's tile n.  Past the piece's end they may pass 2^31.
@@ -445,70 +459,72 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_attend_kernel(KvArgs a, int 
             for (int u = 0; u < 2; ++u) sum[u] += *reinterpret_cast<const f32x4*>(from + ((2 * d8 + u) ^ h) * 4) * f;
         }
         const float inv = total == 0.f ? 0.f : v_scale / total;
-        const float lse = total == 0.f ? -INFINITY : most * fabsf(factor) + __builtin_amdgcn_logf(total) * kLn2;
         const int64_t rh = token * a.heads + kvh * group + block * kKvHeads + h;
         if (pieces == 1) {
-            if (d8 == 0 && a.lse) a.lse[rh] = lse;
+            if (d8 == 0 && a.lse) a.lse[rh] = lse_of(of, most, total);
             *reinterpret_cast<uint4*>(a.out + rh * D + d8 * 8) =
                 uint4{bf16_pair(sum[0][0] * inv, sum[0][1] * inv), bf16_pair(sum[0][2] * inv, sum[0][3] * inv),
                       bf16_pair(sum[1][0] * inv, sum[1][1] * inv), bf16_pair(sum[1][2] * inv, sum[1][3] * inv)};
             continue;
         }
         const int64_t at = (int64_t)(part + piece) * a.heads + kvh * group + block * kKvHeads + h;
-        const bool empty = total == 0.f && most == kNoMax;  // nothing was seen
-        if (d8 == 0) parts.lse[at] = total == 0.f && !empty ? kNoMax : lse;  // the join reads its zeros and NaN
-        if (empty) continue;  // the join reads no values of an empty part
+        if (d8 == 0) parts.stat[at] = float2{most, total};
+        if (most == kNoMax) continue;  // nothing was seen: the join reads no values of such a part
         float* const to = parts.out + at * D + d8 * 8;
         reinterpret_cast<f32x4*>(to)[0] = sum[0] * inv;
         reinterpret_cast<f32x4*>(to)[1] = sum[1] * inv;
     }
 }
 
-// The join of a row and head's pieces: out = sum_s e^(lse_s - lse) part_s.  A
+// The join of a row and head's pieces: with maxima m_s and sums l_s of products, and their largest
+// maximum m, out = sum_s w_s part_s / sum_s w_s, w_s = 2^((m_s - m) c) l_s.  A
 // workgroup takes W elements of one, its threads 4 of them each of every n-th piece,
 // with a running maximum: what they read does not wait for anything.  (64 pieces
 // of 192 (row, head) pairs, one after the other, took 15 us.)
 constexpr int kJoinBlock = 256;
 
 template <int D, int W>
-__global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int heads, uint16_t* __restrict__ out,
-                                                             float* __restrict__ lse) {
+__global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int heads, int group, float scale,
+                                                             const float* __restrict__ k_scales,
+                                                             uint16_t* __restrict__ out, float* __restrict__ lse) {
     constexpr int kColumns = W / 4, kSide = kJoinBlock / kColumns;  // pieces side by side
     __shared__ f32x4 sums[kSide][kColumns];
     __shared__ float totals[kSide], tops[kSide];
     const int64_t rh = blockIdx.x, row = rh / heads;
+    const int head = (int)(rh - row * heads);
     const int col = threadIdx.x % kColumns, side = threadIdx.x / kColumns, d = blockIdx.y * W + col * 4;
     const int2 of_row = parts.rows[row];
     const int splits = of_row.y;
     if (splits == 1) return;  // written by its one workgroup
-    const int64_t first = (int64_t)of_row.x * heads + (rh - row * heads);
-    const float* const stat = parts.lse + first;
+    const KvFactor of = factor_of(scale, k_scales, head / group);
+    const int64_t first = (int64_t)of_row.x * heads + head;
+    const float2* const stat = parts.stat + first;
     const float* const from = parts.out + first * D + d;
-    float m = -INFINITY, total = 0.f;  // m is NaN if any piece's is
+    float m = kNoMax, total = 0.f;  // a piece that saw something has a greater maximum
     f32x4 acc = {};
     constexpr int kAhead = 4;
     for (int s0 = side; s0 < splits; s0 += kSide * kAhead) {
-        float x[kAhead];
+        float2 x[kAhead];
         f32x4 v[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int64_t s = s0 + u * kSide < splits ? s0 + u * kSide : side;
             x[u] = stat[s * heads];
             v[u] = *reinterpret_cast<const f32x4*>(from + s * heads * D);
-            if (s0 + u * kSide >= splits) x[u] = -INFINITY;
+            if (s0 + u * kSide >= splits) x[u].x = kNoMax;
         }
         float top = m;
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) top = __builtin_elementwise_maximum(top, x[u]);
-        if (top == -INFINITY) continue;
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * kLog2e);
+        for (int u = 0; u < kAhead; ++u) top = fmaxf(top, x[u].x);
+        if (top == kNoMax) continue;
+        const float f = __builtin_amdgcn_exp2f((m - top) * of.c);
         total *= f;
         acc *= f;
         m = top;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (x[u] == -INFINITY) continue;  // an empty piece has no values
-            const float w = __builtin_amdgcn_exp2f((x[u] - m) * kLog2e);
+            if (x[u].x == kNoMax) continue;  // an empty piece has no values
+            const float w = __builtin_amdgcn_exp2f((x[u].x - m) * of.c) * x[u].y;
             total += w;
             acc += v[u] * w;
         }
@@ -519,21 +535,20 @@ __global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int 
     if (side > 0) return;
     float most = m;
 #pragma unroll
-    for (int i = 1; i < kSide; ++i) most = __builtin_elementwise_maximum(most, tops[i]);
+    for (int i = 1; i < kSide; ++i) most = fmaxf(most, tops[i]);
     acc = f32x4{};
     total = 0.f;
 #pragma unroll
     for (int i = 0; i < kSide; ++i) {
-        if (tops[i] == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f((tops[i] - most) * kLog2e);
+        if (tops[i] == kNoMax) continue;
+        const float f = __builtin_amdgcn_exp2f((tops[i] - most) * of.c);
         acc += sums[i][col] * f;
         total += totals[i] * f;
     }
-    const float inv = most == -INFINITY ? 0.f : 1.f / total;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
     *reinterpret_cast<uint2*>(out + rh * D + d) =
         uint2{bf16_pair(acc[0] * inv, acc[1] * inv), bf16_pair(acc[2] * inv, acc[3] * inv)};
-    // kNoMax: keys were seen, all with scores of -inf.
-    if (lse && d == 0) lse[rh] = most <= kNoMax ? -INFINITY : most + __builtin_amdgcn_logf(total) * kLn2;
+    if (lse && d == 0) lse[rh] = lse_of(of, most, total);
 }
 
 // Workgroups that a CU has room for, by their LDS.
@@ -574,7 +589,7 @@ KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim
     const int64_t rounds = (all + kKvGoal * p.target - 1) / (kKvGoal * p.target);
     p.rounds = (int)(rounds < kKvRounds ? rounds : kKvRounds);
     // Rows of several pieces have no more than twice the most of them.
-    p.ws_bytes = (size_t)(2 * p.rounds * p.target) * heads * (dim + 1) * 4 + (size_t)rows * 8;
+    p.ws_bytes = (size_t)(2 * p.rounds * p.target) * heads * (dim + 2) * 4 + (size_t)rows * 8;
     p.ws_bytes = (p.ws_bytes + 15) & ~size_t(15);
     return p;
 }
@@ -599,17 +614,19 @@ static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hi
     const int64_t most = (int64_t)plan.target * plan.rounds;
     KvParts parts;
     parts.out = static_cast<float*>(workspace);
-    parts.lse = parts.out + 2 * most * a.heads * D;
-    parts.rows = reinterpret_cast<int2*>(parts.lse + 2 * most * a.heads);
+    parts.stat = reinterpret_cast<float2*>(parts.out + 2 * most * a.heads * D);
+    parts.rows = reinterpret_cast<int2*>(parts.stat + 2 * most * a.heads);
     const int rc = launch_kv_waves<D, E4M3, BIG, kKvWaves>(a, (a.rows + most + 1) * blocks, plan, parts, s);
     if (rc != RTS_OK) return rc;
     // Few of them are cut finer, to have more of the chip read the pieces: 8 heads of one
     // request of 131072 positions 7.3 us, 15.8 whole; 32 heads 5.6 both; 128 (4 requests of 1000) 4.0 and 3.7.
     const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);
+    const int group = a.heads / a.kv_heads;
     if (a.rows * a.heads <= 32)
-        hipLaunchKernelGGL((kv_join_kernel<D, 32>), dim3(pairs.x, D / 32), block, 0, s, parts, a.heads, a.out, a.lse);
+        hipLaunchKernelGGL((kv_join_kernel<D, 32>), dim3(pairs.x, D / 32), block, 0, s, parts, a.heads, group, a.scale,
+                           a.k_scales, a.out, a.lse);
     else
-        hipLaunchKernelGGL((kv_join_kernel<D, D>), pairs, block, 0, s, parts, a.heads, a.out, a.lse);
+        hipLaunchKernelGGL((kv_join_kernel<D, D>), pairs, block, 0, s, parts, a.heads, group, a.scale, a.k_scales, a.out, a.lse);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
