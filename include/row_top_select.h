@@ -728,8 +728,10 @@ int copy_blocks(const rts_cache* caches, int32_t n_caches, const int32_t* pairs,
  * q, the caches, out and their strides must be multiples of 16 bytes.
  * Scores, softmax statistics and sums are held in 32 bits; the weights enter the
  * products with the values as two bf16 terms (2^-16 of a weight is left out).
- * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 1024, cache_rows >= 2^31,
- *         ld_cache > 2^30, a cache of 2^36 bytes or more), RTS_EWORKSPACE, RTS_EHIP.
+ * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (dim, heads > 1024, rows * kv_heads *
+ *         ceil(heads / kv_heads / 16) >= 2^25, rows * heads, cache_rows or
+ *         table_rows >= 2^31, ld_cache > 2^30, ld_head > 2^40, a cache of 2^36
+ *         bytes or more), RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t kv_attend_paged_workspace_size(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype,
                                       int64_t max_len, int64_t window);

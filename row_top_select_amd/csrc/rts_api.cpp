@@ -635,7 +635,8 @@ int kv_args(const rts::KvArgs& a) {
     if (a.ld_q < 0 || a.ld_qhead < a.dim || a.ld_cache < 0 || a.ld_head < a.dim || !(std::fabs(a.scale) <= 0x1p127f))
         return RTS_EINVAL;
     if ((a.dim != 64 && a.dim != 128 && a.dim != 256) || a.heads > 1024 || a.rows > 0x7FFFFFFFll / a.heads ||
-        a.cache_rows > 0x7FFFFFFFll || a.ld_cache > (1ll << 30) || a.ld_head > (1ll << 40))
+        a.cache_rows > 0x7FFFFFFFll || a.ld_cache > (1ll << 30) || a.ld_head > (1ll << 40) ||
+        !rts::kv_attend_fits(a.rows, a.heads, a.kv_heads))
         return RTS_EUNSUPPORTED;
     if (a.rows == 0) return RTS_OK;
     const int64_t unit = a.dtype == RTS_E4M3 ? 16 : 8;  // elements of 16 bytes
@@ -652,7 +653,8 @@ int64_t kv_longest(int64_t max_len, int64_t window) { return window > 0 && windo
 size_t kv_attend_paged_workspace_size(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype,
                                       int64_t max_len, int64_t window) {
     if (rows < 1 || heads < 1 || heads > 1024 || kv_heads < 1 || heads % kv_heads != 0 || rows > 0x7FFFFFFFll / heads ||
-        (dim != 64 && dim != 128 && dim != 256) || (dtype != RTS_BF16 && dtype != RTS_E4M3) || max_len < 0 || window < 0)
+        (dim != 64 && dim != 128 && dim != 256) || (dtype != RTS_BF16 && dtype != RTS_E4M3) || max_len < 0 || window < 0 ||
+        !rts::kv_attend_fits(rows, heads, kv_heads))
         return 0;
     return rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), true).ws_bytes;
 }
@@ -662,7 +664,9 @@ int kv_attend_paged_plan(int64_t rows, int32_t heads, int32_t kv_heads, int32_t 
     if (rows < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dtype != RTS_BF16 && dtype != RTS_E4M3) ||
         max_len < 0 || window < 0 || !plan)
         return RTS_EINVAL;
-    if (heads > 1024 || rows > 0x7FFFFFFFll / heads || (dim != 64 && dim != 128 && dim != 256)) return RTS_EUNSUPPORTED;
+    if (heads > 1024 || rows > 0x7FFFFFFFll / heads || (dim != 64 && dim != 128 && dim != 256) ||
+        !rts::kv_attend_fits(rows, heads, kv_heads))
+        return RTS_EUNSUPPORTED;
     const rts::KvPlan p = rts::plan_kv_attend(rows, heads, kv_heads, dim, dtype, kv_longest(max_len, window), split != 0);
     plan[0] = p.target, plan[1] = rts::kKvLeastKeys;
     return RTS_OK;

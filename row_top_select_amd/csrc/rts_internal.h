@@ -257,6 +257,7 @@ struct KvPlan {
     int rounds;       // as many times that, where they are long
     size_t ws_bytes;
 };
+bool kv_attend_fits(int64_t rows, int32_t heads, int32_t kv_heads);  // into a launch
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
                       bool allow_split);
 int launch_kv_attend(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t stream);

@@ -551,7 +551,6 @@ __global__ __launch_bounds__(kJoinBlock) void kv_join_kernel(KvParts parts, int 
     if (lse && d == 0) lse[rh] = lse_of(of, most, total);
 }
 
-// Workgroups that a CU has room for, by their LDS.
 // Workgroups of a token.
 static int64_t kv_blocks(int32_t heads, int32_t kv_heads) {
     return kv_heads * ((heads / kv_heads + kKvHeads - 1) / kKvHeads);
@@ -567,6 +566,10 @@ static int kv_waves(int64_t workgroups, int row_bytes) {
 static int kv_places(int32_t dim, int dtype) {
     const int wave_bytes = kKvStages * 2 * kKvTile * dim * (dtype == RTS_E4M3 ? 1 : 2) + kKvEntries * 256;
     return 160 * 1024 / (kKvWaves * wave_bytes);  // by the LDS: 1 to 8
+}
+
+bool kv_attend_fits(int64_t rows, int32_t heads, int32_t kv_heads) {
+    return rows * kv_blocks(heads, kv_heads) <= kMaxThreads / (kKvWaves * kWave);
 }
 
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
@@ -596,7 +599,7 @@ KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim
 
 template <int D, bool E4M3, bool BIG, int WAVES>
 static int launch_kv_waves(const KvArgs& a, int64_t grid, const KvPlan& plan, const KvParts& parts, hipStream_t s) {
-    if (grid > kMaxThreads / (WAVES * kWave)) return RTS_EUNSUPPORTED;
+    if (grid > kMaxThreads / (WAVES * kWave)) return RTS_EUNSUPPORTED;  // never: kv_attend_fits, and fewer rows where split
     hipLaunchKernelGGL((kv_attend_kernel<D, E4M3, BIG, WAVES>), dim3((unsigned)grid), dim3(WAVES * kWave),
                        WAVES * (KvShape<D, E4M3>::kWaveB), s, a, plan.target, plan.rounds, parts);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
@@ -605,7 +608,6 @@ static int launch_kv_waves(const KvArgs& a, int64_t grid, const KvPlan& plan, co
 template <int D, bool E4M3, bool BIG>
 static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {
     const int64_t blocks = kv_blocks(a.heads, a.kv_heads);
-    if (a.rows * a.heads > kMaxThreads / kJoinBlock) return RTS_EUNSUPPORTED;
     if (plan.target == 0) {
         constexpr int kWide = wide_waves(KvShape<D, E4M3>::kRowB);
         return a.rows * blocks <= kKvWideMost ? launch_kv_waves<D, E4M3, BIG, kWide>(a, a.rows * blocks, plan, KvParts{}, s)
@@ -620,7 +622,7 @@ static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hi
     if (rc != RTS_OK) return rc;
     // Few of them are cut finer, to have more of the chip read the pieces: 8 heads of one
     // request of 131072 positions 7.3 us, 15.8 whole; 32 heads 5.6 both; 128 (4 requests of 1000) 4.0 and 3.7.
-    const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);
+    const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);  // split calls: 2^22 pairs at most
     const int group = a.heads / a.kv_heads;
     if (a.rows * a.heads <= 32)
         hipLaunchKernelGGL((kv_join_kernel<D, 32>), dim3(pairs.x, D / 32), block, 0, s, parts, a.heads, group, a.scale,
