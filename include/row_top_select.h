@@ -588,7 +588,7 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
  * Maxima and a sum's terms are held in 32 bits, sums over more than 32 terms and
  * values in 64.
  * Errors: RTS_EINVAL, RTS_EUNSUPPORTED (beams, k, vocab >= 2^31, groups * beams
- *         >= 2^31), RTS_EWORKSPACE, RTS_EHIP.
+ *         >= 2^24), RTS_EWORKSPACE, RTS_EHIP.
  */
 size_t beam_select_workspace_size(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k);
 int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, int64_t vocab, int64_t ld_logits,

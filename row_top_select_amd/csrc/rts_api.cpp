@@ -490,7 +490,7 @@ int merge_attend_rank_major(const void* parts, int dtype, const float* part_lse,
 namespace {
 int beam_args(int dtype, int64_t groups, int32_t beams, int64_t vocab, int32_t k) {
     if ((dtype != RTS_F32 && dtype != RTS_BF16) || groups < 0 || beams < 1 || vocab < 1 || k < 1) return RTS_EINVAL;
-    if (beams > rts::kMaxBeams || k > rts::kMaxBeamK || vocab > 0x7FFFFFFFll || groups > 0x7FFFFFFFll / beams)
+    if (beams > rts::kMaxBeams || k > rts::kMaxBeamK || vocab > 0x7FFFFFFFll || groups > rts::kMaxBeamRows / beams)
         return RTS_EUNSUPPORTED;
     return RTS_OK;
 }
@@ -517,8 +517,6 @@ int beam_select(const void* logits, int dtype, int64_t groups, int32_t beams, in
     const rts::BeamPlan plan = rts::plan_beam_select(dtype, groups, beams, vocab, k);
     if (!workspace && (workspace_bytes > 0 || plan.ws_bytes > 0)) return RTS_EINVAL;
     if (workspace_bytes < plan.ws_bytes) return RTS_EWORKSPACE;
-    if (groups * beams * plan.pieces > rts::kMaxThreads / 256 || groups > rts::kMaxThreads / 1024)
-        return RTS_EUNSUPPORTED;
     if (out_scores == scores && k != beams) return RTS_EINVAL;  // a group's would go over another's
     rts::BeamArgs a{};
     a.logits = logits, a.scores = scores, a.out_scores = out_scores, a.ended = ended, a.parents = parents;

@@ -174,6 +174,7 @@ int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int
 
 constexpr int kMaxBeams = 64;
 constexpr int kMaxBeamK = 64;
+constexpr int64_t kMaxBeamRows = (1 << 24) - 1;  // groups * beams: workgroups of 256 threads in a launch
 
 struct BeamArgs {
     const void* logits;

@@ -51,3 +51,30 @@ def test_most_rows_of_attention(rows, heads, kv):
     out[some] = 0
     lse[some] = -math.inf
     assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
+def test_rows_of_a_selection():
+    for groups, beams in ((1 << 24, 1), (1 << 18, 64), (5592406, 3)):
+        assert beam(groups=groups, beams=beams, ld=100000) == EUNSUP
+        assert lib.beam_select_workspace_size(0, groups, beams, 100000, 4) == 0
+        assert lib.beam_select_workspace_size(0, groups - 1, beams, 100000, 4) > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("groups,beams", [((1 << 24) - 1, 1), (4194304, 1), (5592405, 3), (262143, 64)])
+def test_most_rows_of_a_selection(groups, beams):
+    vocab = 3
+    g = torch.Generator(device="cuda").manual_seed(groups)
+    logits = torch.randn(groups * beams, vocab, generator=g, device="cuda")
+    scores = -torch.rand(groups, beams, generator=g, device="cuda")
+    got = rts.beam_select(logits, scores, 2)
+    x = logits.double()
+    v = (scores.double().view(-1, 1) + x - torch.logsumexp(x, 1, keepdim=True)).view(groups, beams * vocab)
+    best, at = v.topk(2, 1)
+    assert float((got.scores.double() - best).abs().max()) < 2e-6
+    # Where the next values are further off than sums are, the picks are those of 64 bits.
+    third = v.topk(3, 1).values if beams * vocab > 2 else None
+    clear = (best[:, 0] - best[:, 1] > 4e-6) & (third[:, 1] - third[:, 2] > 4e-6)
+    row = torch.arange(groups, device="cuda").view(-1, 1) * beams + at // vocab
+    assert int(clear.sum()) > groups * 0.99
+    assert torch.equal(got.parents[clear].long(), row[clear]) and torch.equal(got.tokens[clear].long(), (at % vocab)[clear])
