@@ -1110,7 +1110,7 @@ def kv_attend_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [cache_rows, kv_heads, dim] (bfloat16, or float8_e4m3fn with ``k_scales`` and ``v_scales`` [kv_heads]), a token
     seeing the positions below its ``row_ends``, the last ``window`` of them where that is not 0; ``req_id`` and
     ``row_ends`` as assign_slots writes them.  ``max_len`` bounds row_ends and only steers the split (default: what
-    the table holds).  Returns (out, lse); see kv_attend_paged in the header.  ``workspace`` as in topk_rows.
+    the table holds, which for short contexts in wide tables costs some microseconds).  Returns (out, lse); see kv_attend_paged in the header.  ``workspace`` as in topk_rows.
     Without a backward pass: inputs that require gradients are refused."""
     _no_grad("kv_attend_paged", q, k_cache, v_cache, k_scales, v_scales)
     device = _gpu(q, "q")

@@ -19,8 +19,8 @@
 // Where rows are short and beams few, one workgroup does both.
 //
 // Bound by the reads.  Measured, the scan and the join: 256 x 102400 bf16, k = 8:
-// 15.7 + 5.0 us (3.3 TB/s); 1024 x 131072 bf16 and k = 32, the whole call: 62 us
-// (4.3 TB/s); 1024 x 131071 f32, k = 32: 96 + 6.5 us (5.6 TB/s).  On short rows it is
+// 15.9 + 5.0 us (3.3 TB/s); 1024 x 131072 bf16 and k = 32, the whole call: 62 us
+// (4.3 TB/s); 1024 x 131071 f32, k = 32: 94 to 99 + 7 us (5.4 to 5.7 TB/s).  On short rows it is
 // bound by the chain of steps that a piece is: 2000 clocks to the first group, 850 its
 // sum, 900 a bound, 2500 the end.  Elements appended one at a time as a row passes
 // took the first case 17.3 us.

@@ -20,8 +20,8 @@
 // lost: with one alone the weights' rounding is the larger part of a result's error (2.3e-3
 // for 1.7e-3 of its size, which is the rounding of the output itself).
 //
-// Bound by the reads: 64 requests of up to 16384 positions, 8 key heads of 128, bf16, 569 us
-// (5.7 TB/s); three of 131072, 4 key heads, e4m3, 63 us (4.8 TB/s) and the join 6.5.
+// Bound by the reads: 64 requests of up to 16384 positions, 8 key heads of 128, bf16, 567 us
+// (5.7 TB/s); three of 131072, 4 key heads, e4m3, 66 us (4.6 TB/s) and the join 6.6.
 // Pieces are of one size over all rows, so that the last workgroups end together
 // however ragged the contexts are (a number of pieces a row, and offsets in 64 bits,
 // took 605 and 88 us with the joins, for 573 and 70).
@@ -42,10 +42,10 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kKvTile = 32;     // keys of a stage
 constexpr int kKvStages = 2;
-constexpr int kKvWaves = 2;     // (1: 64 requests of 16384 positions 584 us for 569, 4 of 1000 10.2 for 8.6)
+constexpr int kKvWaves = 2;     // (1: 64 requests of 16384 positions 584 us for 567, 4 of 2000 11.1 for 11.2)
 constexpr int kKvHeads = 16;    // query heads of a workgroup
-// Tiles of a piece at least: one a wave.  Kernels, us, with 2, 4 and 8: 4 requests of 2000 positions 9.0, 10.8
-// and 10.8; of 3800, 64 elements, 7.4, 9.1 and 9.8.
+// Tiles of a piece at least: one a wave.  Kernels, us, with 2, 4 and 8: 4 requests of 2000 positions 11.2, 11.8
+// and 12.0; of 3800, 64 elements, 10.2, 10.3 and 10.7.
 constexpr int kKvLeast = kKvLeastKeys / kKvTile;
 // Tiles of a piece of long contexts.  3 requests of 131072 positions, e4m3, 63 us (24: 74, 96: 62); 64 of
 // 16384, bf16, 569 us (24: 570, 96: 572, whose last pieces end later).
@@ -575,16 +575,26 @@ bool kv_attend_fits(int64_t rows, int32_t heads, int32_t kv_heads) {
 KvPlan plan_kv_attend(int64_t rows, int32_t heads, int32_t kv_heads, int32_t dim, int dtype, int64_t max_len,
                       bool allow_split) {
     const int64_t blocks = kv_blocks(heads, kv_heads);
-    // Rows that a workgroup each has done in the time of the second launch, some 4 us, are not
-    // split: a step of 64 keys takes two waves 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements, and
-    // more waves less.  Calls of 4 rows, split and whole, us: 128 elements, bf16, four waves 17 and 13.5
-    // for 1024 keys, 17 and 23 for 2048; e4m3, eight waves 18.5 and 15.6 for 2048; 64 elements, eight
-    // waves 17 and 13 for 2048; 256 elements, two waves 18 and 15 for 384, 18 and 18 for 512.
-    // Every workgroup of a split call sums up the rows, so calls of very many are not, either.
+    // Rows that a workgroup each has done in the time of the second launch are not split: a step
+    // of 64 keys takes two waves 0.7, 1.0 and 1.85 us for 64, 128 and 256 elements, and more waves less.
+    // The border is that of eager calls, which wait some 4 us more for the host's second launch; replayed from a
+    // graph, calls of few rows gain by a split from about half of it on.  Calls of 4 rows of 32 heads on 8, us,
+    // split and whole, eager, then replayed: 128 elements, bf16, four waves 18.5 and 14.2, 10.6 and 11.7 for 768
+    // keys, 19.9 and 17.3, 13.2 and 16.3 for 1256, 18.4 and 23.5, 14.5 and 22.5 for 2000; e4m3, eight waves 19.1 and
+    // 17.0, 13.0 and 16.1 for 2000; 64 elements, eight waves 18.7 and 18.7, 13.7 and 17.6 for 3000; 256
+    // elements, two waves 18.8 and 16.8, 12.7 and 15.4 for 384.  Of 16 rows: 128 elements 20.6 and 18.6, 19.1 and
+    // 17.8 for 1256, 27 and 31, 26 and 30 for 2000.
+    // Every workgroup of a split call sums up the rows, so calls of very many are not split, either.  Up to some
+    // 2048 rows that pays where one is much longer than the others, and costs where they are alike (a caller
+    // who knows that gives no workspace).  Replayed, us, split and whole, 1 key head of 128, bf16: one row of
+    // 30000 keys among others of 500: of 64 rows 24 and 257, 1024 297 and 539, 2048 300 and 561, 4096 719 and 602;
+    // 1000 to 2000 keys: 64 rows 18 and 23, 256 61 and 48, 1024 187 and 152, 4096 981 and 564; 3000 to 6000 keys:
+    // 256 rows 123 and 114, 4096 1827 and 1655; 8 key heads, 1000 to 2000: 64 rows 88 and 84, 512 599 and 570.
     const int64_t waves = kv_waves(rows * blocks, dim * (dtype == RTS_E4M3 ? 1 : 2));
     if (!allow_split || max_len <= kKvWhole * (waves + 2) / 4 / (dim + 48) || rows > 4096) return KvPlan{0, 0, 0};
     // The grid has room for what max_len may need: workgroups without a piece take
-    // a place for 2 us each (8 times too many of them cost a call of 8 us another 7).
+    // a place for 2 us each.  With 131072 for a bound, 4 rows of 4000 keys take 22 us in place of 17; of 1000, which
+    // are split by it, 16.7 in place of 14.1, and 64 of them 56 in place of 48 split and 45 whole (replayed).
     const int64_t tiles = max_len < (1ll << 31) ? (max_len + kKvTile - 1) / kKvTile : 1ll << 26, all = rows * tiles;
     const int64_t places = (256 * kv_places(dim, dtype) + blocks - 1) / blocks, least = (all + kKvLeast - 1) / kKvLeast;
     KvPlan p;
@@ -621,7 +631,7 @@ static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hi
     const int rc = launch_kv_waves<D, E4M3, BIG, kKvWaves>(a, (a.rows + most + 1) * blocks, plan, parts, s);
     if (rc != RTS_OK) return rc;
     // Few of them are cut finer, to have more of the chip read the pieces: 8 heads of one
-    // request of 131072 positions 7.3 us, 15.8 whole; 32 heads 5.6 both; 128 (4 requests of 1000) 4.0 and 3.7.
+    // request of 131072 positions 7.3 us, 15.8 whole; 32 heads 5.6 both; 128 (4 requests of 2000) 5.0 and 3.9.
     const dim3 pairs((unsigned)(a.rows * a.heads)), block(kJoinBlock);  // split calls: 2^22 pairs at most
     const int group = a.heads / a.kv_heads;
     if (a.rows * a.heads <= 32)
@@ -633,8 +643,8 @@ static int launch_kv_of(const KvArgs& a, const KvPlan& plan, void* workspace, hi
 }
 
 // Offsets into a cache are held in 32 bits: of bytes, or of 16 bytes where it is
-// larger than 4 GB (two more vector instructions a load: 4 requests of 1000 positions 8.6
-// and 9.0 us).
+// larger than 4 GB (two more vector instructions a load: 4 requests of 1000 positions 14.0
+// and 14.2 us, 64 of 16384 567 and 569).
 template <int D, bool E4M3>
 static int launch_kv(const KvArgs& a, const KvPlan& plan, void* workspace, hipStream_t s) {
     const int64_t bytes = a.cache_rows * a.ld_cache * (E4M3 ? 1 : 2);
