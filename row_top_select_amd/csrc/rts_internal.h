@@ -166,9 +166,10 @@ int launch_latent_attend(const AttendArgs& a, const AttendPlan& plan, void* work
 
 // row_limit (device, or nullptr): rows at or past *row_limit are not written.  pieces: the parts are those of
 // one call's rows, where the lse of a part that saw keys, all with scores of -inf, is the lowest finite number.
+// unit: what the parts' lse are in units of.
 int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
                         int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
-                        const int32_t* row_limit, bool pieces, hipStream_t stream);
+                        const int32_t* row_limit, bool pieces, float unit, hipStream_t stream);
 
 // ------------------------------------------------------------ a beam-search step
 

@@ -78,6 +78,8 @@ constexpr float kNoMax = -3.402823466e38f;
 // The next number: a maximum of scores that are all -inf (weights 0, but 0 times what is not finite is NaN).
 constexpr float kLeastMax = -3.402823264e38f;
 constexpr float kLazy = 8.f;       // how far (log2) a score may pass the maximum before O is rescaled
+// What a piece's statistic is in units of: the scale, where that is above 1.
+__host__ __device__ __forceinline__ float part_unit(float scale) { return fabsf(scale) > 1.f ? fabsf(scale) : 1.f; }
 
 template <int DL>
 constexpr int stage_bytes() { return kTile * (DL + kRope) * 2; }
@@ -704,16 +706,18 @@ __global__ __launch_bounds__(kAttendBlock, 1) void latent_attend_kernel(AttendAr
     sums_ready(o);
     if (!row_ok) return;
     const int64_t rh = token * a.heads + head;
-    const float lse = l == 0.f ? -INFINITY : m * fabsf(a.scale) + __builtin_amdgcn_logf(l) * kLn2;
     const int64_t part = (int64_t)split * a.rows * a.heads + rh;
     const bool empty = l == 0.f && m == kNoMax;  // nothing was seen
     if (dp == 0 && half == 0) {
         if (splits > 1) {
-            part_lse[part] = l == 0.f && !empty ? kNoMax : lse;  // the join reads its zeros and NaN
+            // In units of part_unit: a score past 3.4e38 has no logarithm in 32 bits, its product has.
+            const float unit = part_unit(a.scale);
+            const float stat = m * (fabsf(a.scale) / unit) + __builtin_amdgcn_logf(l) * (kLn2 / unit);
+            part_lse[part] = empty ? -INFINITY : l == 0.f ? kNoMax : stat;  // kNoMax: the join reads its zeros and NaN
             if (split == 0)  // the join sees `splits` parts of every row
                 for (int p = pieces; p < splits; ++p) part_lse[(int64_t)p * a.rows * a.heads + rh] = -INFINITY;
         } else if (a.lse)
-            a.lse[rh] = lse;
+            a.lse[rh] = l == 0.f ? -INFINITY : m * fabsf(a.scale) + __builtin_amdgcn_logf(l) * kLn2;
     }
     if (splits > 1) {
         if (empty) return;  // the join reads no values of an empty part
@@ -818,7 +822,7 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& plan, void* work
     if (hipGetLastError() != hipSuccess) return RTS_EHIP;
     if (plan.splits == 1) return RTS_OK;
     return launch_merge_attend(part_out, RTS_F32, part_lse, plan.splits, a.rows, a.heads, DL, a.out, RTS_BF16, a.lse,
-                               PAGED ? a.query_starts + a.reqs : nullptr, true, s);
+                               PAGED ? a.query_starts + a.reqs : nullptr, true, part_unit(a.scale), s);
 }
 
 template <int DL, bool PAGED>
@@ -882,13 +886,15 @@ __device__ __forceinline__ void store8(uint16_t* p, f32x8 v) {
 // a (row, head) from the caches.  kMergeAhead parts are on their way while as
 // many are added, the first also while the maximum is still being found.  Bound
 // by the bytes: 8 ranks x 1000 x 128 x 512 in bf16 take 207 us, 5.7 TB/s.
-// Where no part's lse is above `none` the lse is -inf.
+// Where no part's lse is above `none` the lse is -inf.  The parts' are in units of `unit`.
 constexpr int kMergeAhead = 4;
 
 template <typename In, typename Out>
 __global__ __launch_bounds__(256) void merge_attend_kernel(
     const In* __restrict__ parts, const float* __restrict__ part_lse, int world, int64_t n, int dim8,
-    int heads, const int32_t* __restrict__ row_limit, float none, Out* __restrict__ out, float* __restrict__ lse) {
+    int heads, const int32_t* __restrict__ row_limit, float none, float unit, Out* __restrict__ out,
+    float* __restrict__ lse) {
+    const float c = unit * kLog2e;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n * dim8) return;
     const int64_t rh = i / dim8;
@@ -921,7 +927,7 @@ __global__ __launch_bounds__(256) void merge_attend_kernel(
     auto add = [&](const Group& g) {
 #pragma unroll
         for (int u = 0; u < kMergeAhead; ++u) {
-            const float w = __builtin_amdgcn_exp2f((g.x[u] - m) * kLog2e);
+            const float w = __builtin_amdgcn_exp2f((g.x[u] - m) * c);
             total += w;
             const f32x8 e = g.v[u].widen();
 #pragma unroll
@@ -942,12 +948,12 @@ __global__ __launch_bounds__(256) void merge_attend_kernel(
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
     }
     store8(out + rh * dim8 * 8 + d, acc);
-    if (lse && d == 0) lse[rh] = m <= none ? -INFINITY : m + __builtin_amdgcn_logf(total) * kLn2;
+    if (lse && d == 0) lse[rh] = m <= none ? -INFINITY : fmaf(__builtin_amdgcn_logf(total), kLn2, m * unit);
 }
 
 int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int32_t world, int64_t rows,
                         int32_t heads, int32_t dim, void* out, int out_dtype, float* lse,
-                        const int32_t* row_limit, bool pieces, hipStream_t s) {
+                        const int32_t* row_limit, bool pieces, float unit, hipStream_t s) {
     const float none = pieces ? kNoMax : -INFINITY;
     const int64_t n = rows * heads, blocks = (n * (dim / 8) + 255) / 256;
     if (blocks > kMaxThreads / 256) return RTS_EUNSUPPORTED;
@@ -958,13 +964,13 @@ int launch_merge_attend(const void* parts, int dtype, const float* part_lse, int
     float* of = static_cast<float*>(out);
     uint16_t* oh = static_cast<uint16_t*>(out);
     if (dtype == RTS_F32 && out_dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<float, float>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, of, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<float, float>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, unit, of, lse);
     else if (dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<float, uint16_t>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, oh, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<float, uint16_t>), g, b, 0, s, pf, part_lse, world, n, d8, heads, row_limit, none, unit, oh, lse);
     else if (out_dtype == RTS_F32)
-        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, float>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, of, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, float>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, unit, of, lse);
     else
-        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, uint16_t>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, oh, lse);
+        hipLaunchKernelGGL((merge_attend_kernel<uint16_t, uint16_t>), g, b, 0, s, ph, part_lse, world, n, d8, heads, row_limit, none, unit, oh, lse);
     return hipGetLastError() == hipSuccess ? RTS_OK : RTS_EHIP;
 }
 
