@@ -172,7 +172,7 @@ __device__ __forceinline__ void scan_row(const BeamArgs& a, ScanLds<WAVES>& lds,
     // that sums go over to a new maximum without a rounding.  The sum is taken relative to the
     // maximum's own term, what is computed for x = m: a row whose weight is all on one logit has
     // its logarithm to the last bit, and none is below its largest logit.  A group's terms are added in
-    // 32 bits, groups in 64: 4 to 8 roundings of a row's sum are left, 1e-7 of it.
+    // 32 bits, groups in 64: ten roundings of a row's sum are left at most, some 1e-7 of it.
     // Past 1e6 the difference would come near the range of an exponential, and they are e^(x - m).
     double sum = 0.;
     float c2;
